@@ -45,8 +45,8 @@ def listed():
         _case("attn-gqa5", "attn", 32, 40, 8, 128, 8192, 32, "int8", "f16", low=700),
         # the largest decode: 64 sequences of 32768 tokens, four heads per KV head, weights accumulated for eviction
         _case("attn-32k-acc", "attn", 64, 32, 8, 128, 32768, 64, "e4m3", "bf16", acc=True),
-        # a step that checks three drafted tokens and its own: four queries, eight heads per KV head, causal
-        _case("attn-draft", "attn", 8, 64, 8, 128, 20011, 128, "int8", "bf16", low=9000, n_q=4),
+        # a step that feeds four known tokens of each sequence (a prompt's last piece), eight heads per KV head, causal
+        _case("attn-4q", "attn", 8, 64, 8, 128, 20011, 128, "int8", "bf16", low=9000, n_q=4),
         # one long sequence: choose 64 of up to 2048 blocks
         _case("select-1", "select", 1, 32, 8, 128, 131072, 64, "e4m3", "bf16", n_sel=64),
         # 16 long sequences of ragged lengths
