@@ -15,6 +15,8 @@ extern "C" cudaError_t kvq_internal_status_prefill(cudaStream_t, uint32_t*);
 extern "C" cudaError_t kvq_internal_status_select(cudaStream_t, uint32_t*);
 extern "C" cudaError_t kvq_internal_status_decode(cudaStream_t, uint32_t*);
 extern "C" cudaError_t kvq_internal_status_policy(cudaStream_t, uint32_t*);
+extern "C" cudaError_t kvq_internal_status_block8(cudaStream_t, uint32_t*);
+extern "C" cudaError_t kvq_internal_status_block8_attn(cudaStream_t, uint32_t*);
 
 namespace kvq {
 
@@ -345,6 +347,164 @@ kvq_status minikv_prefill_build(kvq_cache* c, const void* k, const void* v, int 
     return kvq::run_minikv_fused_build(*c, k, v, T, score, k_hh, kmax, w_recent, idx_out, (cudaStream_t)stream);
 }
 
+// ---------------------------------------------------------------- 8-bit block cache
+
+static kvq_status check_block8(const kvq_block8* c, const char* who) {
+    KVQ_REQUIRE(c, KVQ_EINVAL, "%s: null cache", who);
+    KVQ_REQUIRE(c->B > 0 && c->Hq > 0 && c->Hkv > 0 && c->Hq % c->Hkv == 0, KVQ_EINVAL, "%s: bad B/Hq/Hkv", who);
+    KVQ_REQUIRE(c->Hq / c->Hkv <= KVQ_BLOCK8_MAX_GROUP, KVQ_EUNSUPPORTED, "%s: more than %d query heads per KV head",
+                who, KVQ_BLOCK8_MAX_GROUP);
+    KVQ_REQUIRE(c->D == 64 || c->D == 128, KVQ_EUNSUPPORTED, "%s: head dim %d unsupported (64 or 128)", who, c->D);
+    KVQ_REQUIRE(c->dtype == KVQ_F16 || c->dtype == KVQ_BF16, KVQ_EINVAL, "%s: dtype must be f16 or bf16", who);
+    KVQ_REQUIRE(c->code == KVQ_CODE_E4M3 || c->code == KVQ_CODE_INT8, KVQ_EINVAL, "%s: code must be e4m3 or int8", who);
+    KVQ_REQUIRE(c->block == 16 || c->block == 32 || c->block == 64 || c->block == 128, KVQ_EINVAL,
+                "%s: block must be 16, 32, 64 or 128 tokens (got %d)", who, c->block);
+    KVQ_REQUIRE(c->max_blocks > 0 && c->n_blocks > 0, KVQ_EINVAL, "%s: max_blocks and n_blocks must be positive", who);
+    // counts, token numbers and work items (16 tokens each, for every query) are 32-bit
+    KVQ_REQUIRE((long long)c->max_blocks * c->block <= (1LL << 30), KVQ_EUNSUPPORTED, "%s: more than 2^30 tokens per unit",
+                who);
+    KVQ_REQUIRE((long long)c->B * c->Hq <= (1LL << 24) &&
+                    (long long)c->B * c->Hkv <= ((1LL << 35) / KVQ_BLOCK8_MAX_Q) / ((long long)c->max_blocks * c->block),
+                KVQ_EUNSUPPORTED, "%s: cache too large", who);
+    KVQ_REQUIRE(c->k_codes && c->v_codes && c->k_scale && c->v_scale && c->k_bound && c->bound_scale && c->tail_k &&
+                    c->tail_v && c->table && c->count && c->seq_len && c->block_pos && c->acc,
+                KVQ_EINVAL, "%s: null array", who);
+    KVQ_REQUIRE(aligned(c->k_codes, 16) && aligned(c->v_codes, 16) && aligned(c->k_bound, 16) && aligned(c->tail_k, 16) &&
+                    aligned(c->tail_v, 16),
+                KVQ_EINVAL, "%s: codes, bounds and tails must be 16-byte aligned", who);
+    KVQ_REQUIRE(aligned(c->k_scale, 4) && aligned(c->v_scale, 4) && aligned(c->bound_scale, 4) && aligned(c->table, 4) &&
+                    aligned(c->count, 4) && aligned(c->seq_len, 4) && aligned(c->block_pos, 4) && aligned(c->acc, 4),
+                KVQ_EINVAL, "%s: misaligned array", who);
+    return KVQ_OK;
+}
+
+// Element strides {b, h, t} of x [B, H, n, D]; NULL means contiguous.
+static kvq_status row_strides(const void* x, const int64_t* given, int H, int n, int D, const char* who, int64_t* out) {
+    KVQ_REQUIRE(x, KVQ_EINVAL, "%s: null pointer", who);
+    KVQ_REQUIRE(aligned(x, 16), KVQ_EINVAL, "%s: activations must be 16-byte aligned", who);
+    const int64_t dense[3] = {(int64_t)H * n * D, (int64_t)n * D, D};
+    for (int i = 0; i < 3; ++i) {
+        out[i] = given ? given[i] : dense[i];
+        KVQ_REQUIRE(out[i] >= 0 && out[i] % 8 == 0, KVQ_EINVAL, "%s: strides must be >= 0 and multiples of 8 elements",
+                    who);
+    }
+    return KVQ_OK;
+}
+
+kvq_status block8_reset(kvq_block8* c, const int32_t* mask, void* stream) {
+    kvq_status st = check_block8(c, "block8_reset");
+    if (st != KVQ_OK) return st;
+    return cuda_status(kvq::launch_block8_reset(*c, mask, (cudaStream_t)stream), "block8_reset launch");
+}
+
+kvq_status block8_append(kvq_block8* c, const void* k, const int64_t* k_strides, const void* v,
+                         const int64_t* v_strides, int n, const int32_t* n_new, const float* colscore,
+                         void* stream) {
+    kvq_status st = check_block8(c, "block8_append");
+    if (st != KVQ_OK) return st;
+    KVQ_REQUIRE(n >= 0, KVQ_EINVAL, "block8_append: negative size");
+    if (n == 0) return KVQ_OK;
+    KVQ_REQUIRE(n <= c->max_blocks * c->block, KVQ_EINVAL, "block8_append: n = %d tokens exceed the table's %d", n,
+                c->max_blocks * c->block);
+    int64_t ks[3], vs[3];
+    if ((st = row_strides(k, k_strides, c->Hkv, n, c->D, "block8_append", ks)) != KVQ_OK) return st;
+    if ((st = row_strides(v, v_strides, c->Hkv, n, c->D, "block8_append", vs)) != KVQ_OK) return st;
+    return cuda_status(kvq::launch_block8_append(*c, k, ks, v, vs, n, n_new, colscore, (cudaStream_t)stream),
+                       "block8_append launch");
+}
+
+static kvq_status check_queries(const kvq_block8* c, int n_q, const char* who) {
+    kvq_status st = check_block8(c, who);
+    if (st != KVQ_OK) return st;
+    KVQ_REQUIRE(n_q >= 1, KVQ_EINVAL, "%s: n_q must be positive", who);
+    KVQ_REQUIRE(n_q <= KVQ_BLOCK8_MAX_Q, KVQ_EUNSUPPORTED, "%s: more than %d queries per sequence", who,
+                KVQ_BLOCK8_MAX_Q);
+    return KVQ_OK;
+}
+
+static kvq_status check_ws(const void* ws, size_t given, size_t need, const char* who) {
+    KVQ_REQUIRE(need == 0 || (ws && given >= need), KVQ_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who,
+                need, ws ? given : (size_t)0);
+    KVQ_REQUIRE(need == 0 || aligned(ws, 256), KVQ_EINVAL, "%s: workspace must be 256-byte aligned", who);
+    return KVQ_OK;
+}
+
+// Rows of n_sel list entries; the work items (16 tokens) of all lists together are 32-bit.
+static kvq_status check_list(const kvq_block8* c, int n_q, int n_sel, const char* who) {
+    KVQ_REQUIRE(n_sel <= (1 << 20) &&
+                    (long long)n_sel * c->block <= (1LL << 35) / ((long long)c->B * c->Hkv * n_q), KVQ_EUNSUPPORTED,
+                "%s: n_sel = %d is too large", who, n_sel);
+    return KVQ_OK;
+}
+
+size_t block8_attn_workspace_bytes(const kvq_block8* c, int n_q, int n_sel, int accumulate) {
+    const char* who = "block8_attn_workspace_bytes";
+    if (check_queries(c, n_q, who) != KVQ_OK) return (size_t)-1;
+    if (n_sel < 0) {
+        set_error("%s: n_sel must be >= 0", who);
+        return (size_t)-1;
+    }
+    if (check_list(c, n_q, n_sel, who) != KVQ_OK) return (size_t)-1;
+    return kvq::block8_attn_bytes(*c, n_q, n_sel, accumulate);
+}
+
+kvq_status block8_attn(const void* q, const int64_t* q_strides, int n_q, const int32_t* n_new, kvq_block8* c,
+                       float sm_scale, const int32_t* blocks, const int32_t* list_len, int n_sel,
+                       int accumulate, void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    kvq_status st = check_queries(c, n_q, "block8_attn");
+    if (st != KVQ_OK) return st;
+    int64_t qs[3];
+    if ((st = row_strides(q, q_strides, c->Hq, n_q, c->D, "block8_attn", qs)) != KVQ_OK) return st;
+    KVQ_REQUIRE(o && aligned(o, 16) && aligned(lse, 4), KVQ_EINVAL, "block8_attn: o must be given and 16-byte aligned");
+    KVQ_REQUIRE(sm_scale > 0.0f, KVQ_EINVAL, "block8_attn: sm_scale must be positive");
+    if (blocks) {
+        KVQ_REQUIRE(list_len && n_sel >= 1, KVQ_EINVAL, "block8_attn: a block list needs list_len and n_sel >= 1");
+        if ((st = check_list(c, n_q, n_sel, "block8_attn")) != KVQ_OK) return st;
+    } else {
+        KVQ_REQUIRE(!list_len && n_sel == 0, KVQ_EINVAL, "block8_attn: list_len or n_sel without a block list");
+    }
+    if ((st = check_ws(ws, ws_bytes, kvq::block8_attn_bytes(*c, n_q, n_sel, accumulate), "block8_attn")) != KVQ_OK)
+        return st;
+    return cuda_status(kvq::launch_block8_attn(q, qs, n_q, n_new, *c, sm_scale, blocks, list_len, n_sel, accumulate, o,
+                                               lse, ws, (cudaStream_t)stream),
+                       "block8_attn launch");
+}
+
+size_t block8_select_workspace_bytes(const kvq_block8* c, int n_q) {
+    if (check_queries(c, n_q, "block8_select_workspace_bytes") != KVQ_OK) return (size_t)-1;
+    return kvq::block8_select_bytes(*c, n_q);
+}
+
+kvq_status block8_select(const void* q, const int64_t* q_strides, int n_q, const int32_t* n_new, kvq_block8* c,
+                         int n_sel, int n_first, int n_last, int32_t* idx_out, int32_t* n_out, void* ws,
+                         size_t ws_bytes, void* stream) {
+    kvq_status st = check_queries(c, n_q, "block8_select");
+    if (st != KVQ_OK) return st;
+    int64_t qs[3];
+    if ((st = row_strides(q, q_strides, c->Hq, n_q, c->D, "block8_select", qs)) != KVQ_OK) return st;
+    KVQ_REQUIRE(idx_out && n_out, KVQ_EINVAL, "block8_select: null output");
+    KVQ_REQUIRE(n_sel >= 1 && n_first >= 0 && n_last >= 0 && n_first <= n_sel && n_last <= n_sel - n_first, KVQ_EINVAL,
+                "block8_select: n_sel >= 1, n_first, n_last >= 0 and n_first + n_last <= n_sel are needed");
+    KVQ_REQUIRE(c->max_blocks <= (1 << 20), KVQ_EUNSUPPORTED, "block8_select: more than 2^20 blocks per unit");
+    if ((st = check_list(c, n_q, n_sel, "block8_select")) != KVQ_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, kvq::block8_select_bytes(*c, n_q), "block8_select")) != KVQ_OK) return st;
+    return cuda_status(kvq::launch_block8_select(q, qs, n_q, n_new, *c, n_sel, n_first, n_last, idx_out, n_out, ws,
+                                                 (cudaStream_t)stream),
+                       "block8_select launch");
+}
+
+kvq_status block8_evict(kvq_block8* c, const int32_t* keep, int n_first, int n_last, int32_t* n_evicted,
+                        void* stream) {
+    kvq_status st = check_block8(c, "block8_evict");
+    if (st != KVQ_OK) return st;
+    KVQ_REQUIRE(keep, KVQ_EINVAL, "block8_evict: null keep");
+    KVQ_REQUIRE(n_first >= 0 && n_last >= 1 && n_first <= c->max_blocks && n_last <= c->max_blocks, KVQ_EINVAL,
+                "block8_evict: n_first >= 0 and n_last >= 1 (the open block stays), at most max_blocks");
+    KVQ_REQUIRE(c->max_blocks <= 51200, KVQ_EUNSUPPORTED, "block8_evict: more than 51200 blocks per unit");
+    return cuda_status(kvq::launch_block8_evict(*c, keep, n_first, n_last, n_evicted, (cudaStream_t)stream),
+                       "block8_evict launch");
+}
+
 size_t kvq_tier_bytes(int units, int D, int G, int k_bits, int v_bits, int k_axis, int cap,
                       size_t out[8]) {
     if (units <= 0 || D <= 0 || !valid_group(G) || D % G || !valid_bits(k_bits) || !valid_bits(v_bits) || cap < 0)
@@ -372,14 +532,16 @@ kvq_status kvq_debug_withhold_copy(int on) {
 kvq_status kvq_device_status(void* stream, uint32_t* out) {
     KVQ_REQUIRE(out, KVQ_EINVAL, "kvq_device_status: null out");
     cudaStream_t s = (cudaStream_t)stream;
-    uint32_t v[5] = {0, 0, 0, 0, 0};
+    uint32_t v[7] = {0, 0, 0, 0, 0, 0, 0};
     cudaError_t e = kvq_internal_status_quant(s, &v[0]);
     if (e == cudaSuccess) e = kvq_internal_status_prefill(s, &v[1]);
     if (e == cudaSuccess) e = kvq_internal_status_select(s, &v[2]);
     if (e == cudaSuccess) e = kvq_internal_status_decode(s, &v[3]);
     if (e == cudaSuccess) e = kvq_internal_status_policy(s, &v[4]);
+    if (e == cudaSuccess) e = kvq_internal_status_block8(s, &v[5]);
+    if (e == cudaSuccess) e = kvq_internal_status_block8_attn(s, &v[6]);
     if (e != cudaSuccess) return cuda_status(e, "kvq_device_status");
-    uint32_t all = v[0] | v[1] | v[2] | v[3] | v[4];
+    uint32_t all = v[0] | v[1] | v[2] | v[3] | v[4] | v[5] | v[6];
     *out = (all & 1u) ? (uint32_t)KVQ_ETIMEOUT : ((all & 2u) ? (uint32_t)KVQ_EDEVICE : 0u);
     return KVQ_OK;
 }

@@ -54,4 +54,20 @@ kvq_status run_pages_release(const kvq_cache& c, const int32_t* mask, cudaStream
 kvq_status run_minikv_fused_build(const kvq_cache& c, const void* k, const void* v, int T, const float* score,
                                   const int32_t* k_hh, int kmax, int w, int32_t* idx_out, cudaStream_t s);
 
+// 8-bit block cache (arguments validated by the caller; strides of 3).
+cudaError_t launch_block8_reset(const kvq_block8& c, const int32_t* mask, cudaStream_t s);
+cudaError_t launch_block8_append(const kvq_block8& c, const void* k, const int64_t* ks, const void* v,
+                                 const int64_t* vs, int n, const int32_t* n_new, const float* colscore,
+                                 cudaStream_t s);
+size_t block8_attn_bytes(const kvq_block8& c, int n_q, int n_sel, int accumulate);
+cudaError_t launch_block8_attn(const void* q, const int64_t* qs, int n_q, const int32_t* n_new, const kvq_block8& c,
+                               float sm_scale, const int32_t* blocks, const int32_t* list_len, int n_sel,
+                               int accumulate, void* o, float* lse, void* ws, cudaStream_t s);
+size_t block8_select_bytes(const kvq_block8& c, int n_q);
+cudaError_t launch_block8_select(const void* q, const int64_t* qs, int n_q, const int32_t* n_new, const kvq_block8& c,
+                                 int n_sel, int n_first, int n_last, int32_t* idx_out, int32_t* n_out, void* ws,
+                                 cudaStream_t s);
+cudaError_t launch_block8_evict(const kvq_block8& c, const int32_t* keep, int n_first, int n_last, int32_t* n_evicted,
+                                cudaStream_t s);
+
 }  // namespace kvq

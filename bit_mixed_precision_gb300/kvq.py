@@ -27,6 +27,8 @@ MAX_TIERS = 2
 EXPORTS = ["kv_quant_pack", "prefill_attn_scores", "prefill_window_scores", "kvq_score_reduce", "select_tokens",
            "minikv_prefill_build", "requant_demote", "decode_attn_qkv", "decode_attn_qkv_static",
            "kvq_pages_init", "kvq_pages_release",
+           "block8_reset", "block8_append", "block8_attn", "block8_attn_workspace_bytes", "block8_select",
+           "block8_select_workspace_bytes", "block8_evict",
            "kvq_decode_workspace_bytes", "kvq_decode_launches", "kvq_tier_bytes",
            "kvq_last_error", "kvq_device_status", "kvq_debug_withhold_copy", "kvq_version"]
 
@@ -70,6 +72,18 @@ class KvqPolicyParams(ctypes.Structure):
                 ("n_low", ctypes.c_void_p)]
 
 
+class KvqBlock8(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("code", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_bound", ctypes.c_void_p), ("bound_scale", ctypes.c_void_p),
+                ("tail_k", ctypes.c_void_p), ("tail_v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("count", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("block_pos", ctypes.c_void_p),
+                ("acc", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -100,13 +114,24 @@ def lib():
         L.kvq_decode_workspace_bytes.restype = sz
         L.kvq_decode_launches.argtypes = [ctypes.POINTER(KvqCache)]
         L.kvq_decode_launches.restype = ctypes.c_int
+        cache8, strides = ctypes.POINTER(KvqBlock8), ctypes.POINTER(ctypes.c_int64)
+        L.block8_reset.argtypes = [cache8, vp, vp]
+        L.block8_append.argtypes = [cache8, vp, strides, vp, strides, i32, vp, vp, vp]
+        L.block8_attn.argtypes = [vp, strides, i32, vp, cache8, f32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+        L.block8_attn_workspace_bytes.argtypes = [cache8, i32, i32, i32]
+        L.block8_attn_workspace_bytes.restype = sz
+        L.block8_select.argtypes = [vp, strides, i32, vp, cache8, i32, i32, i32, vp, vp, vp, sz, vp]
+        L.block8_select_workspace_bytes.argtypes = [cache8, i32]
+        L.block8_select_workspace_bytes.restype = sz
+        L.block8_evict.argtypes = [cache8, vp, i32, i32, vp, vp]
         L.kvq_tier_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
         L.kvq_tier_bytes.restype = sz
         L.kvq_last_error.restype = ctypes.c_char_p
         L.kvq_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         L.kvq_debug_withhold_copy.argtypes = [i32]
         for name in ["kv_quant_pack", "prefill_attn_scores", "prefill_window_scores", "kvq_score_reduce", "select_tokens",
-                     "minikv_prefill_build", "requant_demote", "kvq_pages_init", "kvq_pages_release", "decode_attn_qkv", "kvq_device_status", "kvq_debug_withhold_copy"]:
+                     "minikv_prefill_build", "requant_demote", "kvq_pages_init", "kvq_pages_release", "decode_attn_qkv", "kvq_device_status", "kvq_debug_withhold_copy",
+                     "block8_reset", "block8_append", "block8_attn", "block8_select", "block8_evict"]:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -542,3 +567,255 @@ def decode_attn_qkv_static(q, k_new, v_new, cache, sm_scale=None, o=None, lse=No
     _check(lib().decode_attn_qkv_static(_ptr(q), _ptr(k_new), _ptr(v_new), ctypes.byref(cache.desc),
                                         float(sm_scale), _ptr(o), _ptr(lse), _stream(stream)))
     return o, lse
+
+
+# ----------------------------------------------------------- 8-bit block cache
+
+BLOCK8_MAX_Q, BLOCK8_MAX_GROUP = 16, 64
+CODE_E4M3, CODE_INT8 = 0, 1
+_CODES = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_INT8}
+
+
+def _bad(what):
+    raise ValueError(what)
+
+
+@dataclass
+class Block8Cache:
+    """One layer's keys and values in 8-bit codes (torch.float8_e4m3fn or torch.int8) with one
+    float32 scale per block of ``block`` tokens and KV head; see kvq.h for the format.
+
+    Built from the caller's own tensors, or by make_block8_cache.  ``table`` [B*Hkv, max_blocks]
+    gives the pool block of each unit's logical block; the entries must be distinct.  ``max_q``:
+    queries per sequence that the workspace allows for in one block8_attn / block8_select call;
+    ``max_sel``: entries of a block list (the table's length by default).  ``ws``: a workspace
+    tensor (uint8, ws_bytes(...) bytes) to share between caches whose calls never overlap on
+    the GPU; one is allocated otherwise.  Calls on one cache must follow one another (one
+    stream, or events), also when they are replayed from CUDA graphs."""
+    B: int
+    Hq: int
+    Hkv: int
+    D: int
+    block: int
+    dtype: torch.dtype
+    k_codes: torch.Tensor       # [n_blocks, block, D]
+    v_codes: torch.Tensor
+    k_scale: torch.Tensor       # [n_blocks] float32
+    v_scale: torch.Tensor
+    k_bound: torch.Tensor       # [n_blocks, 2, D] int8
+    bound_scale: torch.Tensor   # [n_blocks] float32
+    tail_k: torch.Tensor        # [B*Hkv, block, D] dtype
+    tail_v: torch.Tensor
+    table: torch.Tensor         # [B*Hkv, max_blocks] int32
+    count: torch.Tensor         # [B*Hkv] int32
+    seq_len: torch.Tensor
+    block_pos: torch.Tensor     # [n_blocks] int32
+    acc: torch.Tensor           # [n_blocks] float32
+    max_q: int = 1
+    max_sel: int = 0
+    ws: torch.Tensor = None
+    desc: KvqBlock8 = field(default=None, repr=False)
+
+    def __post_init__(self):
+        U, D, P = self.B * self.Hkv, self.D, self.block
+        if self.k_codes.dtype not in _CODES:
+            raise TypeError("codes must be float8_e4m3fn or int8")
+        if self.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("activations must be float16 or bfloat16")
+        if self.table.dim() != 2 or self.k_codes.dim() != 3:
+            _bad("table must be [B*Hkv, max_blocks], codes [n_blocks, block, D]")
+        n, nb, dev = self.k_codes.shape[0], self.table.shape[1], self.k_codes.device
+        i32, f32, code = torch.int32, torch.float32, self.k_codes.dtype
+        for name, shape, dt in (("k_codes", (n, P, D), code), ("v_codes", (n, P, D), code), ("k_scale", (n,), f32),
+                                ("v_scale", (n,), f32), ("k_bound", (n, 2, D), torch.int8), ("bound_scale", (n,), f32),
+                                ("tail_k", (U, P, D), self.dtype), ("tail_v", (U, P, D), self.dtype),
+                                ("table", (U, nb), i32), ("count", (U,), i32), ("seq_len", (U,), i32),
+                                ("block_pos", (n,), i32), ("acc", (n,), f32)):
+            t = getattr(self, name)
+            if tuple(t.shape) != shape or t.dtype != dt or t.device != dev or not t.is_cuda or not t.is_contiguous():
+                _bad(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dt} on one device")
+        d = KvqBlock8(self.B, self.Hq, self.Hkv, D, F16 if self.dtype == torch.float16 else BF16, _CODES[code], P, nb, n)
+        for name, _ in KvqBlock8._fields_[9:]:
+            setattr(d, name, getattr(self, name).data_ptr())
+        self.desc, self._ref, self._device = d, ctypes.byref(d), dev
+        need = self.ws_bytes(self.max_q, self.max_sel)
+        if self.ws is None:
+            self.ws = torch.empty(need + 256, dtype=torch.uint8, device=dev)
+        elif self.ws.device != dev or not self.ws.is_contiguous() or self.ws.dtype != torch.uint8:
+            _bad("ws must be a contiguous uint8 tensor on the cache's device")
+        shift = -self.ws.data_ptr() % 256
+        self._ws, self._ws_bytes = ctypes.c_void_p(self.ws.data_ptr() + shift), self.ws.numel() - shift
+        if self._ws_bytes < need:
+            _bad(f"ws must have {need + 256} bytes")
+
+    @property
+    def units(self):
+        return self.B * self.Hkv
+
+    def ws_bytes(self, n_q, n_sel=0):
+        """Workspace that block8_select and block8_attn (dense, and with lists of n_sel blocks; the
+        table's length if 0) need for n_q queries."""
+        most = 0
+        for q in range(1, n_q + 1):
+            for b in (lib().block8_attn_workspace_bytes(self._ref, q, 0, 1),
+                      lib().block8_attn_workspace_bytes(self._ref, q, n_sel or self.table.shape[1], 1),
+                      lib().block8_select_workspace_bytes(self._ref, q)):
+                if b == ctypes.c_size_t(-1).value:
+                    raise KvqError(KVQ_EINVAL, lib().kvq_last_error().decode())
+                most = max(most, b)
+        return most
+
+    def dequantised(self, u):
+        """Keys and values [count, D] (float32) that unit u holds."""
+        n = int(self.count[u])
+        ids = self.table[u, :-(-n // self.block)].long()
+        return tuple((c.view(torch.uint8)[ids].view(c.dtype).float() * s[ids, None, None]).reshape(-1, self.D)[:n]
+                     for c, s in ((self.k_codes, self.k_scale), (self.v_codes, self.v_scale)))
+
+
+def make_block8_cache(B, Hq, Hkv, D, dtype, max_tokens, block=64, codes=torch.float8_e4m3fn, max_q=1, max_sel=0,
+                      device="cuda", ws=None):
+    """An empty Block8Cache with room for max_tokens tokens per unit; unit u owns the pool's blocks
+    u * max_blocks ... in order."""
+    if block not in (16, 32, 64, 128) or max_tokens < 1:
+        _bad("block must be 16, 32, 64 or 128 and max_tokens positive")
+    nb, U = -(-max_tokens // block), B * Hkv
+    n = U * nb
+    z = lambda *shape, dt: torch.zeros(shape, dtype=dt, device=device)
+    i32, f32 = torch.int32, torch.float32
+    return Block8Cache(B, Hq, Hkv, D, block, dtype,
+                       k_codes=z(n, block, D, dt=torch.uint8).view(codes), v_codes=z(n, block, D, dt=torch.uint8).view(codes),
+                       k_scale=z(n, dt=f32), v_scale=z(n, dt=f32), k_bound=z(n, 2, D, dt=torch.int8),
+                       bound_scale=z(n, dt=f32), tail_k=z(U, block, D, dt=dtype), tail_v=z(U, block, D, dt=dtype),
+                       table=torch.arange(n, dtype=i32, device=device).view(U, nb), count=z(U, dt=i32),
+                       seq_len=z(U, dt=i32), block_pos=z(n, dt=i32), acc=z(n, dt=f32), max_q=max_q, max_sel=max_sel, ws=ws)
+
+
+class _On:
+    """The stream of a block8 call: outputs are allocated on it, and the tensors that a call on
+    another stream than torch's current one reads are kept from reuse until it is done."""
+
+    def __init__(self, cache, stream):
+        if cache._device.index != torch.cuda.current_device():
+            _bad(f"the cache is on {cache._device}, the current device is cuda:{torch.cuda.current_device()}")
+        self.current = torch.cuda.current_stream()
+        self.stream = stream or self.current
+        if self.stream.device != cache._device:
+            _bad("the stream belongs to another device than the cache")
+        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
+
+    def empty(self, like, shape, dtype):
+        if self.stream == self.current:
+            return torch.empty(shape, dtype=dtype, device=like._device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=like._device)
+
+    def used(self, *ts):
+        if self.stream != self.current:
+            for t in ts:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def _rows8(cache, x, heads, name):
+    """x as [B, heads, n, D] with 8-element strides and D contiguous (steps may leave n out)."""
+    if x.dim() == 3:
+        x = x.unsqueeze(2)
+    if x.dim() != 4 or x.shape[0] != cache.B or x.shape[1] != heads or x.shape[3] != cache.D:
+        _bad(f"{name} must be [{cache.B}, {heads}, n, {cache.D}], got {list(x.shape)}")
+    if x.dtype != cache.dtype:
+        raise TypeError(f"{name} must have the cache's dtype {cache.dtype}")
+    if x.device != cache._device:
+        _bad(f"{name} must be on the cache's device")
+    if x.stride(3) != 1:
+        _bad(f"{name}: the last axis must be contiguous")
+    return x, (ctypes.c_int64 * 3)(*[s if n > 1 else 0 for n, s in zip(x.shape[:3], x.stride())])
+
+
+def _ints8(cache, t, shape, name):
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()
+                          or t.device != cache._device):
+        _bad(f"{name} must be a contiguous int32 tensor {list(shape)} on the cache's device")
+
+
+def block8_reset(cache, mask=None, stream=None):
+    """Empties the units with mask[u] != 0 (int32 [B*Hkv]); every unit without a mask."""
+    on = _On(cache, stream)
+    _ints8(cache, mask, (cache.units,), "mask")
+    _check(lib().block8_reset(cache._ref, _ptr(mask), on.ptr))
+    on.used(mask)
+
+
+def block8_append(cache, k, v, n_new=None, colscore=None, stream=None):
+    """Quantises new tokens k, v [B, Hkv, n, D] (or [B, Hkv, D]) into the cache.  n_new int32 [B]: rows
+    of each sequence that count.  colscore float32 [B, Hq, n]: column scores of a prompt
+    (prefill_attn_scores), added to the blocks' acc."""
+    on = _On(cache, stream)
+    k, ks = _rows8(cache, k, cache.Hkv, "k")
+    v, vs = _rows8(cache, v, cache.Hkv, "v")
+    n = k.shape[2]
+    if v.shape != k.shape:
+        _bad("k and v must have one shape")
+    _ints8(cache, n_new, (cache.B,), "n_new")
+    if colscore is not None and (tuple(colscore.shape) != (cache.B, cache.Hq, n) or colscore.dtype != torch.float32
+                                 or not colscore.is_contiguous() or colscore.device != cache._device):
+        _bad(f"colscore must be a contiguous float32 tensor [{cache.B}, {cache.Hq}, {n}] on the cache's device")
+    _check(lib().block8_append(cache._ref, _ptr(k), ks, _ptr(v), vs, n, _ptr(n_new), _ptr(colscore), on.ptr))
+    on.used(k, v, n_new, colscore)
+
+
+def block8_attn(q, cache, sm_scale=None, blocks=None, accumulate=False, n_new=None, o=None, lse=None, stream=None):
+    """Attention of q [B, Hq, n_q, D] (or [B, Hq, D]), the last tokens of the cache; returns (o, lse) in q's
+    shape.  blocks: (idx, n) as block8_select returns them, to read only those blocks.
+    accumulate: adds each block's softmax weight to cache.acc."""
+    on = _On(cache, stream)
+    shape = tuple(q.shape)
+    q, qs = _rows8(cache, q, cache.Hq, "q")
+    n_q = q.shape[2]
+    _ints8(cache, n_new, (cache.B,), "n_new")
+    idx = n = None
+    if blocks is not None:
+        idx, n = blocks
+        _ints8(cache, n, (cache.B, cache.Hkv, n_q), "blocks[1]")
+        _ints8(cache, idx, (cache.B, cache.Hkv, n_q, idx.shape[-1]), "blocks[0]")
+    o = on.empty(cache, shape, cache.dtype) if o is None else o
+    lse = on.empty(cache, shape[:-1], torch.float32) if lse is None else lse
+    for t, s, dt, name in ((o, shape, cache.dtype, "o"), (lse, shape[:-1], torch.float32, "lse")):
+        if tuple(t.shape) != s or t.dtype != dt or not t.is_contiguous() or t.device != cache._device:
+            _bad(f"{name} must be a contiguous tensor {list(s)} of {dt} on the cache's device")
+    _check(lib().block8_attn(_ptr(q), qs, n_q, _ptr(n_new), cache._ref,
+                             1.0 / math.sqrt(cache.D) if sm_scale is None else float(sm_scale), _ptr(idx), _ptr(n),
+                             0 if idx is None else idx.shape[-1], 1 if accumulate else 0, _ptr(o), _ptr(lse),
+                             cache._ws, cache._ws_bytes, on.ptr))
+    on.used(q, n_new, idx, n, o, lse)
+    return o, lse
+
+
+def block8_select(q, cache, n_sel, n_first=1, n_last=1, n_new=None, out=None, stream=None):
+    """The n_sel blocks whose key bounds match q [B, Hq, n_q, D] (or [B, Hq, D]) best, the first n_first and
+    last n_last always among them: (idx [B, Hkv, n_q, n_sel] ascending, -1 behind the last; n [B, Hkv, n_q])."""
+    on = _On(cache, stream)
+    q, qs = _rows8(cache, q, cache.Hq, "q")
+    n_q = q.shape[2]
+    _ints8(cache, n_new, (cache.B,), "n_new")
+    shape = (cache.B, cache.Hkv, n_q)
+    idx, n = out if out is not None else (on.empty(cache, shape + (max(int(n_sel), 0),), torch.int32),
+                                          on.empty(cache, shape, torch.int32))
+    _ints8(cache, idx, shape + (n_sel,), "idx")
+    _ints8(cache, n, shape, "n")
+    _check(lib().block8_select(_ptr(q), qs, n_q, _ptr(n_new), cache._ref, int(n_sel), int(n_first), int(n_last),
+                               _ptr(idx), _ptr(n), cache._ws, cache._ws_bytes, on.ptr))
+    on.used(q, n_new, idx, n)
+    return idx, n
+
+
+def block8_evict(cache, keep, n_first=1, n_last=1, n_evicted=None, stream=None):
+    """Units with more than keep[u] blocks (int32 [B*Hkv]) lose those of the least accumulated attention;
+    returns the number of blocks that left each unit."""
+    on = _On(cache, stream)
+    _ints8(cache, keep, (cache.units,), "keep")
+    n_evicted = on.empty(cache, (cache.units,), torch.int32) if n_evicted is None else n_evicted
+    _ints8(cache, n_evicted, (cache.units,), "n_evicted")
+    _check(lib().block8_evict(cache._ref, _ptr(keep), int(n_first), int(n_last), _ptr(n_evicted), on.ptr))
+    on.used(keep, n_evicted)
+    return n_evicted

@@ -369,6 +369,142 @@ kvq_status kvq_pages_init(kvq_cache* c, void* stream);
  * counts reset. */
 kvq_status kvq_pages_release(kvq_cache* c, const int32_t* release_mask, void* stream);
 
+/* ---------------------------------------------------------------------- */
+/* The 8-bit block cache: one layer's keys and values in 8-bit codes with one
+ * float32 scale per block of tokens and KV head.  Tokens are appended at any
+ * time, attention reads every block or a list of blocks per query, and whole
+ * blocks leave the cache by the attention they received; a block's codes are
+ * never rounded a second time.  No counterpart on the pages named above.
+ *
+ * Unit u = b * Hkv + h holds count[u] tokens in ceil(count / block) logical
+ * blocks, all full but the last ("open") one.  Logical block i of unit u is
+ * block table[u][i] of a pool of n_blocks blocks that all units share; the
+ * caller fills the table (any distinct numbers in [0, n_blocks); entries at
+ * and behind the last block in use are the unit's free blocks, -1 for none).
+ * An entry outside the pool that a call would read or write is a
+ * device-checked error (KVQ_EDEVICE).  Tokens of a unit lie in the order of
+ * their positions; the tokens of a block have consecutive positions.
+ *
+ *   scale = max(fp32(amax * fp32(1/Q)), 2^-64), Q = 448 (e4m3) or 127 (int8),
+ *   code  = RN(fp32(x * fp32(1/scale))), saturated to [-Q, Q],  x_hat = code * scale,
+ * over the block's tokens and channels.  Key bounds per channel, for
+ * block8_select: bound_scale as above with Q = 127, low = floor(fp32(min x *
+ * fp32(1/bound_scale))), high = ceil(...) of the largest, within [-127, 127].
+ * The open block's rows are kept in 16 bits as well (tail_k / tail_v), so
+ * the codes depend on the tokens only, not on how they were split into
+ * calls.  Tokens leave by whole blocks (block8_evict) or all at once
+ * (block8_reset): no call takes back the last tokens, and a caller must not
+ * lower count by itself.  A block that holds a NaN or an infinity gets codes and bounds 0 and
+ * NaN scales: attention over it is NaN, and it ranks first in
+ * block8_select. */
+typedef enum { KVQ_CODE_E4M3 = 0, KVQ_CODE_INT8 = 1 } kvq_code8;
+
+#define KVQ_BLOCK8_MAX_Q 16      /* queries per sequence of one call */
+#define KVQ_BLOCK8_MAX_GROUP 64  /* query heads per KV head */
+
+typedef struct {
+    int32_t B, Hq, Hkv, D;      /* D 64 or 128; Hq / Hkv <= KVQ_BLOCK8_MAX_GROUP */
+    int32_t dtype;              /* kvq_dtype of k, v, q, o and the tail */
+    int32_t code;               /* kvq_code8 */
+    int32_t block;              /* tokens per block: 16, 32, 64 or 128 */
+    int32_t max_blocks;         /* table entries per unit */
+    int32_t n_blocks;           /* blocks of the pool */
+    uint8_t* k_codes;           /* (device) [n_blocks][block][D] */
+    uint8_t* v_codes;           /* (device) [n_blocks][block][D] */
+    float* k_scale;             /* (device) [n_blocks] */
+    float* v_scale;             /* (device) [n_blocks] */
+    int8_t* k_bound;            /* (device) [n_blocks][2][D]: low, high */
+    float* bound_scale;         /* (device) [n_blocks] */
+    void* tail_k;               /* (device) [u][block][D] activations */
+    void* tail_v;               /* (device) [u][block][D] */
+    int32_t* table;             /* (device) [u][max_blocks] */
+    int32_t* count;             /* (device) [u] tokens held */
+    int32_t* seq_len;           /* (device) [u] position of the next token */
+    int32_t* block_pos;         /* (device) [n_blocks] position of the block's first token */
+    float* acc;                 /* (device) [n_blocks] attention weight received */
+} kvq_block8;
+
+/* Queries and new tokens of a call: x [B, H, n, D] with element strides
+ * {b, h, t} (host array of 3, each >= 0 and a multiple of 8; NULL:
+ * contiguous), D contiguous, base 16-byte aligned.  n_new (device, nullable
+ * [B]): sequence b has n_new[b] of the n rows, 0 <= n_new[b] <= n, the others
+ * are padding (NULL: all n).  An n_new out of range is clamped and reported
+ * as KVQ_EDEVICE. */
+
+/* block8_reset -- the units u with mask[u] != 0 (device, [B*Hkv] int32; NULL:
+ * every unit) hold no token any more: count and seq_len become 0.  Their
+ * table rows stay, and with them their blocks. */
+kvq_status block8_reset(kvq_block8* c, const int32_t* mask, void* stream);
+
+/* block8_append -- quantises n new tokens per sequence into the cache.
+ *   k, v (device) [B, Hkv, n, D]; n may exceed the block (a prompt).
+ *   colscore (device, nullable) [B, Hq, n] contiguous: column scores of the
+ *   new tokens (prefill_attn_scores), summed over the group's heads and added
+ *   to acc of the token's block.  A block's acc is set to 0, and its
+ *   block_pos, when its first token arrives.
+ *   A unit whose tokens would not fit its table, or need a table entry
+ *   outside the pool, stays as it is (KVQ_EDEVICE). */
+kvq_status block8_append(kvq_block8* c, const void* k, const int64_t* k_strides, const void* v,
+                         const int64_t* v_strides, int n, const int32_t* n_new, const float* colscore,
+                         void* stream);
+
+/* block8_attn -- attention of n_q queries per sequence, the last tokens of the
+ * cache (append first): query t of sequence b with m = n_new[b] queries sees
+ * the first count[u] - m + t + 1 tokens of its unit.
+ *   q (device) [B, Hq, n_q, D], 1 <= n_q <= KVQ_BLOCK8_MAX_Q; query head h
+ *   reads KV head h / (Hq/Hkv).
+ *   blocks (device, nullable) [B, Hkv, n_q, n_sel] logical block numbers and
+ *   list_len (device) [B, Hkv, n_q] how many of them count: query t then sees
+ *   only the tokens of its listed blocks (each listed once).  A number at or
+ *   behind the unit's last block is skipped (KVQ_EDEVICE).  blocks NULL: all.
+ *   o (device) [B, Hq, n_q, D], lse (device, nullable) [B, Hq, n_q] natural
+ *   log.  A query that sees no token, and the rows t >= n_new[b], get o = 0
+ *   and lse = -inf.
+ *   accumulate != 0: acc[block] += the softmax weights of the block's tokens,
+ *   summed over the queries and the unit's query heads.
+ *   Products with q are exact and sums are float32; the softmax weights enter
+ *   the second product as a pair of fp16 numbers (22 bits).
+ *   ws (device) of at least block8_attn_workspace_bytes(), 256-byte aligned;
+ *   its content between calls is irrelevant. */
+kvq_status block8_attn(const void* q, const int64_t* q_strides, int n_q, const int32_t* n_new, kvq_block8* c,
+                       float sm_scale, const int32_t* blocks, const int32_t* list_len, int n_sel,
+                       int accumulate, void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace of block8_attn for n_q queries, n_sel list entries (0: no list);
+ * (size_t)-1 on invalid arguments. */
+size_t block8_attn_workspace_bytes(const kvq_block8* c, int n_q, int n_sel, int accumulate);
+
+/* block8_select -- the blocks whose keys may match a query best, for each query
+ * and KV head.  With q8 = RN(q / sq), sq = max(amax|q| * fp32(1/127), 2^-64)
+ * per query head, a block's score is
+ *   bound_scale * max over the group's heads of sq * sum_c max(q8_c low_c, q8_c high_c),
+ * an upper bound of q.k up to the rounding of q; the sum is exact.
+ *   q, n_q, n_new as for block8_attn.  Of the blocks that query t sees, the
+ *   first n_first, the last n_last and those of the largest scores are
+ *   chosen, n_sel in all (all blocks if there are no more); ties go to the
+ *   lower block, NaN counts as largest.  n_first, n_last >= 0, n_first +
+ *   n_last <= n_sel, n_sel >= 1.
+ *   idx_out (device) [B, Hkv, n_q, n_sel] ascending, -1 behind the last;
+ *   n_out (device) [B, Hkv, n_q].  max_blocks <= 2^20.
+ *   ws as for block8_attn, block8_select_workspace_bytes(). */
+kvq_status block8_select(const void* q, const int64_t* q_strides, int n_q, const int32_t* n_new, kvq_block8* c,
+                         int n_sel, int n_first, int n_last, int32_t* idx_out, int32_t* n_out, void* ws,
+                         size_t ws_bytes, void* stream);
+size_t block8_select_workspace_bytes(const kvq_block8* c, int n_q);
+
+/* block8_evict -- whole blocks leave the cache by the attention they received.
+ * A unit with more than keep[u] blocks keeps its first n_first, its last
+ * n_last (n_last >= 1: the open block stays) and those of the largest acc,
+ * max(keep[u], n_first + n_last) in all; ties keep the lower block, NaN
+ * counts as largest.
+ *   keep (device) [B*Hkv] blocks per unit.  The table row becomes: the kept
+ *   blocks in their order, then those that left in theirs, then the free
+ *   ones; count drops by the tokens that left, seq_len stays.  No code moves.
+ *   Lists of block8_select made before are invalid afterwards.
+ *   n_evicted (device, nullable) [B*Hkv].  max_blocks <= 51200. */
+kvq_status block8_evict(kvq_block8* c, const int32_t* keep, int n_first, int n_last, int32_t* n_evicted,
+                        void* stream);
+
 /* Bytes each device array of a cache with these sizes needs; out[i] in the
  * order of the kvq_cache fields (see kvq_cache_layout in the Python
  * binding).  Returns the total, 0 on invalid sizes. */

@@ -1,0 +1,625 @@
+"""GPU parity of the 8-bit block cache (block8_*) against the CPU model in oracle/block8.py.
+
+Codes, scales, bounds, positions, tables and chosen blocks are compared exactly.  Tolerances of the attention, derived
+from its arithmetic (u = 2^-24, D channels, n tokens seen):
+  logit      products of 16-bit queries and 8-bit codes are exact, D of them are added in float32 (a tensor core may cut
+             instead of round: 2u each), then four float32 factors:  e = (2 D + 8) u sigma max_j sum_c |q_c k_jc|
+  weight     exp2 of a logit: e, plus 2^-22 of the hardware's exp2 and the rounding of its argument, |s - max| 2u <= 2^-15
+             where weights still count (|s - max| < 128);  the sum of n weights: n u;  the fp16 pair of a weight 2^-22
+  output     n products added: 2 n u;  so |o - ref| <= (2 e + 2^-13 + 4 n u) sum_j p_j |v_j| + half a step of the
+             16-bit output (eps/2 |ref|, 2^-25 below fp16's normal range);  2^-13 holds 2 * 2^-15 and the small terms
+  lse        e + 2^-14 + n u + 2^-22 |lse|;   acc: (2 e + 2^-13 + 2 n u) relative, plus u of the sum it is added to
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block8 as O8
+
+pytestmark = pytest.mark.gpu
+U24 = 2.0 ** -24
+F8, I8 = torch.float8_e4m3fn, torch.int8
+KIND = {F8: "e4m3", I8: "int8"}
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    from bit_mixed_precision_gb300 import kvq
+    yield kvq
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean(kvq):
+    yield
+    assert kvq.device_status() == 0
+
+
+class Pair:
+    """A cache and its CPU model, fed the same tokens."""
+
+    def __init__(self, kvq, B=2, Hq=4, Hkv=2, D=128, block=16, codes=F8, dtype=torch.float16, max_tokens=256, seed=0,
+                 **kw):
+        self.kvq, self.B, self.Hq, self.Hkv, self.D, self.g = kvq, B, Hq, Hkv, D, Hq // Hkv
+        self.rng = np.random.default_rng(seed)
+        self.gen = torch.Generator().manual_seed(seed)
+        self.c = kvq.make_block8_cache(B, Hq, Hkv, D, dtype, max_tokens, block=block, codes=codes, **kw)
+        n = self.c.table.numel()
+        perm = torch.randperm(n, generator=self.gen).to(torch.int32)
+        self.c.table.copy_(perm.view_as(self.c.table))
+        for x in (self.c.k_codes, self.c.v_codes):              # NaN codes (e4m3 0x7f) where nothing was written
+            x.view(torch.uint8).fill_(0x7F)
+        for x in (self.c.k_scale, self.c.v_scale, self.c.bound_scale, self.c.acc):
+            x.fill_(float("nan"))
+        self.units = [O8.Unit(D, block, KIND[codes]) for _ in range(B * Hkv)]
+
+    def rand(self, *shape, outlier=True):
+        x = torch.randn(shape, generator=self.gen)
+        if outlier:
+            x[..., 3] *= 9
+        return x.to(self.c.dtype)
+
+    def append(self, n, n_new=None, colscore=False, k=None, v=None, strided=False):
+        B, Hkv = self.B, self.Hkv
+        k = self.rand(B, Hkv, n, self.D) if k is None else k
+        v = self.rand(B, Hkv, n, self.D, outlier=False) if v is None else v
+        cs = torch.rand((B, self.Hq, n), generator=self.gen) if colscore else None
+        kd, vd = k.cuda(), v.cuda()
+        if strided:                                             # views of one [B, n, heads, D] projection
+            both = torch.empty((B, n, 2 * Hkv + 1, self.D), dtype=k.dtype, device="cuda")
+            both[:, :, 1:1 + Hkv] = kd.transpose(1, 2)
+            both[:, :, 1 + Hkv:] = vd.transpose(1, 2)
+            kd, vd = both[:, :, 1:1 + Hkv].transpose(1, 2), both[:, :, 1 + Hkv:].transpose(1, 2)
+        nn = None if n_new is None else torch.tensor(n_new, dtype=torch.int32, device="cuda")
+        self.kvq.block8_append(self.c, kd, vd, n_new=nn, colscore=None if cs is None else cs.cuda())
+        for u, unit in enumerate(self.units):
+            b, h = divmod(u, Hkv)
+            m = n if n_new is None else n_new[b]
+            w = None if cs is None else cs[b, h * self.g:(h + 1) * self.g, :m].double().sum(0).numpy()
+            unit.append(k[b, h, :m].float().numpy(), v[b, h, :m].float().numpy(), w)
+
+    def check(self, acc_rtol=None):
+        c = self.c
+        cpu = {k: getattr(c, k).cpu() for k in ("table", "count", "seq_len", "k_scale", "v_scale", "bound_scale",
+                                                "k_bound", "block_pos", "acc", "tail_k", "tail_v")}
+        codes = {"k": c.k_codes.view(torch.uint8).cpu().numpy(), "v": c.v_codes.view(torch.uint8).cpu().numpy()}
+        rows_written = np.zeros(codes["k"].shape[:2], bool)
+        for u, unit in enumerate(self.units):
+            assert int(cpu["count"][u]) == unit.count and int(cpu["seq_len"][u]) == unit.seq_len
+            for i, b in enumerate(unit.blocks):
+                at, n = int(cpu["table"][u, i]), len(b.k)
+                rows_written[at, :n] = True
+                for name in ("k", "v"):
+                    want, s = O8.quantise(getattr(b, name), unit.kind)
+                    np.testing.assert_array_equal(codes[name][at, :n], want, err_msg=f"unit {u} block {i} {name}")
+                    np.testing.assert_array_equal(cpu[name + "_scale"][at].numpy(), s)
+                    if n < c.block:
+                        np.testing.assert_array_equal(cpu["tail_" + name][u, :n].float().numpy(), getattr(b, name))
+                bd, s = O8.bounds(b.k)
+                np.testing.assert_array_equal(cpu["k_bound"][at].numpy(), bd)
+                np.testing.assert_array_equal(cpu["bound_scale"][at].numpy(), s)
+                assert int(cpu["block_pos"][at]) == b.pos
+                if acc_rtol is not None:
+                    assert abs(float(cpu["acc"][at]) - b.acc) <= acc_rtol * abs(b.acc) + 1e-30, (u, i)
+        for name in ("k", "v"):                                 # nothing else was written
+            rest = codes[name][~rows_written]
+            assert self.evicted or (rest == 0x7F).all()
+
+    evicted = False
+
+    def attn(self, q, n_new=None, blocks=None, accumulate=False, scale=None, qd=None, **kw):
+        """Runs block8_attn and compares it; returns (o, lse)."""
+        c, B, Hq, n_q = self.c, self.B, self.Hq, q.shape[2]
+        scale = scale or self.D ** -0.5
+        nn = None if n_new is None else torch.tensor(n_new, dtype=torch.int32, device="cuda")
+        acc0 = c.acc.double().cpu().numpy().copy()
+        o, lse = self.kvq.block8_attn(q.cuda() if qd is None else qd, c, scale, blocks=blocks, accumulate=accumulate,
+                                      n_new=nn, **kw)
+        got, glse, acc1 = o.double().cpu().numpy(), lse.double().cpu().numpy(), c.acc.double().cpu().numpy()
+        if blocks is not None:
+            idx, ln = blocks[0].cpu().numpy(), blocks[1].cpu().numpy()
+        table = c.table.cpu().numpy()
+        for u, unit in enumerate(self.units):
+            b, h = divmod(u, self.Hkv)
+            m = n_q if n_new is None else n_new[b]
+            k, v = unit.dequantised()
+            share, share_tol = np.zeros(len(unit.blocks)), np.zeros(len(unit.blocks))
+            for t in range(n_q):
+                limit = unit.count - m + t + 1 if t < m else 0
+                chosen = None if blocks is None else idx[b, h, t, :ln[b, h, t]]
+                mask = np.broadcast_to(unit.seen(limit, chosen), (self.g, unit.count))
+                qq = q[b, h * self.g:(h + 1) * self.g, t].float().numpy()
+                ro, rl, p = O8.attend(qq, k, v, mask, scale)
+                n = int(mask[0].sum())
+                e = np.where(mask, scale * np.abs(qq.astype(np.float64)) @ np.abs(k).T, 0).max(axis=1, initial=0)
+                e = e * (2 * self.D + 8) * U24
+                eps = torch.finfo(c.dtype).eps / 2
+                tol = (2 * e + 2.0 ** -13 + 4 * n * U24)[:, None] * (p @ np.abs(v)) + eps * np.abs(ro) + 2.0 ** -25
+                go, gl = got[b, h * self.g:(h + 1) * self.g, t], glse[b, h * self.g:(h + 1) * self.g, t]
+                if n == 0:
+                    assert (go == 0).all() and (gl == -np.inf).all(), (u, t)
+                    continue
+                err = np.abs(go - ro) - tol
+                assert np.isfinite(go).all() and (err <= 0).all(), (u, t, float(err.max()))
+                assert (np.abs(gl - rl) <= e + 2.0 ** -14 + n * U24 + 2.0 ** -22 * np.abs(rl)).all(), (u, t)
+                pb = np.zeros(len(unit.blocks))
+                np.add.at(pb, np.arange(unit.count) // unit.P, p.sum(0))
+                share += pb
+                share_tol += pb * (2 * e.max() + 2.0 ** -13 + 2 * n * U24)
+            for i, blk in enumerate(unit.blocks):
+                at = table[u, i]
+                if not accumulate:
+                    assert acc1[at] == acc0[at] or np.isnan(acc0[at])
+                    continue
+                want = acc0[at] + share[i]
+                # one addition of a float32 share to a float32 sum (a few, one per query, for lists)
+                assert abs(acc1[at] - want) <= share_tol[i] + (1 + n_q) * U24 * abs(want) + 1e-37, (u, i)
+                blk.acc = acc1[at]
+        return o, lse
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", [F8, I8])
+@pytest.mark.parametrize("D,block", [(128, 16), (64, 16), (128, 32), (64, 64), (128, 64), (64, 128), (128, 128)])
+def test_append_any_split(kvq, D, block, codes, dtype):
+    p = Pair(kvq, D=D, block=block, codes=codes, dtype=dtype, max_tokens=6 * block, seed=block + D)
+    p.append(1)
+    p.check()
+    p.append(3, n_new=[3, 0], strided=True)             # a padded row: sequence 1 has no new token
+    p.append(block - 2, n_new=[block - 4, block - 2])   # sequence 0 fills its block to the last row, 1 stays open
+    p.check()
+    p.append(2 * block + 3, strided=True, colscore=False)   # across three blocks, open at both ends
+    p.check()
+    for _ in range(3):
+        p.append(1)
+    p.append(block, n_new=[block, 1])                   # open block to open block, one CTA
+    p.check()
+
+
+@pytest.mark.parametrize("block", [16, 128])
+def test_append_prompt_with_scores(kvq, block):
+    p = Pair(kvq, B=3, Hq=6, Hkv=2, block=block, codes=I8, max_tokens=1000)
+    p.append(777, n_new=[777, 5, 640], colscore=True)
+    # g * block float32 additions of non-negative numbers
+    p.check(acc_rtol=(3 * block + 2) * U24)
+    p.append(100, n_new=[100, 0, 33], colscore=True)
+    p.check(acc_rtol=(6 * block + 4) * U24)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", [F8, I8])
+def test_append_values_at_the_edges(kvq, codes, dtype):
+    p = Pair(kvq, B=1, Hq=1, Hkv=1, D=64, codes=codes, dtype=dtype, max_tokens=128)
+    k = torch.zeros((1, 1, 96, 64), dtype=dtype)
+    k[0, 0, 16:32] = torch.finfo(dtype).max * torch.linspace(-1, 1, 64).to(dtype)
+    k[0, 0, 32:48, ::2] = -0.0
+    k[0, 0, 33, 7] = torch.finfo(dtype).smallest_normal / 4             # subnormal in the 16-bit type
+    k[0, 0, 48:64] = torch.tensor(2.0 ** -14, dtype=dtype) * torch.arange(64).to(dtype)
+    k[0, 0, 64 + 3, 5], k[0, 0, 80 + 9, 6] = float("nan"), float("-inf")
+    v = k.flip(2).contiguous()
+    p.append(96, k=k, v=v)
+    p.check()
+    # one token at a time, with scales that grow, stand, and become NaN, gives the same codes
+    q = Pair(kvq, B=1, Hq=1, Hkv=1, D=64, codes=codes, dtype=dtype, max_tokens=128)
+    for i in range(96):
+        q.append(1, k=k[:, :, i:i + 1], v=v[:, :, i:i + 1])
+    q.check()
+
+
+def test_append_leaves_a_unit_alone_that_has_no_room(kvq):
+    p = Pair(kvq, B=2, Hq=2, Hkv=2, max_tokens=48)
+    p.append(40)
+    p.c.table[1, 2] = -1                                # the open block of unit 1: in use, and now lost
+    p.c.table[2, 2] = p.c.k_codes.shape[0]              # out of the pool
+    p.append(0)
+    before = [x.clone() for x in (p.c.count, p.c.seq_len, p.c.k_codes.view(torch.uint8), p.c.tail_k)]
+    z = torch.ones((2, 2, 9, 128), dtype=torch.float16, device="cuda")
+    kvq.block8_append(p.c, z, z)                        # 49 tokens fit nowhere
+    kvq.block8_append(p.c, z, z, n_new=torch.tensor([0, -1], dtype=torch.int32, device="cuda"))
+    assert kvq.device_status() == kvq.KVQ_EDEVICE
+    for x, y in zip(before, (p.c.count, p.c.seq_len, p.c.k_codes.view(torch.uint8), p.c.tail_k)):
+        assert torch.equal(x, y)
+    kvq.block8_append(p.c, z[:, :, :3].contiguous(), z[:, :, :3].contiguous())
+    assert kvq.device_status() == kvq.KVQ_EDEVICE
+    assert p.c.count.tolist() == [43, 40, 40, 43]
+
+
+def test_reset(kvq):
+    p = Pair(kvq)
+    p.append(33)
+    kvq.block8_reset(p.c, torch.tensor([0, 1, 0, 2], dtype=torch.int32, device="cuda"))
+    assert p.c.count.tolist() == [33, 0, 33, 0] and p.c.seq_len.tolist() == [33, 0, 33, 0]
+    kvq.block8_reset(p.c)
+    assert p.c.count.tolist() == [0] * 4
+    p.units = [O8.Unit(128, 16, "e4m3") for _ in range(4)]
+    p.evicted = True                                    # old codes lie around
+    p.append(21)
+    p.check()
+
+
+# ------------------------------------------------------------------ attention
+
+def _lengths(p, lens):
+    """Appends so that sequence b holds lens[b] tokens."""
+    if max(lens):
+        p.append(max(lens), n_new=list(lens))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("codes", [F8, I8])
+@pytest.mark.parametrize("D,block,Hq,Hkv", [(128, 16, 4, 4), (128, 64, 10, 2), (64, 32, 16, 2), (128, 128, 24, 2),
+                                            (64, 16, 3, 1), (128, 32, 40, 2), (64, 128, 64, 1)])
+def test_attn_lengths(kvq, D, block, Hq, Hkv, codes, dtype):
+    lens = [0, 1, 15, 16, 17, 33, 129, 512, 801]
+    p = Pair(kvq, B=len(lens), Hq=Hq, Hkv=Hkv, D=D, block=block, codes=codes, dtype=dtype, max_tokens=896, seed=D + Hq)
+    _lengths(p, lens)
+    p.c.acc.zero_()
+    q = p.rand(len(lens), Hq, 1, D)
+    a = p.attn(q, accumulate=True)
+    b = p.attn(q)                                       # the same call twice gives the same bits
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # a step's shape, without the axis of queries
+    o, lse = kvq.block8_attn(q[:, :, 0].cuda(), p.c)
+    assert torch.equal(o, a[0][:, :, 0]) and torch.equal(lse, a[1][:, :, 0])
+
+
+@pytest.mark.parametrize("n_q,Hq,Hkv,D,block,codes", [(2, 4, 4, 128, 16, F8), (3, 10, 2, 128, 64, I8),
+                                                      (8, 8, 1, 64, 32, F8), (16, 4, 2, 128, 128, I8),
+                                                      (5, 24, 2, 64, 16, F8)])
+def test_attn_several_queries(kvq, n_q, Hq, Hkv, D, block, codes):
+    """Causal among the last tokens; ragged numbers of queries, more queries than tokens, padding rows."""
+    lens = [0, 1, 4, 31, 32, 65, 300]
+    p = Pair(kvq, B=len(lens), Hq=Hq, Hkv=Hkv, D=D, block=block, codes=codes, dtype=torch.bfloat16, max_tokens=384,
+             max_q=16, seed=n_q)
+    _lengths(p, lens)
+    p.c.acc.zero_()
+    q = p.rand(len(lens), Hq, n_q, D)
+    p.attn(q, accumulate=True)
+    p.attn(q, n_new=[1, 0, n_q, n_q - 1, 2, n_q, 1], accumulate=True)
+    # a strided query: a view of [B, n_q, heads, D]
+    qd = q.cuda().transpose(1, 2).contiguous().transpose(1, 2)
+    assert not qd.is_contiguous() or n_q == 1
+    p.attn(q, qd=qd)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_attn_extreme_logits_and_scales(kvq, dtype):
+    """Logits far above and below the usual, blocks whose value scales differ by many powers of two."""
+    p = Pair(kvq, B=4, Hq=4, Hkv=1, D=64, block=16, dtype=dtype, max_tokens=512)
+    k, v = p.rand(4, 1, 500, 64), p.rand(4, 1, 500, 64)
+    k[0] *= 40                                          # one token wins, others underflow
+    k[1] = 0                                            # all equal
+    v[2, :, :256] *= 2.0 ** -12                         # later blocks dwarf the first ones
+    v[2, :, 256:] *= 2.0 ** 8
+    k[3, 0, 100] *= 30                                  # the largest logits in the middle
+    v[3, 0, 100] *= 2.0 ** -10
+    p.append(500, k=k, v=v)
+    p.c.acc.zero_()
+    p.attn(p.rand(4, 4, 1, 64), accumulate=True)
+    q = p.rand(4, 4, 1, 64) * 200
+    p.attn(q, accumulate=True)
+    p.attn(torch.zeros_like(q))
+
+
+def test_attn_lists(kvq):
+    B, Hq, Hkv, n_q, n_sel = 3, 6, 2, 2, 7
+    for codes, block in ((F8, 16), (I8, 32), (F8, 128)):
+        p = Pair(kvq, B=B, Hq=Hq, Hkv=Hkv, block=block, codes=codes, max_tokens=20 * block, max_q=2)
+        lens = [20 * block, 7 * block + 5, 3]
+        _lengths(p, lens)
+        p.c.acc.zero_()
+        idx = torch.full((B, Hkv, n_q, n_sel), -1, dtype=torch.int32)
+        n = torch.zeros((B, Hkv, n_q), dtype=torch.int32)
+        for b in range(B):
+            held = -(-lens[b] // block)
+            for h in range(Hkv):
+                for t in range(n_q):
+                    m = int(p.rng.integers(0, min(n_sel, held) + 1)) if (b, h, t) != (0, 0, 0) else 0   # an empty list
+                    pick = p.rng.permutation(held)[:m]              # any order
+                    if m > 1 and held - 1 not in pick:
+                        pick[0] = held - 1                          # the partly filled block among them
+                    idx[b, h, t, :m], n[b, h, t] = torch.from_numpy(pick.astype(np.int32)), m
+        blocks = (idx.cuda(), n.cuda())
+        q = p.rand(B, Hq, n_q, 128)
+        p.attn(q, blocks=blocks, accumulate=True)
+        p.attn(q, blocks=blocks, n_new=[2, 1, 0])
+
+
+def test_attn_list_numbers_that_are_not_there(kvq):
+    p = Pair(kvq, B=1, Hq=2, Hkv=1, D=64, max_tokens=160, max_q=1)
+    p.append(100)
+    q = p.rand(1, 2, 1, 64)
+    good = torch.tensor([[[[1, 3]]]], dtype=torch.int32, device="cuda"), torch.tensor([[[2]]], dtype=torch.int32, device="cuda")
+    want = p.attn(q, blocks=good)
+    bad = torch.tensor([[[[1, 7, -5, 3, 1 << 30]]]], dtype=torch.int32, device="cuda")
+    got = kvq.block8_attn(q.cuda(), p.c, blocks=(bad, torch.tensor([[[9]]], dtype=torch.int32, device="cuda")))
+    assert kvq.device_status() == kvq.KVQ_EDEVICE
+    assert torch.equal(got[0], want[0])
+    p.c.table[0, 2] = -1                                # a lost block is skipped, and told of
+    kvq.block8_attn(q.cuda(), p.c, accumulate=True)
+    assert kvq.device_status() == kvq.KVQ_EDEVICE
+
+
+def test_attn_not_a_number(kvq):
+    """A block that holds a NaN makes NaN of the queries that see it, and of no others."""
+    p = Pair(kvq, B=3, Hq=2, Hkv=1, D=64, max_tokens=64, max_q=2)
+    k, v = p.rand(3, 1, 33, 64), p.rand(3, 1, 33, 64)
+    k[0, 0, 20, 1] = float("nan")                       # block 1
+    v[1, 0, 32, 1] = float("inf")                       # block 2: only the last query sees it
+    p.append(33, k=k, v=v)
+    q = p.rand(3, 2, 2, 64).cuda()
+    o, lse = kvq.block8_attn(q, p.c)
+    assert o[0].isnan().all() and lse[0].isnan().all()
+    assert o[1, :, 1].isnan().all() and not o[1, :, 0].isnan().any() and not o[2].isnan().any()
+    blocks = (torch.tensor([0, 2], dtype=torch.int32, device="cuda").expand(3, 1, 2, 2).contiguous(),
+              torch.full((3, 1, 2), 2, dtype=torch.int32, device="cuda"))
+    o, _ = kvq.block8_attn(q, p.c, blocks=blocks)
+    assert not o[0].isnan().any()                       # block 1 is not listed
+    qn = q.clone()
+    qn[2, 1, 0, 3] = float("nan")
+    o, _ = kvq.block8_attn(qn, p.c)
+    assert o[2, 1, 0].isnan().all() and not o[2, 0].isnan().any() and not o[2, 1, 1].isnan().any()
+
+
+def test_attn_pool_beyond_32_bits(kvq):
+    """Blocks whose byte offsets pass 2^32 in pools of keys and values."""
+    n = (1 << 32) // (128 * 128) + 64
+    p = Pair(kvq, B=1, Hq=2, Hkv=1, block=128, max_tokens=n * 128)
+    p.c.table.copy_(torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda").view(1, n))
+    p.append(333)
+    q = p.rand(1, 2, 1, 128)
+    p.c.acc.zero_()
+    p.attn(q, accumulate=True)
+    idx, m = kvq.block8_select(q.cuda(), p.c, 2)
+    p.attn(q, blocks=(idx, m))
+
+
+# ------------------------------------------------------------------ selection
+
+def _check_select(p, q, n_sel, n_first, n_last, n_new=None):
+    nn = None if n_new is None else torch.tensor(n_new, dtype=torch.int32, device="cuda")
+    idx, n = p.kvq.block8_select(q.cuda(), p.c, n_sel, n_first, n_last, n_new=nn)
+    gi, gn = idx.cpu().numpy(), n.cpu().numpy()
+    for u, unit in enumerate(p.units):
+        b, h = divmod(u, p.Hkv)
+        for t in range(q.shape[2]):
+            m = q.shape[2] if n_new is None else n_new[b]
+            limit = max(0, unit.count - m + t + 1) if t < m else 0
+            seen = unit.blocks[:-(-limit // unit.P)]
+            want = O8.choose(O8.block_scores(q[b, h * p.g:(h + 1) * p.g, t].float().numpy(), seen), n_sel, n_first, n_last)
+            assert gn[b, h, t] == len(want)
+            assert gi[b, h, t].tolist() == want + [-1] * (n_sel - len(want)), (u, t)
+    return idx, n
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,block,codes,dtype", [(4, 2, 128, 16, F8, torch.float16), (12, 1, 64, 16, I8, torch.bfloat16),
+                                                        (2, 2, 64, 32, I8, torch.float16), (40, 2, 128, 16, F8, torch.bfloat16)])
+def test_select(kvq, Hq, Hkv, D, block, codes, dtype):
+    lens = [0, 1, block, 5 * block + 3, 60 * block - 1]
+    p = Pair(kvq, B=5, Hq=Hq, Hkv=Hkv, D=D, block=block, codes=codes, dtype=dtype, max_tokens=60 * block, max_q=3, seed=Hq)
+    _lengths(p, lens)
+    for n_sel, a, b in ((1, 0, 0), (1, 1, 0), (4, 1, 1), (6, 0, 6), (17, 3, 2), (64, 1, 1)):
+        _check_select(p, p.rand(5, Hq, 3, D), n_sel, a, b)
+    _check_select(p, p.rand(5, Hq, 3, D), 5, 1, 1, n_new=[3, 1, 0, 2, 3])
+    _check_select(p, torch.zeros((5, Hq, 1, D), dtype=dtype), 7, 1, 2)          # every score ties
+
+
+def test_select_many_blocks_ties_and_not_a_number(kvq):
+    p = Pair(kvq, B=1, Hq=2, Hkv=2, D=64, block=16, max_tokens=16 * 2500)
+    k = p.rand(1, 2, 16 * 2500, 64)
+    k[:, :, 16 * 100:] = k[:, :, :16 * 2400]            # the scores repeat
+    k[0, 1, 16 * 1234 + 5, 9] = float("inf")
+    p.append(16 * 2500, k=k, v=k)
+    q = p.rand(1, 2, 1, 64)
+    for n_sel in (2, 33, 1100, 2499):
+        idx, _ = _check_select(p, q, n_sel, 0, 1)
+        assert 1234 in idx[0, 1, 0].tolist()
+    q[0, 0, 0, 0] = float("nan")
+    _check_select(p, q, 33, 1, 1)
+
+
+# ------------------------------------------------------------------ eviction
+
+def test_evict(kvq):
+    p = Pair(kvq, B=4, Hq=2, Hkv=2, D=64, max_tokens=16 * 40 + 4 * 21)
+    p.evicted = True
+    _lengths(p, [16 * 40, 16 * 9 + 1, 16 * 8, 0])
+    for rnd in range(4):
+        acc = torch.randn(p.c.acc.shape, generator=p.gen).abs()
+        acc[::3] = 0.5                                  # ties
+        if rnd == 2:
+            acc[::7] = float("nan")
+        p.c.acc.copy_(acc)
+        table = p.c.table.cpu().numpy()
+        for u, unit in enumerate(p.units):
+            for i, b in enumerate(unit.blocks):
+                b.acc = float(acc[table[u, i]])
+        keep, a, b = [([30, 40, 9, 3, 8, 8, 0, 5], 1, 1), ([20, 1, 0, 0, 2, 7, 1, 1], 2, 3),
+                      ([11, 12, -4, 3, 1, 5, 0, 0], 0, 1), ([5] * 8, 1, 1)][rnd]
+        want = [unit.evict(x, a, b) for unit, x in zip(p.units, keep)]
+        gone = kvq.block8_evict(p.c, torch.tensor(keep, dtype=torch.int32, device="cuda"), a, b)
+        assert gone.tolist() == want
+        now = p.c.table.cpu().numpy()
+        for u, unit in enumerate(p.units):              # those that left follow the kept ones, in order; then the free
+            old = table[u].tolist()
+            held = len(unit.blocks)
+            left = [x for x in old[:held + want[u]] if x not in now[u, :held].tolist()]
+            assert now[u, held:].tolist() == left + old[held + want[u]:], (rnd, u)
+        p.check()
+        if rnd != 2:
+            p.c.acc.nan_to_num_(0.5)
+            p.attn(p.rand(4, 2, 1, 64))
+        p.append(21, n_new=[21, 3, 16, 0])
+        p.check()
+
+
+def test_evict_many_blocks(kvq):
+    p = Pair(kvq, B=2, Hq=1, Hkv=1, D=64, max_tokens=16 * 5000)
+    p.evicted = True
+    p.c.count.copy_(torch.tensor([16 * 5000 - 3, 16 * 1025], dtype=torch.int32))
+    acc = torch.rand(p.c.acc.shape, generator=p.gen).round(decimals=3)
+    p.c.acc.copy_(acc)
+    table = p.c.table.cpu()
+    want = [O8.choose(acc[table[u, :n].long()].tolist(), 1024, 4, 1024 - 200) for u, n in ((0, 5000), (1, 1025))]
+    gone = kvq.block8_evict(p.c, torch.full((2,), 1024, dtype=torch.int32, device="cuda"), 4, 824)
+    assert gone.tolist() == [5000 - 1024, 1] and p.c.count.tolist() == [16 * 1024 - 3, 16 * 1024]
+    for u in range(2):
+        assert p.c.table[u, :1024].tolist() == table[u][torch.tensor(want[u])].tolist()
+        assert sorted(p.c.table[u].tolist()) == sorted(table[u].tolist())
+
+
+# ------------------------------------------------------------------ as they are used
+
+def test_decode_with_eviction_and_selection(kvq):
+    """A prompt through prefill_attn_scores, its scores seeding the blocks' weights, then decode steps that append,
+    attend (dense, accumulating) and every few steps evict; a second attention reads selected blocks only."""
+    B, Hq, Hkv, D, T = 2, 8, 2, 128, 300
+    p = Pair(kvq, B=B, Hq=Hq, Hkv=Hkv, D=D, block=16, codes=F8, dtype=torch.bfloat16, max_tokens=512)
+    p.evicted = True
+    q, k, v = p.rand(B, Hq, T, D, outlier=False), p.rand(B, Hkv, T, D), p.rand(B, Hkv, T, D, outlier=False)
+    _, _, cs = kvq.prefill_attn_scores(q.cuda(), k.cuda(), v.cuda())
+    kvq.block8_append(p.c, k.cuda(), v.cuda(), colscore=cs)
+    for u, unit in enumerate(p.units):
+        b, h = divmod(u, Hkv)
+        unit.append(k[b, h].float().numpy(), v[b, h].float().numpy(),
+                    cs[b, h * 4:h * 4 + 4].double().sum(0).cpu().numpy())
+    p.check(acc_rtol=(4 * 16 + 2) * U24)
+    for step in range(24):
+        p.append(1)
+        qs = p.rand(B, Hq, 1, D)
+        p.attn(qs, accumulate=True)                     # takes the kernel's acc over into the model
+        blocks = _check_select(p, qs, 6, 1, 2)
+        p.attn(qs, blocks=blocks)
+        if step % 8 == 7:
+            keep = torch.tensor([12, 10, 30, 5], dtype=torch.int32)
+            want = [unit.evict(int(x), 1, 2) for unit, x in zip(p.units, keep)]
+            assert kvq.block8_evict(p.c, keep.cuda(), 1, 2).tolist() == want
+            p.check()
+    assert p.c.seq_len.tolist() == [T + 24] * 4
+
+
+def _filled(kvq, **kw):
+    p = Pair(kvq, B=2, Hq=8, Hkv=2, max_tokens=640, **kw)
+    p.append(500, n_new=[500, 77])
+    p.c.acc.zero_()
+    return p
+
+
+def test_graph_replay_and_shared_workspace(kvq):
+    """Captured steps of two caches that share one workspace, replayed in turn, against eager steps of their twins."""
+    a, b = _filled(kvq, seed=1), _filled(kvq, seed=2)
+    shared = a.c.ws
+    caches = []
+    for x in (a, b):
+        f = {k: getattr(x.c, k).clone() for k in ("k_codes", "v_codes", "k_scale", "v_scale", "k_bound", "bound_scale",
+                                                  "tail_k", "tail_v", "table", "count", "seq_len", "block_pos", "acc")}
+        caches.append(kvq.Block8Cache(2, 8, 2, 128, 16, torch.float16, ws=shared, **f))
+    k, v = a.rand(2, 2, 1, 128).cuda(), a.rand(2, 2, 1, 128).cuda()
+    q = a.rand(2, 8, 1, 128).cuda()
+    keep = torch.full((4,), 20, dtype=torch.int32, device="cuda")
+
+    def step(c):
+        kvq.block8_append(c, k, v)
+        o1, l1 = kvq.block8_attn(q, c, accumulate=True)
+        idx, n = kvq.block8_select(q, c, 5)
+        o2, l2 = kvq.block8_attn(q, c, blocks=(idx, n))
+        gone = kvq.block8_evict(c, keep)
+        return o1, l1, idx, n, o2, l2, gone
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    for c in caches:
+        arrays = [t.view(torch.uint8) for t in (c.k_codes, c.v_codes)] + [
+            c.k_scale, c.v_scale, c.k_bound, c.bound_scale, c.tail_k, c.tail_v, c.table, c.count, c.seq_len, c.block_pos, c.acc]
+        snap = [t.clone() for t in arrays]
+        with torch.cuda.stream(s):
+            step(c)                                     # before the capture, on the stream it uses
+        s.synchronize()
+        for t, o in zip(arrays, snap):
+            t.copy_(o)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(step(c))
+        graphs.append(g)
+        for t, o in zip(arrays, snap):
+            t.copy_(o)
+    for rep in range(3):
+        for t in (q, k, v):
+            t.copy_(a.rand(*t.shape).cuda())
+        for i, x in enumerate((a, b)):
+            graphs[i].replay()
+            want = step(x.c)
+            torch.cuda.synchronize()
+            for y, z in zip(outs[i], want):
+                assert torch.equal(y, z), (rep, i)
+            for name in ("count", "table", "acc", "k_scale"):
+                y, z = getattr(caches[i], name), getattr(x.c, name)
+                assert torch.equal(y.nan_to_num(), z.nan_to_num()), name
+
+
+def test_other_streams(kvq):
+    """Calls on a stream that is not torch's current one, with inputs freed right after."""
+    p, twin = _filled(kvq, seed=5), _filled(kvq, seed=5)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(5):
+        k, v, q = twin.rand(2, 2, 1, 128), twin.rand(2, 2, 1, 128), twin.rand(2, 8, 1, 128)
+        kvq.block8_append(twin.c, k.cuda(), v.cuda())
+        want = kvq.block8_attn(q.cuda(), twin.c)
+        kd, vd, qd = k.cuda(), v.cuda(), q.cuda()
+        s.wait_stream(torch.cuda.current_stream())
+        kvq.block8_append(p.c, kd, vd, stream=s)
+        got = kvq.block8_attn(qd, p.c, stream=s)
+        del kd, vd, qd
+        torch.full((2, 2, 1, 128), float("nan"), device="cuda", dtype=torch.float16)
+        s.synchronize()
+        assert torch.equal(got[0], want[0])
+
+
+def test_binding_refusals(kvq):
+    p = Pair(kvq, B=2, Hq=4, Hkv=2, max_tokens=64)
+    z = lambda *s, dt=torch.float16: torch.zeros(s, dtype=dt, device="cuda")
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="k must be"):
+        kvq.block8_append(p.c, z(2, 3, 1, 128), z(2, 3, 1, 128))
+    with pytest.raises(ValueError, match="one shape"):
+        kvq.block8_append(p.c, z(2, 2, 1, 128), z(2, 2, 2, 128))
+    with pytest.raises(TypeError):
+        kvq.block8_append(p.c, z(2, 2, 1, 128, dt=torch.bfloat16), z(2, 2, 1, 128))
+    with pytest.raises(ValueError, match="contiguous"):
+        kvq.block8_append(p.c, z(2, 2, 128, 2).transpose(2, 3), z(2, 2, 2, 128))
+    with pytest.raises(kvq.KvqError, match="16-byte"):
+        kvq.block8_append(p.c, z(2 * 2 * 128 + 8)[4:-4].view(2, 2, 1, 128), z(2, 2, 1, 128))
+    with pytest.raises(kvq.KvqError, match="multiples of 8"):
+        kvq.block8_append(p.c, z(2, 2, 2, 132)[..., :128], z(2, 2, 2, 128))
+    with pytest.raises(kvq.KvqError, match="exceed"):
+        kvq.block8_append(p.c, z(2, 2, 65, 128), z(2, 2, 65, 128))
+    with pytest.raises(ValueError, match="n_new"):
+        kvq.block8_append(p.c, z(2, 2, 1, 128), z(2, 2, 1, 128), n_new=i(3))
+    with pytest.raises(ValueError, match="colscore"):
+        kvq.block8_append(p.c, z(2, 2, 1, 128), z(2, 2, 1, 128), colscore=z(2, 2, 1, dt=torch.float32))
+    with pytest.raises(ValueError, match="q must be"):
+        kvq.block8_attn(z(2, 2, 1, 128), p.c)
+    with pytest.raises(kvq.KvqError):
+        kvq.block8_attn(z(2, 4, 17, 128), p.c)
+    with pytest.raises(ValueError, match="blocks"):
+        kvq.block8_attn(z(2, 4, 1, 128), p.c, blocks=(i(2, 2, 3), i(2, 2)))
+    with pytest.raises(ValueError, match="o must be"):
+        kvq.block8_attn(z(2, 4, 1, 128), p.c, o=z(2, 4, 128))
+    with pytest.raises(kvq.KvqError, match="n_first"):
+        kvq.block8_select(z(2, 4, 1, 128), p.c, 2, 2, 1)
+    with pytest.raises(ValueError, match="keep"):
+        kvq.block8_evict(p.c, i(3))
+    with pytest.raises(kvq.KvqError, match="n_last"):
+        kvq.block8_evict(p.c, i(4), 1, 0)
+    with pytest.raises(ValueError, match="ws"):
+        kvq.Block8Cache(**{f: getattr(p.c, f) for f in ("B", "Hq", "Hkv", "D", "block", "dtype", "k_codes", "v_codes",
+                                                         "k_scale", "v_scale", "k_bound", "bound_scale", "tail_k", "tail_v",
+                                                         "table", "count", "seq_len", "block_pos", "acc")},
+                        ws=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="table"):
+        kvq.Block8Cache(**{f: getattr(p.c, f) for f in ("B", "Hq", "Hkv", "D", "block", "dtype", "k_codes", "v_codes",
+                                                         "k_scale", "v_scale", "k_bound", "bound_scale", "tail_k", "tail_v",
+                                                         "count", "seq_len", "block_pos", "acc")}, table=i(3, 4))
