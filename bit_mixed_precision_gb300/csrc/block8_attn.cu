@@ -1,9 +1,34 @@
 // block8_attn: attention of a few queries over the 8-bit block cache, over all
 // tokens or over a list of blocks per query (include/kvq.h has the format).
 //
-// One CTA per (unit, query, head).  Four warps take the blocks in turn, each
-// with its own running maximum, sum and output; the CTA merges the four.  With
-// accumulate a second kernel adds each block's softmax weight to its acc.
+// Mathematics.  A logit is s_j = (q . c_j) k_scale sigma log2(e): codes and
+// 16-bit queries multiply exactly in fp16 MMAs with float32 sums.  With the
+// value scale split as 2^e f (1 <= f < 2), the second product is over the value
+// codes with weights 2^(s_j + e - M) f, M one running reference per query row,
+// so blocks whose value scales lie many powers of two apart share one fp16
+// range; a weight enters as a pair of fp16 numbers (22 bits).  The sum of
+// 2^(s_j + e - M) 2^-e beside it gives the softmax denominator.
+//
+// Work.  The rows that read a unit together (queries x heads of the group, 8 or
+// 16 of them) and its tokens, or a query's listed blocks, form a work unit; its
+// tokens are cut into tiles of 32.  All work units' tiles form one list, split
+// evenly over the resident CTAs, whatever the lengths (each CTA adds up the
+// units' tile counts itself).  In a CTA the four warps take the tiles of its run
+// in turn, each with its own state: tokens are the M rows of the first MMA and
+// channels those of the second, so that 8 rows cost one n = 8 column block.  The
+// codes go from global memory straight to the registers where the fragments
+// want them: a lane's 16-byte pieces of a key row are the k elements of four
+// MMAs (the query fragments use the same channel order), and its 16-byte pieces
+// of four value rows, transposed by byte permutes, are the fragments of eight.
+// A tile's key registers are loaded again for the next tile as soon as the first
+// product has read them, the value registers after the second.  At the end of
+// a unit's run the warps meet in shared memory and the CTA writes one partial
+// state; a second kernel, a programmatic dependent, joins the partials of a unit
+// and, with accumulate, adds the blocks' shares of the weights, in a fixed order.
+//
+// Bound by HBM: 2 D bytes per token and KV head against 4 D g flop.
+#include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "block8_device.cuh"
@@ -17,6 +42,14 @@ namespace {
 
 using namespace b8;
 
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTile = 32;               // tokens a warp takes at a time
+constexpr int kMaxCtas = 1024;          // CTAs of the first kernel at most (sizes the workspace)
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// The reference M moves only when a logit passes it by more than 2^8, and weights carry a factor
+// 2^6: they stay below 2^8 2^6 2 = 2^15 in fp16, and 2^-31 of the largest is still a weight.
+constexpr float kLift = 8.0f, kShift = 6.0f;
+
 struct AttnArgs {
     kvq_block8 c;
     const void* q;
@@ -25,164 +58,756 @@ struct AttnArgs {
     const int32_t* n_new;
     float sm_scale;
     const int32_t *blocks, *list_len;
-    int n_sel, accumulate;
+    int n_sel;
     void* o;
-    float *lse, *lse2;              // lse2: workspace, per (unit, query, head)
+    float* lse;
+    // derived
+    int g, row_tiles, works;            // work units = units (x n_q with lists) x row_tiles
+    int cells;                          // 16-token cells per work unit in `mass`
+    // workspace
+    float *part, *ml, *mass;            // [slot][rows][D], [slot][rows][2], [work][cells][rows]
+    int2* span;                         // [work] first and last CTA
 };
 
-constexpr int kWarps = 4;
-constexpr float kLog2e = 1.4426950408889634f;
+// What a work unit is and sees.
+struct Work {
+    int u, b, t0, rows;                 // unit, sequence, first query (the only one with lists), valid + padding rows
+    int tiles, top;                     // 32-token tiles; tokens that its last query sees
+    int list_n;                         // listed blocks
+};
 
-template <int CODE> __device__ __forceinline__ void four_codes(uint32_t w, float (&f)[4]) {
-    if constexpr (CODE == KVQ_CODE_E4M3) {
-        uint32_t a, b;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((uint16_t)w));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((uint16_t)(w >> 16)));
-        const float2 x = __half22float2(*reinterpret_cast<__half2*>(&a)), y = __half22float2(*reinterpret_cast<__half2*>(&b));
-        f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+template <int NT, bool LIST>
+__device__ __forceinline__ Work work_of(const AttnArgs& a, int w) {
+    Work k;
+    const int rt = w % a.row_tiles, x = w / a.row_tiles;
+    k.u = LIST ? x / a.n_q : x;
+    k.b = k.u / a.c.Hkv;
+    const int m = new_rows(a.n_new, k.b, a.n_q, &g_status_block8_attn);
+    const int count = min(a.c.count[k.u], a.c.max_blocks * a.c.block);
+    const int r0 = rt * 8 * NT, all = LIST ? a.g : a.g * a.n_q;
+    k.rows = min(8 * NT, all - r0);
+    const int first = LIST ? x % a.n_q : r0 / a.g, last = LIST ? first : (r0 + k.rows - 1) / a.g;
+    k.t0 = first;
+    k.top = first < m ? query_limit(count, m, min(last, m - 1)) : 0;
+    k.list_n = 0;
+    if (LIST) {
+        const int n = a.list_len[x];
+        if (n < 0 || n > a.n_sel) atomicOr(&g_status_block8_attn, kDevCheck);
+        k.list_n = k.top > 0 ? min(max(n, 0), a.n_sel) : 0;
+        k.tiles = (k.list_n * (a.c.block / 16) + 1) / 2;
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i));
+        k.tiles = (k.top + kTile - 1) / kTile;
     }
+    return k;
 }
 
-// The warp's dot product of its query with one token's codes.
+// Query and head (within the group) of row i of a work unit.
+template <int NT, bool LIST>
+__device__ __forceinline__ int2 row_of(const AttnArgs& a, const Work& k, int w, int i) {
+    const int r = (w % a.row_tiles) * 8 * NT + i;
+    return LIST ? make_int2(k.t0, r) : make_int2(r / a.g, r % a.g);
+}
+
+// ------------------------------------------------------------------ pieces of the inner loop
+
+__device__ __forceinline__ uint4 load16(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 load8(const uint8_t* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+// Four codes as two fp16 pairs, exactly.  int8: the byte with its sign bit flipped, under the
+// exponent of 1024, is 1152 + code.
 template <int CODE>
-__device__ __forceinline__ float logit(const float (&q)[4], const uint8_t* codes, bool mine) {
-    float s = 0.0f;
-    if (mine) {
-        float f[4];
-        four_codes<CODE>(*reinterpret_cast<const uint32_t*>(codes), f);
-        s = q[0] * f[0] + q[1] * f[1] + q[2] * f[2] + q[3] * f[3];
+__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (CODE == KVQ_CODE_E4M3) {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)w));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
+    } else {
+        const uint32_t x = w ^ 0x80808080u;
+        const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+        uint32_t l = __byte_perm(x, 0x64646464u, 0x4140), h = __byte_perm(x, 0x64646464u, 0x4342);
+        __half2 a = __hsub2(*reinterpret_cast<__half2*>(&l), bias), b = __hsub2(*reinterpret_cast<__half2*>(&h), bias);
+        lo = *reinterpret_cast<uint32_t*>(&a);
+        hi = *reinterpret_cast<uint32_t*>(&b);
     }
-    for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    return s;
 }
 
-template <typename T, int D, int CODE>
-__global__ void __launch_bounds__(kWarps * 32) attn_kernel(AttnArgs a) {
-    __shared__ float part[kWarps][D + 2];
-    const kvq_block8& c = a.c;
-    const int g = c.Hq / c.Hkv, hh = blockIdx.x % g, row = blockIdx.x / g, u = row / a.n_q, t = row % a.n_q;
-    const int b = u / c.Hkv, h = (u % c.Hkv) * g + hh, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int m = new_rows(a.n_new, b, a.n_q, &g_status_block8_attn);
-    const int limit = min(query_limit(c.count[u], m, t), c.max_blocks * c.block);
-    const int32_t* list = a.blocks ? a.blocks + (size_t)row * a.n_sel : nullptr;
-    int nb = (limit + c.block - 1) / c.block;
-    const int held = (min(c.count[u], c.max_blocks * c.block) + c.block - 1) / c.block;
-    if (list) nb = limit > 0 ? min(max(a.list_len[row], 0), a.n_sel) : 0;
-    const bool mine = lane < D / 4;
-    float q[4] = {0, 0, 0, 0}, o[4] = {0, 0, 0, 0}, mx = -INFINITY, l = 0.0f;
-    const T* qp = (const T*)a.q + b * a.qs[0] + h * a.qs[1] + t * a.qs[2];
-    if (mine && t < m)
-        for (int i = 0; i < 4; ++i) q[i] = Elem<T>::to_f(qp[lane * 4 + i]);
-    for (int j = warp; j < nb; j += kWarps) {
-        const int blk = list ? list[j] : j;
-        const int phys = (unsigned)blk < (unsigned)held ? c.table[(size_t)u * c.max_blocks + blk] : -1;
-        if ((unsigned)phys >= (unsigned)c.n_blocks) {
-            if (lane == 0) atomicOr(&g_status_block8_attn, kDevCheck);
-            continue;
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// (a, b) rounded to an fp16 pair and the pair of the remainders.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    __half2 r = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<uint32_t*>(&h);
+    lo = *reinterpret_cast<uint32_t*>(&r);
+}
+
+// One lane's registers of a 16-token cell.
+template <int D> struct KeyRegs { uint4 r[2][D / 64]; };        // rows g, g + 8; pieces of 16 channels
+template <int D> struct ValueRegs { uint32_t r[4][D / 32]; };   // rows 2t, 2t + 1, 2t + 8, 2t + 9; D/8 channels
+
+template <int D>
+__device__ __forceinline__ void load_keys(KeyRegs<D>& k, const uint8_t* codes, uint32_t cell, int g, int t) {
+    if (cell == 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) k.r[i][j] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const uint8_t* p = codes + (size_t)cell * (16 * D) + g * D + t * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) k.r[i][j] = load16(p + i * 8 * D + j * 64);
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(ValueRegs<D>& v, const uint8_t* codes, uint32_t cell, int g, int t) {
+    if (cell == 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) v.r[i][j] = 0;
+        return;
+    }
+    const uint8_t* p = codes + (size_t)cell * (16 * D) + 2 * t * D + g * (D / 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t* row = p + ((i & 1) + (i >> 1) * 8) * D;
+        if constexpr (D == 128) {
+            const uint4 x = load16(row);
+            v.r[i][0] = x.x; v.r[i][1] = x.y; v.r[i][2] = x.z; v.r[i][3] = x.w;
+        } else {
+            const uint2 x = load8(row);
+            v.r[i][0] = x.x; v.r[i][1] = x.y;
         }
-        const float ks = c.k_scale[phys] * a.sm_scale * kLog2e, vs = c.v_scale[phys];
-        const int n = min(c.block, limit - blk * c.block);
-        for (int i = 0; i < n; ++i) {
-            const size_t at = ((size_t)phys * c.block + i) * D + lane * 4;
-            const float s = logit<CODE>(q, c.k_codes + at, mine) * ks;
-            const float nm = fmaxf(mx, s), f0 = mx == nm ? 1.0f : exp2f(mx - nm), p = exp2f(s - nm);
-            mx = nm;
-            l = l * f0 + p;
-            if (mine) {
-                float f[4];
-                four_codes<CODE>(*reinterpret_cast<const uint32_t*>(c.v_codes + at), f);
-                for (int k = 0; k < 4; ++k) o[k] = o[k] * f0 + p * vs * f[k];
+    }
+}
+
+// Where a warp's next 16 tiles lie: lane 2 i + j holds cell j of its i-th tile.
+struct Cells {
+    uint32_t cell;                      // number of the 16-token cell in the pool, ~0 for none
+    int slot;                           // its first token in the unit
+    float ks, vs;                       // k_scale sigma log2(e), v_scale
+};
+
+template <bool LIST>
+__device__ __forceinline__ Cells find_cells(const AttnArgs& a, const Work& k, int w, int tile, int end, int lane) {
+    Cells x;
+    x.cell = 0xffffffffu;
+    x.slot = 0;
+    x.ks = 0.0f;
+    x.vs = 1.0f;
+    const int my = tile + (lane >> 1) * kWarps, cell = 2 * my + (lane & 1);
+    if (my < end) {
+        const int per = a.c.block / 16, j = cell / per, in = cell % per;
+        int blk = j;
+        bool there;
+        if (LIST) {
+            there = j < k.list_n;
+            if (there) {
+                blk = a.blocks[(size_t)(w / a.row_tiles) * a.n_sel + j];
+                const int held = (min(a.c.count[k.u], a.c.max_blocks * a.c.block) + a.c.block - 1) / a.c.block;
+                if ((unsigned)blk >= (unsigned)held) {
+                    atomicOr(&g_status_block8_attn, kDevCheck);
+                    there = false;
+                }
+            }
+        } else {
+            there = cell * 16 < k.top;
+        }
+        if (there) {
+            x.slot = blk * a.c.block + in * 16;
+            if (x.slot < k.top) {
+                const int phys = a.c.table[(size_t)k.u * a.c.max_blocks + blk];
+                if ((unsigned)phys < (unsigned)a.c.n_blocks) {
+                    x.cell = (uint32_t)phys * per + in;
+                    x.ks = a.c.k_scale[phys] * (a.sm_scale * kLog2e);
+                    x.vs = a.c.v_scale[phys];
+                } else {
+                    atomicOr(&g_status_block8_attn, kDevCheck);
+                }
             }
         }
     }
-    if (mine)
-        for (int k = 0; k < 4; ++k) part[warp][lane * 4 + k] = o[k];
-    if (lane == 0) {
-        part[warp][D] = mx;
-        part[warp][D + 1] = l;
+    return x;
+}
+
+template <int D, int NT>
+struct Shared {
+    float o[kWarps][8 * NT][D + 4];
+    float ml[kWarps][8 * NT][2];
+    int scan[kWarps];
+    int start[3];                       // total tiles; first work unit of the CTA, its first tile's number
+};
+
+// First tile of work unit w, for the CTA's first unit: every CTA adds up all units' tiles.
+template <int NT, bool LIST, typename S>
+__device__ __forceinline__ void find_start(const AttnArgs& a, S& sh, int* total, int* per, int* w, int* before) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int each = (a.works + kThreads - 1) / kThreads, w0 = min((int)threadIdx.x * each, a.works),
+              w1 = min(w0 + each, a.works);
+    int sum = 0;
+    for (int i = w0; i < w1; ++i) sum += work_of<NT, LIST>(a, i).tiles;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    __syncthreads();
+    int all = 0, base = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) base += sh.scan[i];
+        all += sh.scan[i];
+    }
+    *total = all;
+    *per = max((all + (int)gridDim.x - 1) / (int)gridDim.x, kWarps);
+    const int from = blockIdx.x * *per;
+    int at = base + incl - sum;
+    if (from >= at && from < at + sum) {
+        int i = w0;
+        for (;; ++i) {
+            const int n = work_of<NT, LIST>(a, i).tiles;
+            if (from < at + n) break;
+            at += n;
+        }
+        sh.start[1] = i;
+        sh.start[2] = at;
     }
     __syncthreads();
-    float top = -INFINITY, total = 0.0f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][D]);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    for (int w = 0; w < kWarps; ++w) total += part[w][D + 1] * exp2f(part[w][D] - ref);
-    const size_t orow = ((size_t)b * c.Hq + h) * a.n_q + t;
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float x = 0.0f;
-        for (int w = 0; w < kWarps; ++w) x += part[w][d] * exp2f(part[w][D] - ref);
-        ((T*)a.o)[orow * D + d] = Elem<T>::from_f(total == 0.0f ? 0.0f : x / total);
-    }
-    if (threadIdx.x == 0) {
-        const float lse2 = total == 0.0f ? -INFINITY : ref + log2f(total);
-        if (a.lse) a.lse[orow] = lse2 / kLog2e;
-        if (a.accumulate) a.lse2[(size_t)row * g + hh] = lse2;
+    *w = sh.start[1];
+    *before = sh.start[2];
+}
+
+template <typename T, int D, int CODE, int NT, bool LIST, bool ACC>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArgs a) {
+    constexpr int R = 8 * NT;
+    __shared__ Shared<D, NT> sh;
+    const kvq_block8& c = a.c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    int total, per, w, before;
+    find_start<NT, LIST>(a, sh, &total, &per, &w, &before);
+    grid_launch_dependents();
+    int from = blockIdx.x * per;
+    const int to = min(from + per, total);
+    for (; from < to; ++w) {
+        const Work k = work_of<NT, LIST>(a, w);
+        if (k.tiles == 0) continue;
+        const int s0 = from - before, s1 = min(k.tiles, to - before);
+        if (s0 == 0 && threadIdx.x == 0) a.span[w] = make_int2(blockIdx.x, (before + k.tiles - 1) / per);
+        // ---- the queries: row g of each column block, channels in the keys' order, as fp16
+        uint32_t qf[NT][D / 16][2];
+        float qi[NT][2];                // what undoes a row's factor, for this lane's columns 2t, 2t + 1
+        int lim[NT][2], least = k.top;  // tokens that the columns' queries see
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int i = 8 * n + g;
+            const int2 th = row_of<NT, LIST>(a, k, w, min(i, k.rows - 1));
+            const T* q = (const T*)a.q + k.b * a.qs[0] + (int64_t)((k.u % c.Hkv) * a.g + th.y) * a.qs[1] + th.x * a.qs[2] +
+                         t * 16;
+            float x[D / 4];
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 r = *reinterpret_cast<const uint4*>(q + j * 64 + e * 8);
+                    const T* y = reinterpret_cast<const T*>(&r);
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) x[j * 16 + e * 8 + z] = Elem<T>::to_f(y[z]);
+                }
+            float undo = 1.0f;
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                // bf16 reaches further than fp16: a power of two brings the row's largest to 2^14 .. 2^15
+                uint32_t mx = 0;
+#pragma unroll
+                for (int z = 0; z < D / 4; ++z) mx = max(mx, __float_as_uint(x[z]) & 0x7fffffffu);
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const int e = min(max((int)(mx >> 23), 28), 254);
+                const float f = mx < 0x7f800000u ? __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23) : 1.0f;
+                undo = mx < 0x7f800000u ? __uint_as_float((uint32_t)(e - 14) << 23) : 1.0f;
+#pragma unroll
+                for (int z = 0; z < D / 4; ++z) x[z] *= f;
+            }
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                __half2 h0 = __floats2half2_rn(x[4 * s], x[4 * s + 1]), h1 = __floats2half2_rn(x[4 * s + 2], x[4 * s + 3]);
+                qf[n][s][0] = *reinterpret_cast<uint32_t*>(&h0);
+                qf[n][s][1] = *reinterpret_cast<uint32_t*>(&h1);
+            }
+            const int m = a.n_new ? min(max(a.n_new[k.b], 0), a.n_q) : a.n_q;
+            const int count = min(c.count[k.u], c.max_blocks * c.block);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = 8 * n + 2 * t + e;
+                qi[n][e] = __shfl_sync(0xffffffffu, undo, (2 * t + e) * 4);
+                lim[n][e] = k.top;      // padding rows: as the last query; nobody reads them
+                const int tq = row_of<NT, LIST>(a, k, w, col).x;
+                if (col < k.rows && tq < m) lim[n][e] = query_limit(count, m, tq);
+                least = min(least, lim[n][e]);
+            }
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        float o[NT][D / 16][4], M[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][i][e] = 0.0f;
+            M[n][0] = M[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+        // ---- the warp's tiles
+        KeyRegs<D> kr[2];
+        ValueRegs<D> vr[2];
+        Cells cells = find_cells<LIST>(a, k, w, s0 + warp, s1, lane);
+        uint32_t cell[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            cell[j] = __shfl_sync(0xffffffffu, cells.cell, j);
+            load_keys<D>(kr[j], c.k_codes, cell[j], g, t);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) load_values<D>(vr[j], c.v_codes, cell[j], g, t);
+        int at = 0;                     // the tile's place among the 16 of `cells`
+        for (int tile = s0 + warp; tile < s1; tile += kWarps) {
+            float ks[2], vs[2];
+            int slot[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ks[j] = __shfl_sync(0xffffffffu, cells.ks, 2 * at + j);
+                vs[j] = __shfl_sync(0xffffffffu, cells.vs, 2 * at + j);
+                slot[j] = __shfl_sync(0xffffffffu, cells.slot, 2 * at + j);
+                if (cell[j] == 0xffffffffu) slot[j] = 0x40000000;       // nothing there: behind every limit
+            }
+            // where the next tile lies
+            if (++at == 16) {
+                cells = find_cells<LIST>(a, k, w, tile + kWarps, s1, lane);
+                at = 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) cell[j] = __shfl_sync(0xffffffffu, cells.cell, 2 * at + j);
+            if (tile + kWarps >= s1) cell[0] = cell[1] = 0xffffffffu;
+            // ---- logits: tokens are rows, queries columns
+            float s[2][NT][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint4 lo = kr[j].r[0][i / 4], hi = kr[j].r[1][i / 4];
+                    const uint32_t wl = i % 4 == 0 ? lo.x : i % 4 == 1 ? lo.y : i % 4 == 2 ? lo.z : lo.w;
+                    const uint32_t wh = i % 4 == 0 ? hi.x : i % 4 == 1 ? hi.y : i % 4 == 2 ? hi.z : hi.w;
+                    uint32_t a0, a1, a2, a3;
+                    to_f16<CODE>(wl, a0, a2);
+                    to_f16<CODE>(wh, a1, a3);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma(s[j][n], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
+                }
+                load_keys<D>(kr[j], c.k_codes, cell[j], g, t);
+            }
+            // ---- weights
+            float over = -INFINITY, back[2], f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // vs = 2^e f; a NaN scale keeps f = NaN and e = 0
+                const uint32_t vb = __float_as_uint(vs[j]);
+                const bool fin = vb < 0x7f800000u;
+                const int e = fin ? (int)(vb >> 23) - 127 : 0;
+                f[j] = fin ? __uint_as_float((vb & 0x7fffffu) | 0x3f800000u) : vs[j];
+                back[j] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float& y = s[j][n][x];
+                        y = fmaf(y, ks[j] * qi[n][x & 1], (float)e);
+                    }
+                if (slot[j] + 16 > least) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (slot[j] + g + (x >> 1) * 8 >= lim[n][x & 1]) s[j][n][x] = -INFINITY;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) over = fmaxf(over, s[j][n][x] - M[n][x & 1]);
+            }
+            // a column's first logits make `over` +inf (or NaN when they are -inf: nothing to do then)
+            if (__any_sync(0xffffffffu, over > kLift)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float now = fmaxf(M[n][e], mx);
+                        const float fac = now == M[n][e] ? 1.0f : ex2_approx(M[n][e] - now);
+                        M[n][e] = now;
+                        l[n][e] *= fac;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[n][i][e] *= fac;
+                            o[n][i][2 + e] *= fac;
+                        }
+                    }
+            }
+            uint32_t bh[2][NT][2], bl[2][NT][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool edge = slot[j] + 16 > least;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float p[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float ref = M[n][x & 1] == -INFINITY ? 0.0f : M[n][x & 1];
+                        p[x] = ex2_approx(s[j][n][x] - ref + kShift);
+                    }
+                    const float sum0 = p[0] + p[2], sum1 = p[1] + p[3];
+                    l[n][0] = fmaf(sum0, back[j], l[n][0]);
+                    l[n][1] = fmaf(sum1, back[j], l[n][1]);
+                    if constexpr (ACC) {
+                        float c0 = sum0, c1 = sum1;
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) {
+                            c0 += __shfl_xor_sync(0xffffffffu, c0, x);
+                            c1 += __shfl_xor_sync(0xffffffffu, c1, x);
+                        }
+                        // log2 of the cell's weights, whatever M is now or becomes
+                        if (g == 0 && slot[j] < 0x40000000)
+                            *reinterpret_cast<float2*>(a.mass + ((size_t)w * a.cells + 2 * tile + j) * R + 8 * n + 2 * t) =
+                                make_float2(__log2f(c0 * back[j]) + (M[n][0] - kShift),
+                                            __log2f(c1 * back[j]) + (M[n][1] - kShift));
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) p[x] *= f[j];
+                    if (edge) {         // a masked token weighs 0 even where its block's scale is NaN
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (slot[j] + g + (x >> 1) * 8 >= lim[n][x & 1]) p[x] = 0.0f;
+                    }
+                    uint32_t h0, l0, h1, l1;
+                    split2(p[0], p[1], h0, l0);
+                    split2(p[2], p[3], h1, l1);
+                    bh[j][n][0] = transpose8x8(h0);
+                    bh[j][n][1] = transpose8x8(h1);
+                    bl[j][n][0] = transpose8x8(l0);
+                    bl[j][n][1] = transpose8x8(l1);
+                }
+                // ---- outputs: channels are rows, queries columns
+                if (slot[j] + 16 > k.top) {             // rows behind the last token may hold anything: 0 x NaN
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (slot[j] + 2 * t + (i & 1) + (i >> 1) * 8 >= k.top)
+#pragma unroll
+                            for (int x = 0; x < D / 32; ++x) vr[j].r[i][x] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint32_t p0 = __byte_perm(vr[j].r[0][i], vr[j].r[1][i], 0x5140);
+                    const uint32_t p1 = __byte_perm(vr[j].r[0][i], vr[j].r[1][i], 0x7362);
+                    const uint32_t p2 = __byte_perm(vr[j].r[2][i], vr[j].r[3][i], 0x5140);
+                    const uint32_t p3 = __byte_perm(vr[j].r[2][i], vr[j].r[3][i], 0x7362);
+                    uint32_t a0, a1, a2, a3;
+                    to_f16<CODE>(p0, a0, a1);
+                    to_f16<CODE>(p2, a2, a3);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma(o[n][2 * i], a0, a1, a2, a3, bh[j][n][0], bh[j][n][1]);
+                        mma(o[n][2 * i], a0, a1, a2, a3, bl[j][n][0], bl[j][n][1]);
+                    }
+                    to_f16<CODE>(p1, a0, a1);
+                    to_f16<CODE>(p3, a2, a3);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma(o[n][2 * i + 1], a0, a1, a2, a3, bh[j][n][0], bh[j][n][1]);
+                        mma(o[n][2 * i + 1], a0, a1, a2, a3, bl[j][n][0], bl[j][n][1]);
+                    }
+                }
+                load_values<D>(vr[j], c.v_codes, cell[j], g, t);
+            }
+        }
+        // ---- the CTA's partial state of this work unit
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = l[n][e];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                const int row = 8 * n + 2 * t + e;
+                if (g == 0) {
+                    sh.ml[warp][row][0] = M[n][e];
+                    sh.ml[warp][row][1] = x;
+                }
+                float* dst = &sh.o[warp][row][g * (D / 8)];
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[n][i][e], o[n][i][2 + e]);
+            }
+        __syncthreads();
+        const size_t slot = (size_t)blockIdx.x + w;
+        for (int x = threadIdx.x; x < R * (D / 4); x += kThreads) {
+            const int row = x / (D / 4), d = x % (D / 4) * 4;
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.ml[i][row][0]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float fac = ex2_approx(sh.ml[i][row][0] - ref);
+                const float4 v = *reinterpret_cast<const float4*>(&sh.o[i][row][d]);
+                y.x = fmaf(v.x, fac, y.x);
+                y.y = fmaf(v.y, fac, y.y);
+                y.z = fmaf(v.z, fac, y.z);
+                y.w = fmaf(v.w, fac, y.w);
+                sum = fmaf(sh.ml[i][row][1], fac, sum);
+            }
+            *reinterpret_cast<float4*>(a.part + (slot * R + row) * D + d) = y;
+            if (d == 0) *reinterpret_cast<float2*>(a.ml + (slot * R + row) * 2) = make_float2(top, sum);
+        }
+        __syncthreads();
+        before += k.tiles;
+        from = before;
     }
 }
 
-// The blocks' softmax weights, one CTA per unit: queries in turn, warps over blocks.
-template <typename T, int D, int CODE>
-__global__ void __launch_bounds__(kWarps * 32) weight_kernel(AttnArgs a) {
-    const kvq_block8& c = a.c;
-    const int g = c.Hq / c.Hkv, u = blockIdx.x, b = u / c.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool mine = lane < D / 4;
-    const int m = new_rows(a.n_new, b, a.n_q, &g_status_block8_attn);
-    const int held = (min(c.count[u], c.max_blocks * c.block) + c.block - 1) / c.block;
-    for (int t = 0; t < m; ++t) {
-        const int row = u * a.n_q + t, limit = min(query_limit(c.count[u], m, t), c.max_blocks * c.block);
-        const int32_t* list = a.blocks ? a.blocks + (size_t)row * a.n_sel : nullptr;
-        int nb = (limit + c.block - 1) / c.block;
-        if (list) nb = limit > 0 ? min(max(a.list_len[row], 0), a.n_sel) : 0;
-        for (int j = warp; j < nb; j += kWarps) {
-            const int blk = list ? list[j] : j;
-            const int phys = (unsigned)blk < (unsigned)held ? c.table[(size_t)u * c.max_blocks + blk] : -1;
-            if ((unsigned)phys >= (unsigned)c.n_blocks) continue;
-            const float ks = c.k_scale[phys] * a.sm_scale * kLog2e;
-            const int n = min(c.block, limit - blk * c.block);
-            float weight = 0.0f;
-            for (int hh = 0; hh < g; ++hh) {
-                float q[4] = {0, 0, 0, 0};
-                const T* qp = (const T*)a.q + b * a.qs[0] + ((u % c.Hkv) * g + hh) * a.qs[1] + t * a.qs[2];
-                if (mine)
-                    for (int i = 0; i < 4; ++i) q[i] = Elem<T>::to_f(qp[lane * 4 + i]);
-                const float lse2 = a.lse2[(size_t)row * g + hh];
-                for (int i = 0; i < n; ++i)
-                    weight += exp2f(logit<CODE>(q, c.k_codes + ((size_t)phys * c.block + i) * D + lane * 4, mine) * ks - lse2);
-            }
-            if (lane == 0 && n > 0) atomicAdd(&c.acc[phys], weight);
-        }
-        __syncthreads();
+// ------------------------------------------------------------------ the second kernel
+
+// log2 of a row's softmax denominator from its partials, by one warp (-inf: the row sees nothing).
+template <int R>
+__device__ __forceinline__ float2 join_ml(const AttnArgs& a, int w, int row, int2 span, int lane) {
+    float top = -INFINITY, sum = 0.0f;
+    for (int i = span.x + lane; i <= span.y; i += 32)
+        top = fmaxf(top, a.ml[(((size_t)i + w) * R + row) * 2]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.0f : top;
+    for (int i = span.x + lane; i <= span.y; i += 32) {
+        const float2 x = *reinterpret_cast<const float2*>(a.ml + (((size_t)i + w) * R + row) * 2);
+        sum = fmaf(x.y, ex2_approx(x.x - ref), sum);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return make_float2(ref, sum);
+}
+
+constexpr int kJoinThreads = 128, kShareBlocks = 128;
+
+// Blocks [0, works * R): one row of a work unit each: o and lse.  Blocks behind them (accumulate):
+// the shares of kShareBlocks blocks of a unit, or of all listed blocks of a unit, one thread per
+// block, summed over queries, heads and cells in a fixed order.
+template <typename T, int D, int NT, bool LIST, bool ACC>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int rows, int chunks) {
+    constexpr int R = 8 * NT;
+    grid_dependency_wait();
+    const kvq_block8& c = a.c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if ((int)blockIdx.x < rows) {
+        const int w = blockIdx.x / R, i = blockIdx.x % R;
+        const Work k = work_of<NT, LIST>(a, w);
+        if (i >= k.rows) return;
+        const int2 th = row_of<NT, LIST>(a, k, w, i);
+        const size_t orow = ((size_t)k.b * c.Hq + (size_t)(k.u % c.Hkv) * a.g + th.y) * a.n_q + th.x;
+        const int m = new_rows(a.n_new, k.b, a.n_q, &g_status_block8_attn);
+        const int2 span = k.tiles ? a.span[w] : make_int2(1, 0);
+        const float2 rl = join_ml<R>(a, w, i, span, lane);
+        const bool sees = k.tiles && th.x < m && rl.y != 0.0f;
+        if ((int)threadIdx.x < D) {
+            const int d = threadIdx.x;
+            float x = 0.0f;
+            if (sees) {
+#pragma unroll 4
+                for (int j = span.x; j <= span.y; ++j) {
+                    const size_t slot = (size_t)j + w;
+                    x = fmaf(a.part[(slot * R + i) * D + d], ex2_approx(a.ml[(slot * R + i) * 2] - rl.x), x);
+                }
+                x /= rl.y;
+            }
+            ((T*)a.o)[orow * D + d] = Elem<T>::from_f(x);
+        }
+        if (threadIdx.x == 0 && a.lse) a.lse[orow] = sees ? (rl.x - kShift + log2f(rl.y)) * kLn2 : -INFINITY;
+        return;
+    }
+    if constexpr (ACC) {
+        __shared__ float lse2[R];
+        const int x = blockIdx.x - rows, u = x / chunks, chunk = x % chunks;
+        const int m = new_rows(a.n_new, u / c.Hkv, a.n_q, &g_status_block8_attn), per = c.block / 16;
+        for (int t = 0; t < (LIST ? m : 1); ++t) {
+            for (int rt = 0; rt < a.row_tiles; ++rt) {
+                const int w = (LIST ? u * a.n_q + t : u) * a.row_tiles + rt;
+                const Work k = work_of<NT, LIST>(a, w);
+                if (k.tiles == 0) continue;
+                __syncthreads();
+                for (int i = warp; i < R; i += kJoinThreads / 32) {
+                    const float2 rl = join_ml<R>(a, w, i, a.span[w], lane);
+                    const bool sees = i < k.rows && row_of<NT, LIST>(a, k, w, i).x < m && rl.y != 0.0f;
+                    if (lane == 0) lse2[i] = sees ? rl.x - kShift + log2f(rl.y) : INFINITY;
+                }
+                __syncthreads();
+                const int n = LIST ? k.list_n : (k.top + c.block - 1) / c.block;
+                for (int j = chunk * kShareBlocks + threadIdx.x; j < (LIST ? n : min(n, (chunk + 1) * kShareBlocks));
+                     j += kJoinThreads) {
+                    const int blk = LIST ? a.blocks[(size_t)(u * a.n_q + t) * a.n_sel + j] : j;
+                    if (LIST && (unsigned)blk >= (unsigned)((min(c.count[u], c.max_blocks * c.block) + c.block - 1) / c.block))
+                        continue;
+                    const int phys = c.table[(size_t)u * c.max_blocks + blk];
+                    if ((unsigned)phys >= (unsigned)c.n_blocks) continue;
+                    const int cells = min(per, (k.top - blk * c.block + 15) / 16);
+                    float share = 0.0f;
+                    for (int y = 0; y < cells; ++y) {
+                        const float* mass = a.mass + ((size_t)w * a.cells + (size_t)j * per + y) * R;
+#pragma unroll
+                        for (int i = 0; i < R; i += 4) {
+                            const float4 z = *reinterpret_cast<const float4*>(mass + i);
+                            share += ex2_approx(z.x - lse2[i]) + ex2_approx(z.y - lse2[i + 1]) +
+                                     (ex2_approx(z.z - lse2[i + 2]) + ex2_approx(z.w - lse2[i + 3]));
+                        }
+                    }
+                    if (LIST) atomicAdd(&c.acc[phys], share);       // a block listed twice adds twice
+                    else c.acc[phys] += share;
+                }
+                __threadfence_block();
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+struct Layout {
+    int nt, row_tiles, works, cells;
+    size_t part, ml, span, mass, total;
+};
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+Layout layout_of(const kvq_block8& c, int n_q, int n_sel, int accumulate) {
+    Layout y;
+    const int units = c.B * c.Hkv, g = c.Hq / c.Hkv, rows = n_sel ? g : g * n_q;
+    y.nt = rows <= 8 ? 1 : 2;
+    y.row_tiles = (rows + 8 * y.nt - 1) / (8 * y.nt);
+    y.works = units * (n_sel ? n_q : 1) * y.row_tiles;
+    y.cells = (n_sel ? n_sel : c.max_blocks) * (c.block / 16);
+    const size_t slots = (size_t)kMaxCtas + y.works, r = 8 * y.nt;
+    y.part = 0;
+    y.ml = y.part + up256(slots * r * c.D * sizeof(float));
+    y.span = y.ml + up256(slots * r * 2 * sizeof(float));
+    y.mass = y.span + up256((size_t)y.works * sizeof(int2));
+    y.total = y.mass + (accumulate ? up256((size_t)y.works * y.cells * r * sizeof(float)) : 0);
+    return y;
+}
+
+// CTAs of the kernel that the current device holds at once.
+template <typename K>
+cudaError_t resident_ctas(K kernel, std::atomic<int>* known, int* out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    int sms = 0, per = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, 0);
+    if (e != cudaSuccess) return e;
+    *out = sms * per > 0 ? sms * per : 1;
+    if (dev < 64) known[dev].store(*out, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+template <typename T, int D, int CODE, int NT, bool LIST, bool ACC>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+    static std::atomic<int> known[64];
+    auto kernel = attn_kernel<T, D, CODE, NT, LIST, ACC>;
+    int ctas = 0;
+    cudaError_t e = resident_ctas(kernel, known, &ctas);
+    if (e != cudaSuccess) return e;
+    // no more CTAs than runs of kWarps tiles in full caches
+    const long long tiles = (long long)a.works * ((a.cells + 1) / 2);
+    const int grid = (int)std::min<long long>(std::min(ctas, kMaxCtas), (tiles + kWarps - 1) / kWarps);
+    kernel<<<grid, kThreads, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int units = a.c.B * a.c.Hkv, rows = a.works * 8 * NT;
+    const int chunks = LIST ? 1 : (a.c.max_blocks + kShareBlocks - 1) / kShareBlocks;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(rows + (ACC ? units * chunks : 0)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<T, D, NT, LIST, ACC>, a, rows, chunks);
 }
 
 }  // namespace
 
-size_t block8_attn_bytes(const kvq_block8& c, int n_q, int, int accumulate) {
-    return accumulate ? (size_t)c.B * c.Hq * n_q * sizeof(float) : 0;
+size_t block8_attn_bytes(const kvq_block8& c, int n_q, int n_sel, int accumulate) {
+    return layout_of(c, n_q, n_sel, accumulate).total;
 }
 
 cudaError_t launch_block8_attn(const void* q, const int64_t* qs, int n_q, const int32_t* n_new, const kvq_block8& c,
                                float sm_scale, const int32_t* blocks, const int32_t* list_len, int n_sel,
                                int accumulate, void* o, float* lse, void* ws, cudaStream_t s) {
-    AttnArgs a{c, q, {qs[0], qs[1], qs[2]}, n_q, n_new, sm_scale, blocks, list_len, n_sel, accumulate, o, lse, (float*)ws};
-    const unsigned grid = (unsigned)(c.B * c.Hq * n_q);
-    auto go = [&](auto t, auto d, auto k) {
-        attn_kernel<decltype(t), decltype(d)::value, decltype(k)::value><<<grid, kWarps * 32, 0, s>>>(a);
-        if (accumulate)
-            weight_kernel<decltype(t), decltype(d)::value, decltype(k)::value>
-                <<<(unsigned)(c.B * c.Hkv), kWarps * 32, 0, s>>>(a);
-        return cudaGetLastError();
-    };
-    auto by_code = [&](auto t, auto d) {
-        return c.code == KVQ_CODE_E4M3 ? go(t, d, std::integral_constant<int, KVQ_CODE_E4M3>{})
-                                       : go(t, d, std::integral_constant<int, KVQ_CODE_INT8>{});
-    };
-    using D64 = std::integral_constant<int, 64>;
-    using D128 = std::integral_constant<int, 128>;
-    if (c.dtype == KVQ_F16) return c.D == 64 ? by_code(__half{}, D64{}) : by_code(__half{}, D128{});
-    return c.D == 64 ? by_code(__nv_bfloat16{}, D64{}) : by_code(__nv_bfloat16{}, D128{});
+    const Layout y = layout_of(c, n_q, n_sel, accumulate);
+    char* base = (char*)ws;
+    AttnArgs a{c, q, {qs[0], qs[1], qs[2]}, n_q, n_new, sm_scale, blocks, list_len, n_sel, o, lse,
+               c.Hq / c.Hkv, y.row_tiles, y.works, y.cells, (float*)(base + y.part), (float*)(base + y.ml),
+               (float*)(base + y.mass), (int2*)(base + y.span)};
+    // one switch after the other turns the runtime choices into template arguments
+    auto on = [](bool x, auto f) { return x ? f(std::true_type{}) : f(std::false_type{}); };
+    return on(c.dtype == KVQ_BF16, [&](auto bf) {
+        using T = std::conditional_t<decltype(bf)::value, __nv_bfloat16, __half>;
+        return on(c.D == 128, [&](auto wide) {
+            constexpr int D = decltype(wide)::value ? 128 : 64;
+            return on(c.code == KVQ_CODE_INT8, [&](auto i8) {
+                constexpr int CODE = decltype(i8)::value ? KVQ_CODE_INT8 : KVQ_CODE_E4M3;
+                return on(y.nt == 2, [&](auto two) {
+                    constexpr int NT = decltype(two)::value ? 2 : 1;
+                    return on(blocks != nullptr, [&](auto list) {
+                        return on(accumulate != 0, [&](auto acc) {
+                            return launch<T, D, CODE, NT, decltype(list)::value, decltype(acc)::value>(a, s);
+                        });
+                    });
+                });
+            });
+        });
+    });
 }
 
 }  // namespace kvq
