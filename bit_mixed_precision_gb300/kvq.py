@@ -644,7 +644,7 @@ class Block8Cache:
         elif self.ws.device != dev or not self.ws.is_contiguous() or self.ws.dtype != torch.uint8:
             _bad("ws must be a contiguous uint8 tensor on the cache's device")
         shift = -self.ws.data_ptr() % 256
-        self._ws, self._ws_bytes = ctypes.c_void_p(self.ws.data_ptr() + shift), self.ws.numel() - shift
+        self._ws, self._ws_bytes = self.ws.data_ptr() + shift, self.ws.numel() - shift
         if self._ws_bytes < need:
             _bad(f"ws must have {need + 256} bytes")
 
@@ -691,131 +691,150 @@ def make_block8_cache(B, Hq, Hkv, D, dtype, max_tokens, block=64, codes=torch.fl
                        seq_len=z(U, dt=i32), block_pos=z(n, dt=i32), acc=z(n, dt=f32), max_q=max_q, max_sel=max_sel, ws=ws)
 
 
-class _On:
-    """The stream of a block8 call: outputs are allocated on it, and the tensors that a call on
-    another stream than torch's current one reads are kept from reuse until it is done."""
+def _stream8(cache, stream):
+    """The raw stream of a block8 call."""
+    if torch.cuda.current_device() != cache._device.index:
+        _bad(f"the cache is on {cache._device}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(cache._device.index)
+    if stream.device != cache._device:
+        _bad("the stream belongs to another device than the cache")
+    return stream.cuda_stream
 
-    def __init__(self, cache, stream):
-        if cache._device.index != torch.cuda.current_device():
-            _bad(f"the cache is on {cache._device}, the current device is cuda:{torch.cuda.current_device()}")
-        self.current = torch.cuda.current_stream()
-        self.stream = stream or self.current
-        if self.stream.device != cache._device:
-            _bad("the stream belongs to another device than the cache")
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
 
-    def empty(self, like, shape, dtype):
-        if self.stream == self.current:
-            return torch.empty(shape, dtype=dtype, device=like._device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=like._device)
+def _empty8(cache, shape, dtype, stream):
+    """An output, allocated on the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache._device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=cache._device)
 
-    def used(self, *ts):
-        if self.stream != self.current:
-            for t in ts:
-                if t is not None:
-                    t.record_stream(self.stream)
+
+def _used8(stream, *ts):
+    """Keeps the memory of tensors that a call on a given stream uses from reuse until it is done."""
+    for t in ts:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _rows8(cache, x, heads, name):
-    """x as [B, heads, n, D] with 8-element strides and D contiguous (steps may leave n out)."""
+    """x as [B, heads, n, D], last axis contiguous (a step may leave n out): pointer, strides, n."""
     if x.dim() == 3:
         x = x.unsqueeze(2)
-    if x.dim() != 4 or x.shape[0] != cache.B or x.shape[1] != heads or x.shape[3] != cache.D:
-        _bad(f"{name} must be [{cache.B}, {heads}, n, {cache.D}], got {list(x.shape)}")
+    shape = x.shape
+    if x.dim() != 4 or shape[0] != cache.B or shape[1] != heads or shape[3] != cache.D:
+        _bad(f"{name} must be [{cache.B}, {heads}, n, {cache.D}], got {list(shape)}")
     if x.dtype != cache.dtype:
         raise TypeError(f"{name} must have the cache's dtype {cache.dtype}")
     if x.device != cache._device:
         _bad(f"{name} must be on the cache's device")
+    if x.is_contiguous():
+        return x.data_ptr(), None, shape[2]
     if x.stride(3) != 1:
         _bad(f"{name}: the last axis must be contiguous")
-    return x, (ctypes.c_int64 * 3)(*[s if n > 1 else 0 for n, s in zip(x.shape[:3], x.stride())])
+    return x.data_ptr(), (ctypes.c_int64 * 3)(*[s if n > 1 else 0 for n, s in zip(shape[:3], x.stride())]), shape[2]
 
 
 def _ints8(cache, t, shape, name):
-    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()
-                          or t.device != cache._device):
+    """The pointer of an int32 argument, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != cache._device:
         _bad(f"{name} must be a contiguous int32 tensor {list(shape)} on the cache's device")
+    return t.data_ptr()
+
+
+def _out8(cache, t, shape, dtype, name):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != cache._device:
+        _bad(f"{name} must be a contiguous tensor {list(shape)} of {dtype} on the cache's device")
 
 
 def block8_reset(cache, mask=None, stream=None):
     """Empties the units with mask[u] != 0 (int32 [B*Hkv]); every unit without a mask."""
-    on = _On(cache, stream)
-    _ints8(cache, mask, (cache.units,), "mask")
-    _check(lib().block8_reset(cache._ref, _ptr(mask), on.ptr))
-    on.used(mask)
+    s = _stream8(cache, stream)
+    _check(lib().block8_reset(cache._ref, _ints8(cache, mask, (cache.units,), "mask"), s))
+    if stream is not None:
+        _used8(stream, mask)
 
 
 def block8_append(cache, k, v, n_new=None, colscore=None, stream=None):
     """Quantises new tokens k, v [B, Hkv, n, D] (or [B, Hkv, D]) into the cache.  n_new int32 [B]: rows
     of each sequence that count.  colscore float32 [B, Hq, n]: column scores of a prompt
     (prefill_attn_scores), added to the blocks' acc."""
-    on = _On(cache, stream)
-    k, ks = _rows8(cache, k, cache.Hkv, "k")
-    v, vs = _rows8(cache, v, cache.Hkv, "v")
-    n = k.shape[2]
-    if v.shape != k.shape:
+    s = _stream8(cache, stream)
+    kp, ks, n = _rows8(cache, k, cache.Hkv, "k")
+    vp, vs, m = _rows8(cache, v, cache.Hkv, "v")
+    if m != n:
         _bad("k and v must have one shape")
-    _ints8(cache, n_new, (cache.B,), "n_new")
-    if colscore is not None and (tuple(colscore.shape) != (cache.B, cache.Hq, n) or colscore.dtype != torch.float32
-                                 or not colscore.is_contiguous() or colscore.device != cache._device):
-        _bad(f"colscore must be a contiguous float32 tensor [{cache.B}, {cache.Hq}, {n}] on the cache's device")
-    _check(lib().block8_append(cache._ref, _ptr(k), ks, _ptr(v), vs, n, _ptr(n_new), _ptr(colscore), on.ptr))
-    on.used(k, v, n_new, colscore)
+    cs = None
+    if colscore is not None:
+        _out8(cache, colscore, (cache.B, cache.Hq, n), torch.float32, "colscore")
+        cs = colscore.data_ptr()
+    _check(lib().block8_append(cache._ref, kp, ks, vp, vs, n, _ints8(cache, n_new, (cache.B,), "n_new"), cs, s))
+    if stream is not None:
+        _used8(stream, k, v, n_new, colscore)
 
 
 def block8_attn(q, cache, sm_scale=None, blocks=None, accumulate=False, n_new=None, o=None, lse=None, stream=None):
     """Attention of q [B, Hq, n_q, D] (or [B, Hq, D]), the last tokens of the cache; returns (o, lse) in q's
     shape.  blocks: (idx, n) as block8_select returns them, to read only those blocks.
     accumulate: adds each block's softmax weight to cache.acc."""
-    on = _On(cache, stream)
-    shape = tuple(q.shape)
-    q, qs = _rows8(cache, q, cache.Hq, "q")
-    n_q = q.shape[2]
-    _ints8(cache, n_new, (cache.B,), "n_new")
-    idx = n = None
+    s = _stream8(cache, stream)
+    qp, qs, n_q = _rows8(cache, q, cache.Hq, "q")
+    idx = n = ip = np_ = None
+    n_sel = 0
     if blocks is not None:
         idx, n = blocks
-        _ints8(cache, n, (cache.B, cache.Hkv, n_q), "blocks[1]")
-        _ints8(cache, idx, (cache.B, cache.Hkv, n_q, idx.shape[-1]), "blocks[0]")
-    o = on.empty(cache, shape, cache.dtype) if o is None else o
-    lse = on.empty(cache, shape[:-1], torch.float32) if lse is None else lse
-    for t, s, dt, name in ((o, shape, cache.dtype, "o"), (lse, shape[:-1], torch.float32, "lse")):
-        if tuple(t.shape) != s or t.dtype != dt or not t.is_contiguous() or t.device != cache._device:
-            _bad(f"{name} must be a contiguous tensor {list(s)} of {dt} on the cache's device")
-    _check(lib().block8_attn(_ptr(q), qs, n_q, _ptr(n_new), cache._ref,
-                             1.0 / math.sqrt(cache.D) if sm_scale is None else float(sm_scale), _ptr(idx), _ptr(n),
-                             0 if idx is None else idx.shape[-1], 1 if accumulate else 0, _ptr(o), _ptr(lse),
-                             cache._ws, cache._ws_bytes, on.ptr))
-    on.used(q, n_new, idx, n, o, lse)
+        n_sel = idx.shape[-1]
+        np_ = _ints8(cache, n, (cache.B, cache.Hkv, n_q), "blocks[1]")
+        ip = _ints8(cache, idx, (cache.B, cache.Hkv, n_q, n_sel), "blocks[0]")
+    shape = q.shape
+    if o is None:
+        o = _empty8(cache, shape, cache.dtype, stream)
+    else:
+        _out8(cache, o, shape, cache.dtype, "o")
+    if lse is None:
+        lse = _empty8(cache, shape[:-1], torch.float32, stream)
+    else:
+        _out8(cache, lse, shape[:-1], torch.float32, "lse")
+    _check(lib().block8_attn(qp, qs, n_q, _ints8(cache, n_new, (cache.B,), "n_new"), cache._ref,
+                             cache.D ** -0.5 if sm_scale is None else float(sm_scale), ip, np_, n_sel,
+                             1 if accumulate else 0, o.data_ptr(), lse.data_ptr(), cache._ws, cache._ws_bytes, s))
+    if stream is not None:
+        _used8(stream, q, n_new, idx, n, o, lse)
     return o, lse
 
 
 def block8_select(q, cache, n_sel, n_first=1, n_last=1, n_new=None, out=None, stream=None):
     """The n_sel blocks whose key bounds match q [B, Hq, n_q, D] (or [B, Hq, D]) best, the first n_first and
     last n_last always among them: (idx [B, Hkv, n_q, n_sel] ascending, -1 behind the last; n [B, Hkv, n_q])."""
-    on = _On(cache, stream)
-    q, qs = _rows8(cache, q, cache.Hq, "q")
-    n_q = q.shape[2]
-    _ints8(cache, n_new, (cache.B,), "n_new")
+    s = _stream8(cache, stream)
+    qp, qs, n_q = _rows8(cache, q, cache.Hq, "q")
     shape = (cache.B, cache.Hkv, n_q)
-    idx, n = out if out is not None else (on.empty(cache, shape + (max(int(n_sel), 0),), torch.int32),
-                                          on.empty(cache, shape, torch.int32))
-    _ints8(cache, idx, shape + (n_sel,), "idx")
-    _ints8(cache, n, shape, "n")
-    _check(lib().block8_select(_ptr(q), qs, n_q, _ptr(n_new), cache._ref, int(n_sel), int(n_first), int(n_last),
-                               _ptr(idx), _ptr(n), cache._ws, cache._ws_bytes, on.ptr))
-    on.used(q, n_new, idx, n)
+    if out is None:
+        idx = _empty8(cache, shape + (max(int(n_sel), 0),), torch.int32, stream)
+        n = _empty8(cache, shape, torch.int32, stream)
+    else:
+        idx, n = out
+        _out8(cache, idx, shape + (n_sel,), torch.int32, "idx")
+        _out8(cache, n, shape, torch.int32, "n")
+    _check(lib().block8_select(qp, qs, n_q, _ints8(cache, n_new, (cache.B,), "n_new"), cache._ref, int(n_sel),
+                               int(n_first), int(n_last), idx.data_ptr(), n.data_ptr(), cache._ws, cache._ws_bytes, s))
+    if stream is not None:
+        _used8(stream, q, n_new, idx, n)
     return idx, n
 
 
 def block8_evict(cache, keep, n_first=1, n_last=1, n_evicted=None, stream=None):
     """Units with more than keep[u] blocks (int32 [B*Hkv]) lose those of the least accumulated attention;
     returns the number of blocks that left each unit."""
-    on = _On(cache, stream)
-    _ints8(cache, keep, (cache.units,), "keep")
-    n_evicted = on.empty(cache, (cache.units,), torch.int32) if n_evicted is None else n_evicted
-    _ints8(cache, n_evicted, (cache.units,), "n_evicted")
-    _check(lib().block8_evict(cache._ref, _ptr(keep), int(n_first), int(n_last), _ptr(n_evicted), on.ptr))
-    on.used(keep, n_evicted)
+    s = _stream8(cache, stream)
+    kp = _ints8(cache, keep, (cache.units,), "keep")
+    if n_evicted is None:
+        n_evicted = _empty8(cache, (cache.units,), torch.int32, stream)
+    else:
+        _out8(cache, n_evicted, (cache.units,), torch.int32, "n_evicted")
+    _check(lib().block8_evict(cache._ref, kp, int(n_first), int(n_last), n_evicted.data_ptr(), s))
+    if stream is not None:
+        _used8(stream, keep, n_evicted)
     return n_evicted
