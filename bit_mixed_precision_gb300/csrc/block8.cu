@@ -44,16 +44,16 @@ struct AppendArgs {
     const float* colscore;
 };
 
-constexpr int kAppendThreads = 256;
-
 // What a call does to unit u: its tokens before, the new ones (0: nothing), the touched blocks.
 struct Plan {
     int count, n, first, last;      // blocks [first, last]
 };
 
-// The whole CTA calls this.  Checks the unit's room and every table entry the call needs; all
-// threads get the same answer, so that a unit is either appended to as a whole or left alone.
-__device__ Plan append_plan(const AppendArgs& a, int u, bool report) {
+// The whole CTA calls this; all threads get the same answer.  `all`: checks every table entry that
+// the call needs, so that a unit is appended to as a whole or left alone.  Only the CTA that may
+// write the unit's open block and tail and the one that sets its counters need that: what the others
+// write lies in the unit's free blocks.
+__device__ Plan append_plan(const AppendArgs& a, int u, bool all, bool report) {
     Plan p;
     p.count = a.c.count[u];
     p.n = a.n_new ? a.n_new[u / a.c.Hkv] : a.n;
@@ -63,7 +63,7 @@ __device__ Plan append_plan(const AppendArgs& a, int u, bool report) {
     p.first = p.count / a.c.block;
     p.last = p.n > 0 ? (int)((end - 1) / a.c.block) : p.first - 1;
     bool fits = p.count >= 0 && end <= (long long)a.c.max_blocks * a.c.block;
-    if (fits && p.n > 0) {
+    if (all && fits && p.n > 0) {
         const int32_t* row = a.c.table + (size_t)u * a.c.max_blocks;
         bool ok = true;
         for (int i = p.first + (int)threadIdx.x; i <= p.last; i += blockDim.x)
@@ -107,245 +107,276 @@ __device__ __forceinline__ float2 unpack2(uint32_t a) {
     return make_float2(Elem<T>::to_f(h[0]), Elem<T>::to_f(h[1]));
 }
 
+template <int THREADS>
 struct AppendShared {
-    uint32_t amax[kAppendThreads / 32];
-    uint32_t lo[kAppendThreads / 32][64], hi[kAppendThreads / 32][64];  // packed channel pairs per warp
-    float sum[kAppendThreads / 32];
+    uint32_t amax[THREADS / 32][2];     // keys, values
+    float sum[THREADS / 32];
+    uint32_t lo[THREADS / 32][64], hi[THREADS / 32][64];        // packed channel pairs per warp
 };
 
-// Keys or values of one block.  Rows [0, fill) are the open block's 16-bit rows, rows
-// [fill, end) new ones (row r is x + (r - fill) * stride); the block stays open if end < P.
-// PASSES rows per thread: thread i holds 8 channels of row i / (D/8), + RPP, + 2 RPP ...
-//
-// A block whose scale does not grow needs only its new rows: the codes of the others stand, and
-// the bounds are the old ones widened by the new rows' (floor and ceil are monotone), exactly
-// what a quantisation of all rows gives.  A scale grows 1/fill of the time, so a decode step
-// reads one row instead of the whole open block.
-template <typename T, int D, int CODE, int PASSES, bool IS_K>
-__device__ void append_block(const kvq_block8& c, int phys, int fill, int end, const T* x, int64_t stride, T* tail,
-                             AppendShared& sh) {
-    constexpr int TPR = D / 8, RPP = kAppendThreads / TPR;
-    const int col = threadIdx.x % TPR, row0 = threadIdx.x / TPR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr uint32_t kInf2 = Packed2<T>::kInf * 0x10001u;
-    float* scale = IS_K ? c.k_scale : c.v_scale;
-    uint8_t* codes = (IS_K ? c.k_codes : c.v_codes) + (size_t)phys * c.block * D;
-    const float old_s = scale[phys], old_b = IS_K ? c.bound_scale[phys] : 0.0f;
-    uint4 r[PASSES];
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-        const int row = p * RPP + row0;
-        r[p] = make_uint4(0, 0, 0, 0);
-        if (row >= fill && row < end)
-            r[p] = *reinterpret_cast<const uint4*>(x + (int64_t)(row - fill) * stride + col * 8);
-    }
-    int from = fill;                    // first row that counts below
-    bool grow, finite;
-    float s, sb;
-    for (;;) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(r[p].x & 0x7fff7fffu, r[p].y & 0x7fff7fffu),
-                                     __vmaxu2(r[p].z & 0x7fff7fffu, r[p].w & 0x7fff7fffu)));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) sh.amax[warp] = m;
-        __syncthreads();
-        m = 0;
-#pragma unroll
-        for (int w = 0; w < kAppendThreads / 32; ++w) m = __vmaxu2(m, sh.amax[w]);
-        __syncthreads();
-        m = max(m & 0xffffu, m >> 16);
-        finite = m < Packed2<T>::kInf;
-        const float amax = unpack2<T>(m).x;
-        s = finite ? scale_of(amax, Code<CODE>::kInvMax) : __int_as_float(0x7fc00000);
-        sb = finite ? scale_of(amax, kInv127) : __int_as_float(0x7fc00000);
-        grow = from > 0 && !(s <= old_s && (!IS_K || sb <= old_b));
-        if (!grow) break;
-        // the scale grows: every row of the block counts
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int row = p * RPP + row0;
-            if (row < fill) r[p] = *reinterpret_cast<const uint4*>(tail + (size_t)row * D + col * 8);
-        }
-        from = 0;
-    }
-    const bool widen = from > 0;        // the old scale stands
-    if (widen) {
-        s = old_s;
-        sb = old_b;
-    }
+// Codes of the thread's rows of one tensor (keys or values) of a block, and its new rows into the
+// tail while the block stays open.
+template <typename T, int D, int CODE, int THREADS, int PASSES>
+__device__ __forceinline__ void write_codes(const uint4 (&r)[PASSES], uint8_t* codes, T* tail, int from, int fill, int end,
+                                            bool open, bool finite, float s) {
+    constexpr int TPR = D / 8, RPP = THREADS / TPR;
+    const int col = threadIdx.x % TPR, row0 = threadIdx.x / TPR;
     const float inv = __frcp_rn(s);
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
         const int row = p * RPP + row0;
-        if (row >= from && row < end) {
-            uint2 q = make_uint2(0, 0);
-            if (finite) {
-                const float2 f0 = unpack2<T>(r[p].x), f1 = unpack2<T>(r[p].y), f2 = unpack2<T>(r[p].z),
-                             f3 = unpack2<T>(r[p].w);
-                q.x = code_pair<CODE>(f0.x, f0.y, inv) | (code_pair<CODE>(f1.x, f1.y, inv) << 16);
-                q.y = code_pair<CODE>(f2.x, f2.y, inv) | (code_pair<CODE>(f3.x, f3.y, inv) << 16);
-            }
-            *reinterpret_cast<uint2*>(codes + (size_t)row * D + col * 8) = q;
-            if (end < c.block && row >= fill) *reinterpret_cast<uint4*>(tail + (size_t)row * D + col * 8) = r[p];
+        if (row < from || row >= end) continue;
+        uint2 q = make_uint2(0, 0);
+        if (finite) {
+            const float2 f0 = unpack2<T>(r[p].x), f1 = unpack2<T>(r[p].y), f2 = unpack2<T>(r[p].z), f3 = unpack2<T>(r[p].w);
+            q.x = code_pair<CODE>(f0.x, f0.y, inv) | (code_pair<CODE>(f1.x, f1.y, inv) << 16);
+            q.y = code_pair<CODE>(f2.x, f2.y, inv) | (code_pair<CODE>(f3.x, f3.y, inv) << 16);
         }
-    }
-    if constexpr (IS_K) {
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            lo[i] = kInf2;
-            hi[i] = kInf2 | 0x80008000u;
-        }
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int row = p * RPP + row0;
-            if (row >= from && row < end) {
-                const uint32_t w[4] = {r[p].x, r[p].y, r[p].z, r[p].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    lo[i] = min2<T>(lo[i], w[i]);
-                    hi[i] = max2<T>(hi[i], w[i]);
-                }
-            }
-        }
-#pragma unroll
-        for (int o = TPR; o < 32; o <<= 1)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo[i] = min2<T>(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-                hi[i] = max2<T>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
-            }
-        if (lane < TPR)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sh.lo[warp][lane * 4 + i] = lo[i];
-                sh.hi[warp][lane * 4 + i] = hi[i];
-            }
-        __syncthreads();
-        if (threadIdx.x < D / 2) {
-            uint32_t l = sh.lo[0][threadIdx.x], h = sh.hi[0][threadIdx.x];
-#pragma unroll
-            for (int w = 1; w < kAppendThreads / 32; ++w) {
-                l = min2<T>(l, sh.lo[w][threadIdx.x]);
-                h = max2<T>(h, sh.hi[w][threadIdx.x]);
-            }
-            const float ib = __frcp_rn(sb);
-            const float2 fl = unpack2<T>(l), fh = unpack2<T>(h);
-            int l0 = 0, l1 = 0, h0 = 0, h1 = 0;
-            if (finite) {
-                l0 = (int)fmaxf(-127.0f, fminf(127.0f, floorf(__fmul_rn(fl.x, ib))));
-                l1 = (int)fmaxf(-127.0f, fminf(127.0f, floorf(__fmul_rn(fl.y, ib))));
-                h0 = (int)fmaxf(-127.0f, fminf(127.0f, ceilf(__fmul_rn(fh.x, ib))));
-                h1 = (int)fmaxf(-127.0f, fminf(127.0f, ceilf(__fmul_rn(fh.y, ib))));
-            }
-            char2* lp = reinterpret_cast<char2*>(c.k_bound + (size_t)phys * 2 * D) + threadIdx.x;
-            char2* hp = lp + D / 2;
-            if (widen) {
-                const char2 ol = *lp, oh = *hp;
-                l0 = min(l0, (int)ol.x);
-                l1 = min(l1, (int)ol.y);
-                h0 = max(h0, (int)oh.x);
-                h1 = max(h1, (int)oh.y);
-            }
-            *lp = make_char2((signed char)l0, (signed char)l1);
-            *hp = make_char2((signed char)h0, (signed char)h1);
-        }
-        __syncthreads();                // sh is used again
-    }
-    if (threadIdx.x == 0) {
-        scale[phys] = s;
-        if (IS_K) c.bound_scale[phys] = sb;
+        *reinterpret_cast<uint2*>(codes + (size_t)row * D + col * 8) = q;
+        if (open && row >= fill) *reinterpret_cast<uint4*>(tail + (size_t)row * D + col * 8) = r[p];
     }
 }
 
-template <typename T, int D, int CODE, int PASSES>
-__device__ void append_one(const AppendArgs& a, const Plan& p, int u, int block, AppendShared& sh) {
+template <int PASSES>
+__device__ __forceinline__ uint32_t largest(const uint4 (&r)[PASSES]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(r[p].x & 0x7fff7fffu, r[p].y & 0x7fff7fffu),
+                                 __vmaxu2(r[p].z & 0x7fff7fffu, r[p].w & 0x7fff7fffu)));
+    return m;
+}
+
+// One block of one unit.  Rows [0, fill) are the open block's 16-bit rows in the tail, rows
+// [fill, end) new ones; the block stays open if end < block.  Thread i holds 8 channels of row
+// i / (D/8), + RPP, + 2 RPP ..., of keys and values at once: at most four pieces each, all
+// requested before the first is used (THREADS grows with the block), and two barriers a block.
+//
+// A block whose scales do not grow needs only its new rows: the codes of the others stand, and
+// the bounds are the old ones widened by the new rows' (floor and ceil are monotone), exactly
+// what a quantisation of all rows gives.  A scale grows 1/fill of the time, so a decode step
+// reads one row instead of the whole open block.
+template <typename T, int D, int CODE, int THREADS, int PASSES>
+__device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block, AppendShared<THREADS>& sh) {
+    constexpr int TPR = D / 8, RPP = THREADS / TPR, W = THREADS / 32;
+    constexpr uint32_t kInf = Packed2<T>::kInf, kInf2 = kInf * 0x10001u;
     const kvq_block8& c = a.c;
+    const int col = threadIdx.x % TPR, row0 = threadIdx.x / TPR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int P = c.block, b = u / c.Hkv, h = u % c.Hkv;
-    const int fill = max(0, p.count - block * P), end = min(P, p.count + p.n - block * P);
-    const int t0 = block * P + fill - p.count;                  // the block's first new token
+    const int fill = max(0, pl.count - block * P), end = min(P, pl.count + pl.n - block * P);
+    const int t0 = block * P + fill - pl.count;                 // the block's first new token
     const int phys = c.table[(size_t)u * c.max_blocks + block];
-    const T* k = (const T*)a.k + b * a.ks[0] + h * a.ks[1] + t0 * a.ks[2];
-    const T* v = (const T*)a.v + b * a.vs[0] + h * a.vs[1] + t0 * a.vs[2];
-    T* tk = (T*)c.tail_k + (size_t)u * P * D;
-    T* tv = (T*)c.tail_v + (size_t)u * P * D;
-    append_block<T, D, CODE, PASSES, true>(c, phys, fill, end, k, a.ks[2], tk, sh);
-    append_block<T, D, CODE, PASSES, false>(c, phys, fill, end, v, a.vs[2], tv, sh);
+    if ((unsigned)phys >= (unsigned)c.n_blocks) return;         // reported with the unit's whole range
+    T* tk = (T*)c.tail_k + (size_t)u * P * D + col * 8;
+    T* tv = (T*)c.tail_v + (size_t)u * P * D + col * 8;
+    uint4 rk[PASSES], rv[PASSES];
+    {
+        const T* k = (const T*)a.k + b * a.ks[0] + h * a.ks[1] + (int64_t)t0 * a.ks[2] + col * 8;
+        const T* v = (const T*)a.v + b * a.vs[0] + h * a.vs[1] + (int64_t)t0 * a.vs[2] + col * 8;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int row = p * RPP + row0;
+            const bool in = row >= fill && row < end;
+            rk[p] = in ? __ldcs(reinterpret_cast<const uint4*>(k + (int64_t)(row - fill) * a.ks[2])) : make_uint4(0, 0, 0, 0);
+            rv[p] = in ? __ldcs(reinterpret_cast<const uint4*>(v + (int64_t)(row - fill) * a.vs[2])) : make_uint4(0, 0, 0, 0);
+        }
+    }
     float sum = 0.0f;
     if (a.colscore) {
         const int g = c.Hq / c.Hkv, m = end - fill;
         const float* cs = a.colscore + ((size_t)b * c.Hq + (size_t)h * g) * a.n + t0;
-        for (int i = threadIdx.x; i < g * m; i += kAppendThreads) sum += cs[(size_t)(i / m) * a.n + i % m];
+        for (int i = threadIdx.x; i < g * m; i += THREADS) sum += cs[(size_t)(i / m) * a.n + i % m];
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if ((threadIdx.x & 31) == 0) sh.sum[threadIdx.x >> 5] = sum;
+        if (lane == 0) sh.sum[warp] = sum;
+    }
+    const float old_k = fill ? c.k_scale[phys] : 0.0f, old_v = fill ? c.v_scale[phys] : 0.0f,
+                old_b = fill ? c.bound_scale[phys] : 0.0f;
+    int from_k = fill, from_v = fill;   // the rows that count from here on
+    float sk, sv, sb;
+    bool fin_k, fin_v;
+    for (;;) {
+        uint32_t mk = largest(rk), mv = largest(rv);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            mk = __vmaxu2(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            mv = __vmaxu2(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+        }
+        if (lane == 0) {
+            sh.amax[warp][0] = mk;
+            sh.amax[warp][1] = mv;
+        }
         __syncthreads();
-        sum = 0.0f;
-        for (int w = 0; w < kAppendThreads / 32; ++w) sum += sh.sum[w];
+        mk = mv = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            mk = __vmaxu2(mk, sh.amax[w][0]);
+            mv = __vmaxu2(mv, sh.amax[w][1]);
+        }
+        mk = max(mk & 0xffffu, mk >> 16);
+        mv = max(mv & 0xffffu, mv >> 16);
+        const float nan = __int_as_float(0x7fc00000);
+        fin_k = mk < kInf;
+        fin_v = mv < kInf;
+        sk = fin_k ? scale_of(unpack2<T>(mk).x, Code<CODE>::kInvMax) : nan;
+        sb = fin_k ? scale_of(unpack2<T>(mk).x, kInv127) : nan;
+        sv = fin_v ? scale_of(unpack2<T>(mv).x, Code<CODE>::kInvMax) : nan;
+        const bool grow_k = from_k > 0 && !(sk <= old_k && sb <= old_b), grow_v = from_v > 0 && !(sv <= old_v);
+        if (!grow_k && !grow_v) break;
+        // a scale grows: every row of that tensor counts
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int row = p * RPP + row0;
+            if (row < fill) {
+                if (grow_k) rk[p] = *reinterpret_cast<const uint4*>(tk + (size_t)row * D);
+                if (grow_v) rv[p] = *reinterpret_cast<const uint4*>(tv + (size_t)row * D);
+            }
+        }
+        if (grow_k) from_k = 0;
+        if (grow_v) from_v = 0;
+    }
+    const bool widen = from_k > 0;      // the old scales stand
+    if (widen) {
+        sk = old_k;
+        sb = old_b;
+    }
+    if (from_v > 0) sv = old_v;
+    // bounds: minimum and maximum per channel over the thread's rows, the warp's, the CTA's
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = kInf2;
+        hi[i] = kInf2 | 0x80008000u;
+    }
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+        const int row = p * RPP + row0;
+        if (row >= from_k && row < end) {
+            const uint32_t w[4] = {rk[p].x, rk[p].y, rk[p].z, rk[p].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = min2<T>(lo[i], w[i]);
+                hi[i] = max2<T>(hi[i], w[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = TPR; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = min2<T>(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+            hi[i] = max2<T>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+        }
+    if (lane < TPR)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sh.lo[warp][lane * 4 + i] = lo[i];
+            sh.hi[warp][lane * 4 + i] = hi[i];
+        }
+    write_codes<T, D, CODE, THREADS, PASSES>(rk, c.k_codes + (size_t)phys * P * D, tk - col * 8, from_k, fill, end, end < P,
+                                             fin_k, sk);
+    write_codes<T, D, CODE, THREADS, PASSES>(rv, c.v_codes + (size_t)phys * P * D, tv - col * 8, from_v, fill, end, end < P,
+                                             fin_v, sv);
+    __syncthreads();
+    for (int x = threadIdx.x; x < D / 2; x += THREADS) {
+        uint32_t l = sh.lo[0][x], hh = sh.hi[0][x];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            l = min2<T>(l, sh.lo[w][x]);
+            hh = max2<T>(hh, sh.hi[w][x]);
+        }
+        const float ib = __frcp_rn(sb);
+        const float2 fl = unpack2<T>(l), fh = unpack2<T>(hh);
+        int l0 = 0, l1 = 0, h0 = 0, h1 = 0;
+        if (fin_k) {
+            l0 = (int)fmaxf(-127.0f, fminf(127.0f, floorf(__fmul_rn(fl.x, ib))));
+            l1 = (int)fmaxf(-127.0f, fminf(127.0f, floorf(__fmul_rn(fl.y, ib))));
+            h0 = (int)fmaxf(-127.0f, fminf(127.0f, ceilf(__fmul_rn(fh.x, ib))));
+            h1 = (int)fmaxf(-127.0f, fminf(127.0f, ceilf(__fmul_rn(fh.y, ib))));
+        }
+        char2* lp = reinterpret_cast<char2*>(c.k_bound + (size_t)phys * 2 * D) + x;
+        char2* hp = lp + D / 2;
+        if (widen) {
+            const char2 ol = *lp, oh = *hp;
+            l0 = min(l0, (int)ol.x);
+            l1 = min(l1, (int)ol.y);
+            h0 = max(h0, (int)oh.x);
+            h1 = max(h1, (int)oh.y);
+        }
+        *lp = make_char2((signed char)l0, (signed char)l1);
+        *hp = make_char2((signed char)h0, (signed char)h1);
     }
     if (threadIdx.x == 0) {
-        if (fill == 0) c.block_pos[phys] = c.seq_len[u] + block * P - p.count;
+        c.k_scale[phys] = sk;
+        c.bound_scale[phys] = sb;
+        c.v_scale[phys] = sv;
+        if (fill == 0) c.block_pos[phys] = c.seq_len[u] + block * P - pl.count;
+        sum = 0.0f;
+        if (a.colscore)
+            for (int w = 0; w < W; ++w) sum += sh.sum[w];
         if (fill == 0 || a.colscore) c.acc[phys] = (fill == 0 ? 0.0f : c.acc[phys]) + sum;
     }
-    __syncthreads();
 }
 
-// Grid: x = unit + units * j.  CTA j = 0 of a unit takes the first touched block and, where that
-// one was open, the last one too if it stays open: both use the unit's tail rows, the first reads
-// them before the last one writes them.  CTA j takes block first + j.  commit: the CTA is alone
-// (n <= block touches at most those two blocks) and sets the counters itself.
-template <typename T, int D, int CODE, int PASSES>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, int commit) {
-    __shared__ AppendShared sh;
-    const int units = a.c.B * a.c.Hkv, u = blockIdx.x % units, j = blockIdx.x / units;
-    const Plan p = append_plan(a, u, j == 0);
+// Grid: x = j + per * unit.  CTA j takes block first + j; CTA 0 takes, where the first touched
+// block was open, the last one too if that stays open: both use the unit's tail rows, and the
+// first reads them before the last writes them.  commit: the CTA is alone (n <= block touches at
+// most those two blocks) and sets the counters itself.
+template <typename T, int D, int CODE, int THREADS, int PASSES>
+__global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int per, int commit) {
+    __shared__ AppendShared<THREADS> sh;
+    const int u = blockIdx.x / per, j = blockIdx.x % per;
+    const Plan p = append_plan(a, u, j == 0, j == 0);
     if (p.n == 0) return;
     const bool open_first = p.count % a.c.block != 0, open_last = (p.count + p.n) % a.c.block != 0;
     const bool pair = open_first && open_last && p.last > p.first;
     if (p.first + j < p.last || (p.first + j == p.last && !(pair && j > 0)))
-        append_one<T, D, CODE, PASSES>(a, p, u, p.first + j, sh);
-    if (j == 0 && pair) append_one<T, D, CODE, PASSES>(a, p, u, p.last, sh);
+        append_one<T, D, CODE, THREADS, PASSES>(a, p, u, p.first + j, sh);
+    if (j == 0 && pair) {
+        __syncthreads();
+        append_one<T, D, CODE, THREADS, PASSES>(a, p, u, p.last, sh);
+    }
     if (commit && threadIdx.x == 0) {
         a.c.count[u] = p.count + p.n;
         a.c.seq_len[u] += p.n;
     }
 }
 
-__global__ void __launch_bounds__(kAppendThreads) append_commit_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(256) append_commit_kernel(AppendArgs a) {
     const int u = blockIdx.x;
-    const Plan p = append_plan(a, u, false);
+    const Plan p = append_plan(a, u, true, false);
     if (threadIdx.x == 0 && p.n > 0) {
         a.c.count[u] = p.count + p.n;
         a.c.seq_len[u] += p.n;
     }
 }
 
-template <typename T, int D, int CODE, int PASSES>
-cudaError_t launch_append_passes(const AppendArgs& a, cudaStream_t s) {
+template <typename T, int D, int CODE, int THREADS, int PASSES>
+cudaError_t launch_append_threads(const AppendArgs& a, cudaStream_t s) {
     const unsigned units = (unsigned)(a.c.B * a.c.Hkv);
     if (a.n <= a.c.block) {
-        append_kernel<T, D, CODE, PASSES><<<units, kAppendThreads, 0, s>>>(a, 1);
+        append_kernel<T, D, CODE, THREADS, PASSES><<<units, THREADS, 0, s>>>(a, 1, 1);
         return cudaGetLastError();
     }
-    const unsigned per = (unsigned)((a.n + a.c.block - 2) / a.c.block + 1);
-    append_kernel<T, D, CODE, PASSES><<<units * per, kAppendThreads, 0, s>>>(a, 0);
+    const int per = (a.n + a.c.block - 2) / a.c.block + 1;
+    append_kernel<T, D, CODE, THREADS, PASSES><<<units * (unsigned)per, THREADS, 0, s>>>(a, per, 0);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    append_commit_kernel<<<units, kAppendThreads, 0, s>>>(a);
+    append_commit_kernel<<<units, 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
+// Threads so that each holds at most four 16-byte pieces of the block's keys (and of its values).
 template <typename T, int D, int CODE>
 cudaError_t launch_append_typed(const AppendArgs& a, cudaStream_t s) {
-    constexpr int RPP = kAppendThreads / (D / 8);
-    const int passes = (a.c.block + RPP - 1) / RPP;
-    if (passes <= 1) return launch_append_passes<T, D, CODE, 1>(a, s);
-    if (passes <= 2) return launch_append_passes<T, D, CODE, 2>(a, s);
-    if (passes <= 4) return launch_append_passes<T, D, CODE, 4>(a, s);
-    return launch_append_passes<T, D, CODE, 8>(a, s);
+    switch (a.c.block * D / 8) {
+        case 128: return launch_append_threads<T, D, CODE, 64, 2>(a, s);        // 16 x 64
+        case 256: return launch_append_threads<T, D, CODE, 64, 4>(a, s);        // 16 x 128, 32 x 64
+        case 512: return launch_append_threads<T, D, CODE, 128, 4>(a, s);
+        case 1024: return launch_append_threads<T, D, CODE, 256, 4>(a, s);
+        default: return launch_append_threads<T, D, CODE, 512, 4>(a, s);        // 128 x 128
+    }
 }
 
 // ------------------------------------------------------------------ select
