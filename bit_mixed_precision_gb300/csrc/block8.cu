@@ -89,16 +89,17 @@ template <> struct Packed2<__nv_bfloat16> {
     static constexpr uint32_t kInf = 0x7f80u;
 };
 
+// Minimum and maximum of pairs; a NaN wins both.
 template <typename T>
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
     using P = typename Packed2<T>::type;
-    P r = __hmin2(*reinterpret_cast<P*>(&a), *reinterpret_cast<P*>(&b));
+    P r = __hmin2_nan(*reinterpret_cast<P*>(&a), *reinterpret_cast<P*>(&b));
     return *reinterpret_cast<uint32_t*>(&r);
 }
 template <typename T>
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     using P = typename Packed2<T>::type;
-    P r = __hmax2(*reinterpret_cast<P*>(&a), *reinterpret_cast<P*>(&b));
+    P r = __hmax2_nan(*reinterpret_cast<P*>(&a), *reinterpret_cast<P*>(&b));
     return *reinterpret_cast<uint32_t*>(&r);
 }
 template <typename T>
@@ -129,14 +130,39 @@ __device__ __forceinline__ void write_codes(const uint4 (&r)[PASSES], uint8_t* c
         uint2 q = make_uint2(0, 0);
         if (finite) {
             const float2 f0 = unpack2<T>(r[p].x), f1 = unpack2<T>(r[p].y), f2 = unpack2<T>(r[p].z), f3 = unpack2<T>(r[p].w);
-            q.x = code_pair<CODE>(f0.x, f0.y, inv) | (code_pair<CODE>(f1.x, f1.y, inv) << 16);
-            q.y = code_pair<CODE>(f2.x, f2.y, inv) | (code_pair<CODE>(f3.x, f3.y, inv) << 16);
+            q.x = code_four<CODE>(f0.x, f0.y, f1.x, f1.y, inv);
+            q.y = code_four<CODE>(f2.x, f2.y, f3.x, f3.y, inv);
         }
-        *reinterpret_cast<uint2*>(codes + (size_t)row * D + col * 8) = q;
-        if (open && row >= fill) *reinterpret_cast<uint4*>(tail + (size_t)row * D + col * 8) = r[p];
+        *reinterpret_cast<uint2*>(codes + row * D + col * 8) = q;
+        if (open && row >= fill) *reinterpret_cast<uint4*>(tail + row * D + col * 8) = r[p];
     }
 }
 
+// Packed channel minima and maxima of the thread's rows [from, end).
+template <typename T, int RPP, int PASSES>
+__device__ __forceinline__ void channel_range(const uint4 (&r)[PASSES], int row0, int from, int end, uint32_t (&lo)[4],
+                                              uint32_t (&hi)[4]) {
+    constexpr uint32_t kInf2 = Packed2<T>::kInf * 0x10001u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = kInf2;
+        hi[i] = kInf2 | 0x80008000u;
+    }
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+        const int row = p * RPP + row0;
+        if (row >= from && row < end) {
+            const uint32_t w[4] = {r[p].x, r[p].y, r[p].z, r[p].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = min2<T>(lo[i], w[i]);
+                hi[i] = max2<T>(hi[i], w[i]);
+            }
+        }
+    }
+}
+
+// Largest magnitude as 16-bit pairs, NaN and infinity above all numbers.
 template <int PASSES>
 __device__ __forceinline__ uint32_t largest(const uint4 (&r)[PASSES]) {
     uint32_t m = 0;
@@ -159,7 +185,7 @@ __device__ __forceinline__ uint32_t largest(const uint4 (&r)[PASSES]) {
 template <typename T, int D, int CODE, int THREADS, int PASSES>
 __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block, AppendShared<THREADS>& sh) {
     constexpr int TPR = D / 8, RPP = THREADS / TPR, W = THREADS / 32;
-    constexpr uint32_t kInf = Packed2<T>::kInf, kInf2 = kInf * 0x10001u;
+    constexpr uint32_t kInf = Packed2<T>::kInf;
     const kvq_block8& c = a.c;
     const int col = threadIdx.x % TPR, row0 = threadIdx.x / TPR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int P = c.block, b = u / c.Hkv, h = u % c.Hkv;
@@ -185,7 +211,8 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
     if (a.colscore) {
         const int g = c.Hq / c.Hkv, m = end - fill;
         const float* cs = a.colscore + ((size_t)b * c.Hq + (size_t)h * g) * a.n + t0;
-        for (int i = threadIdx.x; i < g * m; i += THREADS) sum += cs[(size_t)(i / m) * a.n + i % m];
+        for (int x = 0; x < g; ++x, cs += a.n)
+            for (int i = threadIdx.x; i < m; i += THREADS) sum += cs[i];
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) sh.sum[warp] = sum;
@@ -195,8 +222,14 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
     int from_k = fill, from_v = fill;   // the rows that count from here on
     float sk, sv, sb;
     bool fin_k, fin_v;
+    uint32_t lo[4], hi[4];              // the keys' range per channel, over the thread's rows
     for (;;) {
-        uint32_t mk = largest(rk), mv = largest(rv);
+        uint32_t mk = 0, mv = largest(rv);
+        channel_range<T, RPP, PASSES>(rk, row0, from_k, end, lo, hi);
+        constexpr uint32_t kInf2 = kInf * 0x10001u;
+        if (lo[0] != kInf2 || hi[0] != (kInf2 | 0x80008000u))   // as they start: the thread has no rows
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mk = __vmaxu2(mk, __vmaxu2(lo[i] & 0x7fff7fffu, hi[i] & 0x7fff7fffu));
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             mk = __vmaxu2(mk, __shfl_xor_sync(0xffffffffu, mk, o));
@@ -242,25 +275,7 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
         sb = old_b;
     }
     if (from_v > 0) sv = old_v;
-    // bounds: minimum and maximum per channel over the thread's rows, the warp's, the CTA's
-    uint32_t lo[4], hi[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo[i] = kInf2;
-        hi[i] = kInf2 | 0x80008000u;
-    }
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-        const int row = p * RPP + row0;
-        if (row >= from_k && row < end) {
-            const uint32_t w[4] = {rk[p].x, rk[p].y, rk[p].z, rk[p].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo[i] = min2<T>(lo[i], w[i]);
-                hi[i] = max2<T>(hi[i], w[i]);
-            }
-        }
-    }
+    // bounds: minimum and maximum per channel, over the warp's rows and then the CTA's
 #pragma unroll
     for (int o = TPR; o < 32; o <<= 1)
 #pragma unroll
@@ -324,7 +339,7 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
 // first reads them before the last writes them.  commit: the CTA is alone (n <= block touches at
 // most those two blocks) and sets the counters itself.
 template <typename T, int D, int CODE, int THREADS, int PASSES>
-__global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a, int per, int commit) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(AppendArgs a, int per, int commit) {
     __shared__ AppendShared<THREADS> sh;
     const int u = blockIdx.x / per, j = blockIdx.x % per;
     const Plan p = append_plan(a, u, j == 0, j == 0);

@@ -44,6 +44,10 @@ using namespace b8;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTile = 32;               // tokens a warp takes at a time
+#ifndef KAHEAD
+#define KAHEAD 1
+#endif
+constexpr int kAhead = KAHEAD;
 constexpr int kMaxCtas = 1024;          // CTAs of the first kernel at most (sizes the workspace)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The reference M moves only when a logit passes it by more than 2^8, and weights carry a factor
@@ -255,6 +259,16 @@ __device__ __forceinline__ Cells find_cells(const AttnArgs& a, const Work& k, in
     return x;
 }
 
+// Asks L2 for the cells of the warp's tiles [from, to) of the 16 in `x`; nothing waits for them.
+template <int D>
+__device__ __forceinline__ void ask_l2(const kvq_block8& c, const Cells& x, int from, int to, int lane) {
+    const int i = lane >> 1;
+    if (i >= from && i < to && x.cell != 0xffffffffu) {
+        bulk_prefetch_l2(c.k_codes + (size_t)x.cell * (16 * D), 16 * D);
+        bulk_prefetch_l2(c.v_codes + (size_t)x.cell * (16 * D), 16 * D);
+    }
+}
+
 template <int D, int NT>
 struct Shared {
     float o[kWarps][8 * NT][D + 4];
@@ -396,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
 #pragma unroll
         for (int j = 0; j < 2; ++j) load_values<D>(vr[j], c.v_codes, cell[j], g, t);
         int at = 0;                     // the tile's place among the 16 of `cells`
+        ask_l2<D>(c, cells, 1, kAhead, lane);
         for (int tile = s0 + warp; tile < s1; tile += kWarps) {
             float ks[2], vs[2];
             int slot[2];
@@ -410,7 +425,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
             if (++at == 16) {
                 cells = find_cells<LIST>(a, k, w, tile + kWarps, s1, lane);
                 at = 0;
+                ask_l2<D>(c, cells, 0, kAhead, lane);
             }
+            ask_l2<D>(c, cells, at + kAhead - 1, at + kAhead, lane);
 #pragma unroll
             for (int j = 0; j < 2; ++j) cell[j] = __shfl_sync(0xffffffffu, cells.cell, 2 * at + j);
             if (tile + kWarps >= s1) cell[0] = cell[1] = 0xffffffffu;

@@ -23,17 +23,35 @@ __device__ __forceinline__ float scale_of(float amax, float inv_max) {
     return fmaxf(__fmul_rn(amax, inv_max), kSmallestScale);
 }
 
-// Two codes of RN(x * inv), x0's in the low byte.
+__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Four codes RN(x * inv), x0's in the low byte.  No clamp is needed: |x| <= amax and inv is at most
+// 1 / fp32(amax / Q), so the product stays below Q (1 + 2^-22), which rounds to Q.  int8: adding
+// 1.5 2^23 rounds to a whole number (ties to even) that the low byte holds in two's complement.
+// (The product and the addition are scalar: the assembler joins packed ones into one fused operation,
+// which rounds otherwise.)
 template <int CODE>
-__device__ __forceinline__ uint32_t code_pair(float x0, float x1, float inv) {
-    const float a = __fmul_rn(x0, inv), b = __fmul_rn(x1, inv);
+__device__ __forceinline__ uint32_t code_four(float x0, float x1, float x2, float x3, float inv) {
     if constexpr (CODE == KVQ_CODE_E4M3) {
-        uint16_t r;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-        return r;
+        const unsigned long long inv2 = f2_pack(inv, inv);
+        float y0, y1, y2, y3;
+        f2_unpack(f2_mul(f2_pack(x0, x1), inv2), y0, y1);
+        f2_unpack(f2_mul(f2_pack(x2, x3), inv2), y2, y3);
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y1), "f"(y0));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y3), "f"(y2));
+        return (uint32_t)lo | ((uint32_t)hi << 16);
     } else {
-        const int ia = min(127, max(-127, __float2int_rn(a))), ib = min(127, max(-127, __float2int_rn(b)));
-        return (uint32_t)(ia & 255) | ((uint32_t)(ib & 255) << 8);
+        const float magic = 12582912.0f;
+        const uint32_t y0 = __float_as_uint(__fadd_rn(__fmul_rn(x0, inv), magic)),
+                       y1 = __float_as_uint(__fadd_rn(__fmul_rn(x1, inv), magic)),
+                       y2 = __float_as_uint(__fadd_rn(__fmul_rn(x2, inv), magic)),
+                       y3 = __float_as_uint(__fadd_rn(__fmul_rn(x3, inv), magic));
+        return __byte_perm(__byte_perm(y0, y1, 0x0040), __byte_perm(y2, y3, 0x0040), 0x5410);
     }
 }
 
