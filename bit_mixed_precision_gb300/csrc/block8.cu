@@ -53,16 +53,17 @@ struct Plan {
 // the call needs, so that a unit is appended to as a whole or left alone.  Only the CTA that may
 // write the unit's open block and tail and the one that sets its counters need that: what the others
 // write lies in the unit's free blocks.
+template <int P>
 __device__ Plan append_plan(const AppendArgs& a, int u, bool all, bool report) {
+    static_assert((P & (P - 1)) == 0, "a power of two");
     Plan p;
     p.count = a.c.count[u];
     p.n = a.n_new ? a.n_new[u / a.c.Hkv] : a.n;
     bool bad = p.n < 0 || p.n > a.n;
     p.n = min(max(p.n, 0), a.n);
-    const long long end = (long long)p.count + p.n;
-    p.first = p.count / a.c.block;
-    p.last = p.n > 0 ? (int)((end - 1) / a.c.block) : p.first - 1;
-    bool fits = p.count >= 0 && end <= (long long)a.c.max_blocks * a.c.block;
+    bool fits = p.count >= 0 && (unsigned)p.count + (unsigned)p.n <= (unsigned)(a.c.max_blocks * P);
+    p.first = p.count / P;
+    p.last = p.n > 0 ? (p.count + p.n - 1) / P : p.first - 1;
     if (all && fits && p.n > 0) {
         const int32_t* row = a.c.table + (size_t)u * a.c.max_blocks;
         bool ok = true;
@@ -77,6 +78,12 @@ __device__ Plan append_plan(const AppendArgs& a, int u, bool all, bool report) {
     }
     if (bad && report && threadIdx.x == 0) atomicOr(&g_status_block8, kDevCheck);
     return p;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 template <typename T> struct Packed2;
@@ -117,7 +124,7 @@ struct AppendShared {
 
 // Codes of the thread's rows of one tensor (keys or values) of a block, and its new rows into the
 // tail while the block stays open.
-template <typename T, int D, int CODE, int THREADS, int PASSES>
+template <typename T, int D, int CODE, int THREADS, int PASSES, bool FULL>
 __device__ __forceinline__ void write_codes(const uint4 (&r)[PASSES], uint8_t* codes, T* tail, int from, int fill, int end,
                                             bool open, bool finite, float s) {
     constexpr int TPR = D / 8, RPP = THREADS / TPR;
@@ -126,7 +133,7 @@ __device__ __forceinline__ void write_codes(const uint4 (&r)[PASSES], uint8_t* c
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
         const int row = p * RPP + row0;
-        if (row < from || row >= end) continue;
+        if (!FULL && (row < from || row >= end)) continue;
         uint2 q = make_uint2(0, 0);
         if (finite) {
             const float2 f0 = unpack2<T>(r[p].x), f1 = unpack2<T>(r[p].y), f2 = unpack2<T>(r[p].z), f3 = unpack2<T>(r[p].w);
@@ -134,12 +141,12 @@ __device__ __forceinline__ void write_codes(const uint4 (&r)[PASSES], uint8_t* c
             q.y = code_four<CODE>(f2.x, f2.y, f3.x, f3.y, inv);
         }
         *reinterpret_cast<uint2*>(codes + row * D + col * 8) = q;
-        if (open && row >= fill) *reinterpret_cast<uint4*>(tail + row * D + col * 8) = r[p];
+        if (!FULL && open && row >= fill) *reinterpret_cast<uint4*>(tail + row * D + col * 8) = r[p];
     }
 }
 
 // Packed channel minima and maxima of the thread's rows [from, end).
-template <typename T, int RPP, int PASSES>
+template <typename T, int RPP, int PASSES, bool FULL>
 __device__ __forceinline__ void channel_range(const uint4 (&r)[PASSES], int row0, int from, int end, uint32_t (&lo)[4],
                                               uint32_t (&hi)[4]) {
     constexpr uint32_t kInf2 = Packed2<T>::kInf * 0x10001u;
@@ -151,7 +158,7 @@ __device__ __forceinline__ void channel_range(const uint4 (&r)[PASSES], int row0
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
         const int row = p * RPP + row0;
-        if (row >= from && row < end) {
+        if (FULL || (row >= from && row < end)) {
             const uint32_t w[4] = {r[p].x, r[p].y, r[p].z, r[p].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -168,8 +175,8 @@ __device__ __forceinline__ uint32_t largest(const uint4 (&r)[PASSES]) {
     uint32_t m = 0;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p)
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(r[p].x & 0x7fff7fffu, r[p].y & 0x7fff7fffu),
-                                 __vmaxu2(r[p].z & 0x7fff7fffu, r[p].w & 0x7fff7fffu)));
+        m = max_u16x2(m, max_u16x2(max_u16x2(r[p].x & 0x7fff7fffu, r[p].y & 0x7fff7fffu),
+                                 max_u16x2(r[p].z & 0x7fff7fffu, r[p].w & 0x7fff7fffu)));
     return m;
 }
 
@@ -182,14 +189,16 @@ __device__ __forceinline__ uint32_t largest(const uint4 (&r)[PASSES]) {
 // the bounds are the old ones widened by the new rows' (floor and ceil are monotone), exactly
 // what a quantisation of all rows gives.  A scale grows 1/fill of the time, so a decode step
 // reads one row instead of the whole open block.
-template <typename T, int D, int CODE, int THREADS, int PASSES>
+//
+// FULL: a block that this call fills from its first row to its last (most of a prompt's).
+template <typename T, int D, int CODE, int THREADS, int PASSES, bool FULL>
 __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block, AppendShared<THREADS>& sh) {
-    constexpr int TPR = D / 8, RPP = THREADS / TPR, W = THREADS / 32;
+    constexpr int TPR = D / 8, RPP = THREADS / TPR, W = THREADS / 32, P = RPP * PASSES;
     constexpr uint32_t kInf = Packed2<T>::kInf;
     const kvq_block8& c = a.c;
     const int col = threadIdx.x % TPR, row0 = threadIdx.x / TPR, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int P = c.block, b = u / c.Hkv, h = u % c.Hkv;
-    const int fill = max(0, pl.count - block * P), end = min(P, pl.count + pl.n - block * P);
+    const int b = u / c.Hkv, h = u % c.Hkv;
+    const int fill = FULL ? 0 : max(0, pl.count - block * P), end = FULL ? P : min(P, pl.count + pl.n - block * P);
     const int t0 = block * P + fill - pl.count;                 // the block's first new token
     const int phys = c.table[(size_t)u * c.max_blocks + block];
     if ((unsigned)phys >= (unsigned)c.n_blocks) return;         // reported with the unit's whole range
@@ -197,14 +206,17 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
     T* tv = (T*)c.tail_v + (size_t)u * P * D + col * 8;
     uint4 rk[PASSES], rv[PASSES];
     {
-        const T* k = (const T*)a.k + b * a.ks[0] + h * a.ks[1] + (int64_t)t0 * a.ks[2] + col * 8;
-        const T* v = (const T*)a.v + b * a.vs[0] + h * a.vs[1] + (int64_t)t0 * a.vs[2] + col * 8;
+        const int64_t t = t0 + row0 - fill;                     // below 0 for rows that are not loaded
+        const T* k = (const T*)a.k + b * a.ks[0] + h * a.ks[1] + t * a.ks[2] + col * 8;
+        const T* v = (const T*)a.v + b * a.vs[0] + h * a.vs[1] + t * a.vs[2] + col * 8;
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
+        for (int p = 0; p < PASSES; ++p, k += RPP * a.ks[2], v += RPP * a.vs[2]) {
             const int row = p * RPP + row0;
-            const bool in = row >= fill && row < end;
-            rk[p] = in ? __ldcs(reinterpret_cast<const uint4*>(k + (int64_t)(row - fill) * a.ks[2])) : make_uint4(0, 0, 0, 0);
-            rv[p] = in ? __ldcs(reinterpret_cast<const uint4*>(v + (int64_t)(row - fill) * a.vs[2])) : make_uint4(0, 0, 0, 0);
+            rk[p] = rv[p] = make_uint4(0, 0, 0, 0);
+            if (FULL || (row >= fill && row < end)) {
+                rk[p] = __ldcs(reinterpret_cast<const uint4*>(k));
+                rv[p] = __ldcs(reinterpret_cast<const uint4*>(v));
+            }
         }
     }
     float sum = 0.0f;
@@ -225,15 +237,15 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
     uint32_t lo[4], hi[4];              // the keys' range per channel, over the thread's rows
     for (;;) {
         uint32_t mk = 0, mv = largest(rv);
-        channel_range<T, RPP, PASSES>(rk, row0, from_k, end, lo, hi);
+        channel_range<T, RPP, PASSES, FULL>(rk, row0, from_k, end, lo, hi);
         constexpr uint32_t kInf2 = kInf * 0x10001u;
-        if (lo[0] != kInf2 || hi[0] != (kInf2 | 0x80008000u))   // as they start: the thread has no rows
+        if (FULL || lo[0] != kInf2 || hi[0] != (kInf2 | 0x80008000u))   // as they start: the thread has no rows
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mk = __vmaxu2(mk, __vmaxu2(lo[i] & 0x7fff7fffu, hi[i] & 0x7fff7fffu));
+            for (int i = 0; i < 4; ++i) mk = max_u16x2(mk, max_u16x2(lo[i] & 0x7fff7fffu, hi[i] & 0x7fff7fffu));
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
-            mk = __vmaxu2(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-            mv = __vmaxu2(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+            mk = max_u16x2(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            mv = max_u16x2(mv, __shfl_xor_sync(0xffffffffu, mv, o));
         }
         if (lane == 0) {
             sh.amax[warp][0] = mk;
@@ -243,8 +255,8 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
         mk = mv = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            mk = __vmaxu2(mk, sh.amax[w][0]);
-            mv = __vmaxu2(mv, sh.amax[w][1]);
+            mk = max_u16x2(mk, sh.amax[w][0]);
+            mv = max_u16x2(mv, sh.amax[w][1]);
         }
         mk = max(mk & 0xffffu, mk >> 16);
         mv = max(mv & 0xffffu, mv >> 16);
@@ -255,7 +267,7 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
         sb = fin_k ? scale_of(unpack2<T>(mk).x, kInv127) : nan;
         sv = fin_v ? scale_of(unpack2<T>(mv).x, Code<CODE>::kInvMax) : nan;
         const bool grow_k = from_k > 0 && !(sk <= old_k && sb <= old_b), grow_v = from_v > 0 && !(sv <= old_v);
-        if (!grow_k && !grow_v) break;
+        if (FULL || (!grow_k && !grow_v)) break;
         // a scale grows: every row of that tensor counts
         __syncthreads();
 #pragma unroll
@@ -289,9 +301,9 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
             sh.lo[warp][lane * 4 + i] = lo[i];
             sh.hi[warp][lane * 4 + i] = hi[i];
         }
-    write_codes<T, D, CODE, THREADS, PASSES>(rk, c.k_codes + (size_t)phys * P * D, tk - col * 8, from_k, fill, end, end < P,
+    write_codes<T, D, CODE, THREADS, PASSES, FULL>(rk, c.k_codes + (size_t)phys * P * D, tk - col * 8, from_k, fill, end, end < P,
                                              fin_k, sk);
-    write_codes<T, D, CODE, THREADS, PASSES>(rv, c.v_codes + (size_t)phys * P * D, tv - col * 8, from_v, fill, end, end < P,
+    write_codes<T, D, CODE, THREADS, PASSES, FULL>(rv, c.v_codes + (size_t)phys * P * D, tv - col * 8, from_v, fill, end, end < P,
                                              fin_v, sv);
     __syncthreads();
     for (int x = threadIdx.x; x < D / 2; x += THREADS) {
@@ -339,18 +351,25 @@ __device__ void append_one(const AppendArgs& a, const Plan& pl, int u, int block
 // first reads them before the last writes them.  commit: the CTA is alone (n <= block touches at
 // most those two blocks) and sets the counters itself.
 template <typename T, int D, int CODE, int THREADS, int PASSES>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(AppendArgs a, int per, int commit) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(AppendArgs a, unsigned per, int commit) {
+    constexpr int P = THREADS * PASSES * 8 / D;
     __shared__ AppendShared<THREADS> sh;
     const int u = blockIdx.x / per, j = blockIdx.x % per;
-    const Plan p = append_plan(a, u, j == 0, j == 0);
+    const Plan p = append_plan<P>(a, u, j == 0, j == 0);
     if (p.n == 0) return;
-    const bool open_first = p.count % a.c.block != 0, open_last = (p.count + p.n) % a.c.block != 0;
+    const bool open_first = p.count % P != 0, open_last = (p.count + p.n) % P != 0;
     const bool pair = open_first && open_last && p.last > p.first;
-    if (p.first + j < p.last || (p.first + j == p.last && !(pair && j > 0)))
-        append_one<T, D, CODE, THREADS, PASSES>(a, p, u, p.first + j, sh);
-    if (j == 0 && pair) {
-        __syncthreads();
-        append_one<T, D, CODE, THREADS, PASSES>(a, p, u, p.last, sh);
+    int block = p.first + j;
+    if (block > p.last) return;
+    const bool full = block * P >= p.count && (block + 1) * P <= p.count + p.n;
+    if (full) {
+        append_one<T, D, CODE, THREADS, PASSES, true>(a, p, u, block, sh);
+    } else if (!(pair && j > 0)) {
+        for (;; block = p.last) {
+            append_one<T, D, CODE, THREADS, PASSES, false>(a, p, u, block, sh);
+            if (!pair || block == p.last) break;
+            __syncthreads();
+        }
     }
     if (commit && threadIdx.x == 0) {
         a.c.count[u] = p.count + p.n;
@@ -358,9 +377,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(AppendA
     }
 }
 
+template <int P>
 __global__ void __launch_bounds__(256) append_commit_kernel(AppendArgs a) {
     const int u = blockIdx.x;
-    const Plan p = append_plan(a, u, true, false);
+    const Plan p = append_plan<P>(a, u, true, false);
     if (threadIdx.x == 0 && p.n > 0) {
         a.c.count[u] = p.count + p.n;
         a.c.seq_len[u] += p.n;
@@ -369,20 +389,22 @@ __global__ void __launch_bounds__(256) append_commit_kernel(AppendArgs a) {
 
 template <typename T, int D, int CODE, int THREADS, int PASSES>
 cudaError_t launch_append_threads(const AppendArgs& a, cudaStream_t s) {
+    constexpr int P = THREADS * PASSES * 8 / D;
     const unsigned units = (unsigned)(a.c.B * a.c.Hkv);
-    if (a.n <= a.c.block) {
+    if (a.n <= P) {
         append_kernel<T, D, CODE, THREADS, PASSES><<<units, THREADS, 0, s>>>(a, 1, 1);
         return cudaGetLastError();
     }
-    const int per = (a.n + a.c.block - 2) / a.c.block + 1;
-    append_kernel<T, D, CODE, THREADS, PASSES><<<units * (unsigned)per, THREADS, 0, s>>>(a, per, 0);
+    const unsigned per = (unsigned)((a.n + P - 2) / P + 1);
+    append_kernel<T, D, CODE, THREADS, PASSES><<<units * per, THREADS, 0, s>>>(a, per, 0);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    append_commit_kernel<<<units, 256, 0, s>>>(a);
+    append_commit_kernel<P><<<units, 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-// Threads so that each holds at most four 16-byte pieces of the block's keys (and of its values).
+// Threads so that each holds at most four 16-byte pieces of the block's keys (and of its values);
+// threads, passes and D give the block's size.
 template <typename T, int D, int CODE>
 cudaError_t launch_append_typed(const AppendArgs& a, cudaStream_t s) {
     switch (a.c.block * D / 8) {
