@@ -5,9 +5,9 @@
 //          in registers, one pass finds the largest magnitude and the keys'
 //          minimum and maximum per channel, a second one (from registers)
 //          writes the codes.  Bound by HBM: 16-bit rows in, 8-bit codes out.
-// select   a score kernel (one thread per block and query: exact integer dot
-//          products of the 8-bit query with the 8-bit key bounds) and a top-k
-//          kernel (one CTA per query and unit).
+// select   a score kernel (exact products of the 8-bit queries with the 8-bit
+//          key bounds on the tensor cores) and, as its programmatic dependent, a
+//          top-k kernel (one CTA per query and unit).
 // evict    one CTA per unit: top-k over the blocks' accumulated weights and a
 //          stable partition of the table row; no codes move.
 #include <type_traits>
@@ -429,30 +429,58 @@ struct SelectArgs {
     float* score;                   // workspace [u][n_q][max_blocks]
 };
 
-constexpr int kScoreThreads = 128;
-constexpr int kHeadTile = 8;        // heads whose sums a thread holds at once
+constexpr int kScoreThreads = 128, kScoreWarps = kScoreThreads / 32;
 
-// One thread per (block, query): sum_c max(q8 low, q8 high) = q8+ . high + q8- . low per head, exact
-// in int32 (4-byte dot products), then the largest of the group's heads.  q8+ and q8- of the
-// group sit in shared memory and are read by all lanes at once; a thread reads its own block's
-// 2 D bytes of bounds in 16-byte pieces.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Scores of `per` blocks for one query and unit: sum_c max(q8 low, q8 high) = q8- . low + q8+ . high
+// is one product of the bounds (16 blocks are the rows of an MMA, their 2 D bounds its k axis) with
+// the group's queries, eight heads to a column block.  Whole numbers below 2^21 in fp16 operands and
+// float32 sums: exact.  Bound rows go from global memory into the fragments, a lane's 16-byte pieces
+// being the k elements of four MMAs; the next 16 blocks' are requested before the current ones' are used.
 template <typename T, int D>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a) {
-    extern __shared__ __align__(16) uint32_t q8[];      // [g][2][D/4]
+__global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int per) {
+    constexpr int S = 2 * D / 16, PAD = 2 * D + 8;      // MMA steps; halves per head in shared memory
+    extern __shared__ __align__(16) __half q8[];        // [heads, a multiple of 8][2][D], rows padded
     __shared__ float sq[KVQ_BLOCK8_MAX_GROUP];
     const kvq_block8& c = a.c;
-    const int units = c.B * c.Hkv, rows = units * a.n_q;
+    const int rows = c.B * c.Hkv * a.n_q;
     const int row = blockIdx.x % rows, chunk = blockIdx.x / rows;
     const int u = row / a.n_q, t = row % a.n_q, b = u / c.Hkv, h = u % c.Hkv, g = c.Hq / c.Hkv;
+    grid_launch_dependents();
     const int m = new_rows(a.n_new, b, a.n_q, &g_status_block8);
     const int limit = min(query_limit(c.count[u], m, t), c.max_blocks * c.block);
     const int nb = (limit + c.block - 1) / c.block;
-    if (chunk * kScoreThreads >= nb || nb <= a.n_sel) return;        // few blocks: all are chosen
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int hh = warp; hh < g; hh += kScoreThreads / 32) {
-        const T* q = (const T*)a.q + b * a.qs[0] + (int64_t)(h * g + hh) * a.qs[1] + t * a.qs[2];
+    const int from = chunk * per, to = min(from + per, nb);
+    if (from >= nb || nb <= a.n_sel) return;            // few blocks: all are chosen
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lt = lane & 3;
+    const int32_t* table = a.c.table + (size_t)u * c.max_blocks;
+    uint4 r[2][S / 4];                                  // rows lg, lg + 8: low, then high bounds
+    float scale[2];
+    bool there[2];
+    auto request = [&](int i0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = i0 + lg + 8 * x;
+            const int phys = i < to ? table[i] : 0;
+            there[x] = (unsigned)phys < (unsigned)c.n_blocks;
+            const uint8_t* p = (const uint8_t*)c.k_bound + (size_t)(there[x] ? phys : 0) * 2 * D + lt * 16;
+            scale[x] = there[x] ? c.bound_scale[phys] : 0.0f;
+#pragma unroll
+            for (int y = 0; y < S / 4; ++y) r[x][y] = load16(p + y * 64);
+        }
+    };
+    int i0 = from + warp * 16;
+    if (i0 < to) request(i0);
+    const int heads = (g + 7) & ~7;
+    for (int hh = warp; hh < heads; hh += kScoreWarps) {
         float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (lane < D / 4) {
+        if (hh < g && lane < D / 4) {
+            const T* q = (const T*)a.q + b * a.qs[0] + (int64_t)(h * g + hh) * a.qs[1] + t * a.qs[2];
             const uint2 w = *reinterpret_cast<const uint2*>(q + lane * 4);
             const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
@@ -465,83 +493,171 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a) {
         const bool finite = mx < 0x7f800000u;
         const float s = finite ? scale_of(__uint_as_float(mx), kInv127) : __int_as_float(0x7fc00000);
         const float inv = __frcp_rn(s);
-        uint32_t pos = 0, neg = 0;
+        if (lane < D / 4)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int v = finite ? min(127, max(-127, __float2int_rn(__fmul_rn(x[i], inv)))) : 0;
-            pos |= (uint32_t)(max(v, 0) & 255) << (8 * i);
-            neg |= (uint32_t)(min(v, 0) & 255) << (8 * i);
-        }
-        if (lane < D / 4) {
-            q8[(hh * 2 + 0) * (D / 4) + lane] = pos;
-            q8[(hh * 2 + 1) * (D / 4) + lane] = neg;
-        }
-        if (lane == 0) sq[hh] = s;
+            for (int i = 0; i < 4; ++i) {
+                const float v = finite ? fminf(127.0f, fmaxf(-127.0f, rintf(__fmul_rn(x[i], inv)))) : 0.0f;
+                q8[hh * PAD + lane * 4 + i] = __float2half_rn(fminf(v, 0.0f));
+                q8[hh * PAD + D + lane * 4 + i] = __float2half_rn(fmaxf(v, 0.0f));
+            }
+        if (lane == 0 && hh < g) sq[hh] = s;
     }
     __syncthreads();
-    const int i = chunk * kScoreThreads + threadIdx.x;
-    if (i >= nb) return;
-    const int phys = c.table[(size_t)u * c.max_blocks + i];
-    float best = -INFINITY;
-    if ((unsigned)phys < (unsigned)c.n_blocks) {
-        const uint4* bound = reinterpret_cast<const uint4*>(c.k_bound + (size_t)phys * 2 * D);
-        bool nan = false;
-        for (int h0 = 0; h0 < g; h0 += kHeadTile) {
-            int acc[kHeadTile] = {};
-            for (int ch = 0; ch < D / 16; ++ch) {
-                const uint4 lo = bound[ch], hi = bound[D / 16 + ch];
+    uint32_t qf[S][2];
+    auto take = [&](int h0) {                           // channels in the order of the lane's pieces
 #pragma unroll
-                for (int k = 0; k < kHeadTile; ++k) {
-                    if (h0 + k < g) {
-                        const uint4 p = reinterpret_cast<const uint4*>(q8)[(h0 + k) * (2 * D / 16) + ch];
-                        const uint4 n = reinterpret_cast<const uint4*>(q8)[(h0 + k) * (2 * D / 16) + D / 16 + ch];
-                        int s = acc[k];
-                        s = __dp4a((int)hi.x, (int)p.x, s);
-                        s = __dp4a((int)hi.y, (int)p.y, s);
-                        s = __dp4a((int)hi.z, (int)p.z, s);
-                        s = __dp4a((int)hi.w, (int)p.w, s);
-                        s = __dp4a((int)lo.x, (int)n.x, s);
-                        s = __dp4a((int)lo.y, (int)n.y, s);
-                        s = __dp4a((int)lo.z, (int)n.z, s);
-                        s = __dp4a((int)lo.w, (int)n.w, s);
-                        acc[k] = s;
-                    }
-                }
-            }
+        for (int s = 0; s < S; ++s) {
+            const uint2 w = *reinterpret_cast<const uint2*>(q8 + (h0 + lg) * PAD + (s / 4) * 64 + lt * 16 + (s % 4) * 4);
+            qf[s][0] = w.x;
+            qf[s][1] = w.y;
+        }
+    };
+    take(0);
+    for (; i0 < to; i0 += kScoreWarps * 16) {
+        uint32_t f[S][4];
 #pragma unroll
-            for (int k = 0; k < kHeadTile; ++k)
-                if (h0 + k < g) {
-                    const float f = __fmul_rn((float)acc[k], sq[h0 + k]);
-                    nan = nan || isnan(f);
-                    best = fmaxf(best, f);
+        for (int s = 0; s < S; ++s) {
+            const uint4 x = r[0][s / 4], y = r[1][s / 4];
+            to_f16<KVQ_CODE_INT8>(s % 4 == 0 ? x.x : s % 4 == 1 ? x.y : s % 4 == 2 ? x.z : x.w, f[s][0], f[s][2]);
+            to_f16<KVQ_CODE_INT8>(s % 4 == 0 ? y.x : s % 4 == 1 ? y.y : s % 4 == 2 ? y.z : y.w, f[s][1], f[s][3]);
+        }
+        const float bs[2] = {scale[0], scale[1]};
+        const bool ok[2] = {there[0], there[1]};
+        if (i0 + kScoreWarps * 16 < to) request(i0 + kScoreWarps * 16);
+        float best[2] = {-INFINITY, -INFINITY};
+        for (int h0 = 0; h0 < g; h0 += 8) {
+            if (g > 8) take(h0);
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < S; ++s) mma(d, f[s][0], f[s][1], f[s][2], f[s][3], qf[s][0], qf[s][1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (h0 + 2 * lt + e < g) {
+                    best[0] = max_or_nan(best[0], __fmul_rn(d[e], sq[h0 + 2 * lt + e]));
+                    best[1] = max_or_nan(best[1], __fmul_rn(d[2 + e], sq[h0 + 2 * lt + e]));
                 }
         }
-        best = nan ? __int_as_float(0x7fc00000) : __fmul_rn(best, c.bound_scale[phys]);
-    } else {
-        atomicOr(&g_status_block8, kDevCheck);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            best[x] = max_or_nan(best[x], __shfl_xor_sync(0xffffffffu, best[x], 1));
+            best[x] = max_or_nan(best[x], __shfl_xor_sync(0xffffffffu, best[x], 2));
+            const int i = i0 + lg + 8 * x;
+            if (lt == 0 && i < to) {
+                if (!ok[x]) atomicOr(&g_status_block8, kDevCheck);
+                a.score[(size_t)row * c.max_blocks + i] = ok[x] ? __fmul_rn(best[x], bs[x]) : -INFINITY;
+            }
+        }
     }
-    a.score[(size_t)row * c.max_blocks + i] = best;
 }
 
-// Block [first, n - last) of n: writes the k of the largest key(i) in ascending order from out[at].
+// ------------------------------------------------------------------ top-k in order
+
+// Which of the keys key(0) .. key(n - 1) are the k largest, ties to the lower index: put(i, chosen,
+// before) for each i, before = how many of lower index are chosen.  k < n.
+//
+// The keys stay in registers, KPT a thread, in index order.  The k-th largest is found two bits a
+// round from the highest bit in which the keys differ: one count of the CTA against three candidates,
+// one barrier.  As soon as a count is k exactly there is nothing more to find (for keys without ties
+// after about log2 n bits).  One scan gives every key its place.
+template <int KPT, typename KeyFn, typename PutFn>
+__device__ void choose_regs(KeyFn key, int n, int k, TopkShared& sh, PutFn put) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5, i0 = threadIdx.x * KPT;
+    uint32_t x[KPT], lo = 0xffffffffu, hi = 0u;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+        x[j] = i0 + j < n ? key(i0 + j) : 0u;           // 0 is no key (rank_key > 0) and never counted
+        hi = max(hi, x[j]);
+        if (i0 + j < n) lo = min(lo, x[j]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    uint2* buf = reinterpret_cast<uint2*>(sh.hist);     // two halves of 32, used in turn
+    if (lane == 0) buf[warp] = make_uint2(lo, hi);
+    __syncthreads();
+    const uint2 ends = lane < nw ? buf[lane] : make_uint2(0xffffffffu, 0u);
+    lo = __reduce_min_sync(0xffffffffu, ends.x);
+    hi = __reduce_max_sync(0xffffffffu, ends.y);
+    uint32_t at = hi;                                   // all keys equal: the k-th largest
+    bool exact = false;
+    if (lo != hi) {
+        int bit = (31 - __clz(lo ^ hi)) & ~1;           // rounds of bits (bit + 1, bit)
+        at = hi >> bit >> 1 >> 1 << bit << 1 << 1;      // what all keys share
+        for (int half = 32; bit >= 0 && !exact; bit -= 2, half ^= 32) {
+            const uint32_t c1 = at | (1u << bit), c2 = at | (2u << bit), c3 = at | (3u << bit);
+            uint32_t n1 = 0, n23 = 0;
+#pragma unroll
+            for (int j = 0; j < KPT; ++j) {
+                n1 += x[j] >= c1 ? 1u : 0u;
+                n23 += (x[j] >= c2 ? 1u : 0u) + (x[j] >= c3 ? 0x10000u : 0u);
+            }
+            n1 = __reduce_add_sync(0xffffffffu, n1);
+            n23 = __reduce_add_sync(0xffffffffu, n23);
+            if (lane == 0) buf[half + warp] = make_uint2(n1, n23);
+            __syncthreads();
+            const uint2 y = lane < nw ? buf[half + lane] : make_uint2(0u, 0u);
+            n1 = __reduce_add_sync(0xffffffffu, y.x);
+            n23 = __reduce_add_sync(0xffffffffu, y.y);
+            const uint32_t kk = (uint32_t)k, n2 = n23 & 0xffffu, n3 = n23 >> 16;
+            exact = n1 == kk || n2 == kk || n3 == kk;
+            if (n3 >= kk) at = c3;
+            else if (n2 >= kk) at = c2;
+            else if (n1 >= kk) at = c1;
+        }
+    }
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+        gt += (exact ? x[j] >= at : x[j] > at) ? 1u : 0u;
+        eq += !exact && x[j] == at ? 1u : 0u;
+    }
+    uint32_t total;
+    const uint32_t before = block_excl_scan(gt << 16 | eq, sh, &total);
+    const uint32_t take = (uint32_t)k - (total >> 16);  // equal keys that are chosen
+    uint32_t g = before >> 16, e = before & 0xffffu;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+        const bool more = exact ? x[j] >= at : x[j] > at, same = !exact && x[j] == at;
+        if (i0 + j < n) put(i0 + j, more || (same && e < take), g + min(e, take));
+        g += more ? 1u : 0u;
+        e += same ? 1u : 0u;
+    }
+}
+
+// The same for any n: radix select with the keys read again in every pass.
 template <typename KeyFn, typename PutFn>
-__device__ void choose(KeyFn key, int first, int n, int k, TopkShared& sh, PutFn put) {
-    uint32_t kstar = 0, take_eq = 0;
-    if (k > 0) block_radix_select([&](int i) { return key(first + i); }, n, k, sh, &kstar, &take_eq);
-    uint32_t eq_base = 0;
+__device__ void choose_many(KeyFn key, int n, int k, TopkShared& sh, PutFn put) {
+    uint32_t kstar = 0xffffffffu, take_eq = 0;
+    if (k > 0) block_radix_select(key, n, k, sh, &kstar, &take_eq);
+    uint32_t eq_base = 0, sel_base = 0;
     for (int c0 = 0; c0 < n; c0 += blockDim.x) {
         const int i = c0 + threadIdx.x;
-        const uint32_t kv = i < n ? key(first + i) : 0u;
-        const uint32_t gt = (k > 0 && i < n && kv > kstar) ? 1u : 0u;
-        const uint32_t eq = (k > 0 && i < n && kv == kstar) ? 1u : 0u;
-        uint32_t eq_tot;
-        const uint32_t eq_rank = block_excl_scan(eq, sh, &eq_tot);
-        put(first + i, i < n, gt | (eq & (eq_base + eq_rank < take_eq ? 1u : 0u)));
-        eq_base += eq_tot;
+        const uint32_t kv = i < n ? key(i) : 0u;
+        const uint32_t eq = k > 0 && i < n && kv == kstar ? 1u : 0u;
+        uint32_t tot;
+        const uint32_t eq_rank = block_excl_scan(eq, sh, &tot);
+        const uint32_t sel = k > 0 && i < n && (kv > kstar || (eq && eq_base + eq_rank < take_eq)) ? 1u : 0u;
+        eq_base += tot;
+        const uint32_t before = block_excl_scan(sel, sh, &tot);
+        if (i < n) put(i, sel != 0, sel_base + before);
+        sel_base += tot;
     }
 }
 
-__global__ void __launch_bounds__(kTopkBlock) choose_kernel(SelectArgs a) {
+constexpr int kChooseThreads = 256;
+
+template <typename KeyFn, typename PutFn>
+__device__ __forceinline__ void choose(KeyFn key, int n, int k, TopkShared& sh, PutFn put) {
+    if (k == 0)
+        for (int i = threadIdx.x; i < n; i += blockDim.x) put(i, false, 0u);
+    else if (n <= 8 * kChooseThreads)
+        choose_regs<8>(key, n, k, sh, put);
+    else if (n <= 32 * kChooseThreads)
+        choose_regs<32>(key, n, k, sh, put);
+    else
+        choose_many(key, n, k, sh, put);
+}
+
+__global__ void __launch_bounds__(kChooseThreads) choose_kernel(SelectArgs a) {
     __shared__ TopkShared sh;
     const kvq_block8& c = a.c;
     const int row = blockIdx.x, u = row / a.n_q, t = row % a.n_q;
@@ -549,32 +665,29 @@ __global__ void __launch_bounds__(kTopkBlock) choose_kernel(SelectArgs a) {
     const int limit = min(query_limit(c.count[u], m, t), c.max_blocks * c.block);
     const int nb = (limit + c.block - 1) / c.block;
     int32_t* out = a.idx_out + (size_t)row * a.n_sel;
-    const int n = min(nb, a.n_sel);
+    if (threadIdx.x == 0) a.n_out[row] = min(nb, a.n_sel);
     if (nb <= a.n_sel) {
         for (int i = threadIdx.x; i < a.n_sel; i += blockDim.x) out[i] = i < nb ? i : -1;
-    } else {
-        const float* score = a.score + (size_t)row * c.max_blocks;
-        for (int i = threadIdx.x; i < a.n_first; i += blockDim.x) out[i] = i;
-        for (int i = threadIdx.x; i < a.n_last; i += blockDim.x) out[a.n_sel - a.n_last + i] = nb - a.n_last + i;
-        uint32_t base = (uint32_t)a.n_first;
-        choose([&](int i) { return rank_key(score[i]); }, a.n_first, nb - a.n_first - a.n_last,
-               a.n_sel - a.n_first - a.n_last, sh, [&](int i, bool, uint32_t sel) {
-                   uint32_t tot;
-                   const uint32_t pos = block_excl_scan(sel, sh, &tot);
-                   if (sel) out[base + pos] = i;
-                   base += tot;
-               });
+        grid_dependency_wait();         // what follows in the stream follows both kernels
+        return;
     }
-    if (threadIdx.x == 0) a.n_out[row] = n;
+    grid_dependency_wait();
+    const float* score = a.score + (size_t)row * c.max_blocks + a.n_first;
+    for (int i = threadIdx.x; i < a.n_first; i += blockDim.x) out[i] = i;
+    for (int i = threadIdx.x; i < a.n_last; i += blockDim.x) out[a.n_sel - a.n_last + i] = nb - a.n_last + i;
+    choose([&](int i) { return rank_key(score[i]); }, nb - a.n_first - a.n_last, a.n_sel - a.n_first - a.n_last, sh,
+           [&](int i, bool chosen, uint32_t before) {
+               if (chosen) out[a.n_first + before] = a.n_first + i;
+           });
 }
 
 // ------------------------------------------------------------------ evict
 
-// keys[i]: the rank key of block i's weight; once block i has been placed, entry e <= i holds the
-// e-th block that left (the table row is rewritten front to back, each entry after it was read).
-__global__ void __launch_bounds__(kTopkBlock) evict_kernel(kvq_block8 c, const int32_t* __restrict__ keep, int n_first,
-                                                          int n_last, int32_t* __restrict__ n_evicted) {
-    extern __shared__ uint32_t keys[];
+// ids: the unit's table row, read once; the new row is written from it.  Where the keys do not fit
+// the registers they are gathered again from acc in every pass.
+__global__ void __launch_bounds__(kChooseThreads) evict_kernel(kvq_block8 c, const int32_t* __restrict__ keep, int n_first,
+                                                              int n_last, int32_t* __restrict__ n_evicted) {
+    extern __shared__ int32_t ids[];
     __shared__ TopkShared sh;
     const int u = blockIdx.x, count = min(max(c.count[u], 0), c.max_blocks * c.block);
     const int nb = (count + c.block - 1) / c.block;
@@ -584,34 +697,21 @@ __global__ void __launch_bounds__(kTopkBlock) evict_kernel(kvq_block8 c, const i
         return;
     }
     int32_t* row = c.table + (size_t)u * c.max_blocks;
-    for (int i = threadIdx.x; i < nb; i += blockDim.x) {
-        const int phys = row[i];
-        const bool ok = (unsigned)phys < (unsigned)c.n_blocks;
-        if (!ok) atomicOr(&g_status_block8, kDevCheck);
-        keys[i] = ok ? rank_key(c.acc[phys]) : 0u;
-    }
+    for (int i = threadIdx.x; i < nb; i += blockDim.x) ids[i] = row[i];
     __syncthreads();
-    uint32_t kept = (uint32_t)n_first, gone = 0;
-    choose([&](int i) { return keys[i]; }, n_first, nb - n_first - n_last, want - n_first - n_last, sh,
-           [&](int i, bool in, uint32_t sel) {
-               const int phys = in ? row[i] : 0;
-               uint32_t tot, out_tot;
-               const uint32_t pos = block_excl_scan(sel, sh, &tot);
-               const uint32_t out = block_excl_scan(in && !sel ? 1u : 0u, sh, &out_tot);
-               if (in && sel) row[kept + pos] = phys;
-               if (in && !sel) keys[gone + out] = (uint32_t)phys;
-               kept += tot;
-               gone += out_tot;
-               __syncthreads();
-           });
-    for (int i0 = 0; i0 < n_last; i0 += blockDim.x) {   // front to back: kept + i <= nb - n_last + i
-        const int i = i0 + threadIdx.x;
-        const int phys = i < n_last ? row[nb - n_last + i] : 0;
-        __syncthreads();
-        if (i < n_last) row[kept + i] = phys;
-        __syncthreads();
-    }
-    for (uint32_t i = threadIdx.x; i < gone; i += blockDim.x) row[want + i] = (int32_t)keys[i];
+    const int mid = want - n_first - n_last;
+    choose(
+        [&](int i) {
+            const int phys = ids[n_first + i];
+            if ((unsigned)phys < (unsigned)c.n_blocks) return rank_key(c.acc[phys]);
+            atomicOr(&g_status_block8, kDevCheck);
+            return 1u;                                  // a lost block goes first
+        },
+        nb - n_first - n_last, mid, sh,
+        [&](int i, bool chosen, uint32_t before) {
+            row[chosen ? n_first + (int)before : want + i - (int)before] = ids[n_first + i];
+        });
+    for (int i = threadIdx.x; i < n_last; i += blockDim.x) row[want - n_last + i] = ids[nb - n_last + i];
     if (threadIdx.x == 0) {
         c.count[u] = count - (nb - want) * c.block;
         if (n_evicted) n_evicted[u] = nb - want;
@@ -677,17 +777,29 @@ cudaError_t launch_block8_select(const void* q, const int64_t* qs, int n_q, cons
     a.score = (float*)ws;
     const unsigned rows = (unsigned)(c.B * c.Hkv * n_q);
     if (c.max_blocks > n_sel) {
-        const unsigned chunks = (unsigned)((c.max_blocks + kScoreThreads - 1) / kScoreThreads);
+        // blocks per CTA: enough for a few rounds of its warps, few enough for some CTAs per SM
+        const long long all = (long long)rows * c.max_blocks;
+        const int per = all >= 152LL * 8 * 512 ? 512 : all >= 152LL * 8 * 128 ? 256 : 128;
+        const unsigned chunks = (unsigned)((c.max_blocks + per - 1) / per);
         cudaError_t e = by_type(c, [&](auto t, auto d) {
             using T = decltype(t);
             constexpr int D = decltype(d)::value;
-            score_kernel<T, D><<<rows * chunks, kScoreThreads, (size_t)(c.Hq / c.Hkv) * 2 * D, s>>>(a);
+            const size_t smem = (size_t)((c.Hq / c.Hkv + 7) & ~7) * (2 * D + 8) * sizeof(__half);
+            score_kernel<T, D><<<rows * chunks, kScoreThreads, smem, s>>>(a, per);
             return cudaGetLastError();
         });
         if (e != cudaSuccess) return e;
     }
-    choose_kernel<<<rows, kTopkBlock, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(rows);
+    cfg.blockDim = dim3(kChooseThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = c.max_blocks > n_sel ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, choose_kernel, a);
 }
 
 cudaError_t launch_block8_evict(const kvq_block8& c, const int32_t* keep, int n_first, int n_last, int32_t* n_evicted,
@@ -697,7 +809,7 @@ cudaError_t launch_block8_evict(const kvq_block8& c, const int32_t* keep, int n_
         cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 51200 * 4);
         if (e != cudaSuccess) return e;
     }
-    evict_kernel<<<(unsigned)(c.B * c.Hkv), kTopkBlock, smem, s>>>(c, keep, n_first, n_last, n_evicted);
+    evict_kernel<<<(unsigned)(c.B * c.Hkv), kChooseThreads, smem, s>>>(c, keep, n_first, n_last, n_evicted);
     return cudaGetLastError();
 }
 

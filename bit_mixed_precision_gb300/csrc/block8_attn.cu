@@ -114,42 +114,10 @@ __device__ __forceinline__ int2 row_of(const AttnArgs& a, const Work& k, int w, 
 
 // ------------------------------------------------------------------ pieces of the inner loop
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 __device__ __forceinline__ uint2 load8(const uint8_t* p) {
     uint2 v;
     asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
-}
-
-// Four codes as two fp16 pairs, exactly.  int8: the byte with its sign bit flipped, under the
-// exponent of 1024, is 1152 + code.
-template <int CODE>
-__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    if constexpr (CODE == KVQ_CODE_E4M3) {
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)w));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
-    } else {
-        const uint32_t x = w ^ 0x80808080u;
-        const __half2 bias = __half2half2(__ushort_as_half(0x6480));
-        uint32_t l = __byte_perm(x, 0x64646464u, 0x4140), h = __byte_perm(x, 0x64646464u, 0x4342);
-        __half2 a = __hsub2(*reinterpret_cast<__half2*>(&l), bias), b = __hsub2(*reinterpret_cast<__half2*>(&h), bias);
-        lo = *reinterpret_cast<uint32_t*>(&a);
-        hi = *reinterpret_cast<uint32_t*>(&b);
-    }
-}
-
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
