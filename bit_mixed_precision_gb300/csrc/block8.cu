@@ -10,6 +10,7 @@
 //          top-k kernel (one CTA per query and unit).
 // evict    one CTA per unit: top-k over the blocks' accumulated weights and a
 //          stable partition of the table row; no codes move.
+#include <algorithm>
 #include <type_traits>
 
 #include "block8_device.cuh"
@@ -437,116 +438,141 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
     return d;
 }
 
-// Scores of `per` blocks for one query and unit: sum_c max(q8 low, q8 high) = q8- . low + q8+ . high
+// Blocks that query t of the unit of row (unit, t) sees, or 0 where all of them are chosen anyway.
+__device__ __forceinline__ int blocks_to_score(const SelectArgs& a, int row) {
+    const kvq_block8& c = a.c;
+    const int u = row / a.n_q, t = row % a.n_q;
+    const int m = new_rows(a.n_new, u / c.Hkv, a.n_q, &g_status_block8);
+    const int limit = min(query_limit(c.count[u], m, t), c.max_blocks * c.block);
+    const int nb = (limit + c.block - 1) / c.block;
+    return nb > a.n_sel ? nb : 0;
+}
+
+// Scores of blocks for the queries of their unit: sum_c max(q8 low, q8 high) = q8- . low + q8+ . high
 // is one product of the bounds (16 blocks are the rows of an MMA, their 2 D bounds its k axis) with
 // the group's queries, eight heads to a column block.  Whole numbers below 2^21 in fp16 operands and
 // float32 sums: exact.  Bound rows go from global memory into the fragments, a lane's 16-byte pieces
-// being the k elements of four MMAs; the next 16 blocks' are requested before the current ones' are used.
+// being the k elements of four MMAs.  All queries' groups of 16 blocks form one list that is split over
+// the resident CTAs; a CTA quantises a query once per run of groups, its warps take the groups in turn,
+// each with the next group's bounds requested before the current ones are used.
 template <typename T, int D>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int per) {
-    constexpr int S = 2 * D / 16, PAD = 2 * D + 8;      // MMA steps; halves per head in shared memory
+__global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(SelectArgs a) {
+    constexpr int S = 2 * D / 16, PAD = 2 * D + 4;      // MMA steps; halves per head in shared memory
     extern __shared__ __align__(16) __half q8[];        // [heads, a multiple of 8][2][D], rows padded
     __shared__ float sq[KVQ_BLOCK8_MAX_GROUP];
+    __shared__ RunShared<kScoreThreads> run;
     const kvq_block8& c = a.c;
-    const int rows = c.B * c.Hkv * a.n_q;
-    const int row = blockIdx.x % rows, chunk = blockIdx.x / rows;
-    const int u = row / a.n_q, t = row % a.n_q, b = u / c.Hkv, h = u % c.Hkv, g = c.Hq / c.Hkv;
+    const int g = c.Hq / c.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lt = lane & 3;
+    int total, per, row, before;
+    find_run<kScoreThreads>(c.B * c.Hkv * a.n_q, [&](int i) { return (blocks_to_score(a, i) + 15) / 16; }, kScoreWarps, run,
+                            &total, &per, &row, &before);
     grid_launch_dependents();
-    const int m = new_rows(a.n_new, b, a.n_q, &g_status_block8);
-    const int limit = min(query_limit(c.count[u], m, t), c.max_blocks * c.block);
-    const int nb = (limit + c.block - 1) / c.block;
-    const int from = chunk * per, to = min(from + per, nb);
-    if (from >= nb || nb <= a.n_sel) return;            // few blocks: all are chosen
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lt = lane & 3;
-    const int32_t* table = a.c.table + (size_t)u * c.max_blocks;
-    uint4 r[2][S / 4];                                  // rows lg, lg + 8: low, then high bounds
-    float scale[2];
-    bool there[2];
-    auto request = [&](int i0) {
+    int from = blockIdx.x * per;
+    const int to = min(from + per, total);
+    for (; from < to; ++row) {
+        const int nb = blocks_to_score(a, row), groups = (nb + 15) / 16;
+        if (groups == 0) continue;
+        const int u = row / a.n_q, t = row % a.n_q, b = u / c.Hkv, h = u % c.Hkv;
+        const int first = from - before, last = min(groups, to - before);      // groups of this query: [first, last)
+        const int32_t* table = a.c.table + (size_t)u * c.max_blocks;
+        uint4 r[2][S / 4];                              // rows lg, lg + 8: low, then high bounds
+        float scale[2];
+        bool there[2];
+        // pool blocks of two of the warp's groups, i and i + kScoreWarps, one a lane; asked for two
+        // groups before they are used
+        auto find = [&](int i) {
+            const int at = 16 * (i + (lane >> 4) * kScoreWarps) + (lane & 15);
+            return at < nb && i < last ? table[at] : 0;
+        };
+        int i = first + warp, ids = find(i), ids2 = find(i + 2 * kScoreWarps);
+        auto request = [&](int half) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int i = i0 + lg + 8 * x;
-            const int phys = i < to ? table[i] : 0;
-            there[x] = (unsigned)phys < (unsigned)c.n_blocks;
-            const uint8_t* p = (const uint8_t*)c.k_bound + (size_t)(there[x] ? phys : 0) * 2 * D + lt * 16;
-            scale[x] = there[x] ? c.bound_scale[phys] : 0.0f;
+            for (int x = 0; x < 2; ++x) {
+                const int phys = __shfl_sync(0xffffffffu, ids, half * 16 + lg + 8 * x);
+                there[x] = (unsigned)phys < (unsigned)c.n_blocks;
+                const int at = there[x] ? phys : 0;
+                const uint8_t* p = (const uint8_t*)c.k_bound + (size_t)at * 2 * D + lt * 16;
 #pragma unroll
-            for (int y = 0; y < S / 4; ++y) r[x][y] = load16(p + y * 64);
-        }
-    };
-    int i0 = from + warp * 16;
-    if (i0 < to) request(i0);
-    const int heads = (g + 7) & ~7;
-    for (int hh = warp; hh < heads; hh += kScoreWarps) {
-        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (hh < g && lane < D / 4) {
-            const T* q = (const T*)a.q + b * a.qs[0] + (int64_t)(h * g + hh) * a.qs[1] + t * a.qs[2];
-            const uint2 w = *reinterpret_cast<const uint2*>(q + lane * 4);
-            const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = Elem<T>::to_f(e[i]);
-        }
-        uint32_t mx = 0;                                // magnitudes as bits: NaN and infinity rank above all
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7fffffffu);
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        const bool finite = mx < 0x7f800000u;
-        const float s = finite ? scale_of(__uint_as_float(mx), kInv127) : __int_as_float(0x7fc00000);
-        const float inv = __frcp_rn(s);
-        if (lane < D / 4)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float v = finite ? fminf(127.0f, fmaxf(-127.0f, rintf(__fmul_rn(x[i], inv)))) : 0.0f;
-                q8[hh * PAD + lane * 4 + i] = __float2half_rn(fminf(v, 0.0f));
-                q8[hh * PAD + D + lane * 4 + i] = __float2half_rn(fmaxf(v, 0.0f));
+                for (int y = 0; y < S / 4; ++y) r[x][y] = load16(p + y * 64);
+                scale[x] = c.bound_scale[at];
             }
-        if (lane == 0 && hh < g) sq[hh] = s;
-    }
-    __syncthreads();
-    uint32_t qf[S][2];
-    auto take = [&](int h0) {                           // channels in the order of the lane's pieces
+        };
+        // the first query row's load and the table's are on their way together
+        const T* q = (const T*)a.q + b * a.qs[0] + (int64_t)(h * g) * a.qs[1] + t * a.qs[2] + lane * 4;
+        uint2 w = make_uint2(0, 0);
+        if (warp < g && lane < D / 4) w = *reinterpret_cast<const uint2*>(q + warp * a.qs[1]);
+        if (i < last) request(0);
+        for (int hh = warp; hh < ((g + 7) & ~7); hh += kScoreWarps) {
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (hh >= kScoreWarps && hh < g && lane < D / 4) w = *reinterpret_cast<const uint2*>(q + hh * a.qs[1]);
+            if (hh < g && lane < D / 4) {
+                const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const uint2 w = *reinterpret_cast<const uint2*>(q8 + (h0 + lg) * PAD + (s / 4) * 64 + lt * 16 + (s % 4) * 4);
-            qf[s][0] = w.x;
-            qf[s][1] = w.y;
-        }
-    };
-    take(0);
-    for (; i0 < to; i0 += kScoreWarps * 16) {
-        uint32_t f[S][4];
+                for (int j = 0; j < 4; ++j) x[j] = Elem<T>::to_f(e[j]);
+            }
+            uint32_t mx = 0;                            // magnitudes as bits: NaN and infinity rank above all
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const uint4 x = r[0][s / 4], y = r[1][s / 4];
-            to_f16<KVQ_CODE_INT8>(s % 4 == 0 ? x.x : s % 4 == 1 ? x.y : s % 4 == 2 ? x.z : x.w, f[s][0], f[s][2]);
-            to_f16<KVQ_CODE_INT8>(s % 4 == 0 ? y.x : s % 4 == 1 ? y.y : s % 4 == 2 ? y.z : y.w, f[s][1], f[s][3]);
-        }
-        const float bs[2] = {scale[0], scale[1]};
-        const bool ok[2] = {there[0], there[1]};
-        if (i0 + kScoreWarps * 16 < to) request(i0 + kScoreWarps * 16);
-        float best[2] = {-INFINITY, -INFINITY};
-        for (int h0 = 0; h0 < g; h0 += 8) {
-            if (g > 8) take(h0);
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < 4; ++j) mx = max(mx, __float_as_uint(x[j]) & 0x7fffffffu);
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            const bool finite = mx < 0x7f800000u;
+            const float s = finite ? scale_of(__uint_as_float(mx), kInv127) : __int_as_float(0x7fc00000);
+            const float inv = __frcp_rn(s);
+            if (lane < D / 4)
 #pragma unroll
-            for (int s = 0; s < S; ++s) mma(d, f[s][0], f[s][1], f[s][2], f[s][3], qf[s][0], qf[s][1]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (h0 + 2 * lt + e < g) {
-                    best[0] = max_or_nan(best[0], __fmul_rn(d[e], sq[h0 + 2 * lt + e]));
-                    best[1] = max_or_nan(best[1], __fmul_rn(d[2 + e], sq[h0 + 2 * lt + e]));
+                for (int j = 0; j < 4; ++j) {
+                    const float v = finite ? fminf(127.0f, fmaxf(-127.0f, rintf(__fmul_rn(x[j], inv)))) : 0.0f;
+                    q8[hh * PAD + lane * 4 + j] = __float2half_rn(fminf(v, 0.0f));
+                    q8[hh * PAD + D + lane * 4 + j] = __float2half_rn(fmaxf(v, 0.0f));
                 }
+            if (lane == 0 && hh < g) sq[hh] = s;
         }
+        __syncthreads();
+        const __half* mine = q8 + lg * PAD + lt * 16;   // fragments: channels in the order of the lane's pieces
+        for (int half = 1; i < last; i += kScoreWarps, half ^= 1) {
+            const float bs[2] = {scale[0], scale[1]};
+            const bool ok[2] = {there[0], there[1]};
+            float best[2] = {-INFINITY, -INFINITY};
+            for (int h0 = 0; h0 < g; h0 += 8) {
+                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d2[4] = {0.0f, 0.0f, 0.0f, 0.0f};     // two chains of products
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            best[x] = max_or_nan(best[x], __shfl_xor_sync(0xffffffffu, best[x], 1));
-            best[x] = max_or_nan(best[x], __shfl_xor_sync(0xffffffffu, best[x], 2));
-            const int i = i0 + lg + 8 * x;
-            if (lt == 0 && i < to) {
-                if (!ok[x]) atomicOr(&g_status_block8, kDevCheck);
-                a.score[(size_t)row * c.max_blocks + i] = ok[x] ? __fmul_rn(best[x], bs[x]) : -INFINITY;
+                for (int s = 0; s < S; ++s) {
+                    const uint4 x = r[0][s / 4], y = r[1][s / 4];
+                    const uint2 q = *reinterpret_cast<const uint2*>(mine + h0 * PAD + (s / 4) * 64 + (s % 4) * 4);
+                    uint32_t a0, a1, a2, a3;
+                    to_f16<KVQ_CODE_INT8>(s % 4 == 0 ? x.x : s % 4 == 1 ? x.y : s % 4 == 2 ? x.z : x.w, a0, a2);
+                    to_f16<KVQ_CODE_INT8>(s % 4 == 0 ? y.x : s % 4 == 1 ? y.y : s % 4 == 2 ? y.z : y.w, a1, a3);
+                    mma(s & 1 ? d2 : d, a0, a1, a2, a3, q.x, q.y);
+                }
+                if (h0 + 8 >= g) {                      // the bounds are read: ask for the next ones
+                    if (half == 0) {
+                        ids = ids2;
+                        ids2 = find(i + 3 * kScoreWarps);
+                    }
+                    if (i + kScoreWarps < last) request(half);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] += d2[e];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (h0 + 2 * lt + e < g) {
+                        best[0] = max_or_nan(best[0], __fmul_rn(d[e], sq[h0 + 2 * lt + e]));
+                        best[1] = max_or_nan(best[1], __fmul_rn(d[2 + e], sq[h0 + 2 * lt + e]));
+                    }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                best[x] = max_or_nan(best[x], __shfl_xor_sync(0xffffffffu, best[x], 1));
+                best[x] = max_or_nan(best[x], __shfl_xor_sync(0xffffffffu, best[x], 2));
+                const int at = 16 * i + lg + 8 * x;
+                if (lt == 0 && at < nb) {
+                    if (!ok[x]) atomicOr(&g_status_block8, kDevCheck);
+                    a.score[(size_t)row * c.max_blocks + at] = ok[x] ? __fmul_rn(best[x], bs[x]) : -INFINITY;
+                }
             }
         }
+        __syncthreads();                                // q8 and sq are written again
+        before += groups;
+        from = before;
     }
 }
 
@@ -777,15 +803,17 @@ cudaError_t launch_block8_select(const void* q, const int64_t* qs, int n_q, cons
     a.score = (float*)ws;
     const unsigned rows = (unsigned)(c.B * c.Hkv * n_q);
     if (c.max_blocks > n_sel) {
-        // blocks per CTA: enough for a few rounds of its warps, few enough for some CTAs per SM
-        const long long all = (long long)rows * c.max_blocks;
-        const int per = all >= 152LL * 8 * 512 ? 512 : all >= 152LL * 8 * 128 ? 256 : 128;
-        const unsigned chunks = (unsigned)((c.max_blocks + per - 1) / per);
         cudaError_t e = by_type(c, [&](auto t, auto d) {
             using T = decltype(t);
             constexpr int D = decltype(d)::value;
-            const size_t smem = (size_t)((c.Hq / c.Hkv + 7) & ~7) * (2 * D + 8) * sizeof(__half);
-            score_kernel<T, D><<<rows * chunks, kScoreThreads, smem, s>>>(a, per);
+            static std::atomic<int> known[64];
+            const size_t smem = (size_t)((c.Hq / c.Hkv + 7) & ~7) * (2 * D + 4) * sizeof(__half);
+            int ctas = 0;
+            cudaError_t r = resident_ctas(score_kernel<T, D>, kScoreThreads, 0, known, &ctas);
+            if (r != cudaSuccess) return r;
+            const long long groups = (long long)rows * ((c.max_blocks + 15) / 16);
+            const unsigned grid = (unsigned)std::min<long long>(ctas, (groups + kScoreWarps - 1) / kScoreWarps);
+            score_kernel<T, D><<<grid, kScoreThreads, smem, s>>>(a);
             return cudaGetLastError();
         });
         if (e != cudaSuccess) return e;

@@ -28,7 +28,6 @@
 //
 // Bound by HBM: 2 D bytes per token and KV head against 4 D g flop.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "block8_device.cuh"
@@ -241,50 +240,8 @@ template <int D, int NT>
 struct Shared {
     float o[kWarps][8 * NT][D + 4];
     float ml[kWarps][8 * NT][2];
-    int scan[kWarps];
-    int start[3];                       // total tiles; first work unit of the CTA, its first tile's number
+    RunShared<kThreads> run;
 };
-
-// First tile of work unit w, for the CTA's first unit: every CTA adds up all units' tiles.
-template <int NT, bool LIST, typename S>
-__device__ __forceinline__ void find_start(const AttnArgs& a, S& sh, int* total, int* per, int* w, int* before) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int each = (a.works + kThreads - 1) / kThreads, w0 = min((int)threadIdx.x * each, a.works),
-              w1 = min(w0 + each, a.works);
-    int sum = 0;
-    for (int i = w0; i < w1; ++i) sum += work_of<NT, LIST>(a, i).tiles;
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sh.scan[warp] = incl;
-    __syncthreads();
-    int all = 0, base = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) base += sh.scan[i];
-        all += sh.scan[i];
-    }
-    *total = all;
-    *per = max((all + (int)gridDim.x - 1) / (int)gridDim.x, kWarps);
-    const int from = blockIdx.x * *per;
-    int at = base + incl - sum;
-    if (from >= at && from < at + sum) {
-        int i = w0;
-        for (;; ++i) {
-            const int n = work_of<NT, LIST>(a, i).tiles;
-            if (from < at + n) break;
-            at += n;
-        }
-        sh.start[1] = i;
-        sh.start[2] = at;
-    }
-    __syncthreads();
-    *w = sh.start[1];
-    *before = sh.start[2];
-}
 
 template <typename T, int D, int CODE, int NT, bool LIST, bool ACC>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArgs a) {
@@ -293,7 +250,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
     const kvq_block8& c = a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int total, per, w, before;
-    find_start<NT, LIST>(a, sh, &total, &per, &w, &before);
+    find_run<kThreads>(a.works, [&](int i) { return work_of<NT, LIST>(a, i).tiles; }, kWarps, sh.run, &total, &per, &w,
+                       &before);
     grid_launch_dependents();
     int from = blockIdx.x * per;
     const int to = min(from + per, total);
@@ -302,23 +260,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
         if (k.tiles == 0) continue;
         const int s0 = from - before, s1 = min(k.tiles, to - before);
         if (s0 == 0 && threadIdx.x == 0) a.span[w] = make_int2(blockIdx.x, (before + k.tiles - 1) / per);
+        // ---- requests, in the order of their latencies: the table, the queries, the first tile
+        KeyRegs<D> kr[2];
+        ValueRegs<D> vr[2];
+        Cells cells = find_cells<LIST>(a, k, w, s0 + warp, s1, lane);
+        uint4 raw[NT][D / 64][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int2 th = row_of<NT, LIST>(a, k, w, min(8 * n + g, k.rows - 1));
+            const T* q = (const T*)a.q + k.b * a.qs[0] + (int64_t)((k.u % c.Hkv) * a.g + th.y) * a.qs[1] + th.x * a.qs[2] +
+                         t * 16;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) raw[n][j][e] = *reinterpret_cast<const uint4*>(q + j * 64 + e * 8);
+        }
+        uint32_t cell[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            cell[j] = __shfl_sync(0xffffffffu, cells.cell, j);
+            load_keys<D>(kr[j], c.k_codes, cell[j], g, t);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) load_values<D>(vr[j], c.v_codes, cell[j], g, t);
         // ---- the queries: row g of each column block, channels in the keys' order, as fp16
         uint32_t qf[NT][D / 16][2];
         float qi[NT][2];                // what undoes a row's factor, for this lane's columns 2t, 2t + 1
         int lim[NT][2], least = k.top;  // tokens that the columns' queries see
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int i = 8 * n + g;
-            const int2 th = row_of<NT, LIST>(a, k, w, min(i, k.rows - 1));
-            const T* q = (const T*)a.q + k.b * a.qs[0] + (int64_t)((k.u % c.Hkv) * a.g + th.y) * a.qs[1] + th.x * a.qs[2] +
-                         t * 16;
             float x[D / 4];
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint4 r = *reinterpret_cast<const uint4*>(q + j * 64 + e * 8);
-                    const T* y = reinterpret_cast<const T*>(&r);
+                    const T* y = reinterpret_cast<const T*>(&raw[n][j][e]);
 #pragma unroll
                     for (int z = 0; z < 8; ++z) x[j * 16 + e * 8 + z] = Elem<T>::to_f(y[z]);
                 }
@@ -366,19 +342,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
             l[n][0] = l[n][1] = 0.0f;
         }
         // ---- the warp's tiles
-        KeyRegs<D> kr[2];
-        ValueRegs<D> vr[2];
-        Cells cells = find_cells<LIST>(a, k, w, s0 + warp, s1, lane);
-        uint32_t cell[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            cell[j] = __shfl_sync(0xffffffffu, cells.cell, j);
-            load_keys<D>(kr[j], c.k_codes, cell[j], g, t);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) load_values<D>(vr[j], c.v_codes, cell[j], g, t);
         int at = 0;                     // the tile's place among the 16 of `cells`
-        ask_l2<D>(c, cells, 1, kAhead, lane);
         for (int tile = s0 + warp; tile < s1; tile += kWarps) {
             float ks[2], vs[2];
             int slot[2];
@@ -593,83 +557,155 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
 
 // ------------------------------------------------------------------ the second kernel
 
-// log2 of a row's softmax denominator from its partials, by one warp (-inf: the row sees nothing).
-template <int R>
-__device__ __forceinline__ float2 join_ml(const AttnArgs& a, int w, int row, int2 span, int lane) {
-    float top = -INFINITY, sum = 0.0f;
-    for (int i = span.x + lane; i <= span.y; i += 32)
-        top = fmaxf(top, a.ml[(((size_t)i + w) * R + row) * 2]);
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+
+// A row's partials j = first, first + step, ... <= last joined by one warp: the reference M and the
+// sum l that belong to it, and D / 32 output channels a lane (o, if OUT).  Four partials are in flight
+// at a time.
+template <int D, int R, bool OUT>
+__device__ __forceinline__ float2 join_row(const AttnArgs& a, int w, int row, int first, int last, int step, int lane,
+                                           float (&o)[D / 32]) {
+    constexpr int V = D / 32;
+    float M = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    for (int i = span.x + lane; i <= span.y; i += 32) {
-        const float2 x = *reinterpret_cast<const float2*>(a.ml + (((size_t)i + w) * R + row) * 2);
-        sum = fmaf(x.y, ex2_approx(x.x - ref), sum);
+    for (int v = 0; v < V; ++v) o[v] = 0.0f;
+    for (int j = first; j <= last; j += 4 * step) {
+        float2 ml[4];
+        float x[4][V];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            const size_t at = ((size_t)(j + i * step) + w) * R + row;
+            if (j + i * step <= last) {
+                ml[i] = *reinterpret_cast<const float2*>(a.ml + at * 2);
+                if (OUT) {
+                    const float* p = a.part + at * D + lane * V;
+                    if constexpr (V == 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(p);
+                        x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+                    } else {
+                        const float2 y = *reinterpret_cast<const float2*>(p);
+                        x[i][0] = y.x; x[i][1] = y.y;
+                    }
+                }
+            } else if (OUT) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[i][v] = 0.0f;
+            }
+        }
+        const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+        const float ref = top == -INFINITY ? 0.0f : top, old = ex2_approx(M - ref);
+        M = top;
+        l *= old;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] *= old;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = ex2_approx(ml[i].x - ref);
+            l = fmaf(ml[i].y, f, l);
+            if (OUT)
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = fmaf(x[i][v], f, o[v]);
+        }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return make_float2(ref, sum);
+    return make_float2(M, l);
 }
 
-constexpr int kJoinThreads = 128, kShareBlocks = 128;
-
-// Blocks [0, works * R): one row of a work unit each: o and lse.  Blocks behind them (accumulate):
-// the shares of kShareBlocks blocks of a unit, or of all listed blocks of a unit, one thread per
-// block, summed over queries, heads and cells in a fixed order.
-template <typename T, int D, int NT, bool LIST, bool ACC>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int rows, int chunks) {
-    constexpr int R = 8 * NT;
-    grid_dependency_wait();
+// Blocks [0, works * R * SPLIT / kJoinWarps): SPLIT warps join one row of a work unit: o and lse.
+// Blocks behind them (accumulate): the shares of kJoinThreads blocks of a unit, or of all listed blocks
+// of a unit, one thread per block, summed over queries, heads and cells in a fixed order.  What does
+// not come from the first kernel is read before the wait for it.
+template <typename T, int D, int NT, bool LIST, bool ACC, int SPLIT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int row_blocks, int chunks) {
+    constexpr int R = 8 * NT, V = D / 32;
     const kvq_block8& c = a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if ((int)blockIdx.x < rows) {
-        const int w = blockIdx.x / R, i = blockIdx.x % R;
+    if ((int)blockIdx.x < row_blocks) {
+        __shared__ float2 sml[kJoinWarps];
+        __shared__ float so[kJoinWarps][D];
+        const int x = blockIdx.x * (kJoinWarps / SPLIT) + warp / SPLIT, w = x / R, i = x % R, part = warp % SPLIT;
         const Work k = work_of<NT, LIST>(a, w);
-        if (i >= k.rows) return;
-        const int2 th = row_of<NT, LIST>(a, k, w, i);
-        const size_t orow = ((size_t)k.b * c.Hq + (size_t)(k.u % c.Hkv) * a.g + th.y) * a.n_q + th.x;
         const int m = new_rows(a.n_new, k.b, a.n_q, &g_status_block8_attn);
-        const int2 span = k.tiles ? a.span[w] : make_int2(1, 0);
-        const float2 rl = join_ml<R>(a, w, i, span, lane);
-        const bool sees = k.tiles && th.x < m && rl.y != 0.0f;
-        if ((int)threadIdx.x < D) {
-            const int d = threadIdx.x;
-            float x = 0.0f;
-            if (sees) {
-#pragma unroll 4
-                for (int j = span.x; j <= span.y; ++j) {
-                    const size_t slot = (size_t)j + w;
-                    x = fmaf(a.part[(slot * R + i) * D + d], ex2_approx(a.ml[(slot * R + i) * 2] - rl.x), x);
-                }
-                x /= rl.y;
-            }
-            ((T*)a.o)[orow * D + d] = Elem<T>::from_f(x);
+        const int2 th = row_of<NT, LIST>(a, k, w, min(i, k.rows - 1));
+        const bool live = i < k.rows && k.tiles > 0 && th.x < m;
+        grid_dependency_wait();
+        float o[V], l = 0.0f, M = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = 0.0f;
+        if (live) {
+            const int2 span = a.span[w];
+            const float2 ml = join_row<D, R, true>(a, w, i, span.x + part, span.y, SPLIT, lane, o);
+            M = ml.x;
+            l = ml.y;
         }
-        if (threadIdx.x == 0 && a.lse) a.lse[orow] = sees ? (rl.x - kShift + log2f(rl.y)) * kLn2 : -INFINITY;
+        if (SPLIT > 1) {
+            if (lane == 0) sml[warp] = make_float2(M, l);
+#pragma unroll
+            for (int v = 0; v < V; ++v) so[warp][lane * V + v] = o[v];
+            __syncthreads();
+            if (part) return;
+            float top = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < SPLIT; ++p) top = fmaxf(top, sml[warp + p].x);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            M = top;
+            l = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = 0.0f;
+#pragma unroll
+            for (int p = 0; p < SPLIT; ++p) {
+                const float f = ex2_approx(sml[warp + p].x - ref);
+                l = fmaf(sml[warp + p].y, f, l);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = fmaf(so[warp + p][lane * V + v], f, o[v]);
+            }
+        }
+        if (i >= k.rows) return;
+        const bool sees = live && l != 0.0f;
+        const float inv = sees ? 1.0f / l : 0.0f;
+        const size_t orow = ((size_t)k.b * c.Hq + (size_t)(k.u % c.Hkv) * a.g + th.y) * a.n_q + th.x;
+        T y[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[v] = Elem<T>::from_f(sees ? o[v] * inv : 0.0f);
+        T* dst = (T*)a.o + orow * D + lane * V;
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(y);
+        else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<uint32_t*>(y);
+        if (lane == 0 && a.lse)
+            a.lse[orow] = sees ? ((M == -INFINITY ? 0.0f : M) - kShift + log2f(l)) * kLn2 : -INFINITY;
         return;
     }
     if constexpr (ACC) {
         __shared__ float lse2[R];
-        const int x = blockIdx.x - rows, u = x / chunks, chunk = x % chunks;
+        const int x = blockIdx.x - row_blocks, u = x / chunks, chunk = x % chunks;
         const int m = new_rows(a.n_new, u / c.Hkv, a.n_q, &g_status_block8_attn), per = c.block / 16;
+        const int held = (min(c.count[u], c.max_blocks * c.block) + c.block - 1) / c.block;
+        grid_dependency_wait();
         for (int t = 0; t < (LIST ? m : 1); ++t) {
             for (int rt = 0; rt < a.row_tiles; ++rt) {
                 const int w = (LIST ? u * a.n_q + t : u) * a.row_tiles + rt;
                 const Work k = work_of<NT, LIST>(a, w);
-                if (k.tiles == 0) continue;
+                const int n = LIST ? k.list_n : (k.top + c.block - 1) / c.block;
+                if (n <= chunk * kJoinThreads) continue;
+                const int2 span = a.span[w];
                 __syncthreads();
-                for (int i = warp; i < R; i += kJoinThreads / 32) {
-                    const float2 rl = join_ml<R>(a, w, i, a.span[w], lane);
-                    const bool sees = i < k.rows && row_of<NT, LIST>(a, k, w, i).x < m && rl.y != 0.0f;
-                    if (lane == 0) lse2[i] = sees ? rl.x - kShift + log2f(rl.y) : INFINITY;
+                for (int i = warp; i < R; i += kJoinWarps) {
+                    float none[V];
+                    const float2 ml = join_row<D, R, false>(a, w, i, span.x + lane, span.y, 32, lane, none);
+                    float top = ml.x;
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float ref = top == -INFINITY ? 0.0f : top;
+                    float l = ml.y * ex2_approx(ml.x - ref);
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                    const bool sees = i < k.rows && row_of<NT, LIST>(a, k, w, i).x < m && l != 0.0f;
+                    if (lane == 0) lse2[i] = sees ? ref - kShift + log2f(l) : INFINITY;
                 }
                 __syncthreads();
-                const int n = LIST ? k.list_n : (k.top + c.block - 1) / c.block;
-                for (int j = chunk * kShareBlocks + threadIdx.x; j < (LIST ? n : min(n, (chunk + 1) * kShareBlocks));
+                for (int j = chunk * kJoinThreads + threadIdx.x; j < (LIST ? n : min(n, (chunk + 1) * kJoinThreads));
                      j += kJoinThreads) {
                     const int blk = LIST ? a.blocks[(size_t)(u * a.n_q + t) * a.n_sel + j] : j;
-                    if (LIST && (unsigned)blk >= (unsigned)((min(c.count[u], c.max_blocks * c.block) + c.block - 1) / c.block))
-                        continue;
+                    if ((unsigned)blk >= (unsigned)held) continue;
                     const int phys = c.table[(size_t)u * c.max_blocks + blk];
                     if ((unsigned)phys >= (unsigned)c.n_blocks) continue;
                     const int cells = min(per, (k.top - blk * c.block + 15) / 16);
@@ -686,7 +722,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int rows
                     if (LIST) atomicAdd(&c.acc[phys], share);       // a block listed twice adds twice
                     else c.acc[phys] += share;
                 }
-                __threadfence_block();
             }
         }
     }
@@ -717,20 +752,20 @@ Layout layout_of(const kvq_block8& c, int n_q, int n_sel, int accumulate) {
     return y;
 }
 
-// CTAs of the kernel that the current device holds at once.
-template <typename K>
-cudaError_t resident_ctas(K kernel, std::atomic<int>* known, int* out) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64 && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-    int sms = 0, per = 0;
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, 0);
-    if (e != cudaSuccess) return e;
-    *out = sms * per > 0 ? sms * per : 1;
-    if (dev < 64) known[dev].store(*out, std::memory_order_relaxed);
-    return cudaSuccess;
+template <typename T, int D, int NT, bool LIST, bool ACC, int SPLIT>
+cudaError_t launch_join(const AttnArgs& a, cudaStream_t s) {
+    const int units = a.c.B * a.c.Hkv, row_blocks = a.works * 8 * NT * SPLIT / kJoinWarps;
+    const int chunks = LIST ? 1 : (a.c.max_blocks + kJoinThreads - 1) / kJoinThreads;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(row_blocks + (ACC ? units * chunks : 0)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<T, D, NT, LIST, ACC, SPLIT>, a, row_blocks, chunks);
 }
 
 template <typename T, int D, int CODE, int NT, bool LIST, bool ACC>
@@ -738,7 +773,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     static std::atomic<int> known[64];
     auto kernel = attn_kernel<T, D, CODE, NT, LIST, ACC>;
     int ctas = 0;
-    cudaError_t e = resident_ctas(kernel, known, &ctas);
+    cudaError_t e = resident_ctas(kernel, kThreads, 0, known, &ctas);
     if (e != cudaSuccess) return e;
     // no more CTAs than runs of kWarps tiles in full caches
     const long long tiles = (long long)a.works * ((a.cells + 1) / 2);
@@ -746,18 +781,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     kernel<<<grid, kThreads, 0, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int units = a.c.B * a.c.Hkv, rows = a.works * 8 * NT;
-    const int chunks = LIST ? 1 : (a.c.max_blocks + kShareBlocks - 1) / kShareBlocks;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(rows + (ACC ? units * chunks : 0)));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<T, D, NT, LIST, ACC>, a, rows, chunks);
+    // four warps a row where a unit has many partials, one where it has few
+    return grid >= 4 * a.works ? launch_join<T, D, NT, LIST, ACC, 4>(a, s) : launch_join<T, D, NT, LIST, ACC, 1>(a, s);
 }
 
 }  // namespace

@@ -2,6 +2,8 @@
 // queries' limits, exact conversions of 8-bit codes to fp16 pairs.
 #pragma once
 
+#include <atomic>
+
 #include "kvq_common.cuh"
 
 namespace kvq {
@@ -72,6 +74,71 @@ __device__ __forceinline__ uint32_t rank_key(float f) {
     if (isnan(f)) return 0xffffffffu;
     const uint32_t u = __float_as_uint(f + 0.0f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Work units 0 .. works - 1 of tiles(i) tiles each, in one list that is split evenly over the grid's
+// CTAs, whatever the units' sizes (known on the device only): every CTA adds all of them up.  CTA c
+// takes the tiles [c per, c per + per) of the list; *w is the unit of its first one and *before the
+// tiles of the units ahead of that (both only where c per < *total).  The whole CTA calls this.
+template <int THREADS>
+struct RunShared {
+    int scan[THREADS / 32], start[2];
+};
+
+template <int THREADS, typename TilesFn>
+__device__ __forceinline__ void find_run(int works, TilesFn tiles, int least, RunShared<THREADS>& sh, int* total, int* per,
+                                         int* w, int* before) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int each = (works + THREADS - 1) / THREADS, w0 = min((int)threadIdx.x * each, works), w1 = min(w0 + each, works);
+    int sum = 0;
+    for (int i = w0; i < w1; ++i) sum += tiles(i);
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    __syncthreads();
+    int all = 0, base = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) base += sh.scan[i];
+        all += sh.scan[i];
+    }
+    *total = all;
+    *per = max((all + (int)gridDim.x - 1) / (int)gridDim.x, least);
+    const int from = (int)blockIdx.x * *per;
+    int at = base + incl - sum;
+    if (from >= at && from < at + sum) {
+        int i = w0;
+        for (;; ++i) {
+            const int n = tiles(i);
+            if (from < at + n) break;
+            at += n;
+        }
+        sh.start[0] = i;
+        sh.start[1] = at;
+    }
+    __syncthreads();
+    *w = sh.start[0];
+    *before = sh.start[1];
+}
+
+// CTAs of the kernel that the current device holds at once.
+template <typename K>
+inline cudaError_t resident_ctas(K kernel, int threads, size_t smem, std::atomic<int>* known, int* out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    int sms = 0, per = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    *out = sms * per > 0 ? sms * per : 1;
+    if (dev < 64) known[dev].store(*out, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 // 16 bytes that are read once.
