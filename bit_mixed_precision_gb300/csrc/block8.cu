@@ -460,20 +460,19 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(SelectArgs a) {
     constexpr int S = 2 * D / 16, PAD = 2 * D + 4;      // MMA steps; halves per head in shared memory
     extern __shared__ __align__(16) __half q8[];        // [heads, a multiple of 8][2][D], rows padded
     __shared__ float sq[KVQ_BLOCK8_MAX_GROUP];
-    __shared__ RunShared<kScoreThreads> run;
+    __shared__ RunShared<kScoreThreads> run_sh;
     const kvq_block8& c = a.c;
     const int g = c.Hq / c.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lt = lane & 3;
-    int total, per, row, before;
-    find_run<kScoreThreads>(c.B * c.Hkv * a.n_q, [&](int i) { return (blocks_to_score(a, i) + 15) / 16; }, kScoreWarps, run,
-                            &total, &per, &row, &before);
+    const Run run = find_run<kScoreThreads>(
+        c.B * c.Hkv * a.n_q, [&](int i) { return (blocks_to_score(a, i) + 15) / 16; }, kScoreWarps, run_sh);
     grid_launch_dependents();
-    int from = blockIdx.x * per;
-    const int to = min(from + per, total);
-    for (; from < to; ++row) {
+    for (int row = run.work, from = run.from, before = run.before; from < run.to; ++row) {
         const int nb = blocks_to_score(a, row), groups = (nb + 15) / 16;
         if (groups == 0) continue;
         const int u = row / a.n_q, t = row % a.n_q, b = u / c.Hkv, h = u % c.Hkv;
-        const int first = from - before, last = min(groups, to - before);      // groups of this query: [first, last)
+        // groups of this query: [first, last)
+        const int first = max(from - before - run.start, 0), last = min(groups, run.to - before - run.start);
+        if (last <= 0) break;                           // the run ends ahead of the query's groups
         const int32_t* table = a.c.table + (size_t)u * c.max_blocks;
         uint4 r[2][S / 4];                              // rows lg, lg + 8: low, then high bounds
         float scale[2];
@@ -571,7 +570,7 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(SelectArgs a) {
             }
         }
         __syncthreads();                                // q8 and sq are written again
-        before += groups;
+        before += groups + run.start;
         from = before;
     }
 }

@@ -42,11 +42,6 @@ namespace {
 using namespace b8;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 32;               // tokens a warp takes at a time
-#ifndef KAHEAD
-#define KAHEAD 1
-#endif
-constexpr int kAhead = KAHEAD;
 constexpr int kMaxCtas = 1024;          // CTAs of the first kernel at most (sizes the workspace)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The reference M moves only when a logit passes it by more than 2^8, and weights carry a factor
@@ -72,10 +67,19 @@ struct AttnArgs {
     int2* span;                         // [work] first and last CTA
 };
 
+// Shapes by the number of 8-row column blocks.  One (up to 8 rows): tiles of two cells, query fragments
+// in registers, three CTAs per SM.  Two and four share a tile's converted codes among 16 or 32 rows;
+// their accumulators leave room for one cell, and the fragments are read from shared memory.
+template <int NT> struct Shape {
+    static constexpr int C = NT == 1 ? 2 : 1;           // 16-token cells of a tile
+    static constexpr int kCtas = NT == 4 ? 2 : 3;       // resident CTAs per SM
+    static constexpr bool kSharedQ = NT > 1;
+};
+
 // What a work unit is and sees.
 struct Work {
     int u, b, t0, rows;                 // unit, sequence, first query (the only one with lists), valid + padding rows
-    int tiles, top;                     // 32-token tiles; tokens that its last query sees
+    int tiles, top;                     // tiles; tokens that its last query sees
     int list_n;                         // listed blocks
 };
 
@@ -97,9 +101,9 @@ __device__ __forceinline__ Work work_of(const AttnArgs& a, int w) {
         const int n = a.list_len[x];
         if (n < 0 || n > a.n_sel) atomicOr(&g_status_block8_attn, kDevCheck);
         k.list_n = k.top > 0 ? min(max(n, 0), a.n_sel) : 0;
-        k.tiles = (k.list_n * (a.c.block / 16) + 1) / 2;
+        k.tiles = (k.list_n * (a.c.block / 16) + Shape<NT>::C - 1) / Shape<NT>::C;
     } else {
-        k.tiles = (k.top + kTile - 1) / kTile;
+        k.tiles = (k.top + 16 * Shape<NT>::C - 1) / (16 * Shape<NT>::C);
     }
     return k;
 }
@@ -177,21 +181,21 @@ __device__ __forceinline__ void load_values(ValueRegs<D>& v, const uint8_t* code
     }
 }
 
-// Where a warp's next 16 tiles lie: lane 2 i + j holds cell j of its i-th tile.
+// Where a warp's next 32 / C tiles lie: lane C i + j holds cell j of its i-th tile.
 struct Cells {
     uint32_t cell;                      // number of the 16-token cell in the pool, ~0 for none
     int slot;                           // its first token in the unit
     float ks, vs;                       // k_scale sigma log2(e), v_scale
 };
 
-template <bool LIST>
+template <int C, bool LIST>
 __device__ __forceinline__ Cells find_cells(const AttnArgs& a, const Work& k, int w, int tile, int end, int lane) {
     Cells x;
     x.cell = 0xffffffffu;
     x.slot = 0;
     x.ks = 0.0f;
     x.vs = 1.0f;
-    const int my = tile + (lane >> 1) * kWarps, cell = 2 * my + (lane & 1);
+    const int my = tile + (lane / C) * kWarps, cell = C * my + lane % C;
     if (my < end) {
         const int per = a.c.block / 16, j = cell / per, in = cell % per;
         int blk = j;
@@ -226,11 +230,10 @@ __device__ __forceinline__ Cells find_cells(const AttnArgs& a, const Work& k, in
     return x;
 }
 
-// Asks L2 for the cells of the warp's tiles [from, to) of the 16 in `x`; nothing waits for them.
-template <int D>
-__device__ __forceinline__ void ask_l2(const kvq_block8& c, const Cells& x, int from, int to, int lane) {
-    const int i = lane >> 1;
-    if (i >= from && i < to && x.cell != 0xffffffffu) {
+// Asks L2 for the cells of tile i of those in `x`; nothing waits for them.
+template <int D, int C>
+__device__ __forceinline__ void ask_l2(const kvq_block8& c, const Cells& x, int i, int lane) {
+    if (lane / C == i && x.cell != 0xffffffffu) {
         bulk_prefetch_l2(c.k_codes + (size_t)x.cell * (16 * D), 16 * D);
         bulk_prefetch_l2(c.v_codes + (size_t)x.cell * (16 * D), 16 * D);
     }
@@ -238,36 +241,40 @@ __device__ __forceinline__ void ask_l2(const kvq_block8& c, const Cells& x, int 
 
 template <int D, int NT>
 struct Shared {
-    float o[kWarps][8 * NT][D + 4];
+    float o[kWarps][8][D + 4];          // one column block at a time
     float ml[kWarps][8 * NT][2];
+    __half q[Shape<NT>::kSharedQ ? 8 * NT : 1][D + 4];          // queries as fp16, rows padded
+    float undo[8 * NT];
     RunShared<kThreads> run;
 };
 
 template <typename T, int D, int CODE, int NT, bool LIST, bool ACC>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArgs a) {
-    constexpr int R = 8 * NT;
+__global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnArgs a) {
+    constexpr int R = 8 * NT, C = Shape<NT>::C, LANES = 32 / C;
+    constexpr bool SQ = Shape<NT>::kSharedQ;
     __shared__ Shared<D, NT> sh;
     const kvq_block8& c = a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    int total, per, w, before;
-    find_run<kThreads>(a.works, [&](int i) { return work_of<NT, LIST>(a, i).tiles; }, kWarps, sh.run, &total, &per, &w,
-                       &before);
+    const Run run = find_run<kThreads>(a.works, [&](int i) { return work_of<NT, LIST>(a, i).tiles; }, kWarps, sh.run);
     grid_launch_dependents();
-    int from = blockIdx.x * per;
-    const int to = min(from + per, total);
-    for (; from < to; ++w) {
+    for (int w = run.work, from = run.from, before = run.before; from < run.to; ++w) {
         const Work k = work_of<NT, LIST>(a, w);
         if (k.tiles == 0) continue;
-        const int s0 = from - before, s1 = min(k.tiles, to - before);
-        if (s0 == 0 && threadIdx.x == 0) a.span[w] = make_int2(blockIdx.x, (before + k.tiles - 1) / per);
+        const int s0 = max(from - before - run.start, 0), s1 = min(k.tiles, run.to - before - run.start);
+        if (s1 <= 0) break;                     // the run ends ahead of the unit's tiles
+        if (s0 == 0 && threadIdx.x == 0)
+            a.span[w] = make_int2(blockIdx.x, (before + run.start + k.tiles - 1) / run.per);
         // ---- requests, in the order of their latencies: the table, the queries, the first tile
-        KeyRegs<D> kr[2];
-        ValueRegs<D> vr[2];
-        Cells cells = find_cells<LIST>(a, k, w, s0 + warp, s1, lane);
-        uint4 raw[NT][D / 64][2];
+        KeyRegs<D> kr[C];
+        ValueRegs<D> vr[C];
+        Cells cells = find_cells<C, LIST>(a, k, w, s0 + warp, s1, lane);
+        // a column block's query row g: all column blocks where fragments stay in registers, else block
+        // `warp` of this warp, for all warps
+        constexpr int QN = SQ ? 1 : NT;
+        uint4 raw[QN][D / 64][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int2 th = row_of<NT, LIST>(a, k, w, min(8 * n + g, k.rows - 1));
+        for (int n = 0; n < QN; ++n) {
+            const int2 th = row_of<NT, LIST>(a, k, w, min(8 * (SQ ? warp : n) + g, k.rows - 1));
             const T* q = (const T*)a.q + k.b * a.qs[0] + (int64_t)((k.u % c.Hkv) * a.g + th.y) * a.qs[1] + th.x * a.qs[2] +
                          t * 16;
 #pragma unroll
@@ -275,20 +282,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
 #pragma unroll
                 for (int e = 0; e < 2; ++e) raw[n][j][e] = *reinterpret_cast<const uint4*>(q + j * 64 + e * 8);
         }
-        uint32_t cell[2];
+        uint32_t cell[C];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < C; ++j) {
             cell[j] = __shfl_sync(0xffffffffu, cells.cell, j);
             load_keys<D>(kr[j], c.k_codes, cell[j], g, t);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) load_values<D>(vr[j], c.v_codes, cell[j], g, t);
-        // ---- the queries: row g of each column block, channels in the keys' order, as fp16
-        uint32_t qf[NT][D / 16][2];
-        float qi[NT][2];                // what undoes a row's factor, for this lane's columns 2t, 2t + 1
-        int lim[NT][2], least = k.top;  // tokens that the columns' queries see
+        for (int j = 0; j < C; ++j) load_values<D>(vr[j], c.v_codes, cell[j], g, t);
+        // ---- the queries, channels in the keys' order, as fp16
+        uint32_t qf[QN][D / 16][2];
+        float undo[QN];                 // what undoes a row's factor
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < QN; ++n) {
             float x[D / 4];
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
@@ -298,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
 #pragma unroll
                     for (int z = 0; z < 8; ++z) x[j * 16 + e * 8 + z] = Elem<T>::to_f(y[z]);
                 }
-            float undo = 1.0f;
+            undo[n] = 1.0f;
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                 // bf16 reaches further than fp16: a power of two brings the row's largest to 2^14 .. 2^15
                 uint32_t mx = 0;
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
                 mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const int e = min(max((int)(mx >> 23), 28), 254);
                 const float f = mx < 0x7f800000u ? __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23) : 1.0f;
-                undo = mx < 0x7f800000u ? __uint_as_float((uint32_t)(e - 14) << 23) : 1.0f;
+                undo[n] = mx < 0x7f800000u ? __uint_as_float((uint32_t)(e - 14) << 23) : 1.0f;
 #pragma unroll
                 for (int z = 0; z < D / 4; ++z) x[z] *= f;
             }
@@ -318,17 +324,34 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
                 qf[n][s][0] = *reinterpret_cast<uint32_t*>(&h0);
                 qf[n][s][1] = *reinterpret_cast<uint32_t*>(&h1);
             }
+        }
+        if constexpr (SQ) {             // (the CTA's last unit's queries were read before its merge's barrier)
+            if (warp < NT) {
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s)
+                    *reinterpret_cast<uint2*>(&sh.q[8 * warp + g][(s / 4) * 64 + t * 16 + (s % 4) * 4]) =
+                        make_uint2(qf[0][s][0], qf[0][s][1]);
+                if (t == 0) sh.undo[8 * warp + g] = undo[0];
+            }
+            __syncthreads();
+        }
+        float qi[NT][2];                // undo for this lane's columns 2t, 2t + 1
+        int lim[NT][2], least = k.top;  // tokens that the columns' queries see
+        {
             const int m = a.n_new ? min(max(a.n_new[k.b], 0), a.n_q) : a.n_q;
             const int count = min(c.count[k.u], c.max_blocks * c.block);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int col = 8 * n + 2 * t + e;
-                qi[n][e] = __shfl_sync(0xffffffffu, undo, (2 * t + e) * 4);
-                lim[n][e] = k.top;      // padding rows: as the last query; nobody reads them
-                const int tq = row_of<NT, LIST>(a, k, w, col).x;
-                if (col < k.rows && tq < m) lim[n][e] = query_limit(count, m, tq);
-                least = min(least, lim[n][e]);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int col = 8 * n + 2 * t + e;
+                    if constexpr (SQ) qi[n][e] = sh.undo[col];
+                    else qi[n][e] = __shfl_sync(0xffffffffu, undo[n], (2 * t + e) * 4);
+                    lim[n][e] = k.top;  // padding rows: as the last query; nobody reads them
+                    const int tq = row_of<NT, LIST>(a, k, w, col).x;
+                    if (col < k.rows && tq < m) lim[n][e] = query_limit(count, m, tq);
+                    least = min(least, lim[n][e]);
+                }
         }
         least = __reduce_min_sync(0xffffffffu, least);
         float o[NT][D / 16][4], M[NT][2], l[NT][2];
@@ -342,31 +365,32 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
             l[n][0] = l[n][1] = 0.0f;
         }
         // ---- the warp's tiles
-        int at = 0;                     // the tile's place among the 16 of `cells`
+        int at = 0;                     // the tile's place among those of `cells`
         for (int tile = s0 + warp; tile < s1; tile += kWarps) {
-            float ks[2], vs[2];
-            int slot[2];
+            float ks[C], vs[C];
+            int slot[C];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ks[j] = __shfl_sync(0xffffffffu, cells.ks, 2 * at + j);
-                vs[j] = __shfl_sync(0xffffffffu, cells.vs, 2 * at + j);
-                slot[j] = __shfl_sync(0xffffffffu, cells.slot, 2 * at + j);
+            for (int j = 0; j < C; ++j) {
+                ks[j] = __shfl_sync(0xffffffffu, cells.ks, C * at + j);
+                vs[j] = __shfl_sync(0xffffffffu, cells.vs, C * at + j);
+                slot[j] = __shfl_sync(0xffffffffu, cells.slot, C * at + j);
                 if (cell[j] == 0xffffffffu) slot[j] = 0x40000000;       // nothing there: behind every limit
             }
             // where the next tile lies
-            if (++at == 16) {
-                cells = find_cells<LIST>(a, k, w, tile + kWarps, s1, lane);
+            if (++at == LANES) {
+                cells = find_cells<C, LIST>(a, k, w, tile + kWarps, s1, lane);
                 at = 0;
-                ask_l2<D>(c, cells, 0, kAhead, lane);
             }
-            ask_l2<D>(c, cells, at + kAhead - 1, at + kAhead, lane);
+            ask_l2<D, C>(c, cells, at, lane);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) cell[j] = __shfl_sync(0xffffffffu, cells.cell, 2 * at + j);
-            if (tile + kWarps >= s1) cell[0] = cell[1] = 0xffffffffu;
+            for (int j = 0; j < C; ++j) cell[j] = __shfl_sync(0xffffffffu, cells.cell, C * at + j);
+            if (tile + kWarps >= s1)
+#pragma unroll
+                for (int j = 0; j < C; ++j) cell[j] = 0xffffffffu;
             // ---- logits: tokens are rows, queries columns
-            float s[2][NT][4];
+            float s[C][NT][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < C; ++j) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.0f;
 #pragma unroll
@@ -378,14 +402,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
                     to_f16<CODE>(wl, a0, a2);
                     to_f16<CODE>(wh, a1, a3);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma(s[j][n], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        uint2 q;
+                        if constexpr (SQ)
+                            q = *reinterpret_cast<const uint2*>(&sh.q[8 * n + g][(i / 4) * 64 + t * 16 + (i % 4) * 4]);
+                        else
+                            q = make_uint2(qf[n][i][0], qf[n][i][1]);
+                        mma(s[j][n], a0, a1, a2, a3, q.x, q.y);
+                    }
                 }
                 load_keys<D>(kr[j], c.k_codes, cell[j], g, t);
             }
             // ---- weights
-            float over = -INFINITY, back[2], f[2];
+            float over = -INFINITY, back[C], f[C];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < C; ++j) {
                 // vs = 2^e f; a NaN scale keeps f = NaN and e = 0
                 const uint32_t vb = __float_as_uint(vs[j]);
                 const bool fin = vb < 0x7f800000u;
@@ -417,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+                        float mx = fmaxf(s[0][n][e], s[0][n][2 + e]);
+                        if constexpr (C == 2) mx = fmaxf(mx, fmaxf(s[C - 1][n][e], s[C - 1][n][2 + e]));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -432,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
                         }
                     }
             }
-            uint32_t bh[2][NT][2], bl[2][NT][2];
+            uint32_t bh[C][NT][2], bl[C][NT][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < C; ++j) {
                 const bool edge = slot[j] + 16 > least;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -456,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
                         }
                         // log2 of the cell's weights, whatever M is now or becomes
                         if (g == 0 && slot[j] < 0x40000000)
-                            *reinterpret_cast<float2*>(a.mass + ((size_t)w * a.cells + 2 * tile + j) * R + 8 * n + 2 * t) =
+                            *reinterpret_cast<float2*>(a.mass + ((size_t)w * a.cells + C * tile + j) * R + 8 * n + 2 * t) =
                                 make_float2(__log2f(c0 * back[j]) + (M[n][0] - kShift),
                                             __log2f(c1 * back[j]) + (M[n][1] - kShift));
                     }
@@ -517,40 +549,42 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_kernel(AttnArg
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                const int row = 8 * n + 2 * t + e;
-                if (g == 0) {
-                    sh.ml[warp][row][0] = M[n][e];
-                    sh.ml[warp][row][1] = x;
-                }
-                float* dst = &sh.o[warp][row][g * (D / 8)];
+                if (g == 0) *reinterpret_cast<float2*>(sh.ml[warp][8 * n + 2 * t + e]) = make_float2(M[n][e], x);
+            }
+        const size_t slot = (size_t)blockIdx.x + w;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float* dst = &sh.o[warp][2 * t + e][g * (D / 8)];
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[n][i][e], o[n][i][2 + e]);
             }
-        __syncthreads();
-        const size_t slot = (size_t)blockIdx.x + w;
-        for (int x = threadIdx.x; x < R * (D / 4); x += kThreads) {
-            const int row = x / (D / 4), d = x % (D / 4) * 4;
-            float top = -INFINITY, sum = 0.0f;
+            __syncthreads();
+            for (int x = threadIdx.x; x < 8 * (D / 4); x += kThreads) {
+                const int col = x / (D / 4), row = 8 * n + col, d = x % (D / 4) * 4;
+                float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.ml[i][row][0]);
-            const float ref = top == -INFINITY ? 0.0f : top;
-            float4 y = make_float4(0, 0, 0, 0);
+                for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sh.ml[i][row][0]);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                float4 y = make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                const float fac = ex2_approx(sh.ml[i][row][0] - ref);
-                const float4 v = *reinterpret_cast<const float4*>(&sh.o[i][row][d]);
-                y.x = fmaf(v.x, fac, y.x);
-                y.y = fmaf(v.y, fac, y.y);
-                y.z = fmaf(v.z, fac, y.z);
-                y.w = fmaf(v.w, fac, y.w);
-                sum = fmaf(sh.ml[i][row][1], fac, sum);
+                for (int i = 0; i < kWarps; ++i) {
+                    const float fac = ex2_approx(sh.ml[i][row][0] - ref);
+                    const float4 v = *reinterpret_cast<const float4*>(&sh.o[i][col][d]);
+                    y.x = fmaf(v.x, fac, y.x);
+                    y.y = fmaf(v.y, fac, y.y);
+                    y.z = fmaf(v.z, fac, y.z);
+                    y.w = fmaf(v.w, fac, y.w);
+                    sum = fmaf(sh.ml[i][row][1], fac, sum);
+                }
+                *reinterpret_cast<float4*>(a.part + (slot * R + row) * D + d) = y;
+                if (d == 0) *reinterpret_cast<float2*>(a.ml + (slot * R + row) * 2) = make_float2(top, sum);
             }
-            *reinterpret_cast<float4*>(a.part + (slot * R + row) * D + d) = y;
-            if (d == 0) *reinterpret_cast<float2*>(a.ml + (slot * R + row) * 2) = make_float2(top, sum);
+            __syncthreads();
         }
-        __syncthreads();
-        before += k.tiles;
+        before += k.tiles + run.start;
         from = before;
     }
 }
@@ -739,7 +773,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 Layout layout_of(const kvq_block8& c, int n_q, int n_sel, int accumulate) {
     Layout y;
     const int units = c.B * c.Hkv, g = c.Hq / c.Hkv, rows = n_sel ? g : g * n_q;
-    y.nt = rows <= 8 ? 1 : 2;
+    y.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     y.row_tiles = (rows + 8 * y.nt - 1) / (8 * y.nt);
     y.works = units * (n_sel ? n_q : 1) * y.row_tiles;
     y.cells = (n_sel ? n_sel : c.max_blocks) * (c.block / 16);
@@ -776,7 +810,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     cudaError_t e = resident_ctas(kernel, kThreads, 0, known, &ctas);
     if (e != cudaSuccess) return e;
     // no more CTAs than runs of kWarps tiles in full caches
-    const long long tiles = (long long)a.works * ((a.cells + 1) / 2);
+    const long long tiles = (long long)a.works * ((a.cells + Shape<NT>::C - 1) / Shape<NT>::C);
     const int grid = (int)std::min<long long>(std::min(ctas, kMaxCtas), (tiles + kWarps - 1) / kWarps);
     kernel<<<grid, kThreads, 0, s>>>(a);
     e = cudaGetLastError();
@@ -807,12 +841,12 @@ cudaError_t launch_block8_attn(const void* q, const int64_t* qs, int n_q, const 
             constexpr int D = decltype(wide)::value ? 128 : 64;
             return on(c.code == KVQ_CODE_INT8, [&](auto i8) {
                 constexpr int CODE = decltype(i8)::value ? KVQ_CODE_INT8 : KVQ_CODE_E4M3;
-                return on(y.nt == 2, [&](auto two) {
-                    constexpr int NT = decltype(two)::value ? 2 : 1;
-                    return on(blocks != nullptr, [&](auto list) {
-                        return on(accumulate != 0, [&](auto acc) {
-                            return launch<T, D, CODE, NT, decltype(list)::value, decltype(acc)::value>(a, s);
-                        });
+                return on(blocks != nullptr, [&](auto list) {
+                    return on(accumulate != 0, [&](auto acc) {
+                        constexpr bool LIST = decltype(list)::value, ACC = decltype(acc)::value;
+                        return y.nt == 1   ? launch<T, D, CODE, 1, LIST, ACC>(a, s)
+                               : y.nt == 2 ? launch<T, D, CODE, 2, LIST, ACC>(a, s)
+                                           : launch<T, D, CODE, 4, LIST, ACC>(a, s);
                     });
                 });
             });
