@@ -3,11 +3,12 @@
 //
 // Mathematics.  A logit is s_j = (q . c_j) k_scale sigma log2(e): codes and
 // 16-bit queries multiply exactly in fp16 MMAs with float32 sums.  With the
-// value scale split as 2^e f (1 <= f < 2), the second product is over the value
-// codes with weights 2^(s_j + e - M) f, M one running reference per query row,
-// so blocks whose value scales lie many powers of two apart share one fp16
-// range; a weight enters as a pair of fp16 numbers (22 bits).  The sum of
-// 2^(s_j + e - M) 2^-e beside it gives the softmax denominator.
+// value scale v as a power of two in the exponent, the second product is over the
+// value codes with weights 2^(s_j + log2 v - M), M one running reference per query
+// row, so blocks whose value scales lie many powers of two apart share one fp16
+// range; a weight enters as a pair of fp16 numbers (22 bits).  The sum of the same
+// weights times 1 / v beside it gives the softmax denominator, so that the
+// rounding of log2 v (2^-22) only shifts a block's logits by as much.
 //
 // Work.  The rows that read a unit together (queries x heads of the group, 8 or
 // 16 of them) and its tokens, or a query's listed blocks, form a work unit; its
@@ -44,9 +45,10 @@ using namespace b8;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kMaxCtas = 1024;          // CTAs of the first kernel at most (sizes the workspace)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// The reference M moves only when a logit passes it by more than 2^8, and weights carry a factor
-// 2^6: they stay below 2^8 2^6 2 = 2^15 in fp16, and 2^-31 of the largest is still a weight.
-constexpr float kLift = 8.0f, kShift = 6.0f;
+// The reference starts 2^7 below a row's largest weight and moves only when one passes it by 2^15:
+// weights fit fp16, and 2^-31 of the largest is still a weight.  kNone: no logit yet (finite, so that
+// differences of references are numbers).
+constexpr float kShift = 7.0f, kLift = 15.0f, kNone = -1.0e38f;
 
 struct AttnArgs {
     kvq_block8 c;
@@ -185,7 +187,7 @@ __device__ __forceinline__ void load_values(ValueRegs<D>& v, const uint8_t* code
 struct Cells {
     uint32_t cell;                      // number of the 16-token cell in the pool, ~0 for none
     int slot;                           // its first token in the unit
-    float ks, vs;                       // k_scale sigma log2(e), v_scale
+    float ks, lv, rv;                   // k_scale sigma log2(e); log2 and reciprocal of v_scale (NaN: NaN and 0)
 };
 
 template <int C, bool LIST>
@@ -194,7 +196,8 @@ __device__ __forceinline__ Cells find_cells(const AttnArgs& a, const Work& k, in
     x.cell = 0xffffffffu;
     x.slot = 0;
     x.ks = 0.0f;
-    x.vs = 1.0f;
+    x.lv = 0.0f;
+    x.rv = 1.0f;
     const int my = tile + (lane / C) * kWarps, cell = C * my + lane % C;
     if (my < end) {
         const int per = a.c.block / 16, j = cell / per, in = cell % per;
@@ -220,7 +223,9 @@ __device__ __forceinline__ Cells find_cells(const AttnArgs& a, const Work& k, in
                 if ((unsigned)phys < (unsigned)a.c.n_blocks) {
                     x.cell = (uint32_t)phys * per + in;
                     x.ks = a.c.k_scale[phys] * (a.sm_scale * kLog2e);
-                    x.vs = a.c.v_scale[phys];
+                    const float vs = a.c.v_scale[phys];
+                    x.lv = log2f(vs);
+                    x.rv = isnan(vs) ? 0.0f : __frcp_rn(vs);
                 } else {
                     atomicOr(&g_status_block8_attn, kDevCheck);
                 }
@@ -361,18 +366,19 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[n][i][e] = 0.0f;
-            M[n][0] = M[n][1] = -INFINITY;
+            M[n][0] = M[n][1] = kNone;
             l[n][0] = l[n][1] = 0.0f;
         }
         // ---- the warp's tiles
         int at = 0;                     // the tile's place among those of `cells`
         for (int tile = s0 + warp; tile < s1; tile += kWarps) {
-            float ks[C], vs[C];
+            float ks[C], lv[C], rv[C];
             int slot[C];
 #pragma unroll
             for (int j = 0; j < C; ++j) {
                 ks[j] = __shfl_sync(0xffffffffu, cells.ks, C * at + j);
-                vs[j] = __shfl_sync(0xffffffffu, cells.vs, C * at + j);
+                lv[j] = __shfl_sync(0xffffffffu, cells.lv, C * at + j);
+                rv[j] = __shfl_sync(0xffffffffu, cells.rv, C * at + j);
                 slot[j] = __shfl_sync(0xffffffffu, cells.slot, C * at + j);
                 if (cell[j] == 0xffffffffu) slot[j] = 0x40000000;       // nothing there: behind every limit
             }
@@ -414,22 +420,12 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
                 load_keys<D>(kr[j], c.k_codes, cell[j], g, t);
             }
             // ---- weights
-            float over = -INFINITY, back[C], f[C];
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                // vs = 2^e f; a NaN scale keeps f = NaN and e = 0
-                const uint32_t vb = __float_as_uint(vs[j]);
-                const bool fin = vb < 0x7f800000u;
-                const int e = fin ? (int)(vb >> 23) - 127 : 0;
-                f[j] = fin ? __uint_as_float((vb & 0x7fffffu) | 0x3f800000u) : vs[j];
-                back[j] = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        float& y = s[j][n][x];
-                        y = fmaf(y, ks[j] * qi[n][x & 1], (float)e);
-                    }
+                    for (int x = 0; x < 4; ++x) s[j][n][x] = fmaf(s[j][n][x], ks[j] * qi[n][x & 1], lv[j]);
                 if (slot[j] + 16 > least) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -437,24 +433,27 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
                         for (int x = 0; x < 4; ++x)
                             if (slot[j] + g + (x >> 1) * 8 >= lim[n][x & 1]) s[j][n][x] = -INFINITY;
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) over = fmaxf(over, s[j][n][x] - M[n][x & 1]);
             }
-            // a column's first logits make `over` +inf (or NaN when they are -inf: nothing to do then)
+            float over = -INFINITY;
+            auto column_max = [&](int n, int e) {
+                float mx = fmaxf(s[0][n][e], s[0][n][2 + e]);
+                if constexpr (C == 2) mx = fmaxf(mx, fmaxf(s[C - 1][n][e], s[C - 1][n][2 + e]));
+                return mx;
+            };
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) over = fmaxf(over, column_max(n, e) - M[n][e]);
             if (__any_sync(0xffffffffu, over > kLift)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(s[0][n][e], s[0][n][2 + e]);
-                        if constexpr (C == 2) mx = fmaxf(mx, fmaxf(s[C - 1][n][e], s[C - 1][n][2 + e]));
+                        float mx = column_max(n, e);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float now = fmaxf(M[n][e], mx);
-                        const float fac = now == M[n][e] ? 1.0f : ex2_approx(M[n][e] - now);
+                        const float now = fmaxf(M[n][e], mx - kShift), fac = ex2_approx(M[n][e] - now);
                         M[n][e] = now;
                         l[n][e] *= fac;
 #pragma unroll
@@ -467,18 +466,14 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
             uint32_t bh[C][NT][2], bl[C][NT][2];
 #pragma unroll
             for (int j = 0; j < C; ++j) {
-                const bool edge = slot[j] + 16 > least;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float p[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float ref = M[n][x & 1] == -INFINITY ? 0.0f : M[n][x & 1];
-                        p[x] = ex2_approx(s[j][n][x] - ref + kShift);
-                    }
+                    for (int x = 0; x < 4; ++x) p[x] = ex2_approx(s[j][n][x] - M[n][x & 1]);
                     const float sum0 = p[0] + p[2], sum1 = p[1] + p[3];
-                    l[n][0] = fmaf(sum0, back[j], l[n][0]);
-                    l[n][1] = fmaf(sum1, back[j], l[n][1]);
+                    l[n][0] = fmaf(sum0, rv[j], l[n][0]);
+                    l[n][1] = fmaf(sum1, rv[j], l[n][1]);
                     if constexpr (ACC) {
                         float c0 = sum0, c1 = sum1;
 #pragma unroll
@@ -489,15 +484,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
                         // log2 of the cell's weights, whatever M is now or becomes
                         if (g == 0 && slot[j] < 0x40000000)
                             *reinterpret_cast<float2*>(a.mass + ((size_t)w * a.cells + C * tile + j) * R + 8 * n + 2 * t) =
-                                make_float2(__log2f(c0 * back[j]) + (M[n][0] - kShift),
-                                            __log2f(c1 * back[j]) + (M[n][1] - kShift));
-                    }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) p[x] *= f[j];
-                    if (edge) {         // a masked token weighs 0 even where its block's scale is NaN
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (slot[j] + g + (x >> 1) * 8 >= lim[n][x & 1]) p[x] = 0.0f;
+                                make_float2(__log2f(c0 * rv[j]) + M[n][0], __log2f(c1 * rv[j]) + M[n][1]);
                     }
                     uint32_t h0, l0, h1, l1;
                     split2(p[0], p[1], h0, l0);
@@ -705,7 +692,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int row_
         if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(y);
         else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<uint32_t*>(y);
         if (lane == 0 && a.lse)
-            a.lse[orow] = sees ? ((M == -INFINITY ? 0.0f : M) - kShift + log2f(l)) * kLn2 : -INFINITY;
+            a.lse[orow] = sees ? (M + log2f(l)) * kLn2 : -INFINITY;
         return;
     }
     if constexpr (ACC) {
@@ -733,7 +720,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int row_
 #pragma unroll
                     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
                     const bool sees = i < k.rows && row_of<NT, LIST>(a, k, w, i).x < m && l != 0.0f;
-                    if (lane == 0) lse2[i] = sees ? ref - kShift + log2f(l) : INFINITY;
+                    if (lane == 0) lse2[i] = sees ? ref + log2f(l) : INFINITY;
                 }
                 __syncthreads();
                 for (int j = chunk * kJoinThreads + threadIdx.x; j < (LIST ? n : min(n, (chunk + 1) * kJoinThreads));
