@@ -637,7 +637,8 @@ class Block8Cache:
         d = KvqBlock8(self.B, self.Hq, self.Hkv, D, F16 if self.dtype == torch.float16 else BF16, _CODES[code], P, nb, n)
         for name, _ in KvqBlock8._fields_[9:]:
             setattr(d, name, getattr(self, name).data_ptr())
-        self.desc, self._ref, self._device = d, ctypes.byref(d), dev
+        self.desc, self._ref, self._device, self._index = d, ctypes.byref(d), dev, dev.index
+        self._lib = lib()
         need = self.ws_bytes(self.max_q, self.max_sel)
         if self.ws is None:
             self.ws = torch.empty(need + 256, dtype=torch.uint8, device=dev)
@@ -693,11 +694,11 @@ def make_block8_cache(B, Hq, Hkv, D, dtype, max_tokens, block=64, codes=torch.fl
 
 def _stream8(cache, stream):
     """The raw stream of a block8 call."""
-    if torch.cuda.current_device() != cache._device.index:
-        _bad(f"the cache is on {cache._device}, the current device is cuda:{torch.cuda.current_device()}")
+    if torch._C._cuda_getDevice() != cache._index:
+        _bad(f"the cache is on cuda:{cache._index}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(cache._device.index)
-    if stream.device != cache._device:
+        return torch._C._cuda_getCurrentRawStream(cache._index)
+    if stream.device.index != cache._index:
         _bad("the stream belongs to another device than the cache")
     return stream.cuda_stream
 
@@ -719,14 +720,15 @@ def _used8(stream, *ts):
 
 def _rows8(cache, x, heads, name):
     """x as [B, heads, n, D], last axis contiguous (a step may leave n out): pointer, strides, n."""
-    if x.dim() == 3:
-        x = x.unsqueeze(2)
     shape = x.shape
-    if x.dim() != 4 or shape[0] != cache.B or shape[1] != heads or shape[3] != cache.D:
+    if len(shape) == 3:
+        x = x.unsqueeze(2)
+        shape = x.shape
+    if len(shape) != 4 or shape[0] != cache.B or shape[1] != heads or shape[3] != cache.D:
         _bad(f"{name} must be [{cache.B}, {heads}, n, {cache.D}], got {list(shape)}")
     if x.dtype != cache.dtype:
         raise TypeError(f"{name} must have the cache's dtype {cache.dtype}")
-    if x.device != cache._device:
+    if x.get_device() != cache._index:
         _bad(f"{name} must be on the cache's device")
     if x.is_contiguous():
         return x.data_ptr(), None, shape[2]
@@ -735,24 +737,19 @@ def _rows8(cache, x, heads, name):
     return x.data_ptr(), (ctypes.c_int64 * 3)(*[s if n > 1 else 0 for n, s in zip(shape[:3], x.stride())]), shape[2]
 
 
-def _ints8(cache, t, shape, name):
-    """The pointer of an int32 argument, or None."""
+def _ptr8(cache, t, shape, dtype, name):
+    """The pointer of an argument or output, or None."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != cache._device:
-        _bad(f"{name} must be a contiguous int32 tensor {list(shape)} on the cache's device")
-    return t.data_ptr()
-
-
-def _out8(cache, t, shape, dtype, name):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != cache._device:
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != cache._index:
         _bad(f"{name} must be a contiguous tensor {list(shape)} of {dtype} on the cache's device")
+    return t.data_ptr()
 
 
 def block8_reset(cache, mask=None, stream=None):
     """Empties the units with mask[u] != 0 (int32 [B*Hkv]); every unit without a mask."""
     s = _stream8(cache, stream)
-    _check(lib().block8_reset(cache._ref, _ints8(cache, mask, (cache.units,), "mask"), s))
+    _check(cache._lib.block8_reset(cache._ref, _ptr8(cache, mask, (cache.units,), torch.int32, "mask"), s))
     if stream is not None:
         _used8(stream, mask)
 
@@ -766,11 +763,9 @@ def block8_append(cache, k, v, n_new=None, colscore=None, stream=None):
     vp, vs, m = _rows8(cache, v, cache.Hkv, "v")
     if m != n:
         _bad("k and v must have one shape")
-    cs = None
-    if colscore is not None:
-        _out8(cache, colscore, (cache.B, cache.Hq, n), torch.float32, "colscore")
-        cs = colscore.data_ptr()
-    _check(lib().block8_append(cache._ref, kp, ks, vp, vs, n, _ints8(cache, n_new, (cache.B,), "n_new"), cs, s))
+    _check(cache._lib.block8_append(cache._ref, kp, ks, vp, vs, n,
+                                    _ptr8(cache, n_new, (cache.B,), torch.int32, "n_new"),
+                                    _ptr8(cache, colscore, (cache.B, cache.Hq, n), torch.float32, "colscore"), s))
     if stream is not None:
         _used8(stream, k, v, n_new, colscore)
 
@@ -786,20 +781,17 @@ def block8_attn(q, cache, sm_scale=None, blocks=None, accumulate=False, n_new=No
     if blocks is not None:
         idx, n = blocks
         n_sel = idx.shape[-1]
-        np_ = _ints8(cache, n, (cache.B, cache.Hkv, n_q), "blocks[1]")
-        ip = _ints8(cache, idx, (cache.B, cache.Hkv, n_q, n_sel), "blocks[0]")
+        np_ = _ptr8(cache, n, (cache.B, cache.Hkv, n_q), torch.int32, "blocks[1]")
+        ip = _ptr8(cache, idx, (cache.B, cache.Hkv, n_q, n_sel), torch.int32, "blocks[0]")
     shape = q.shape
     if o is None:
         o = _empty8(cache, shape, cache.dtype, stream)
-    else:
-        _out8(cache, o, shape, cache.dtype, "o")
     if lse is None:
         lse = _empty8(cache, shape[:-1], torch.float32, stream)
-    else:
-        _out8(cache, lse, shape[:-1], torch.float32, "lse")
-    _check(lib().block8_attn(qp, qs, n_q, _ints8(cache, n_new, (cache.B,), "n_new"), cache._ref,
-                             cache.D ** -0.5 if sm_scale is None else float(sm_scale), ip, np_, n_sel,
-                             1 if accumulate else 0, o.data_ptr(), lse.data_ptr(), cache._ws, cache._ws_bytes, s))
+    _check(cache._lib.block8_attn(qp, qs, n_q, _ptr8(cache, n_new, (cache.B,), torch.int32, "n_new"), cache._ref,
+                                  cache.D ** -0.5 if sm_scale is None else float(sm_scale), ip, np_, n_sel,
+                                  1 if accumulate else 0, _ptr8(cache, o, shape, cache.dtype, "o"),
+                                  _ptr8(cache, lse, shape[:-1], torch.float32, "lse"), cache._ws, cache._ws_bytes, s))
     if stream is not None:
         _used8(stream, q, n_new, idx, n, o, lse)
     return o, lse
@@ -816,10 +808,10 @@ def block8_select(q, cache, n_sel, n_first=1, n_last=1, n_new=None, out=None, st
         n = _empty8(cache, shape, torch.int32, stream)
     else:
         idx, n = out
-        _out8(cache, idx, shape + (n_sel,), torch.int32, "idx")
-        _out8(cache, n, shape, torch.int32, "n")
-    _check(lib().block8_select(qp, qs, n_q, _ints8(cache, n_new, (cache.B,), "n_new"), cache._ref, int(n_sel),
-                               int(n_first), int(n_last), idx.data_ptr(), n.data_ptr(), cache._ws, cache._ws_bytes, s))
+    _check(cache._lib.block8_select(qp, qs, n_q, _ptr8(cache, n_new, (cache.B,), torch.int32, "n_new"), cache._ref,
+                                    int(n_sel), int(n_first), int(n_last),
+                                    _ptr8(cache, idx, shape + (max(int(n_sel), 0),), torch.int32, "idx"),
+                                    _ptr8(cache, n, shape, torch.int32, "n"), cache._ws, cache._ws_bytes, s))
     if stream is not None:
         _used8(stream, q, n_new, idx, n)
     return idx, n
@@ -829,12 +821,11 @@ def block8_evict(cache, keep, n_first=1, n_last=1, n_evicted=None, stream=None):
     """Units with more than keep[u] blocks (int32 [B*Hkv]) lose those of the least accumulated attention;
     returns the number of blocks that left each unit."""
     s = _stream8(cache, stream)
-    kp = _ints8(cache, keep, (cache.units,), "keep")
+    kp = _ptr8(cache, keep, (cache.units,), torch.int32, "keep")
     if n_evicted is None:
         n_evicted = _empty8(cache, (cache.units,), torch.int32, stream)
-    else:
-        _out8(cache, n_evicted, (cache.units,), torch.int32, "n_evicted")
-    _check(lib().block8_evict(cache._ref, kp, int(n_first), int(n_last), n_evicted.data_ptr(), s))
+    _check(cache._lib.block8_evict(cache._ref, kp, int(n_first), int(n_last),
+                                   _ptr8(cache, n_evicted, (cache.units,), torch.int32, "n_evicted"), s))
     if stream is not None:
         _used8(stream, keep, n_evicted)
     return n_evicted
