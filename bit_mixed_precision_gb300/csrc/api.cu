@@ -366,6 +366,7 @@ static kvq_status check_block8(const kvq_block8* c, const char* who) {
     KVQ_REQUIRE((long long)c->B * c->Hq <= (1LL << 24) &&
                     (long long)c->B * c->Hkv <= ((1LL << 35) / KVQ_BLOCK8_MAX_Q) / ((long long)c->max_blocks * c->block),
                 KVQ_EUNSUPPORTED, "%s: cache too large", who);
+    KVQ_REQUIRE((long long)c->n_blocks * c->block <= (1LL << 35), KVQ_EUNSUPPORTED, "%s: pool too large", who);
     KVQ_REQUIRE(c->k_codes && c->v_codes && c->k_scale && c->v_scale && c->k_bound && c->bound_scale && c->tail_k &&
                     c->tail_v && c->table && c->count && c->seq_len && c->block_pos && c->acc,
                 KVQ_EINVAL, "%s: null array", who);
@@ -429,11 +430,14 @@ static kvq_status check_ws(const void* ws, size_t given, size_t need, const char
     return KVQ_OK;
 }
 
-// Rows of n_sel list entries; the work items (16 tokens) of all lists together are 32-bit.
+// Rows of n_sel list entries (0: no lists).  What one call works through, 16 tokens for up to 32 rows
+// at a time (at least 8), is counted in 32 bits.
 static kvq_status check_list(const kvq_block8* c, int n_q, int n_sel, const char* who) {
-    KVQ_REQUIRE(n_sel <= (1 << 20) &&
-                    (long long)n_sel * c->block <= (1LL << 35) / ((long long)c->B * c->Hkv * n_q), KVQ_EUNSUPPORTED,
-                "%s: n_sel = %d is too large", who, n_sel);
+    KVQ_REQUIRE(n_sel <= (1 << 20), KVQ_EUNSUPPORTED, "%s: n_sel = %d is too large", who, n_sel);
+    const long long g = c->Hq / c->Hkv, rows = n_sel ? g : g * n_q, sets = (long long)c->B * c->Hkv * (n_sel ? n_q : 1);
+    const long long cells = (long long)(n_sel ? n_sel : c->max_blocks) * (c->block / 16);
+    KVQ_REQUIRE(cells <= (1LL << 30) / (sets * ((rows + 31) / 32)), KVQ_EUNSUPPORTED,
+                "%s: too many tokens for one call (%lld units or lists of %lld x 16)", who, sets, cells);
     return KVQ_OK;
 }
 
@@ -459,10 +463,10 @@ kvq_status block8_attn(const void* q, const int64_t* q_strides, int n_q, const i
     KVQ_REQUIRE(sm_scale > 0.0f, KVQ_EINVAL, "block8_attn: sm_scale must be positive");
     if (blocks) {
         KVQ_REQUIRE(list_len && n_sel >= 1, KVQ_EINVAL, "block8_attn: a block list needs list_len and n_sel >= 1");
-        if ((st = check_list(c, n_q, n_sel, "block8_attn")) != KVQ_OK) return st;
     } else {
         KVQ_REQUIRE(!list_len && n_sel == 0, KVQ_EINVAL, "block8_attn: list_len or n_sel without a block list");
     }
+    if ((st = check_list(c, n_q, n_sel, "block8_attn")) != KVQ_OK) return st;
     if ((st = check_ws(ws, ws_bytes, kvq::block8_attn_bytes(*c, n_q, n_sel, accumulate), "block8_attn")) != KVQ_OK)
         return st;
     return cuda_status(kvq::launch_block8_attn(q, qs, n_q, n_new, *c, sm_scale, blocks, list_len, n_sel, accumulate, o,

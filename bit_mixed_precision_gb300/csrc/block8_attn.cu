@@ -775,7 +775,7 @@ Layout layout_of(const kvq_block8& c, int n_q, int n_sel, int accumulate) {
 
 template <typename T, int D, int NT, bool LIST, bool ACC, int SPLIT>
 cudaError_t launch_join(const AttnArgs& a, cudaStream_t s) {
-    const int units = a.c.B * a.c.Hkv, row_blocks = a.works * 8 * NT * SPLIT / kJoinWarps;
+    const int units = a.c.B * a.c.Hkv, row_blocks = a.works * (NT * SPLIT);    // 8 rows each column block, 8 warps
     const int chunks = LIST ? 1 : (a.c.max_blocks + kJoinThreads - 1) / kJoinThreads;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];

@@ -266,7 +266,8 @@ def test_attn_lengths(kvq, D, block, Hq, Hkv, codes, dtype):
 
 @pytest.mark.parametrize("n_q,Hq,Hkv,D,block,codes", [(2, 4, 4, 128, 16, F8), (3, 10, 2, 128, 64, I8),
                                                       (8, 8, 1, 64, 32, F8), (16, 4, 2, 128, 128, I8),
-                                                      (5, 24, 2, 64, 16, F8)])
+                                                      (5, 24, 2, 64, 16, F8), (16, 64, 1, 128, 16, I8),
+                                                      (9, 3, 1, 128, 32, F8)])
 def test_attn_several_queries(kvq, n_q, Hq, Hkv, D, block, codes):
     """Causal among the last tokens; ragged numbers of queries, more queries than tokens, padding rows."""
     lens = [0, 1, 4, 31, 32, 65, 300]
@@ -360,6 +361,54 @@ def test_attn_not_a_number(kvq):
     qn[2, 1, 0, 3] = float("nan")
     o, _ = kvq.block8_attn(qn, p.c)
     assert o[2, 1, 0].isnan().all() and not o[2, 0].isnan().any() and not o[2, 1, 1].isnan().any()
+
+
+@pytest.mark.parametrize("Hq,n_q,dtype", [(8, 1, torch.float16), (16, 1, torch.bfloat16), (5, 8, torch.bfloat16)])
+def test_attn_one_long_unit(kvq, Hq, n_q, dtype):
+    """One unit's tokens spread over every CTA: many partials a row."""
+    p = Pair(kvq, B=1, Hq=Hq, Hkv=1, block=64, codes=F8, dtype=dtype, max_tokens=30000, max_q=8)
+    p.append(29991)
+    p.c.acc.zero_()
+    p.attn(p.rand(1, Hq, n_q, 128), accumulate=True)
+    idx, n = kvq.block8_select(p.rand(1, Hq, n_q, 128).cuda(), p.c, 300)
+    p.attn(p.rand(1, Hq, n_q, 128), blocks=(idx, n), accumulate=True)
+
+
+def test_empty_cache(kvq):
+    p = Pair(kvq, B=3, Hq=4, Hkv=2, max_q=2)
+    p.c.acc.zero_()
+    q = p.rand(3, 4, 2, 128)
+    p.attn(q, accumulate=True)
+    idx, n = kvq.block8_select(q.cuda(), p.c, 3)
+    assert (idx == -1).all() and (n == 0).all()
+    p.attn(q, blocks=(idx, n), accumulate=True)
+    assert kvq.block8_evict(p.c, torch.zeros(6, dtype=torch.int32, device="cuda")).tolist() == [0] * 6
+    p.append(1, n_new=[0, 0, 0])
+    p.check()
+
+
+def test_counters_out_of_range_are_refused_or_read_as_empty(kvq):
+    """Counters that no call writes: nothing outside the cache is touched."""
+    p = Pair(kvq, B=2, Hq=2, Hkv=1, max_tokens=64)
+    p.append(40)
+    p.c.acc.zero_()
+    p.c.count.copy_(torch.tensor([-5, 1 << 30], dtype=torch.int32))
+    z = torch.ones((2, 1, 1, 128), dtype=torch.float16, device="cuda")
+    kvq.block8_append(p.c, z, z)
+    assert kvq.device_status() == kvq.KVQ_EDEVICE and p.c.count.tolist() == [-5, 1 << 30]
+    q = p.rand(2, 2, 1, 128).cuda()
+    p.c.v_codes.view(torch.uint8).zero_()               # the 24 rows behind the 40 tokens are read as well here
+    p.c.k_codes.view(torch.uint8).zero_()
+    p.c.k_scale.fill_(1.0)
+    p.c.v_scale.fill_(1.0)
+    p.c.bound_scale.fill_(1.0)
+    o, lse = kvq.block8_attn(q, p.c, accumulate=True)
+    assert (lse[0] == -np.inf).all() and (o[0] == 0).all()
+    assert torch.allclose(lse[1], torch.full_like(lse[1], float(np.log(64))), atol=1e-4)
+    idx, n = kvq.block8_select(q, p.c, 2)
+    assert n.flatten().tolist() == [0, 2]
+    kvq.block8_evict(p.c, torch.full((2,), 2, dtype=torch.int32, device="cuda"))
+    assert kvq.device_status() == 0
 
 
 def test_attn_pool_beyond_32_bits(kvq):

@@ -100,7 +100,7 @@ BAD_CACHES = [(dict(B=0), "EINVAL"), (dict(Hkv=3), "EINVAL"), (dict(Hq=2 * 65), 
               (dict(D=96), "EUNSUPPORTED"), (dict(dtype=2), "EINVAL"), (dict(code=2), "EINVAL"),
               (dict(block=48), "EINVAL"), (dict(max_blocks=0), "EINVAL"), (dict(n_blocks=0), "EINVAL"),
               (dict(max_blocks=(1 << 24) + 1), "EUNSUPPORTED"), (dict(B=1 << 20, max_blocks=1 << 20), "EUNSUPPORTED"),
-              (dict(acc=0), "EINVAL"), (dict(k_codes=8 + (1 << 20)), "EINVAL"), (dict(table=2 + (1 << 20)), "EINVAL")]
+              (dict(n_blocks=(1 << 31) - 1, block=128), "EUNSUPPORTED"), (dict(acc=0), "EINVAL"), (dict(k_codes=8 + (1 << 20)), "EINVAL"), (dict(table=2 + (1 << 20)), "EINVAL")]
 
 
 @pytest.mark.parametrize("kw,status", BAD_CACHES)
@@ -156,6 +156,11 @@ def test_bad_arguments_are_refused(L):
     assert L.block8_evict(c, None, 1, 1, p, None) == E
     assert L.block8_evict(c, p, -1, 1, p, None) == E and L.block8_evict(c, p, 1, 0, p, None) == E
     assert L.block8_evict(c, p, 9, 1, p, None) == E
+    # 1024 units of 2^21 tokens for 1024 rows each are more than one call counts
+    wide = ctypes.byref(_desc(B=1024, Hkv=1, Hq=64, max_blocks=1 << 14, block=128))
+    assert L.block8_attn(p, None, 16, None, wide, f, None, None, 0, 0, p, p, p, big, None) == X
+    assert L.block8_attn_workspace_bytes(wide, 16, 0, 0) == ctypes.c_size_t(-1).value
+    assert L.block8_attn_workspace_bytes(wide, 1, 0, 0) != ctypes.c_size_t(-1).value
     d.max_blocks = 51201
     assert L.block8_evict(c, p, 1, 1, p, None) == X
 
