@@ -404,16 +404,21 @@ cudaError_t launch_append_threads(const AppendArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Threads so that each holds at most four 16-byte pieces of the block's keys (and of its values);
-// threads, passes and D give the block's size.
+// Threads so that each holds at most four 16-byte pieces of the block's keys (and of its values), 64
+// at least; threads, passes and D give the block's size.
+template <typename T, int D, int CODE, int P>
+cudaError_t launch_append_block(const AppendArgs& a, cudaStream_t s) {
+    constexpr int kPieces = P * D / 8, kThreads = kPieces / 4 < 64 ? 64 : kPieces / 4;
+    return launch_append_threads<T, D, CODE, kThreads, kPieces / kThreads>(a, s);
+}
+
 template <typename T, int D, int CODE>
 cudaError_t launch_append_typed(const AppendArgs& a, cudaStream_t s) {
-    switch (a.c.block * D / 8) {
-        case 128: return launch_append_threads<T, D, CODE, 64, 2>(a, s);        // 16 x 64
-        case 256: return launch_append_threads<T, D, CODE, 64, 4>(a, s);        // 16 x 128, 32 x 64
-        case 512: return launch_append_threads<T, D, CODE, 128, 4>(a, s);
-        case 1024: return launch_append_threads<T, D, CODE, 256, 4>(a, s);
-        default: return launch_append_threads<T, D, CODE, 512, 4>(a, s);        // 128 x 128
+    switch (a.c.block) {
+        case 16: return launch_append_block<T, D, CODE, 16>(a, s);
+        case 32: return launch_append_block<T, D, CODE, 32>(a, s);
+        case 64: return launch_append_block<T, D, CODE, 64>(a, s);
+        default: return launch_append_block<T, D, CODE, 128>(a, s);
     }
 }
 
@@ -670,18 +675,27 @@ __device__ void choose_many(KeyFn key, int n, int k, TopkShared& sh, PutFn put) 
 
 constexpr int kChooseThreads = 256;
 
-template <typename KeyFn, typename PutFn>
+// KPT keys a thread in registers, or 0: any number of keys.  The launch takes the smallest that holds
+// max_blocks keys (8 a thread leave six CTAs per SM, 32 two; evict of 512 units of 2000 blocks with all
+// three in one kernel ran in two waves).
+template <int KPT, typename KeyFn, typename PutFn>
 __device__ __forceinline__ void choose(KeyFn key, int n, int k, TopkShared& sh, PutFn put) {
-    if (k == 0)
+    if (k == 0) {
         for (int i = threadIdx.x; i < n; i += blockDim.x) put(i, false, 0u);
-    else if (n <= 8 * kChooseThreads)
-        choose_regs<8>(key, n, k, sh, put);
-    else if (n <= 32 * kChooseThreads)
-        choose_regs<32>(key, n, k, sh, put);
-    else
-        choose_many(key, n, k, sh, put);
+    } else {
+        if constexpr (KPT > 0) choose_regs<KPT>(key, n, k, sh, put);
+        else choose_many(key, n, k, sh, put);
+    }
 }
 
+template <typename F>
+cudaError_t by_keys(int most, F f) {
+    if (most <= 8 * kChooseThreads) return f(std::integral_constant<int, 8>{});
+    if (most <= 32 * kChooseThreads) return f(std::integral_constant<int, 32>{});
+    return f(std::integral_constant<int, 0>{});
+}
+
+template <int KPT>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(SelectArgs a) {
     __shared__ TopkShared sh;
     const kvq_block8& c = a.c;
@@ -700,7 +714,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(SelectArgs a) {
     const float* score = a.score + (size_t)row * c.max_blocks + a.n_first;
     for (int i = threadIdx.x; i < a.n_first; i += blockDim.x) out[i] = i;
     for (int i = threadIdx.x; i < a.n_last; i += blockDim.x) out[a.n_sel - a.n_last + i] = nb - a.n_last + i;
-    choose([&](int i) { return rank_key(score[i]); }, nb - a.n_first - a.n_last, a.n_sel - a.n_first - a.n_last, sh,
+    choose<KPT>([&](int i) { return rank_key(score[i]); }, nb - a.n_first - a.n_last, a.n_sel - a.n_first - a.n_last, sh,
            [&](int i, bool chosen, uint32_t before) {
                if (chosen) out[a.n_first + before] = a.n_first + i;
            });
@@ -710,6 +724,7 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(SelectArgs a) {
 
 // ids: the unit's table row, read once; the new row is written from it.  Where the keys do not fit
 // the registers they are gathered again from acc in every pass.
+template <int KPT>
 __global__ void __launch_bounds__(kChooseThreads) evict_kernel(kvq_block8 c, const int32_t* __restrict__ keep, int n_first,
                                                               int n_last, int32_t* __restrict__ n_evicted) {
     extern __shared__ int32_t ids[];
@@ -725,7 +740,7 @@ __global__ void __launch_bounds__(kChooseThreads) evict_kernel(kvq_block8 c, con
     for (int i = threadIdx.x; i < nb; i += blockDim.x) ids[i] = row[i];
     __syncthreads();
     const int mid = want - n_first - n_last;
-    choose(
+    choose<KPT>(
         [&](int i) {
             const int phys = ids[n_first + i];
             if ((unsigned)phys < (unsigned)c.n_blocks) return rank_key(c.acc[phys]);
@@ -826,18 +841,21 @@ cudaError_t launch_block8_select(const void* q, const int64_t* qs, int n_q, cons
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = c.max_blocks > n_sel ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, choose_kernel, a);
+    return by_keys(c.max_blocks, [&](auto k) { return cudaLaunchKernelEx(&cfg, choose_kernel<decltype(k)::value>, a); });
 }
 
 cudaError_t launch_block8_evict(const kvq_block8& c, const int32_t* keep, int n_first, int n_last, int32_t* n_evicted,
                                 cudaStream_t s) {
-    const size_t smem = (size_t)c.max_blocks * sizeof(uint32_t);
-    if (smem > 40 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 51200 * 4);
-        if (e != cudaSuccess) return e;
-    }
-    evict_kernel<<<(unsigned)(c.B * c.Hkv), kChooseThreads, smem, s>>>(c, keep, n_first, n_last, n_evicted);
-    return cudaGetLastError();
+    const size_t smem = (size_t)c.max_blocks * sizeof(int32_t);
+    return by_keys(c.max_blocks, [&](auto k) {
+        auto kernel = evict_kernel<decltype(k)::value>;
+        if (smem > 40 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 51200 * 4);
+            if (e != cudaSuccess) return e;
+        }
+        kernel<<<(unsigned)(c.B * c.Hkv), kChooseThreads, smem, s>>>(c, keep, n_first, n_last, n_evicted);
+        return cudaGetLastError();
+    });
 }
 
 }  // namespace kvq
