@@ -33,7 +33,7 @@ every float32 step below is one IEEE round-to-nearest operation.
 Modules: ``quant`` (quantise / pack / dequantise), ``attention`` (prefill
 pass 1 and 2, decode attention), ``select`` (budgets, heavy hitters + recent
 window), ``policies`` (the MiniKV, DiffKV and MiKV cache life cycles),
-``accounting`` (cache byte counts).
+``accounting`` (cache byte counts), ``block8`` (the 8-bit block cache).
 
 Parity status of every function is listed in its docstring; functions whose
 result the pages fix nowhere are marked "parity unpinned".
