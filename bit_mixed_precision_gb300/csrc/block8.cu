@@ -186,6 +186,11 @@ __device__ __forceinline__ uint32_t largest(const uint4 (&r)[PASSES]) {
 // i / (D/8), + RPP, + 2 RPP ..., of keys and values at once: at most four pieces each, all
 // requested before the first is used (THREADS grows with the block), and two barriers a block.
 //
+// 16 x 32 prompts of 16384 tokens of 128 channels, blocks of 32, int8, with column scores: 1077 us,
+// 0.90 of the measured HBM rate (2910 us with 256 threads a block and the tensors one after the other;
+// blocks that are not FULL on the same path as the others, and divisions by a block size that the compiler
+// does not know, 1285).  A step's row of 512 units: 8 us, four dependent loads and the launch.
+//
 // A block whose scales do not grow needs only its new rows: the codes of the others stand, and
 // the bounds are the old ones widened by the new rows' (floor and ceil are monotone), exactly
 // what a quantisation of all rows gives.  A scale grows 1/fill of the time, so a decode step
@@ -460,6 +465,10 @@ __device__ __forceinline__ int blocks_to_score(const SelectArgs& a, int row) {
 // being the k elements of four MMAs.  All queries' groups of 16 blocks form one list that is split over
 // the resident CTAs; a CTA quantises a query once per run of groups, its warps take the groups in turn,
 // each with the next group's bounds requested before the current ones are used.
+// 128 units of up to 2048 blocks: the call 22 us against 7.5 of HBM time; the groups stream at 7.6 TB/s,
+// but the first ones arrive 4 us after the start (counters, table, bounds) and a second unit in a run
+// costs 3 us.  One thread per block with four-byte dot products: 31 us; grids of 64 to 512 blocks per
+// CTA: 20 (for these units, 15 for eight) to 33.
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(SelectArgs a) {
     constexpr int S = 2 * D / 16, PAD = 2 * D + 4;      // MMA steps; halves per head in shared memory
@@ -588,7 +597,8 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(SelectArgs a) {
 // The keys stay in registers, KPT a thread, in index order.  The k-th largest is found two bits a
 // round from the highest bit in which the keys differ: one count of the CTA against three candidates,
 // one barrier.  As soon as a count is k exactly there is nothing more to find (for keys without ties
-// after about log2 n bits).  One scan gives every key its place.
+// after about log2 n bits).  One scan gives every key its place.  At 2048 keys about 6 us with the launch,
+// against 9 of the radix select's four passes over memory and one bit a round in 512 threads.
 template <int KPT, typename KeyFn, typename PutFn>
 __device__ void choose_regs(KeyFn key, int n, int k, TopkShared& sh, PutFn put) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5, i0 = threadIdx.x * KPT;
@@ -697,7 +707,7 @@ cudaError_t by_keys(int most, F f) {
 
 template <int KPT>
 __global__ void __launch_bounds__(kChooseThreads) choose_kernel(SelectArgs a) {
-    __shared__ TopkShared sh;
+    __shared__ __align__(16) TopkShared sh;
     const kvq_block8& c = a.c;
     const int row = blockIdx.x, u = row / a.n_q, t = row % a.n_q;
     const int m = new_rows(a.n_new, u / c.Hkv, a.n_q, &g_status_block8);
@@ -723,12 +733,14 @@ __global__ void __launch_bounds__(kChooseThreads) choose_kernel(SelectArgs a) {
 // ------------------------------------------------------------------ evict
 
 // ids: the unit's table row, read once; the new row is written from it.  Where the keys do not fit
-// the registers they are gathered again from acc in every pass.
+// the registers they are gathered again from acc in every pass.  Bound by latency (counter, row, weights
+// at random places of acc, about ten rounds of counting): 512 units of up to 2048 blocks 16 us with a
+// copy of the table.
 template <int KPT>
 __global__ void __launch_bounds__(kChooseThreads) evict_kernel(kvq_block8 c, const int32_t* __restrict__ keep, int n_first,
                                                               int n_last, int32_t* __restrict__ n_evicted) {
     extern __shared__ int32_t ids[];
-    __shared__ TopkShared sh;
+    __shared__ __align__(16) TopkShared sh;
     const int u = blockIdx.x, count = min(max(c.count[u], 0), c.max_blocks * c.block);
     const int nb = (count + c.block - 1) / c.block;
     const int want = max(keep[u], n_first + n_last);

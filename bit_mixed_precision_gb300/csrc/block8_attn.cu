@@ -10,9 +10,9 @@
 // weights times 1 / v beside it gives the softmax denominator, so that the
 // rounding of log2 v (2^-22) only shifts a block's logits by as much.
 //
-// Work.  The rows that read a unit together (queries x heads of the group, 8 or
-// 16 of them) and its tokens, or a query's listed blocks, form a work unit; its
-// tokens are cut into tiles of 32.  All work units' tiles form one list, split
+// Work.  The rows that read a unit together (queries x heads of the group, up to
+// 8, 16 or 32 of them) and its tokens, or a query's listed blocks, form a work unit;
+// its tokens are cut into tiles of 32 (16 for more than 8 rows).  All work units' tiles form one list, split
 // evenly over the resident CTAs, whatever the lengths (each CTA adds up the
 // units' tile counts itself).  In a CTA the four warps take the tiles of its run
 // in turn, each with its own state: tokens are the M rows of the first MMA and
@@ -27,7 +27,11 @@
 // state; a second kernel, a programmatic dependent, joins the partials of a unit
 // and, with accumulate, adds the blocks' shares of the weights, in a fixed order.
 //
-// Bound by HBM: 2 D bytes per token and KV head against 4 D g flop.
+// Bound by HBM: 2 D bytes per token and KV head against 4 D g flop.  512 units of 32768 tokens, D 128,
+// four heads, e4m3, weights accumulated: 673 us, 0.94 of the measured 6.79 TB/s; 256 ragged units of up
+// to 8192, five heads, int8: 55 us, 0.78 (5 us go before the first tile, int8 codes take 380 warp
+// instructions per 16 tokens).  With 32 rows the tensor cores' share is larger than HBM's: 64 units of up
+// to 20011 tokens 86 us, 0.41, behind fixed-latency waits of two warps per scheduler.
 #include <algorithm>
 #include <type_traits>
 
@@ -71,7 +75,8 @@ struct AttnArgs {
 
 // Shapes by the number of 8-row column blocks.  One (up to 8 rows): tiles of two cells, query fragments
 // in registers, three CTAs per SM.  Two and four share a tile's converted codes among 16 or 32 rows;
-// their accumulators leave room for one cell, and the fragments are read from shared memory.
+// their accumulators leave room for one cell, and the fragments are read from shared memory.  32 rows in
+// one pass of four column blocks took 86 us where two passes of two took 94 to 97.
 template <int NT> struct Shape {
     static constexpr int C = NT == 1 ? 2 : 1;           // 16-token cells of a tile
     static constexpr int kCtas = NT == 4 ? 2 : 3;       // resident CTAs per SM
@@ -235,7 +240,9 @@ __device__ __forceinline__ Cells find_cells(const AttnArgs& a, const Work& k, in
     return x;
 }
 
-// Asks L2 for the cells of tile i of those in `x`; nothing waits for them.
+// Asks L2 for the cells of tile i of those in `x`; nothing waits for them.  One tile ahead (the tile
+// whose registers are loaded next): 712 -> 681 us on 512 units of 32768 tokens; two, three and five
+// ahead 691, 695, 709.
 template <int D, int C>
 __device__ __forceinline__ void ask_l2(const kvq_block8& c, const Cells& x, int i, int lane) {
     if (lane / C == i && x.cell != 0xffffffffu) {
@@ -245,7 +252,7 @@ __device__ __forceinline__ void ask_l2(const kvq_block8& c, const Cells& x, int 
 }
 
 template <int D, int NT>
-struct Shared {
+struct alignas(16) Shared {
     float o[kWarps][8][D + 4];          // one column block at a time
     float ml[kWarps][8 * NT][2];
     __half q[Shape<NT>::kSharedQ ? 8 * NT : 1][D + 4];          // queries as fp16, rows padded
@@ -578,6 +585,12 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
 
 // ------------------------------------------------------------------ the second kernel
 
+// A cell's weight (log2) as a part of its row's sum (log2; infinity for rows that count nothing, whose
+// cells may hold anything).
+__device__ __forceinline__ float part_of(float mass, float lse2) {
+    return lse2 == INFINITY ? 0.0f : ex2_approx(mass - lse2);
+}
+
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 // A row's partials j = first, first + step, ... <= last joined by one warp: the reference M and the
@@ -632,10 +645,12 @@ __device__ __forceinline__ float2 join_row(const AttnArgs& a, int w, int row, in
     return make_float2(M, l);
 }
 
+// A few partials a row: bound by the latency of three dependent loads (span, partials, and the counters
+// before them), so all of a row's are asked for at once, and what does not come from the first kernel is
+// read before the wait (2 to 3 us less than one block per row that took the partials in turn).
 // Blocks [0, works * R * SPLIT / kJoinWarps): SPLIT warps join one row of a work unit: o and lse.
 // Blocks behind them (accumulate): the shares of kJoinThreads blocks of a unit, or of all listed blocks
-// of a unit, one thread per block, summed over queries, heads and cells in a fixed order.  What does
-// not come from the first kernel is read before the wait for it.
+// of a unit, one thread per block, summed over queries, heads and cells in a fixed order.
 template <typename T, int D, int NT, bool LIST, bool ACC, int SPLIT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int row_blocks, int chunks) {
     constexpr int R = 8 * NT, V = D / 32;
@@ -736,8 +751,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int row_
 #pragma unroll
                         for (int i = 0; i < R; i += 4) {
                             const float4 z = *reinterpret_cast<const float4*>(mass + i);
-                            share += ex2_approx(z.x - lse2[i]) + ex2_approx(z.y - lse2[i + 1]) +
-                                     (ex2_approx(z.z - lse2[i + 2]) + ex2_approx(z.w - lse2[i + 3]));
+                            share += part_of(z.x, lse2[i]) + part_of(z.y, lse2[i + 1]) +
+                                     (part_of(z.z, lse2[i + 2]) + part_of(z.w, lse2[i + 3]));
                         }
                     }
                     if (LIST) atomicAdd(&c.acc[phys], share);       // a block listed twice adds twice

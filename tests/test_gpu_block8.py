@@ -284,6 +284,26 @@ def test_attn_several_queries(kvq, n_q, Hq, Hkv, D, block, codes):
     p.attn(q, qd=qd)
 
 
+@pytest.mark.parametrize("Hq,n_q", [(2, 4), (4, 3), (12, 3)])
+def test_padding_rows_may_hold_anything(kvq, Hq, n_q):
+    """Rows t >= n_new[b] of q, k and v are not looked at: NaN and infinities there change nothing."""
+    p = Pair(kvq, B=4, Hq=Hq, Hkv=1, D=64, block=32, max_tokens=128, max_q=n_q)
+    n_new = [1, n_q, 0, n_q - 1]
+    _lengths(p, [70, 33, 64, 100])
+    k, v, q = (p.rand(4, h, n_q, 64) for h in (1, 1, Hq))
+    for b, m in enumerate(n_new):
+        k[b, :, m:], v[b, :, m:], q[b, :, m:] = float("nan"), float("inf"), float("nan")
+    p.append(n_q, n_new=n_new, k=k, v=v)
+    p.check()
+    p.c.acc.zero_()
+    clean = torch.nan_to_num(q, 0.0)
+    for blocks in (None, kvq.block8_select(q.cuda(), p.c, 3, n_new=torch.tensor(n_new, dtype=torch.int32, device="cuda"))):
+        p.attn(clean, n_new=n_new, blocks=blocks, accumulate=True, qd=q.cuda())
+        assert torch.isfinite(p.c.acc).all()
+    if blocks is not None:
+        _check_select(p, clean, 3, 1, 1, n_new=n_new)
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_attn_extreme_logits_and_scales(kvq, dtype):
     """Logits far above and below the usual, blocks whose value scales differ by many powers of two."""
