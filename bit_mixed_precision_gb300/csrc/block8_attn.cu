@@ -92,15 +92,16 @@ struct Work {
 
 template <int NT, bool LIST>
 __device__ __forceinline__ Work work_of(const AttnArgs& a, int w) {
-    Work k;
-    const int rt = w % a.row_tiles, x = w / a.row_tiles;
-    k.u = LIST ? x / a.n_q : x;
+    Work k;                             // one row tile, one query: the usual case, without the divisions
+    const bool tiled = a.row_tiles > 1, one = a.n_q == 1;
+    const int rt = tiled ? w % a.row_tiles : 0, x = tiled ? w / a.row_tiles : w;
+    k.u = LIST && !one ? x / a.n_q : x;
     k.b = k.u / a.c.Hkv;
-    const int m = new_rows(a.n_new, k.b, a.n_q, &g_status_block8_attn);
+    const int m = a.n_new ? new_rows(a.n_new, k.b, a.n_q, &g_status_block8_attn) : a.n_q;
     const int count = min(a.c.count[k.u], a.c.max_blocks * a.c.block);
     const int r0 = rt * 8 * NT, all = LIST ? a.g : a.g * a.n_q;
     k.rows = min(8 * NT, all - r0);
-    const int first = LIST ? x % a.n_q : r0 / a.g, last = LIST ? first : (r0 + k.rows - 1) / a.g;
+    const int first = one ? 0 : LIST ? x % a.n_q : r0 / a.g, last = one ? 0 : LIST ? first : (r0 + k.rows - 1) / a.g;
     k.t0 = first;
     k.top = first < m ? query_limit(count, m, min(last, m - 1)) : 0;
     k.list_n = 0;
@@ -118,8 +119,8 @@ __device__ __forceinline__ Work work_of(const AttnArgs& a, int w) {
 // Query and head (within the group) of row i of a work unit.
 template <int NT, bool LIST>
 __device__ __forceinline__ int2 row_of(const AttnArgs& a, const Work& k, int w, int i) {
-    const int r = (w % a.row_tiles) * 8 * NT + i;
-    return LIST ? make_int2(k.t0, r) : make_int2(r / a.g, r % a.g);
+    const int r = a.row_tiles > 1 ? (w % a.row_tiles) * 8 * NT + i : i;
+    return LIST || a.n_q == 1 ? make_int2(k.t0, r) : make_int2(r / a.g, r % a.g);
 }
 
 // ------------------------------------------------------------------ pieces of the inner loop
