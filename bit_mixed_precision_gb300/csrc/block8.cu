@@ -477,8 +477,8 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(SelectArgs a) {
     __shared__ RunShared<kScoreThreads> run_sh;
     const kvq_block8& c = a.c;
     const int g = c.Hq / c.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane >> 2, lt = lane & 3;
-    const Run run = find_run<kScoreThreads>(
-        c.B * c.Hkv * a.n_q, [&](int i) { return (blocks_to_score(a, i) + 15) / 16; }, kScoreWarps, run_sh);
+    const auto run = find_run<kScoreThreads, kScoreWarps>(
+        c.B * c.Hkv * a.n_q, [&](int i) { return (blocks_to_score(a, i) + 15) / 16; }, run_sh);
     grid_launch_dependents();
     for (int row = run.work, from = run.from, before = run.before; from < run.to; ++row) {
         const int nb = blocks_to_score(a, row), groups = (nb + 15) / 16;
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kScoreThreads, 5) score_kernel(SelectArgs a) {
             }
         }
         __syncthreads();                                // q8 and sq are written again
-        before += groups + run.start;
+        before += run.places(groups);
         from = before;
     }
 }
@@ -837,8 +837,8 @@ cudaError_t launch_block8_select(const void* q, const int64_t* qs, int n_q, cons
             int ctas = 0;
             cudaError_t r = resident_ctas(score_kernel<T, D>, kScoreThreads, 0, known, &ctas);
             if (r != cudaSuccess) return r;
-            const long long groups = (long long)rows * ((c.max_blocks + 15) / 16);
-            const unsigned grid = (unsigned)std::min<long long>(ctas, (groups + kScoreWarps - 1) / kScoreWarps);
+            const int run = kScoreWarps * 16;           // blocks of a round
+            const unsigned grid = (unsigned)std::min<long long>(ctas, (long long)rows * ((c.max_blocks + run - 1) / run));
             score_kernel<T, D><<<grid, kScoreThreads, smem, s>>>(a);
             return cudaGetLastError();
         });

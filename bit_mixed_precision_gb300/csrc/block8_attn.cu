@@ -26,6 +26,7 @@
 // a unit's run the warps meet in shared memory and the CTA writes one partial
 // state; a second kernel, a programmatic dependent, joins the partials of a unit
 // and, with accumulate, adds the blocks' shares of the weights, in a fixed order.
+// Small caches (kDirectCells) take one CTA per work unit and no second kernel.
 //
 // Bound by HBM: 2 D bytes per token and KV head against 4 D g flop.  512 units of 32768 tokens, D 128,
 // four heads, e4m3, weights accumulated: 673 us, 0.94 of the measured 6.79 TB/s; 256 ragged units of up
@@ -54,6 +55,13 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // differences of references are numbers).
 constexpr float kShift = 7.0f, kLift = 15.0f, kNone = -1.0e38f;
 
+// Work units of at most this many 16-token cells (twice as many where the units alone give every SM a
+// CTA) are each taken by one CTA that writes o and lse itself, without the second kernel: 2 to 32 units
+// of 64, 128 and 256 tokens 4.1 to 4.5, 4.3 to 4.7, 5.5 to 5.8 us against 6.3 to 7.7 the other way; of 512
+// 7.5 to 7.9 against 7.2 to 7.9, of 1024 11.5 against 7.6.  512 units of 512 tokens 18.7 against 21.8, of
+// 1024 35.6 against 31.8.  (By room, not by tokens held: the host does not know those.)
+constexpr int kDirectCells = 16;
+
 struct AttnArgs {
     kvq_block8 c;
     const void* q;
@@ -67,7 +75,8 @@ struct AttnArgs {
     float* lse;
     // derived
     int g, row_tiles, works;            // work units = units (x n_q with lists) x row_tiles
-    int cells;                          // 16-token cells per work unit in `mass`
+    int cells;                          // 16-token cells per work unit at most
+    int direct;                         // one CTA per work unit that writes o and lse itself
     // workspace
     float *part, *ml, *mass;            // [slot][rows][D], [slot][rows][2], [work][cells][rows]
     int2* span;                         // [work] first and last CTA
@@ -252,6 +261,21 @@ __device__ __forceinline__ void ask_l2(const kvq_block8& c, const Cells& x, int 
     }
 }
 
+// Channels d .. d + 3 of a row's output, and lse with the first ones.
+template <typename T, int NT, bool LIST>
+__device__ __forceinline__ void write_row(const AttnArgs& a, const Work& k, int w, int row, int d, float4 y, float ref,
+                                          float sum) {
+    const int2 th = row_of<NT, LIST>(a, k, w, row);
+    const int m = a.n_new ? min(max(a.n_new[k.b], 0), a.n_q) : a.n_q;
+    const bool sees = th.x < m && sum != 0.0f;
+    const float inv = sees ? 1.0f / sum : 0.0f;
+    const size_t orow = ((size_t)k.b * a.c.Hq + (size_t)(k.u % a.c.Hkv) * a.g + th.y) * a.n_q + th.x;
+    T t[4] = {Elem<T>::from_f(sees ? y.x * inv : 0.0f), Elem<T>::from_f(sees ? y.y * inv : 0.0f),
+              Elem<T>::from_f(sees ? y.z * inv : 0.0f), Elem<T>::from_f(sees ? y.w * inv : 0.0f)};
+    *reinterpret_cast<uint2*>((T*)a.o + orow * a.c.D + d) = *reinterpret_cast<uint2*>(t);
+    if (d == 0 && a.lse) a.lse[orow] = sees ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+}
+
 template <int D, int NT>
 struct alignas(16) Shared {
     float o[kWarps][8][D + 4];          // one column block at a time
@@ -268,15 +292,21 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
     __shared__ Shared<D, NT> sh;
     const kvq_block8& c = a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const Run run = find_run<kThreads>(a.works, [&](int i) { return work_of<NT, LIST>(a, i).tiles; }, kWarps, sh.run);
+    Run<kWarps> run = {0, 1, (int)blockIdx.x, 0, true, 0, 1};   // direct: the CTA's own unit, whole
+    if (!a.direct)
+        run = find_run<kThreads, kWarps>(a.works, [&](int i) { return work_of<NT, LIST>(a, i).tiles; }, sh.run);
     grid_launch_dependents();
     for (int w = run.work, from = run.from, before = run.before; from < run.to; ++w) {
         const Work k = work_of<NT, LIST>(a, w);
-        if (k.tiles == 0) continue;
-        const int s0 = max(from - before - run.start, 0), s1 = min(k.tiles, run.to - before - run.start);
-        if (s1 <= 0) break;                     // the run ends ahead of the unit's tiles
-        if (s0 == 0 && threadIdx.x == 0)
-            a.span[w] = make_int2(blockIdx.x, (before + run.start + k.tiles - 1) / run.per);
+        int s0 = 0, s1 = k.tiles;
+        if (!a.direct) {
+            if (k.tiles == 0) continue;
+            s0 = max(from - before - run.start, 0);
+            s1 = min(k.tiles, run.to - before - run.start);
+            if (s1 <= 0) break;                 // the run ends ahead of the unit's tiles
+            if (s0 == 0 && threadIdx.x == 0)
+                a.span[w] = make_int2(blockIdx.x, (before + run.start + k.tiles - 1) / run.per);
+        }
         // ---- requests, in the order of their latencies: the table, the queries, the first tile
         KeyRegs<D> kr[C];
         ValueRegs<D> vr[C];
@@ -574,12 +604,17 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
                     y.w = fmaf(v.w, fac, y.w);
                     sum = fmaf(sh.ml[i][row][1], fac, sum);
                 }
-                *reinterpret_cast<float4*>(a.part + (slot * R + row) * D + d) = y;
-                if (d == 0) *reinterpret_cast<float2*>(a.ml + (slot * R + row) * 2) = make_float2(top, sum);
+                if (a.direct) {
+                    if (row < k.rows) write_row<T, NT, LIST>(a, k, w, row, d, y, top, sum);
+                } else {
+                    *reinterpret_cast<float4*>(a.part + (slot * R + row) * D + d) = y;
+                    if (d == 0) *reinterpret_cast<float2*>(a.ml + (slot * R + row) * 2) = make_float2(top, sum);
+                }
             }
             __syncthreads();
         }
-        before += k.tiles + run.start;
+        if (a.direct) break;
+        before += run.places(k.tiles);
         from = before;
     }
 }
@@ -806,15 +841,20 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t s) {
 }
 
 template <typename T, int D, int CODE, int NT, bool LIST, bool ACC>
-cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch(AttnArgs a, cudaStream_t s) {
     static std::atomic<int> known[64];
     auto kernel = attn_kernel<T, D, CODE, NT, LIST, ACC>;
     int ctas = 0;
     cudaError_t e = resident_ctas(kernel, kThreads, 0, known, &ctas);
     if (e != cudaSuccess) return e;
+    if (!ACC && a.cells <= (a.works >= ctas / Shape<NT>::kCtas ? 2 : 1) * kDirectCells) {
+        a.direct = 1;
+        kernel<<<(unsigned)a.works, kThreads, 0, s>>>(a);
+        return cudaGetLastError();
+    }
     // no more CTAs than runs of kWarps tiles in full caches
-    const long long tiles = (long long)a.works * ((a.cells + Shape<NT>::C - 1) / Shape<NT>::C);
-    const int grid = (int)std::min<long long>(std::min(ctas, kMaxCtas), (tiles + kWarps - 1) / kWarps);
+    constexpr int kRun = kWarps * Shape<NT>::C;
+    const int grid = (int)std::min<long long>(std::min(ctas, kMaxCtas), (long long)a.works * ((a.cells + kRun - 1) / kRun));
     kernel<<<grid, kThreads, 0, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -834,7 +874,7 @@ cudaError_t launch_block8_attn(const void* q, const int64_t* qs, int n_q, const 
     const Layout y = layout_of(c, n_q, n_sel, accumulate);
     char* base = (char*)ws;
     AttnArgs a{c, q, {qs[0], qs[1], qs[2]}, n_q, n_new, sm_scale, blocks, list_len, n_sel, o, lse,
-               c.Hq / c.Hkv, y.row_tiles, y.works, y.cells, (float*)(base + y.part), (float*)(base + y.ml),
+               c.Hq / c.Hkv, y.row_tiles, y.works, y.cells, 0, (float*)(base + y.part), (float*)(base + y.ml),
                (float*)(base + y.mass), (int2*)(base + y.span)};
     // one switch after the other turns the runtime choices into template arguments
     auto on = [](bool x, auto f) { return x ? f(std::true_type{}) : f(std::false_type{}); };

@@ -76,67 +76,80 @@ __device__ __forceinline__ uint32_t rank_key(float f) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Work units 0 .. works - 1 of tiles(i) tiles each, in one list that is split evenly over the grid's
-// CTAs, whatever the units' sizes (known on the device only): every CTA adds all of them up.  A unit's
-// first tile stands behind `start` places without work, since a CTA that comes to another unit in its
-// run spends the time of about eight tiles on starting there (at most a quarter of a CTA's tiles, none
-// where a CTA has a round or two: attn of 32 units of 4096 tokens 15.2 -> 13.4 us, ragged 256 units 58 -> 56).
+// Work units 0 .. works - 1 of tiles(i) tiles each, as one list of places that is cut into equal runs
+// for the grid's CTAs, whatever the units' sizes (known on the device only): every CTA adds all of them
+// up.  Starting on a unit costs a CTA the time of about eight tiles (counters, table, first tile).  So
+//  - where the grid has a CTA for every `least` tiles of every unit, a unit's tiles are filled up to a
+//    multiple of `least` places and a run is `least` places: no CTA comes to a second unit (32 ragged
+//    units of up to 64 tokens 14.6 -> 7.5 us);
+//  - else a unit's first tile stands behind `start` places without work, at most a quarter of a CTA's
+//    tiles (attn of 32 units of 4096 tokens 15.2 -> 13.4 us, ragged 256 units 58 -> 56).
+template <int LEAST>
 struct Run {
     int from, to;               // the CTA's places in the list
     int work, before;           // unit of the first place, and the places ahead of that unit
-    int start, per;             // places ahead of a unit's tiles; places per CTA (CTA c: [c per, c per + per))
+    bool whole;                 // the first of the two ways
+    int start;                  // places ahead of a unit's tiles
+    int per;                    // places per CTA (CTA c: [c per, c per + per))
+
+    __device__ __forceinline__ int places(int tiles) const {
+        return whole ? (tiles + LEAST - 1) / LEAST * LEAST : tiles > 0 ? start + tiles : 0;
+    }
 };
 template <int THREADS>
 struct RunShared {
-    int2 scan[THREADS / 32];
+    int scan[THREADS / 32][3];
     int at[2];
 };
 
 // The whole CTA calls this.
-template <int THREADS, typename TilesFn>
-__device__ __forceinline__ Run find_run(int works, TilesFn tiles, int least, RunShared<THREADS>& sh) {
+template <int THREADS, int LEAST, typename TilesFn>
+__device__ __forceinline__ Run<LEAST> find_run(int works, TilesFn tiles, RunShared<THREADS>& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int each = (works + THREADS - 1) / THREADS, w0 = min((int)threadIdx.x * each, works), w1 = min(w0 + each, works);
-    int2 sum = make_int2(0, 0);                 // tiles, units that have any
+    int sum[3] = {0, 0, 0};                     // tiles, units that have any, runs of LEAST tiles
     for (int i = w0; i < w1; ++i) {
         const int n = tiles(i);
-        sum.x += n;
-        sum.y += n > 0 ? 1 : 0;
+        sum[0] += n;
+        sum[1] += n > 0 ? 1 : 0;
+        sum[2] += (n + LEAST - 1) / LEAST;
     }
-    int2 incl = sum;
+    int incl[3] = {sum[0], sum[1], sum[2]};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
-        if (lane >= o) {
-            incl.x += x;
-            incl.y += y;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int x = __shfl_up_sync(0xffffffffu, incl[k], o);
+            if (lane >= o) incl[k] += x;
         }
-    }
-    if (lane == 31) sh.scan[warp] = incl;
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sh.scan[warp][k] = incl[k];
     __syncthreads();
-    int2 all = make_int2(0, 0), base = make_int2(0, 0);
+    int all[3] = {0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-        const int2 x = sh.scan[i];
-        if (i < warp) {
-            base.x += x.x;
-            base.y += x.y;
+    for (int i = 0; i < THREADS / 32; ++i)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int x = sh.scan[i][k];
+            if (i < warp) incl[k] += x;
+            all[k] += x;
         }
-        all.x += x.x;
-        all.y += x.y;
-    }
-    Run r;
-    const int mean = all.x / (int)gridDim.x;
-    r.start = mean >= 2 * least ? min(8, mean / 4) : 0;
-    const int places = all.x + r.start * all.y;
-    r.per = max((places + (int)gridDim.x - 1) / (int)gridDim.x, least);
-    r.from = (int)min((long long)blockIdx.x * r.per, (long long)places);
-    r.to = min(r.from + r.per, places);
-    int at = base.x + incl.x - sum.x + r.start * (base.y + incl.y - sum.y);
-    if (r.from < places && r.from >= at && r.from < at + sum.x + r.start * sum.y) {
+    const int grid = (int)gridDim.x;
+    const bool whole = all[2] <= grid;
+    Run<LEAST> r;
+    r.whole = whole;
+    r.start = whole ? 0 : min(8, all[0] / grid / 4);
+    const int list = whole ? all[2] * LEAST : all[0] + r.start * all[1];
+    r.per = max((list + grid - 1) / grid, LEAST);
+    r.from = (int)min((long long)blockIdx.x * r.per, (long long)list);
+    r.to = min(r.from + r.per, list);
+    int at = whole ? (incl[2] - sum[2]) * LEAST : incl[0] - sum[0] + r.start * (incl[1] - sum[1]);
+    const int own = whole ? sum[2] * LEAST : sum[0] + r.start * sum[1];
+    if (r.from < list && r.from >= at && r.from < at + own) {
         int i = w0;
         for (;; ++i) {
-            const int n = tiles(i), p = n > 0 ? n + r.start : 0;
+            const int p = r.places(tiles(i));
             if (r.from < at + p) break;
             at += p;
         }

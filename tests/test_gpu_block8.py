@@ -284,6 +284,38 @@ def test_attn_several_queries(kvq, n_q, Hq, Hkv, D, block, codes):
     p.attn(q, qd=qd)
 
 
+@pytest.mark.parametrize("D,block,Hq,Hkv,n_q,codes,dtype", [
+    (128, 16, 4, 4, 1, F8, torch.float16), (64, 64, 10, 2, 1, I8, torch.bfloat16), (128, 128, 12, 1, 1, F8, torch.bfloat16),
+    (64, 16, 3, 1, 3, F8, torch.float16), (128, 32, 8, 1, 4, I8, torch.float16), (128, 16, 40, 1, 2, F8, torch.bfloat16)])
+def test_attn_small_caches(kvq, D, block, Hq, Hkv, n_q, codes, dtype):
+    """Room for 256 tokens a unit: one CTA per work unit writes the output itself."""
+    lens = [0, 1, 15, 16, 17, 100, 255, 256]
+    p = Pair(kvq, B=len(lens), Hq=Hq, Hkv=Hkv, D=D, block=block, codes=codes, dtype=dtype, max_tokens=256, max_q=4, seed=Hq)
+    _lengths(p, lens)
+    q = p.rand(len(lens), Hq, n_q, D)
+    p.attn(q)
+    n_new = [n_q, 1, 0, n_q, 1, n_q - 1, 1, n_q]
+    qn = q.clone()
+    for b, m in enumerate(n_new):
+        qn[b, :, m:] = float("nan")
+    p.attn(q, n_new=n_new, qd=qn.cuda())
+    idx, n = kvq.block8_select(q.cuda(), p.c, max(2, 128 // block))
+    p.attn(q, blocks=(idx, n))
+    p.attn(q, blocks=(idx, torch.zeros_like(n)))
+
+
+@pytest.mark.parametrize("room", [512, 544])
+def test_attn_many_small_units(kvq, room):
+    """320 units with room just at, and just above, what one CTA each takes; most hold little."""
+    lens = [int(x) for x in np.random.default_rng(room).integers(0, 40, 160)]
+    lens[7], lens[100] = room, 300
+    p = Pair(kvq, B=160, Hq=2, Hkv=2, D=64, block=32, codes=I8, max_tokens=room)
+    _lengths(p, lens)
+    p.attn(p.rand(160, 2, 1, 64))
+    p.c.acc.zero_()
+    p.attn(p.rand(160, 2, 1, 64), accumulate=True)
+
+
 @pytest.mark.parametrize("Hq,n_q", [(2, 4), (4, 3), (12, 3)])
 def test_padding_rows_may_hold_anything(kvq, Hq, n_q):
     """Rows t >= n_new[b] of q, k and v are not looked at: NaN and infinities there change nothing."""
