@@ -591,7 +591,8 @@ class Block8Cache:
     ``max_sel``: entries of a block list (the table's length by default).  ``ws``: a workspace
     tensor (uint8, ws_bytes(...) bytes) to share between caches whose calls never overlap on
     the GPU; one is allocated otherwise.  Calls on one cache must follow one another (one
-    stream, or events), also when they are replayed from CUDA graphs."""
+    stream, or events), also when they are replayed from CUDA graphs.  The calls hold the tensors'
+    addresses: write into the tensors, do not put others in their place."""
     B: int
     Hq: int
     Hkv: int

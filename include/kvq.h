@@ -462,8 +462,9 @@ kvq_status block8_append(kvq_block8* c, const void* k, const int64_t* k_strides,
  *   and lse = -inf.
  *   accumulate != 0: acc[block] += the softmax weights of the block's tokens,
  *   summed over the queries and the unit's query heads.
- *   Products with q are exact and sums are float32; the softmax weights enter
- *   the second product as a pair of fp16 numbers (22 bits).
+ *   Products with q are exact (bf16: but for elements below 2^-31 of their
+ *   row's largest, which round) and sums are float32; the softmax weights
+ *   enter the second product as a pair of fp16 numbers (22 bits).
  *   ws (device) of at least block8_attn_workspace_bytes(), 256-byte aligned;
  *   its content between calls is irrelevant. */
 kvq_status block8_attn(const void* q, const int64_t* q_strides, int n_q, const int32_t* n_new, kvq_block8* c,

@@ -183,6 +183,9 @@ def test_append_prompt_with_scores(kvq, block):
     p.append(777, n_new=[777, 5, 640], colscore=True)
     # g * block float32 additions of non-negative numbers
     p.check(acc_rtol=(3 * block + 2) * U24)
+    for u in (0, 2, 5):                                 # code x scale, rounded to float32 once
+        for got, want in zip(p.c.dequantised(u), p.units[u].dequantised()):
+            np.testing.assert_allclose(got.cpu().numpy(), want, rtol=U24, atol=0)
     p.append(100, n_new=[100, 0, 33], colscore=True)
     p.check(acc_rtol=(6 * block + 4) * U24)
 
