@@ -177,6 +177,22 @@ def test_append_any_split(kvq, D, block, codes, dtype):
     p.check()
 
 
+@pytest.mark.parametrize("D,block", [(64, 16), (128, 32), (128, 128)])
+def test_append_whole_blocks(kvq, D, block):
+    """Calls that end on a block's last row, alone and among others, and a block filled row by row."""
+    p = Pair(kvq, D=D, block=block, max_tokens=8 * block)
+    p.append(block)
+    p.check()
+    p.append(block, n_new=[block, 0], colscore=True)
+    p.append(2 * block, n_new=[2 * block, block])
+    p.check()
+    for _ in range(block if block == 16 else 3):
+        p.append(1)
+    p.check()
+    p.append(block, n_new=[block - 3, block - 1] if block > 16 else [block, block])
+    p.check()
+
+
 @pytest.mark.parametrize("block", [16, 128])
 def test_append_prompt_with_scores(kvq, block):
     p = Pair(kvq, B=3, Hq=6, Hkv=2, block=block, codes=I8, max_tokens=1000)
