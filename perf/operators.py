@@ -170,16 +170,21 @@ def prepare(case, seed):
         st["v_codes"], st["v_scale"] = _quantise(case, torch.randn((N, P, D), generator=gen, device=dev))[:2]
     else:
         st["v_codes"], st["v_scale"] = torch.zeros_like(st["k_codes"]), torch.ones(N, device=dev)
-    # counters and table share one array, so that one copy brings them back to where they were
-    meta = torch.empty(U * (nb + 2), dtype=torch.int32, device=dev)
+    # counters and table share one array, so that one copy brings them back to where they were; for append the scales
+    # too: an open block's must be the old ones, or no new token would be larger than what the block holds already
+    held = U * (nb + 2)
+    meta = torch.empty(held + (3 * N if case["op"] == "append" else 0), dtype=torch.int32, device=dev)
+    if case["op"] == "append":
+        for name, x in zip(("k_scale", "v_scale", "bound_scale"), meta[held:].view(torch.float32).view(3, N)):
+            st[name] = x.copy_(st[name])
     count = torch.tensor(_lengths(case), dtype=torch.int32, device=dev)
     meta[:U] = count
     meta[U:2 * U] = count + 11 * 16                     # some tokens were dropped before
-    meta[2 * U:] = torch.randperm(N, generator=gen, device=dev).to(torch.int32)
+    meta[2 * U:held] = torch.randperm(N, generator=gen, device=dev).to(torch.int32)
     if case["op"] == "append" and case["T"] == 0:
         meta[U:2 * U] = 0
     st["meta"], st["meta0"] = meta, meta.clone()
-    st["count"], st["seq_len"], st["table"] = meta[:U], meta[U:2 * U], meta[2 * U:].view(U, nb)
+    st["count"], st["seq_len"], st["table"] = meta[:U], meta[U:2 * U], meta[2 * U:held].view(U, nb)
     # what attention left in the blocks: mostly little, much in a few
     st["acc0"] = torch.exp(2.0 * torch.randn(N, generator=gen, device=dev))
     st["acc"] = st["acc0"].clone()
@@ -193,6 +198,7 @@ def prepare(case, seed):
         st["colscore"] = torch.rand((B, Hq, n), generator=gen, device=dev) ** 4 if case["acc"] else None
         if case["T"]:
             _open_blocks(case, st, gen)
+            st["meta0"].copy_(meta)
     else:
         st["q"] = torch.randn((B, Hq, case["n_q"], D), generator=gen, device=dev).to(dt)
         st["sm_scale"] = 1.0 / math.sqrt(D)
