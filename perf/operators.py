@@ -385,7 +385,7 @@ def _plain_select(case, st):
     U, g = B * Hkv, Hq // Hkv
     q = st["q"].view(B, Hkv, g, n_q, D).permute(0, 1, 3, 2, 4).reshape(U, n_q, g, D).float()
     sq = _scale(q.abs().amax(dim=-1), 127.0)
-    q8 = (q * sq.reciprocal()[..., None]).round().clamp(-127.0, 127.0).view(U, n_q * g, D)
+    q8 = (q * sq.reciprocal()[..., None]).round().clamp(-127.0, 127.0).reshape(U, n_q * g, D)
     bound = st["k_bound"][st["table"].long()].float()
     # sums of products of whole numbers below 2^24: float32 holds them exactly, in any order
     x = torch.matmul(q8.clamp_min(0.0), bound[:, :, 1].transpose(-1, -2))
