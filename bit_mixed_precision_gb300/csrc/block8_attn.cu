@@ -8,7 +8,8 @@
 // row, so blocks whose value scales lie many powers of two apart share one fp16
 // range; a weight enters as a pair of fp16 numbers (22 bits).  The sum of the same
 // weights times 1 / v beside it gives the softmax denominator, so that the
-// rounding of log2 v (2^-22) only shifts a block's logits by as much.
+// rounding of log2 v (2^-22) only shifts a block's logits by as much.  bf16 value
+// scales may be so far apart that float32 loses weights that count there: kFar below.
 //
 // Work.  The rows that read a unit together (queries x heads of the group, up to
 // 8, 16 or 32 of them) and its tokens, or a query's listed blocks, form a work unit;
@@ -54,6 +55,23 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // weights fit fp16, and 2^-31 of the largest is still a weight.  kNone: no logit yet (finite, so that
 // differences of references are numbers).
 constexpr float kShift = 7.0f, kLift = 15.0f, kNone = -1.0e38f;
+
+// The softmax denominator does not know the value scales, the exponents above do.  fp16 values keep
+// log2 v within -64 .. 9.1, and what float32 flushes (2^-126) is then below 2^-53 of the denominator.
+// bf16 values reach from -64 (a block of zeros) to 121.  So for bf16 a warp whose cells' log2 v span
+// more than kFar takes the part of the lower ones in the denominator from a second exponential without
+// log2 v (with kBias more: the largest value scale alone puts the denominator at 2^-114), beside the
+// rare moves of the reference; and a reference that far below another lowers its denominator in two steps.
+constexpr float kFar = 80.0f, kBias = 24.0f, kBiasInv = 1.0f / 16777216.0f;
+template <typename T> constexpr bool kWide = std::is_same<T, __nv_bfloat16>::value;
+
+// l 2^d, d <= 0: l may be as large as 2^(64 + kLift) a token while 2^d alone is flushed.
+template <bool WIDE>
+__device__ __forceinline__ float lowered(float l, float d) {
+    if constexpr (!WIDE) return l * ex2_approx(d);
+    const float f = ex2_approx(d < -64.0f ? 0.5f * d : d);
+    return l * f * (d < -64.0f ? f : 1.0f);
+}
 
 // Work units of at most this many 16-token cells (twice as many where the units alone give every SM a
 // CTA) are each taken by one CTA that writes o and lse itself, without the second kernel: 2 to 32 units
@@ -250,6 +268,22 @@ __device__ __forceinline__ Cells find_cells(const AttnArgs& a, const Work& k, in
     return x;
 }
 
+// Takes the lanes' log2 v into the warp's range: whether it is wider than kFar.
+__device__ __forceinline__ bool scales_apart(float2& range, float lv, float2 before) {
+    float hi = lv, lo = lv;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, x));
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, x));
+    }
+    hi = fmaxf(hi, before.x);
+    lo = fminf(lo, before.y);
+    __syncwarp();                       // `before` may be the range: every lane has read it
+    if ((threadIdx.x & 31) == 0) range = make_float2(hi, lo);
+    __syncwarp();
+    return hi - lo > kFar;
+}
+
 // Asks L2 for the cells of tile i of those in `x`; nothing waits for them.  One tile ahead (the tile
 // whose registers are loaded next): 712 -> 681 us on 512 units of 32768 tokens; two, three and five
 // ahead 691, 695, 709.
@@ -282,6 +316,7 @@ struct alignas(16) Shared {
     float ml[kWarps][8 * NT][2];
     __half q[Shape<NT>::kSharedQ ? 8 * NT : 1][D + 4];          // queries as fp16, rows padded
     float undo[8 * NT];
+    float2 lv[kWarps];                  // largest and least log2 v of the cells that a warp has looked up
     RunShared<kThreads> run;
 };
 
@@ -409,6 +444,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
         }
         // ---- the warp's tiles
         int at = 0;                     // the tile's place among those of `cells`
+        bool wide = false;              // value scales more than kFar apart so far (for the whole warp)
+        if constexpr (kWide<T>) wide = scales_apart(sh.lv[warp], cells.lv, make_float2(-INFINITY, INFINITY));
         for (int tile = s0 + warp; tile < s1; tile += kWarps) {
             float ks[C], lv[C], rv[C];
             int slot[C];
@@ -424,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
             if (++at == LANES) {
                 cells = find_cells<C, LIST>(a, k, w, tile + kWarps, s1, lane);
                 at = 0;
+                if constexpr (kWide<T>) wide = scales_apart(sh.lv[warp], cells.lv, sh.lv[warp]);
             }
             ask_l2<D, C>(c, cells, at, lane);
 #pragma unroll
@@ -472,7 +510,21 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
                             if (slot[j] + g + (x >> 1) * 8 >= lim[n][x & 1]) s[j][n][x] = -INFINITY;
                 }
             }
-            float over = -INFINITY;
+            // log2 of a cell's weights, whatever M is now or becomes; sum0 and sum1 count `unit` each
+            [[maybe_unused]] auto put_mass = [&](int j, int n, float sum0, float sum1, float unit) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    sum0 += __shfl_xor_sync(0xffffffffu, sum0, x);
+                    sum1 += __shfl_xor_sync(0xffffffffu, sum1, x);
+                }
+                if (g == 0 && slot[j] < 0x40000000)
+                    *reinterpret_cast<float2*>(a.mass + ((size_t)w * a.cells + C * tile + j) * R + 8 * n + 2 * t) =
+                        make_float2(__log2f(sum0 * unit) + M[n][0], __log2f(sum1 * unit) + M[n][1]);
+            };
+            [[maybe_unused]] bool counted[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j) counted[j] = false;
+            float over = wide ? INFINITY : -INFINITY;
             auto column_max = [&](int n, int e) {
                 float mx = fmaxf(s[0][n][e], s[0][n][2 + e]);
                 if constexpr (C == 2) mx = fmaxf(mx, fmaxf(s[C - 1][n][e], s[C - 1][n][2 + e]));
@@ -492,14 +544,33 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         const float now = fmaxf(M[n][e], mx - kShift), fac = ex2_approx(M[n][e] - now);
+                        l[n][e] = lowered<kWide<T>>(l[n][e], M[n][e] - now);
                         M[n][e] = now;
-                        l[n][e] *= fac;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             o[n][i][e] *= fac;
                             o[n][i][2 + e] *= fac;
                         }
                     }
+                if constexpr (kWide<T>) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+                        if (sh.lv[warp].x - lv[j] > kFar) {             // (the whole warp)
+                            const float up = kBias - lv[j];
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                float sum[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    sum[e] = ex2_approx(s[j][n][e] - M[n][e] + up) + ex2_approx(s[j][n][2 + e] - M[n][e] + up);
+                                    l[n][e] = fmaf(sum[e], kBiasInv, l[n][e]);
+                                }
+                                if constexpr (ACC) put_mass(j, n, sum[0], sum[1], kBiasInv);
+                            }
+                            rv[j] = 0.0f;
+                            counted[j] = true;
+                        }
+                }
             }
             uint32_t bh[C][NT][2], bl[C][NT][2];
 #pragma unroll
@@ -512,18 +583,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
                     const float sum0 = p[0] + p[2], sum1 = p[1] + p[3];
                     l[n][0] = fmaf(sum0, rv[j], l[n][0]);
                     l[n][1] = fmaf(sum1, rv[j], l[n][1]);
-                    if constexpr (ACC) {
-                        float c0 = sum0, c1 = sum1;
-#pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) {
-                            c0 += __shfl_xor_sync(0xffffffffu, c0, x);
-                            c1 += __shfl_xor_sync(0xffffffffu, c1, x);
-                        }
-                        // log2 of the cell's weights, whatever M is now or becomes
-                        if (g == 0 && slot[j] < 0x40000000)
-                            *reinterpret_cast<float2*>(a.mass + ((size_t)w * a.cells + C * tile + j) * R + 8 * n + 2 * t) =
-                                make_float2(__log2f(c0 * rv[j]) + M[n][0], __log2f(c1 * rv[j]) + M[n][1]);
-                    }
+                    if constexpr (ACC)
+                        if (!counted[j]) put_mass(j, n, sum0, sum1, rv[j]);
                     uint32_t h0, l0, h1, l1;
                     split2(p[0], p[1], h0, l0);
                     split2(p[2], p[3], h1, l1);
@@ -602,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas) attn_kernel(AttnAr
                     y.y = fmaf(v.y, fac, y.y);
                     y.z = fmaf(v.z, fac, y.z);
                     y.w = fmaf(v.w, fac, y.w);
-                    sum = fmaf(sh.ml[i][row][1], fac, sum);
+                    if constexpr (kWide<T>) sum += lowered<true>(sh.ml[i][row][1], sh.ml[i][row][0] - ref);
+                    else sum = fmaf(sh.ml[i][row][1], fac, sum);
                 }
                 if (a.direct) {
                     if (row < k.rows) write_row<T, NT, LIST>(a, k, w, row, d, y, top, sum);
@@ -632,7 +694,7 @@ constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 // A row's partials j = first, first + step, ... <= last joined by one warp: the reference M and the
 // sum l that belong to it, and D / 32 output channels a lane (o, if OUT).  Four partials are in flight
 // at a time.
-template <int D, int R, bool OUT>
+template <int D, int R, bool OUT, bool WIDE>
 __device__ __forceinline__ float2 join_row(const AttnArgs& a, int w, int row, int first, int last, int step, int lane,
                                            float (&o)[D / 32]) {
     constexpr int V = D / 32;
@@ -665,14 +727,14 @@ __device__ __forceinline__ float2 join_row(const AttnArgs& a, int w, int row, in
         }
         const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
         const float ref = top == -INFINITY ? 0.0f : top, old = ex2_approx(M - ref);
+        l = WIDE ? lowered<WIDE>(l, M - ref) : l * old;
         M = top;
-        l *= old;
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] *= old;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float f = ex2_approx(ml[i].x - ref);
-            l = fmaf(ml[i].y, f, l);
+            l = WIDE ? l + lowered<WIDE>(ml[i].y, ml[i].x - ref) : fmaf(ml[i].y, f, l);
             if (OUT)
 #pragma unroll
                 for (int v = 0; v < V; ++v) o[v] = fmaf(x[i][v], f, o[v]);
@@ -706,7 +768,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int row_
         for (int v = 0; v < V; ++v) o[v] = 0.0f;
         if (live) {
             const int2 span = a.span[w];
-            const float2 ml = join_row<D, R, true>(a, w, i, span.x + part, span.y, SPLIT, lane, o);
+            const float2 ml = join_row<D, R, true, kWide<T>>(a, w, i, span.x + part, span.y, SPLIT, lane, o);
             M = ml.x;
             l = ml.y;
         }
@@ -727,7 +789,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int row_
 #pragma unroll
             for (int p = 0; p < SPLIT; ++p) {
                 const float f = ex2_approx(sml[warp + p].x - ref);
-                l = fmaf(sml[warp + p].y, f, l);
+                l = kWide<T> ? l + lowered<kWide<T>>(sml[warp + p].y, sml[warp + p].x - ref) : fmaf(sml[warp + p].y, f, l);
 #pragma unroll
                 for (int v = 0; v < V; ++v) o[v] = fmaf(so[warp + p][lane * V + v], f, o[v]);
             }
@@ -762,12 +824,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int row_
                 __syncthreads();
                 for (int i = warp; i < R; i += kJoinWarps) {
                     float none[V];
-                    const float2 ml = join_row<D, R, false>(a, w, i, span.x + lane, span.y, 32, lane, none);
+                    const float2 ml = join_row<D, R, false, kWide<T>>(a, w, i, span.x + lane, span.y, 32, lane, none);
                     float top = ml.x;
 #pragma unroll
                     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const float ref = top == -INFINITY ? 0.0f : top;
-                    float l = ml.y * ex2_approx(ml.x - ref);
+                    float l = lowered<kWide<T>>(ml.y, ml.x - ref);
 #pragma unroll
                     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
                     const bool sees = i < k.rows && row_of<NT, LIST>(a, k, w, i).x < m && l != 0.0f;

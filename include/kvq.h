@@ -463,8 +463,12 @@ kvq_status block8_append(kvq_block8* c, const void* k, const int64_t* k_strides,
  *   accumulate != 0: acc[block] += the softmax weights of the block's tokens,
  *   summed over the queries and the unit's query heads.
  *   Products with q are exact (bf16: but for elements below 2^-31 of their
- *   row's largest, which round) and sums are float32; the softmax weights
- *   enter the second product as a pair of fp16 numbers (22 bits).
+ *   row's largest, which round) and sums are float32.  A softmax weight enters
+ *   the second product times its block's value scale, as a pair of fp16
+ *   numbers: 22 bits, and nothing finer than 2^-32 of the row's largest such
+ *   product.  The denominator (o, lse, acc) holds for all value scales that
+ *   the cache can have.  acc: a block's share is exp2 of a difference of two
+ *   float32 logarithms, so that its error grows with their size (2^-22 of it).
  *   ws (device) of at least block8_attn_workspace_bytes(), 256-byte aligned;
  *   its content between calls is irrelevant. */
 kvq_status block8_attn(const void* q, const int64_t* q_strides, int n_q, const int32_t* n_new, kvq_block8* c,

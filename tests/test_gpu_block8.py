@@ -10,6 +10,8 @@ from its arithmetic (u = 2^-24, D channels, n tokens seen):
              16-bit output (eps/2 |ref|, 2^-25 below fp16's normal range);  2^-13 holds 2 * 2^-15 and the small terms
   lse        e + 2^-14 + n u + 2^-22 |lse|;   acc: (2 e + 2^-13 + 2 n u) relative, plus u of the sum it is added to
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -372,6 +374,37 @@ def test_attn_extreme_logits_and_scales(kvq, dtype):
     q = p.rand(4, 4, 1, 64) * 200
     p.attn(q, accumulate=True)
     p.attn(torch.zeros_like(q))
+
+
+@pytest.mark.parametrize("D,block,Hq,n_q,codes,room", [(64, 16, 1, 1, F8, 256), (128, 32, 4, 1, I8, 256), (64, 16, 12, 1, I8, 256),
+                                                       (128, 16, 4, 1, F8, 2048), (64, 32, 6, 2, I8, 2048), (128, 64, 8, 4, F8, 2048)])
+def test_attn_value_scales_over_all_of_bf16(kvq, D, block, Hq, n_q, codes, room):
+    """Value scales from 2^-64 (a block of zeros) to 2^120: blocks of small values keep their part of the softmax, in
+    the outputs, lse and acc; one kernel for a unit (room 256, no acc) and the joined partials of many."""
+    n = min(room, 1400) - 7
+    p = Pair(kvq, B=6, Hq=Hq, Hkv=1, D=D, block=block, codes=codes, dtype=torch.bfloat16, max_tokens=room, max_q=4, seed=D + Hq)
+    k, v = p.rand(6, 1, n, D), torch.rand((6, 1, n, D), generator=p.gen) + 0.5
+    v = v * torch.where(torch.rand(v.shape, generator=p.gen) < 0.5, -1.0, 1.0)
+    power = torch.full((6, n), -math.inf)               # log2 of the values' size; -inf: zeros
+    at = torch.arange(n) // block
+    power[0, at == 3] = 80.0                            # equal logits, one block far above many of zeros
+    power[1, at < 2] = 126.0                            # the large ones first
+    power[2, at == int(at[-1]) - 1] = 126.0             # and last
+    power[2, at == 0] = 0.0
+    power[3] = torch.tensor([-100.0, -20.0, 0.0, 45.0, 126.0, -math.inf])[torch.randint(0, 6, (int(at[-1]) + 1,), generator=p.gen)[at]]
+    power[4] = 0.0                                      # large values only where the softmax has next to nothing
+    power[4, at == 1] = 100.0
+    power[5] = 126.0                                    # and everywhere
+    k[:3], k[4, 0, at == 1] = 0, k[4, 0, at == 1] * 0 + 8
+    p.append(n, k=k, v=(v * torch.exp2(power)[:, None, :, None]).to(torch.bfloat16))
+    q = p.rand(6, Hq, n_q, D)
+    q[4] = -q[4].abs()
+    p.c.acc.zero_()
+    p.attn(q)
+    p.attn(q, accumulate=True)
+    held = int(at[-1]) + 1
+    idx = torch.arange(held - 1, -1, -1, dtype=torch.int32, device="cuda").expand(6, 1, n_q, held).contiguous()
+    p.attn(q, blocks=(idx, torch.full((6, 1, n_q), held, dtype=torch.int32, device="cuda")), accumulate=True)
 
 
 def test_attn_lists(kvq):
