@@ -435,7 +435,7 @@ static kvq_status check_ws(const void* ws, size_t given, size_t need, const char
 static kvq_status check_list(const kvq_block8* c, int n_q, int n_sel, const char* who) {
     KVQ_REQUIRE(n_sel <= (1 << 20), KVQ_EUNSUPPORTED, "%s: n_sel = %d is too large", who, n_sel);
     const long long g = c->Hq / c->Hkv, rows = n_sel ? g : g * n_q, sets = (long long)c->B * c->Hkv * (n_sel ? n_q : 1);
-    const long long cells = (long long)(n_sel ? n_sel : c->max_blocks) * (c->block / 16);
+    const long long cells = (long long)(n_sel && n_sel < c->max_blocks ? n_sel : c->max_blocks) * (c->block / 16);
     KVQ_REQUIRE(cells <= (1LL << 30) / (sets * ((rows + 31) / 32)), KVQ_EUNSUPPORTED,
                 "%s: too many tokens for one call (%lld units or lists of %lld x 16)", who, sets, cells);
     return KVQ_OK;

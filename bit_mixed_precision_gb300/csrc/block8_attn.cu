@@ -92,6 +92,7 @@ struct AttnArgs {
     void* o;
     float* lse;
     // derived
+    int n_list;                         // entries of a list that can count
     int g, row_tiles, works;            // work units = units (x n_q with lists) x row_tiles
     int cells;                          // 16-token cells per work unit at most
     int direct;                         // one CTA per work unit that writes o and lse itself
@@ -134,8 +135,8 @@ __device__ __forceinline__ Work work_of(const AttnArgs& a, int w) {
     k.list_n = 0;
     if (LIST) {
         const int n = a.list_len[x];
-        if (n < 0 || n > a.n_sel) atomicOr(&g_status_block8_attn, kDevCheck);
-        k.list_n = k.top > 0 ? min(max(n, 0), a.n_sel) : 0;
+        if (n < 0 || n > a.n_list) atomicOr(&g_status_block8_attn, kDevCheck);
+        k.list_n = k.top > 0 ? min(max(n, 0), a.n_list) : 0;
         k.tiles = (k.list_n * (a.c.block / 16) + Shape<NT>::C - 1) / Shape<NT>::C;
     } else {
         k.tiles = (k.top + 16 * Shape<NT>::C - 1) / (16 * Shape<NT>::C);
@@ -876,7 +877,7 @@ Layout layout_of(const kvq_block8& c, int n_q, int n_sel, int accumulate) {
     y.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     y.row_tiles = (rows + 8 * y.nt - 1) / (8 * y.nt);
     y.works = units * (n_sel ? n_q : 1) * y.row_tiles;
-    y.cells = (n_sel ? n_sel : c.max_blocks) * (c.block / 16);
+    y.cells = (n_sel ? std::min(n_sel, c.max_blocks) : c.max_blocks) * (c.block / 16);
     const size_t slots = (size_t)kMaxCtas + y.works, r = 8 * y.nt;
     y.part = 0;
     y.ml = y.part + up256(slots * r * c.D * sizeof(float));
@@ -936,8 +937,8 @@ cudaError_t launch_block8_attn(const void* q, const int64_t* qs, int n_q, const 
     const Layout y = layout_of(c, n_q, n_sel, accumulate);
     char* base = (char*)ws;
     AttnArgs a{c, q, {qs[0], qs[1], qs[2]}, n_q, n_new, sm_scale, blocks, list_len, n_sel, o, lse,
-               c.Hq / c.Hkv, y.row_tiles, y.works, y.cells, 0, (float*)(base + y.part), (float*)(base + y.ml),
-               (float*)(base + y.mass), (int2*)(base + y.span)};
+               std::min(n_sel, c.max_blocks), c.Hq / c.Hkv, y.row_tiles, y.works, y.cells, 0, (float*)(base + y.part),
+               (float*)(base + y.ml), (float*)(base + y.mass), (int2*)(base + y.span)};
     // one switch after the other turns the runtime choices into template arguments
     auto on = [](bool x, auto f) { return x ? f(std::true_type{}) : f(std::false_type{}); };
     return on(c.dtype == KVQ_BF16, [&](auto bf) {

@@ -454,9 +454,10 @@ kvq_status block8_append(kvq_block8* c, const void* k, const int64_t* k_strides,
  *   q (device) [B, Hq, n_q, D], 1 <= n_q <= KVQ_BLOCK8_MAX_Q; query head h
  *   reads KV head h / (Hq/Hkv).
  *   blocks (device, nullable) [B, Hkv, n_q, n_sel] logical block numbers and
- *   list_len (device) [B, Hkv, n_q] how many of them count: query t then sees
- *   only the tokens of its listed blocks (each listed once).  A number at or
- *   behind the unit's last block is skipped (KVQ_EDEVICE).  blocks NULL: all.
+ *   list_len (device) [B, Hkv, n_q] how many of them count, at most n_sel and
+ *   max_blocks (clamped and reported as KVQ_EDEVICE): query t then sees only
+ *   the tokens of its listed blocks (each listed once).  A number at or behind
+ *   the unit's last block is skipped (KVQ_EDEVICE).  blocks NULL: all.
  *   o (device) [B, Hq, n_q, D], lse (device, nullable) [B, Hq, n_q] natural
  *   log.  A query that sees no token, and the rows t >= n_new[b], get o = 0
  *   and lse = -inf.
@@ -476,7 +477,8 @@ kvq_status block8_attn(const void* q, const int64_t* q_strides, int n_q, const i
                        int accumulate, void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace of block8_attn for n_q queries, n_sel list entries (0: no list);
- * (size_t)-1 on invalid arguments. */
+ * as much for n_sel above max_blocks as for max_blocks.  (size_t)-1 on invalid
+ * arguments. */
 size_t block8_attn_workspace_bytes(const kvq_block8* c, int n_q, int n_sel, int accumulate);
 
 /* block8_select -- the blocks whose keys may match a query best, for each query

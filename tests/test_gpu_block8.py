@@ -572,6 +572,23 @@ def test_select_many_blocks_ties_and_not_a_number(kvq):
     _check_select(p, q, 33, 1, 1)
 
 
+def test_lists_longer_than_the_table(kvq):
+    """n_sel above the units' number of blocks: what select returns is taken back by attn, with accumulate too."""
+    p = Pair(kvq, B=2, Hq=8, Hkv=2, max_tokens=16 * 32)
+    p.append(16 * 32 - 3)
+    p.c.acc.zero_()
+    q = p.rand(2, 8, 1, 128)
+    blocks = _check_select(p, q, 64, 1, 1)
+    a = p.attn(q, blocks=blocks, accumulate=True)
+    b = p.attn(q, blocks=blocks)
+    assert torch.equal(a[0], b[0])
+    # more entries than blocks exist: the first ones count, and the call is told of
+    p.attn(q, blocks=(blocks[0], torch.full_like(blocks[1], 32)))
+    got = kvq.block8_attn(q.cuda(), p.c, blocks=(blocks[0], torch.full_like(blocks[1], 33)))
+    assert kvq.device_status() == kvq.KVQ_EDEVICE
+    assert torch.equal(got[0], b[0])
+
+
 # ------------------------------------------------------------------ eviction
 
 def test_evict(kvq):

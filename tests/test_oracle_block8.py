@@ -191,3 +191,13 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         kvq.make_block8_cache(1, 2, 1, 64, torch.float16, 64, block=20, device="cpu")
     with pytest.raises(TypeError, match="codes"):
         kvq.make_block8_cache(1, 2, 1, 64, torch.float16, 64, codes=torch.uint8, device="cpu")
+
+
+def test_workspace_of_lists_longer_than_the_table(L):
+    """A unit has no more than max_blocks blocks to list, so longer lists need no more room (room for lists of the table's
+    length is what a cache allocates)."""
+    c = ctypes.byref(_desc())
+    for acc in (0, 1):
+        need = L.block8_attn_workspace_bytes(c, 2, 8, acc)
+        assert need > L.block8_attn_workspace_bytes(c, 2, 7, acc) or not acc
+        assert L.block8_attn_workspace_bytes(c, 2, 9, acc) == L.block8_attn_workspace_bytes(c, 2, 1 << 20, acc) == need
