@@ -591,8 +591,10 @@ class Block8Cache:
     ``max_sel``: entries of a block list (the table's length by default).  ``ws``: a workspace
     tensor (uint8, ws_bytes(...) bytes) to share between caches whose calls never overlap on
     the GPU; one is allocated otherwise.  Calls on one cache must follow one another (one
-    stream, or events), also when they are replayed from CUDA graphs.  The calls hold the tensors'
-    addresses: write into the tensors, do not put others in their place."""
+    stream, or events), also when they are replayed from CUDA graphs.  The calls hold the tensors
+    themselves: write into them, others put in their place are not looked at.  A cache may be dropped
+    right after a call on any stream (its memory is not used again before the call is done), but not
+    before the graphs that captured its calls."""
     B: int
     Hq: int
     Hkv: int
@@ -649,6 +651,8 @@ class Block8Cache:
         self._ws, self._ws_bytes = self.ws.data_ptr() + shift, self.ws.numel() - shift
         if self._ws_bytes < need:
             _bad(f"ws must have {need + 256} bytes")
+        self._tensors = [getattr(self, name) for name, _ in KvqBlock8._fields_[9:]] + [self.ws]
+        self._streams = set()       # raw streams that the allocator knows to use the tensors
 
     @property
     def units(self):
@@ -698,10 +702,15 @@ def _stream8(cache, stream):
     if torch._C._cuda_getDevice() != cache._index:
         _bad(f"the cache is on cuda:{cache._index}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(cache._index)
-    if stream.device.index != cache._index:
-        _bad("the stream belongs to another device than the cache")
-    return stream.cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(cache._index)
+    else:
+        if stream.device.index != cache._index:
+            _bad("the stream belongs to another device than the cache")
+        raw = stream.cuda_stream
+    if raw not in cache._streams:   # once: when the cache is dropped, the allocator waits for all it knows
+        _used8(torch.cuda.current_stream(cache._index) if stream is None else stream, *cache._tensors)
+        cache._streams.add(raw)
+    return raw
 
 
 def _empty8(cache, shape, dtype, stream):

@@ -748,6 +748,33 @@ def test_other_streams(kvq):
         assert torch.equal(got[0], want[0])
 
 
+def test_cache_dropped_behind_a_call_on_another_stream(kvq):
+    """Its memory is not given out again while the call runs."""
+    p = _filled(kvq, seed=9)
+    names = ("k_codes", "v_codes", "k_scale", "v_scale", "k_bound", "bound_scale", "tail_k", "tail_v", "table", "count",
+             "seq_len", "block_pos", "acc", "ws")
+    sizes = [(getattr(p.c, x).data_ptr(), getattr(p.c, x).numel() * getattr(p.c, x).element_size()) for x in names]
+    q = p.rand(2, 8, 1, 128).cuda()
+    want = kvq.block8_attn(q, p.c)
+    count, p.c.count = p.c.count, torch.zeros_like(p.c.count)       # a tensor put in another's place changes nothing
+    assert count.data_ptr() == sizes[9][0]
+    s = torch.cuda.Stream()
+    new = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in sizes]      # memory that the allocator has ready below
+    del new
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1 << 27)                      # a bounded wait of some 60 ms
+    got = kvq.block8_attn(q, p.c, stream=s)
+    del p, count
+    new = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _, n in sizes]
+    assert not s.query()
+    for x in new:
+        for at, n in sizes:
+            assert x.data_ptr() + x.numel() <= at or at + n <= x.data_ptr()
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_binding_refusals(kvq):
     p = Pair(kvq, B=2, Hq=4, Hkv=2, max_tokens=64)
     z = lambda *s, dt=torch.float16: torch.zeros(s, dtype=dt, device="cuda")

@@ -201,3 +201,21 @@ def test_workspace_of_lists_longer_than_the_table(L):
         need = L.block8_attn_workspace_bytes(c, 2, 8, acc)
         assert need > L.block8_attn_workspace_bytes(c, 2, 7, acc) or not acc
         assert L.block8_attn_workspace_bytes(c, 2, 9, acc) == L.block8_attn_workspace_bytes(c, 2, 1 << 20, acc) == need
+
+
+def test_calls_keep_the_cache_for_the_streams_they_run_on(monkeypatch):
+    """The first call on a stream, given or torch's current one, tells the allocator that the stream uses the cache's
+    tensors and its workspace; otherwise a cache that is dropped behind a call would be overwritten under it."""
+    from types import SimpleNamespace as N
+    from bit_mixed_precision_gb300 import kvq
+    uses = []
+    cache = N(_index=0, _streams=set(), _tensors=[N(record_stream=lambda s, i=i: uses.append((i, s.cuda_stream))) for i in range(14)])
+    current = N(cuda_stream=5, device=N(index=0))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: current.cuda_stream, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda i: current)
+    for stream, raw in ((None, 5), (None, 5), (N(cuda_stream=9, device=N(index=0)), 9), (None, 5)):
+        assert kvq._stream8(cache, stream) == raw
+    assert uses == [(i, 5) for i in range(14)] + [(i, 9) for i in range(14)]
+    with pytest.raises(ValueError, match="another device"):
+        kvq._stream8(cache, N(cuda_stream=9, device=N(index=1)))
