@@ -571,7 +571,6 @@ def decode_attn_qkv_static(q, k_new, v_new, cache, sm_scale=None, o=None, lse=No
 
 # ----------------------------------------------------------- 8-bit block cache
 
-BLOCK8_MAX_Q, BLOCK8_MAX_GROUP = 16, 64
 CODE_E4M3, CODE_INT8 = 0, 1
 _CODES = {torch.float8_e4m3fn: CODE_E4M3, torch.int8: CODE_INT8}
 
