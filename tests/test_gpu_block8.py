@@ -407,6 +407,56 @@ def test_attn_value_scales_over_all_of_bf16(kvq, D, block, Hq, n_q, codes, room)
     p.attn(q, blocks=(idx, torch.full((6, 1, n_q), held, dtype=torch.int32, device="cuda")), accumulate=True)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("Hq,D,codes,n,room", [(1, 64, I8, 250, 256), (8, 128, F8, 250, 256), (12, 128, I8, 250, 256), (32, 64, F8, 250, 256),
+                                               (4, 128, I8, 2000, 2048), (16, 64, F8, 2000, 2048), (32, 128, I8, 2000, 2048)])
+def test_attn_weights_have_22_bits(kvq, Hq, D, codes, n, room, dtype):
+    """Two kinds of tokens, logit L with value 1 and logit 0 with value -1, in numbers that nearly cancel: the output is
+    small, so that its own rounding hides nothing, and an error of the weights shows beside sum p |v| = 1.
+
+    Only one channel of q and k is not 0, so a logit's products and their sum are exact.  It takes three float32 factors
+    (each within u of |s| < 2) and two additions of numbers below 16 (each within 2^-21): 2^-19.9 in the exponent, ln 2 of
+    that in the weight, 2^-22 of exp2, 2^-22 of the fp16 pair: the ratio of the two weights is within 2^-19, the output
+    moves by half of it.  The sums: at most 32 additions of a warp (2000 tokens in 125 cells, 2 products each, spread
+    over 8 warps at least, 250 in 16 cells over 4), cut instead of rounded: 2^-23 each of at most 1, 2^-18.  So 2^-17.
+    With weights of fp16 alone the ratio would be off by 2^-12.6 at least, as the test asserts of its numbers."""
+    n_a = n * 3 // 10
+    sigma = D ** -0.5
+    best = None
+    for x in torch.arange(2.0, 16.0, 1 / 32).to(dtype).unique().tolist():       # q's only channel
+        r = math.exp(-sigma * x)                        # weight of the second kind to the first's
+        off = abs(float(np.float16(128 * r)) / (128 * r) - 1)
+        o = (n_a - (n - n_a) * r) / (n_a + (n - n_a) * r)
+        if off > 2.0 ** -12.6 and (best is None or abs(o) < abs(best[1])):
+            best = x, o, off
+    x, o, off = best
+    assert abs(o) < 2.0 ** -5 and off / 2 > 4 * 2.0 ** -17
+    p = Pair(kvq, B=1, Hq=Hq, Hkv=1, D=D, block=16, codes=codes, dtype=dtype, max_tokens=room)
+    first = torch.zeros(n, dtype=torch.bool)
+    first[torch.randperm(n, generator=p.gen)[:n_a]] = True
+    k, v = torch.zeros((1, 1, n, D), dtype=dtype), torch.ones((1, 1, n, D), dtype=dtype)
+    k[0, 0, first, 5] = 1.0
+    v[0, 0, ~first] = -1.0
+    p.append(n, k=k, v=v)
+    q = torch.zeros((1, Hq, 1, D), dtype=dtype)
+    q[..., 5] = x
+    p.c.acc.zero_()
+    kd, vd = p.units[0].dequantised()
+    ro, rl, w = O8.attend(q[0, :, 0].float().numpy(), kd, vd, np.ones((Hq, n), bool), sigma)
+    for accumulate in (False, True):
+        got, lse = kvq.block8_attn(q.cuda(), p.c, accumulate=accumulate)
+        err = np.abs(got[0, :, 0].double().cpu().numpy() - ro)
+        assert (err <= 2.0 ** -17 + torch.finfo(dtype).eps / 2 * np.abs(ro)).all(), float(err.max())
+        # the exponent's error, 32 additions (u each), log2 of a sum below 2^18 and its addition to the reference (2^-20 each)
+        assert np.abs(lse[0, :, 0].double().cpu().numpy() - rl).max() <= 2.0 ** -17
+    # acc: log2 of a cell's weights and of the sum, each added to a reference (numbers below 32: 2^-20 a rounding, ln 2 of
+    # which counts), the sum's 32 additions and those of up to 32 heads (u each): 2^-17.3
+    acc = p.c.acc[p.c.table[0].long()].double().cpu().numpy()
+    want = np.zeros(-(-n // 16))
+    np.add.at(want, np.arange(n) // 16, w.sum(0))
+    assert (np.abs(acc[:len(want)] - want) <= 2.0 ** -17 * want).all()
+
+
 def test_attn_lists(kvq):
     B, Hq, Hkv, n_q, n_sel = 3, 6, 2, 2, 7
     for codes, block in ((F8, 16), (I8, 32), (F8, 128)):
