@@ -578,6 +578,108 @@ def test_attn_pool_beyond_32_bits(kvq):
     p.attn(q, blocks=(idx, m))
 
 
+class StoredUnit(O8.Unit):
+    """A unit known by its codes and scales."""
+
+    def __init__(self, D, block, kind, n, k, v):
+        super().__init__(D, block, kind)
+        self.n, self.rows, self.seq_len, self.blocks = n, [k, v], n, [O8.Block(0, D) for _ in range(-(-n // block))]
+
+    count = property(lambda self: self.n)
+
+    def dequantised(self):
+        return self.rows
+
+
+class Stored(Pair):
+    """A cache of lens[u] tokens whose codes, scales and bounds are random: many units without appending to each."""
+
+    def __init__(self, kvq, lens, Hq, Hkv, D, block, codes, dtype, max_tokens, seed=0, values=True, **kw):
+        B, dev = len(lens) // Hkv, "cuda"
+        self.kvq, self.B, self.Hq, self.Hkv, self.D, self.g = kvq, B, Hq, Hkv, D, Hq // Hkv
+        self.rng, self.gen = np.random.default_rng(seed), torch.Generator().manual_seed(seed)
+        self.c = c = kvq.make_block8_cache(B, Hq, Hkv, D, dtype, max_tokens, block=block, codes=codes, **kw)
+        gen, n = torch.Generator(dev).manual_seed(seed), c.table.numel()
+        c.table.copy_(torch.randperm(n, generator=gen, device=dev).to(torch.int32).view_as(c.table))
+        c.count.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.seq_len.copy_(c.count)
+        for x in (c.k_codes, c.v_codes):
+            if values:
+                y = torch.randn(x.shape, generator=gen, device=dev) * 40
+                x.view(torch.uint8).copy_((y.to(F8) if codes == F8 else y.round().clamp(-127, 127).to(I8)).view(torch.uint8))
+        for x in (c.k_scale, c.v_scale, c.bound_scale):
+            x.copy_(0.02 * torch.exp(0.3 * torch.randn(n, generator=gen, device=dev)))
+        c.k_bound.copy_(torch.randint(-127, 128, c.k_bound.shape, generator=gen, device=dev).sort(dim=1).values.to(I8))
+        table, cpu = c.table.cpu(), {}
+        for name in ("k", "v"):
+            cpu[name] = getattr(c, name + "_codes").view(torch.uint8).cpu().numpy(), getattr(c, name + "_scale").double().cpu().numpy()
+        self.units = []
+        for u, m in enumerate(lens):
+            ids = table[u, :-(-m // block)].numpy()
+            rows = [(O8.decode(x[ids], KIND[codes]) * s[ids, None, None]).reshape(-1, D)[:m] if values else None
+                    for x, s in cpu.values()]
+            self.units.append(StoredUnit(D, block, KIND[codes], m, *rows))
+
+
+def _stale(p, n_q, n_sel=0):
+    """NaN where the workspace holds partial outputs, and cells' weights with accumulate."""
+    c, g = p.c, p.g
+    rows, sets = (g, p.B * p.Hkv * n_q) if n_sel else (g * n_q, p.B * p.Hkv)
+    r = 8 if rows <= 8 else 16 if rows <= 16 else 32
+    works = sets * -(-rows // r)
+    at = -c.ws.data_ptr() % 256
+    mass = works * (min(n_sel, c.table.shape[1]) or c.table.shape[1]) * (c.block // 16) * r * 4
+    total = p.kvq.lib().block8_attn_workspace_bytes(c._ref, n_q, n_sel, 1)
+    c.ws[at:at + (1024 + works) * r * p.D * 4] = 0xFF
+    c.ws[at + total - (mass + 255) // 256 * 256:at + total] = 0xFF
+
+
+# (sequences, most tokens, heads, KV heads, queries, D, block, codes, dtype): more runs of tiles than CTAs fit the GPU, so that
+# CTAs come to several units, and units' first tiles stand behind 1 to 8 places without work
+MANY = [(150, 700, 16, 4, 1, 128, 32, F8, torch.bfloat16), (300, 3500, 2, 1, 1, 64, 64, I8, torch.float16),
+        (150, 700, 5, 5, 1, 128, 16, I8, torch.bfloat16), (200, 900, 24, 2, 1, 64, 128, F8, torch.float16),
+        (160, 600, 16, 2, 4, 128, 16, I8, torch.bfloat16), (170, 700, 40, 1, 1, 64, 32, F8, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("B,most,Hq,Hkv,n_q,D,block,codes,dtype", MANY)
+def test_attn_runs_over_many_units(kvq, B, most, Hq, Hkv, n_q, D, block, codes, dtype):
+    lens = np.random.default_rng(most).integers(0, most + 1, B * Hkv)
+    lens[::7], lens[3::50], lens[-4:] = 0, 1, (0, 0, most, 0)
+    p = Stored(kvq, [int(x) for x in lens], Hq, Hkv, D, block, codes, dtype, most, seed=B, max_q=n_q)
+    q = p.rand(B, Hq, n_q, D, outlier=False)
+    p.c.acc.zero_()
+    _stale(p, n_q)
+    a = p.attn(q, accumulate=True)
+    _stale(p, n_q)
+    b = p.attn(q)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    n_new = [int(x) for x in np.random.default_rng(B).integers(0, n_q + 1, B)]
+    p.attn(q, n_new=n_new, accumulate=True)
+
+
+@pytest.mark.parametrize("Hq,Hkv,n_q,D,block,codes,dtype", [(8, 2, 2, 64, 32, F8, torch.bfloat16), (12, 1, 1, 128, 64, I8, torch.float16),
+                                                            (20, 1, 3, 64, 16, F8, torch.float16)])
+def test_attn_lists_over_many_units(kvq, Hq, Hkv, n_q, D, block, codes, dtype):
+    B, n_sel = 320 // Hkv, {16: 40, 32: 24, 64: 12}[block]
+    lens = [int(x) for x in np.random.default_rng(D).integers(0, 40 * block, B * Hkv)]
+    lens[5] = lens[-1] = 0
+    p = Stored(kvq, lens, Hq, Hkv, D, block, codes, dtype, 40 * block, seed=Hq, max_q=n_q, max_sel=n_sel)
+    idx, n = np.full((B * Hkv, n_q, n_sel), -1, np.int32), np.zeros((B * Hkv, n_q), np.int32)
+    for u, m in enumerate(lens):
+        for t in range(n_q):
+            held = -(-m // block)
+            n[u, t] = int(p.rng.integers(0, min(n_sel, held) + 1)) if u % 9 else 0      # every ninth unit's lists are empty
+            idx[u, t, :n[u, t]] = p.rng.permutation(held)[:n[u, t]]
+    blocks = (torch.from_numpy(idx.reshape(B, Hkv, n_q, n_sel)).cuda(), torch.from_numpy(n.reshape(B, Hkv, n_q)).cuda())
+    q = p.rand(B, Hq, n_q, D, outlier=False)
+    p.c.acc.zero_()
+    _stale(p, n_q, n_sel)
+    a = p.attn(q, blocks=blocks, accumulate=True)
+    _stale(p, n_q, n_sel)
+    b = p.attn(q, blocks=blocks)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 # ------------------------------------------------------------------ selection
 
 def _check_select(p, q, n_sel, n_first, n_last, n_new=None):
