@@ -741,6 +741,67 @@ def test_lists_longer_than_the_table(kvq):
     assert torch.equal(got[0], b[0])
 
 
+def _scores(p, q, u, t, nb):
+    """float32 scores of unit u's first nb blocks for query t, from the bounds that the cache holds."""
+    if not hasattr(p, "bounds"):
+        p.bounds = p.c.k_bound.cpu().numpy().astype(np.int64), p.c.bound_scale.cpu().numpy(), p.c.table.cpu().numpy()
+    kb, sb, table = p.bounds
+    b, h = divmod(u, p.Hkv)
+    x = q[b, h * p.g:(h + 1) * p.g, t].float().numpy()
+    ids, best = table[u, :nb], None
+    for row in x:
+        s = O8.scale_of(row, 127.0)
+        q8 = np.clip(np.rint(row * (np.float32(1.0) / s)), -127, 127).astype(np.int64)
+        y = (kb[ids, 0] @ np.minimum(q8, 0) + kb[ids, 1] @ np.maximum(q8, 0)).astype(np.float32) * s
+        best = y if best is None else np.maximum(best, y)
+    return best * sb[ids]
+
+
+def _choose(score, n_sel, n_first, n_last):
+    """O8.choose for many blocks without NaN."""
+    n = len(score)
+    if n <= n_sel:
+        return np.arange(n)
+    order = np.argsort(-score[n_first:n - n_last], kind="stable")[:n_sel - n_first - n_last] + n_first
+    return np.sort(np.concatenate([np.arange(n_first), order, np.arange(n - n_last, n)]))
+
+
+def _check_stored_select(p, q, n_sel, n_first, n_last):
+    n_q = q.shape[2]
+    p.c.ws.fill_(0xFF)                                  # NaN scores would be chosen first
+    idx, n = p.kvq.block8_select(q.cuda(), p.c, n_sel, n_first, n_last)
+    gi, gn = idx.cpu().numpy(), n.cpu().numpy()
+    for u, unit in enumerate(p.units):
+        b, h = divmod(u, p.Hkv)
+        for t in range(n_q):
+            nb = -(-max(0, unit.count - n_q + t + 1) // unit.P)
+            want = _choose(_scores(p, q, u, t, nb), n_sel, n_first, n_last) if nb else np.zeros(0, int)
+            assert gn[b, h, t] == len(want), (u, t)
+            assert np.array_equal(gi[b, h, t, :len(want)], want) and (gi[b, h, t, len(want):] == -1).all(), (u, t)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,n_q,D,dtype", [(250, 24, 2, 2, 64, torch.float16), (600, 2, 2, 1, 128, torch.bfloat16)])
+def test_select_runs_over_many_units(kvq, B, Hq, Hkv, n_q, D, dtype):
+    """More runs of 64 blocks than CTAs fit the GPU: CTAs come to several queries, runs end inside one.  Units that are
+    empty or hold no more than n_sel blocks between the others."""
+    lens = np.random.default_rng(B).integers(0, 16 * 200 + 1, B * Hkv)
+    lens[::6], lens[4::31], lens[-3:] = 0, 16 * 8, (0, 3200, 0)
+    p = Stored(kvq, [int(x) for x in lens], Hq, Hkv, D, 16, I8, dtype, 3200, seed=D, values=False, max_q=n_q)
+    q = p.rand(B, Hq, n_q, D, outlier=False)
+    _check_stored_select(p, q, 8, 1, 1)
+    _check_stored_select(p, q, 100, 0, 3)
+
+
+def test_select_more_blocks_than_the_registers_hold(kvq):
+    """Above 8192 blocks the top-k reads the scores again in every pass."""
+    p = Stored(kvq, [16 * 9000 - 5, 16 * 8500, 0, 16 * 300], 4, 2, 64, 16, I8, torch.float16, 16 * 9000, values=False)
+    p.c.k_bound.copy_(p.c.k_bound // 64)                # many scores are equal
+    p.c.bound_scale.fill_(0.25)
+    q = p.rand(2, 4, 1, 64)
+    for n_sel, a, b in ((500, 1, 1), (1, 0, 0), (8999, 2, 3), (4000, 0, 4000), (8400, 0, 1)):
+        _check_stored_select(p, q, n_sel, a, b)
+
+
 # ------------------------------------------------------------------ eviction
 
 def test_evict(kvq):
