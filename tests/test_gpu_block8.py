@@ -852,6 +852,33 @@ def test_evict_many_blocks(kvq):
         assert sorted(p.c.table[u].tolist()) == sorted(table[u].tolist())
 
 
+@pytest.mark.parametrize("max_blocks", [12000, 51200])
+def test_evict_more_blocks_than_the_registers_hold(kvq, max_blocks):
+    """More than 8192 blocks, and table rows of more than 40 KB in shared memory, up to the most that is allowed."""
+    p = Pair(kvq, B=3, Hq=1, Hkv=1, D=64, max_tokens=16 * max_blocks)
+    for rnd, (keep, a, b) in enumerate((([max_blocks // 3, 9000, 5], 1, 1), ([8200, max_blocks - 1, 700], 300, 400), ([0, 1, 2], 40, 60))):
+        held = [max_blocks, max_blocks - 1, 8193]
+        p.c.count.copy_(torch.tensor([16 * max_blocks - 3, 16 * held[1], 16 * held[2] - 9], dtype=torch.int32))
+        before = p.c.count.tolist()
+        acc = torch.rand(p.c.acc.shape, generator=p.gen).round(decimals=3)          # ties
+        if rnd == 1:
+            acc[::1111] = float("nan")
+        p.c.acc.copy_(acc)
+        table, acc = p.c.table.cpu().numpy(), acc.numpy()
+        gone = p.kvq.block8_evict(p.c, torch.tensor(keep, dtype=torch.int32, device="cuda"), a, b).tolist()
+        now, count = p.c.table.cpu().numpy(), p.c.count.tolist()
+        for u in range(3):
+            n, want = held[u], max(keep[u], a + b)
+            if n <= want:
+                assert gone[u] == 0 and count[u] == before[u] and np.array_equal(now[u], table[u])
+                continue
+            score = acc[table[u, :n]]
+            kept = _choose(np.where(np.isnan(score), np.inf, score), want, a, b)
+            rest = np.setdiff1d(np.arange(n), kept)
+            assert gone[u] == n - want and count[u] == before[u] - 16 * (n - want)
+            assert np.array_equal(now[u], np.concatenate([table[u, kept], table[u, rest], table[u, n:]])), (rnd, u)
+
+
 # ------------------------------------------------------------------ as they are used
 
 def test_decode_with_eviction_and_selection(kvq):
