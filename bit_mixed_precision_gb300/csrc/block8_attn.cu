@@ -30,10 +30,11 @@
 // Small caches (kDirectCells) take one CTA per work unit and no second kernel.
 //
 // Bound by HBM: 2 D bytes per token and KV head against 4 D g flop.  512 units of 32768 tokens, D 128,
-// four heads, e4m3, weights accumulated: 673 us, 0.94 of the measured 6.79 TB/s; 256 ragged units of up
+// four heads, e4m3, weights accumulated: 678 us, 0.93 of the measured 6.79 TB/s; 256 ragged units of up
 // to 8192, five heads, int8: 55 us, 0.78 (5 us go before the first tile, int8 codes take 380 warp
 // instructions per 16 tokens).  With 32 rows the tensor cores' share is larger than HBM's: 64 units of up
-// to 20011 tokens 86 us, 0.41, behind fixed-latency waits of two warps per scheduler.
+// to 20011 tokens 88 us, 0.40, behind fixed-latency waits of two warps per scheduler.  With D 128 the
+// variants of up to 16 rows use 168 registers, those of 32 rows 255, and spill up to 60 bytes.
 #include <algorithm>
 #include <type_traits>
 
@@ -62,6 +63,8 @@ constexpr float kShift = 7.0f, kLift = 15.0f, kNone = -1.0e38f;
 // more than kFar takes the part of the lower ones in the denominator from a second exponential without
 // log2 v (with kBias more: the largest value scale alone puts the denominator at 2^-114), beside the
 // rare moves of the reference; and a reference that far below another lowers its denominator in two steps.
+// It costs bf16 1 to 2 % (512 units of 32768 tokens 670 -> 678 us, 32 rows 86.1 -> 88.1, 32 units of up to
+// 64 tokens 7.2 -> 7.6); tested in the loop for every tile, 32 rows took 90.5.
 constexpr float kFar = 80.0f, kBias = 24.0f, kBiasInv = 1.0f / 16777216.0f;
 template <typename T> constexpr bool kWide = std::is_same<T, __nv_bfloat16>::value;
 

@@ -81,7 +81,7 @@ __device__ __forceinline__ uint32_t rank_key(float f) {
 // up.  Starting on a unit costs a CTA the time of about eight tiles (counters, table, first tile).  So
 //  - where the grid has a CTA for every `least` tiles of every unit, a unit's tiles are filled up to a
 //    multiple of `least` places and a run is `least` places: no CTA comes to a second unit (32 ragged
-//    units of up to 64 tokens 14.6 -> 7.5 us);
+//    units of up to 64 tokens 14.6 -> 7.1 us);
 //  - else a unit's first tile stands behind `start` places without work, at most a quarter of a CTA's
 //    tiles (attn of 32 units of 4096 tokens 15.2 -> 13.4 us, ragged 256 units 58 -> 56).
 template <int LEAST>

@@ -587,7 +587,8 @@ class Block8Cache:
     Built from the caller's own tensors, or by make_block8_cache.  ``table`` [B*Hkv, max_blocks]
     gives the pool block of each unit's logical block; the entries must be distinct.  ``max_q``:
     queries per sequence that the workspace allows for in one block8_attn / block8_select call;
-    ``max_sel``: entries of a block list (the table's length by default).  ``ws``: a workspace
+    ``max_sel``: entries of a block list (the table's length by default; set it where max_q is large,
+    or the workspace is).  ``ws``: a workspace
     tensor (uint8, ws_bytes(...) bytes) to share between caches whose calls never overlap on
     the GPU; one is allocated otherwise.  Calls on one cache must follow one another (one
     stream, or events), also when they are replayed from CUDA graphs.  The calls hold the tensors

@@ -420,7 +420,9 @@ typedef struct {
     int32_t* table;             /* (device) [u][max_blocks] */
     int32_t* count;             /* (device) [u] tokens held */
     int32_t* seq_len;           /* (device) [u] position of the next token */
-    int32_t* block_pos;         /* (device) [n_blocks] position of the block's first token */
+    int32_t* block_pos;         /* (device) [n_blocks] position of the block's first token: written by
+                                   block8_append, read by no call; with it a caller finds the
+                                   positions that a unit still holds after block8_evict */
     float* acc;                 /* (device) [n_blocks] attention weight received */
 } kvq_block8;
 
@@ -452,7 +454,7 @@ kvq_status block8_append(kvq_block8* c, const void* k, const int64_t* k_strides,
  * cache (append first): query t of sequence b with m = n_new[b] queries sees
  * the first count[u] - m + t + 1 tokens of its unit.
  *   q (device) [B, Hq, n_q, D], 1 <= n_q <= KVQ_BLOCK8_MAX_Q; query head h
- *   reads KV head h / (Hq/Hkv).
+ *   reads KV head h / (Hq/Hkv).  sm_scale > 0.
  *   blocks (device, nullable) [B, Hkv, n_q, n_sel] logical block numbers and
  *   list_len (device) [B, Hkv, n_q] how many of them count, at most n_sel and
  *   max_blocks (clamped and reported as KVQ_EDEVICE): query t then sees only
@@ -468,7 +470,9 @@ kvq_status block8_append(kvq_block8* c, const void* k, const int64_t* k_strides,
  *   the second product times its block's value scale, as a pair of fp16
  *   numbers: 22 bits, and nothing finer than 2^-32 of the row's largest such
  *   product.  The denominator (o, lse, acc) holds for all value scales that
- *   the cache can have.  acc: a block's share is exp2 of a difference of two
+ *   the cache can have.  Logits are float32: where a query's largest element
+ *   times a block's largest key element times sm_scale passes 2^120, a result
+ *   may be NaN.  acc: a block's share is exp2 of a difference of two
  *   float32 logarithms, so that its error grows with their size (2^-22 of it).
  *   ws (device) of at least block8_attn_workspace_bytes(), 256-byte aligned;
  *   its content between calls is irrelevant. */
