@@ -594,7 +594,7 @@ class StoredUnit(O8.Unit):
 class Stored(Pair):
     """A cache of lens[u] tokens whose codes, scales and bounds are random: many units without appending to each."""
 
-    def __init__(self, kvq, lens, Hq, Hkv, D, block, codes, dtype, max_tokens, seed=0, values=True, **kw):
+    def __init__(self, kvq, lens, Hq, Hkv, D, block, codes, dtype, max_tokens, seed=0, values=True, v_power=None, **kw):
         B, dev = len(lens) // Hkv, "cuda"
         self.kvq, self.B, self.Hq, self.Hkv, self.D, self.g = kvq, B, Hq, Hkv, D, Hq // Hkv
         self.rng, self.gen = np.random.default_rng(seed), torch.Generator().manual_seed(seed)
@@ -609,6 +609,8 @@ class Stored(Pair):
                 x.view(torch.uint8).copy_((y.to(F8) if codes == F8 else y.round().clamp(-127, 127).to(I8)).view(torch.uint8))
         for x in (c.k_scale, c.v_scale, c.bound_scale):
             x.copy_(0.02 * torch.exp(0.3 * torch.randn(n, generator=gen, device=dev)))
+        if v_power is not None:                         # log2 of the value scales [unit, logical block]
+            c.v_scale[c.table.long()] = torch.exp2(v_power).cuda()
         c.k_bound.copy_(torch.randint(-127, 128, c.k_bound.shape, generator=gen, device=dev).sort(dim=1).values.to(I8))
         table, cpu = c.table.cpu(), {}
         for name in ("k", "v"):
@@ -677,6 +679,23 @@ def test_attn_lists_over_many_units(kvq, Hq, Hkv, n_q, D, block, codes, dtype):
     a = p.attn(q, blocks=blocks, accumulate=True)
     _stale(p, n_q, n_sel)
     b = p.attn(q, blocks=blocks)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,codes", [(8, 2, 128, F8), (12, 1, 64, I8), (32, 1, 128, I8)])
+def test_attn_runs_over_many_units_of_far_apart_value_scales(kvq, Hq, Hkv, D, codes):
+    """CTAs come from units whose value scales span 2^170 to units whose scales do not, and back."""
+    B = 480 // Hkv
+    lens = [int(x) for x in np.random.default_rng(D).integers(0, 1001, B * Hkv)]
+    gen = torch.Generator().manual_seed(D)
+    power = torch.tensor([-64.0, -30.0, 0.0, 40.0, 100.0, 105.0])[torch.randint(0, 6, (B * Hkv, 32), generator=gen)]
+    power[::3] = 0.0                                    # every third unit as usual
+    p = Stored(kvq, lens, Hq, Hkv, D, 32, codes, torch.bfloat16, 1000, seed=Hq, v_power=power)
+    p.c.acc.zero_()
+    _stale(p, 1)
+    x = p.rand(B, Hq, 1, D, outlier=False)
+    a = p.attn(x, accumulate=True)
+    b = p.attn(x)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
@@ -967,6 +986,34 @@ def test_graph_replay_and_shared_workspace(kvq):
             for name in ("count", "table", "acc", "k_scale"):
                 y, z = getattr(caches[i], name), getattr(x.c, name)
                 assert torch.equal(y.nan_to_num(), z.nan_to_num()), name
+
+
+def test_first_calls_inside_a_capture(kvq):
+    """Nothing of a cache has run before, on the capture's stream or any other."""
+    p, twin = Pair(kvq, B=2, Hq=8, Hkv=2, max_tokens=640, seed=3), Pair(kvq, B=2, Hq=8, Hkv=2, max_tokens=640, seed=3)
+    k, v, q = (p.rand(2, h, n, 128).cuda() for h, n in ((2, 300), (2, 300), (8, 1)))
+    keep = torch.full((4,), 9, dtype=torch.int32, device="cuda")
+
+    def calls(c):
+        kvq.block8_reset(c)
+        kvq.block8_append(c, k, v)
+        o = kvq.block8_attn(q, c, accumulate=True)
+        blocks = kvq.block8_select(q, c, 5)
+        return *o, *blocks, *kvq.block8_attn(q, c, blocks=blocks), kvq.block8_evict(c, keep)
+
+    table = p.c.table.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = calls(p.c)
+    want = calls(twin.c)
+    for _ in range(2):
+        p.c.table.copy_(table)
+        g.replay()
+        torch.cuda.synchronize()
+        for y, z in zip(got, want):
+            assert torch.equal(y, z)
+    del g, got, p                                       # the graph first, then the cache that it wrote to
 
 
 def test_other_streams(kvq):
