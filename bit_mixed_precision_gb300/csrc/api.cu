@@ -509,6 +509,105 @@ kvq_status block8_evict(kvq_block8* c, const int32_t* keep, int n_first, int n_l
                        "block8_evict launch");
 }
 
+// ---------------------------------------------------------------- norm and rotation per head
+
+static kvq_status check_rope(const kvq_rope* r, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D, float eps,
+                             const char* who) {
+    KVQ_REQUIRE(r, KVQ_EINVAL, "%s: null rope", who);
+    KVQ_REQUIRE(dt == KVQ_F16 || dt == KVQ_BF16, KVQ_EINVAL, "%s: dtype must be f16 or bf16", who);
+    KVQ_REQUIRE(B >= 0 && T >= 0 && Hq > 0 && Hkv > 0 && Hq % Hkv == 0, KVQ_EINVAL, "%s: bad B/T/Hq/Hkv", who);
+    KVQ_REQUIRE(D == 64 || D == 128, KVQ_EUNSUPPORTED, "%s: head dim %d unsupported (64 or 128)", who, D);
+    KVQ_REQUIRE(Hq <= (1 << 20) && (long long)B * T <= (1LL << 30), KVQ_EUNSUPPORTED, "%s: too large", who);
+    KVQ_REQUIRE(r->rot >= 0 && r->rot <= D && r->rot % 16 == 0, KVQ_EINVAL,
+                "%s: rot = %d must be a multiple of 16 in [0, D]", who, r->rot);
+    KVQ_REQUIRE(r->interleaved == 0 || r->interleaved == 1, KVQ_EINVAL, "%s: interleaved must be 0 or 1", who);
+    KVQ_REQUIRE(r->n_axes >= 1 && r->n_axes <= KVQ_ROPE_MAX_AXES, KVQ_EINVAL, "%s: n_axes must be 1 to %d", who,
+                KVQ_ROPE_MAX_AXES);
+    for (int i = 0; i < r->rot / 2; ++i)
+        KVQ_REQUIRE(r->axis[i] < r->n_axes, KVQ_EINVAL, "%s: pair %d has axis %d of %d", who, i, r->axis[i], r->n_axes);
+    KVQ_REQUIRE(eps >= 0.0f && eps < 1e30f, KVQ_EINVAL, "%s: eps must be >= 0 and finite", who);
+    return KVQ_OK;
+}
+
+// Strides {b, t, head} of rows [B, T, H, D].
+static kvq_status head_strides(const void* x, const int64_t* given, int T, int H, int D, const char* who, int64_t* out) {
+    KVQ_REQUIRE(x, KVQ_EINVAL, "%s: null pointer", who);
+    KVQ_REQUIRE(aligned(x, 16), KVQ_EINVAL, "%s: activations must be 16-byte aligned", who);
+    const int64_t dense[3] = {(int64_t)T * H * D, (int64_t)H * D, D};
+    for (int i = 0; i < 3; ++i) {
+        out[i] = given ? given[i] : dense[i];
+        KVQ_REQUIRE(out[i] >= 0 && out[i] % 8 == 0, KVQ_EINVAL, "%s: strides must be >= 0 and multiples of 8 elements",
+                    who);
+    }
+    return KVQ_OK;
+}
+
+kvq_status qk_norm_rope(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D, const void* q,
+                        const void* k, const void* v, const int64_t* strides, const int32_t* pos, const void* q_weight,
+                        const void* k_weight, int weight_f32, float eps, void* q_out, void* k_out, void* v_out,
+                        void* stream) {
+    const char* who = "qk_norm_rope";
+    kvq_status st = check_rope(rope, dt, B, T, Hq, Hkv, D, eps, who);
+    if (st != KVQ_OK || B == 0 || T == 0) return st;
+    kvq::RopeCall c = {};
+    c.rope = rope, c.dt = dt, c.B = B, c.T = T, c.Hq = Hq, c.Hkv = Hkv, c.D = D, c.q = q, c.k = k, c.v = v;
+    c.pos = pos, c.qw = q_weight, c.kw = k_weight, c.w_f32 = weight_f32 != 0, c.eps = eps;
+    c.qo = q_out, c.ko = k_out, c.vo = v_out;
+    if ((st = head_strides(q, strides, T, Hq, D, who, c.strides[0])) != KVQ_OK) return st;
+    if ((st = head_strides(k, strides ? strides + 3 : nullptr, T, Hkv, D, who, c.strides[1])) != KVQ_OK) return st;
+    if (v && (st = head_strides(v, strides ? strides + 6 : nullptr, T, Hkv, D, who, c.strides[2])) != KVQ_OK) return st;
+    KVQ_REQUIRE(q_out && k_out && (v_out || !v) && (pos || rope->rot == 0), KVQ_EINVAL, "%s: null pointer", who);
+    KVQ_REQUIRE(aligned(q_out, 16) && aligned(k_out, 16) && aligned(v_out, 16) && aligned(q_weight, 16) &&
+                    aligned(k_weight, 16) && aligned(pos, 4),
+                KVQ_EINVAL, "%s: misaligned pointer", who);
+    return cuda_status(kvq::launch_rope(c, (cudaStream_t)stream), "qk_norm_rope launch");
+}
+
+size_t qk_norm_rope_bwd_workspace_bytes(int B, int T, int D, int norm) {
+    if (B < 0 || T < 0 || (D != 64 && D != 128)) {
+        set_error("qk_norm_rope_bwd_workspace_bytes: bad sizes");
+        return (size_t)-1;
+    }
+    return norm ? (size_t)kvq::rope_bwd_ctas(B, T) * 2 * D * sizeof(float) : 0;
+}
+
+kvq_status qk_norm_rope_bwd(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D, const void* dq,
+                            const void* dk, const void* dv, const void* q, const void* k, const int64_t* strides,
+                            const int32_t* pos, const void* q_weight, const void* k_weight, int weight_f32, float eps,
+                            void* gq, void* gk, void* gv, const int64_t* g_strides, float* gq_weight, float* gk_weight,
+                            void* ws, size_t ws_bytes, void* stream) {
+    const char* who = "qk_norm_rope_bwd";
+    kvq_status st = check_rope(rope, dt, B, T, Hq, Hkv, D, eps, who);
+    if (st != KVQ_OK) return st;
+    KVQ_REQUIRE((gq_weight || !q_weight) && (gk_weight || !k_weight), KVQ_EINVAL, "%s: null weight gradient", who);
+    KVQ_REQUIRE(aligned(gq_weight, 4) && aligned(gk_weight, 4), KVQ_EINVAL, "%s: misaligned pointer", who);
+    if (B == 0 || T == 0) {         // sums of nothing
+        cudaError_t e = q_weight ? cudaMemsetAsync(gq_weight, 0, D * sizeof(float), (cudaStream_t)stream) : cudaSuccess;
+        if (e == cudaSuccess && k_weight) e = cudaMemsetAsync(gk_weight, 0, D * sizeof(float), (cudaStream_t)stream);
+        return cuda_status(e, who);
+    }
+    kvq::RopeCall c = {};
+    c.rope = rope, c.dt = dt, c.B = B, c.T = T, c.Hq = Hq, c.Hkv = Hkv, c.D = D;
+    c.q = q_weight ? q : nullptr, c.k = k_weight ? k : nullptr;
+    c.pos = pos, c.qw = q_weight, c.kw = k_weight, c.w_f32 = weight_f32 != 0, c.eps = eps;
+    c.qo = const_cast<void*>(dq), c.ko = const_cast<void*>(dk), c.vo = const_cast<void*>(dv);
+    c.gq = gq, c.gk = gk, c.gv = gv, c.gqw = gq_weight, c.gkw = gk_weight, c.ws = ws;
+    if (q_weight && (st = head_strides(q, strides, T, Hq, D, who, c.strides[0])) != KVQ_OK) return st;
+    if (k_weight && (st = head_strides(k, strides ? strides + 3 : nullptr, T, Hkv, D, who, c.strides[1])) != KVQ_OK)
+        return st;
+    if ((st = head_strides(gq, g_strides, T, Hq, D, who, c.gstrides[0])) != KVQ_OK) return st;
+    if ((st = head_strides(gk, g_strides ? g_strides + 3 : nullptr, T, Hkv, D, who, c.gstrides[1])) != KVQ_OK) return st;
+    if (dv && (st = head_strides(gv, g_strides ? g_strides + 6 : nullptr, T, Hkv, D, who, c.gstrides[2])) != KVQ_OK)
+        return st;
+    KVQ_REQUIRE(dq && dk && (pos || rope->rot == 0), KVQ_EINVAL, "%s: null pointer", who);
+    KVQ_REQUIRE(aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16) && aligned(q_weight, 16) && aligned(k_weight, 16) &&
+                    aligned(pos, 4),
+                KVQ_EINVAL, "%s: misaligned pointer", who);
+    st = check_ws(ws, ws_bytes, qk_norm_rope_bwd_workspace_bytes(B, T, D, q_weight || k_weight), who);
+    if (st != KVQ_OK) return st;
+    return cuda_status(kvq::launch_rope_bwd(c, (cudaStream_t)stream), "qk_norm_rope_bwd launch");
+}
+
 size_t kvq_tier_bytes(int units, int D, int G, int k_bits, int v_bits, int k_axis, int cap,
                       size_t out[8]) {
     if (units <= 0 || D <= 0 || !valid_group(G) || D % G || !valid_bits(k_bits) || !valid_bits(v_bits) || cap < 0)

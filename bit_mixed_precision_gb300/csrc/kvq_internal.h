@@ -70,4 +70,24 @@ cudaError_t launch_block8_select(const void* q, const int64_t* qs, int n_q, cons
 cudaError_t launch_block8_evict(const kvq_block8& c, const int32_t* keep, int n_first, int n_last, int32_t* n_evicted,
                                 cudaStream_t s);
 
+// Per-head norm and rotation, and its gradient (arguments validated by the caller).
+struct RopeCall {
+    const kvq_rope* rope;
+    int dt, B, T, Hq, Hkv, D;
+    const void *q, *k, *v;          // raw rows [B, T, heads, D]; v NULL: none
+    int64_t strides[3][3];
+    const int32_t* pos;
+    const void *qw, *kw;
+    int w_f32;
+    float eps;
+    void *qo, *ko, *vo;             // [B, heads, T, D]: outputs; backward: the gradients that come in
+    void *gq, *gk, *gv;             // backward: [B, T, heads, D]
+    int64_t gstrides[3][3];
+    float *gqw, *gkw;
+    void* ws;
+};
+cudaError_t launch_rope(const RopeCall& c, cudaStream_t s);
+cudaError_t launch_rope_bwd(const RopeCall& c, cudaStream_t s);
+int rope_bwd_ctas(int B, int T);
+
 }  // namespace kvq

@@ -29,6 +29,7 @@ EXPORTS = ["kv_quant_pack", "prefill_attn_scores", "prefill_window_scores", "kvq
            "kvq_pages_init", "kvq_pages_release",
            "block8_reset", "block8_append", "block8_attn", "block8_attn_workspace_bytes", "block8_select",
            "block8_select_workspace_bytes", "block8_evict",
+           "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
            "kvq_decode_workspace_bytes", "kvq_decode_launches", "kvq_tier_bytes",
            "kvq_last_error", "kvq_device_status", "kvq_debug_withhold_copy", "kvq_version"]
 
@@ -84,6 +85,11 @@ class KvqBlock8(ctypes.Structure):
                 ("acc", ctypes.c_void_p)]
 
 
+class KvqRope(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 64), ("turn", ctypes.c_uint64 * 64)]
+
+
 _lib = None
 
 
@@ -124,6 +130,13 @@ def lib():
         L.block8_select_workspace_bytes.argtypes = [cache8, i32]
         L.block8_select_workspace_bytes.restype = sz
         L.block8_evict.argtypes = [cache8, vp, i32, i32, vp, vp]
+        rope = ctypes.POINTER(KvqRope)
+        L.qk_norm_rope.argtypes = [rope, i32, i32, i32, i32, i32, i32, vp, vp, vp, strides, vp, vp, vp, i32, f32, vp, vp,
+                                   vp, vp]
+        L.qk_norm_rope_bwd.argtypes = [rope, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, strides, vp, vp, vp, i32,
+                                       f32, vp, vp, vp, strides, vp, vp, vp, sz, vp]
+        L.qk_norm_rope_bwd_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.qk_norm_rope_bwd_workspace_bytes.restype = sz
         L.kvq_tier_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
         L.kvq_tier_bytes.restype = sz
         L.kvq_last_error.restype = ctypes.c_char_p
@@ -131,7 +144,8 @@ def lib():
         L.kvq_debug_withhold_copy.argtypes = [i32]
         for name in ["kv_quant_pack", "prefill_attn_scores", "prefill_window_scores", "kvq_score_reduce", "select_tokens",
                      "minikv_prefill_build", "requant_demote", "kvq_pages_init", "kvq_pages_release", "decode_attn_qkv", "kvq_device_status", "kvq_debug_withhold_copy",
-                     "block8_reset", "block8_append", "block8_attn", "block8_select", "block8_evict"]:
+                     "block8_reset", "block8_append", "block8_attn", "block8_select", "block8_evict",
+                     "qk_norm_rope", "qk_norm_rope_bwd"]:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -839,3 +853,188 @@ def block8_evict(cache, keep, n_first=1, n_last=1, n_evicted=None, stream=None):
     if stream is not None:
         _used8(stream, keep, n_evicted)
     return n_evicted
+
+
+# ----------------------------------------------------------- norm and rotation per head
+
+@dataclass
+class Rope:
+    """How queries and keys of D channels turn with their positions (see kvq_rope in kvq.h).  Holds no
+    device memory: one for all layers, devices and streams."""
+    D: int
+    desc: KvqRope = field(repr=False)
+
+    def __post_init__(self):
+        self._ref = ctypes.byref(self.desc)
+
+
+def make_rope(D, rot=None, base=10000.0, inv_freq=None, axis=None, interleaved=False):
+    """A Rope of the first ``rot`` channels (all by default; a multiple of 16): pair i of them turns by
+    pos * inv_freq[i] radians, inv_freq[i] = base ** (-2 i / rot) by default (floats, or a float64 tensor, which is
+    read on the host).  ``axis``: each pair's position axis (0 to 3; 0 by default).  Pairs are the
+    channels (i, i + rot / 2), or (2 i, 2 i + 1) if ``interleaved``."""
+    if rot is None:
+        rot = D if inv_freq is None else 2 * len(inv_freq)
+    if D not in (64, 128) or rot % 16 or not 0 <= rot <= D:
+        _bad("D must be 64 or 128, rot a multiple of 16 in [0, D]")
+    n = rot // 2
+    f = [base ** (-i / n) for i in range(n)] if inv_freq is None else [float(x) for x in inv_freq]
+    axis = [0] * n if axis is None else [int(x) for x in axis]
+    if len(f) != n or len(axis) != n:
+        _bad(f"inv_freq and axis must have {n} entries")
+    if not all(math.isfinite(x) for x in f) or not all(0 <= x < 4 for x in axis):
+        _bad("inv_freq must be finite, axis in 0 .. 3")
+    d = KvqRope(rot, 1 if interleaved else 0, max(axis, default=0) + 1)
+    for i in range(n):
+        d.axis[i] = axis[i]
+        d.turn[i] = int(round(math.ldexp(math.fmod(f[i] / (2.0 * math.pi), 1.0), 64))) % (1 << 64)
+    return Rope(D, d)
+
+
+def _call_stream(index, stream):
+    """The raw stream of a call on tensors of device `index`, which has to be the current one."""
+    if torch._C._cuda_getDevice() != index:
+        _bad(f"the tensors are on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        _bad("the stream belongs to another device than the tensors")
+    return stream.cuda_stream
+
+
+def _new(shape, like, dtype, stream):
+    """An output or workspace, allocated on the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _heads(x, shape, like, name):
+    """Rows of x, [B, T, H, D] or for a step [B, H, D], D contiguous: pointer and strides {b, t, head}."""
+    if tuple(x.shape) != shape or x.dtype != like.dtype or x.get_device() != like.get_device() or not x.is_cuda:
+        _bad(f"{name} must be a CUDA tensor {list(shape)} of {like.dtype} on q's device, got {list(x.shape)} of {x.dtype}")
+    st = x.stride()
+    if st[-1] != 1:
+        _bad(f"{name}: the last axis must be contiguous")
+    st = [s if n > 1 else 0 for n, s in zip(shape, st)]
+    return x.data_ptr(), (st[0], 0 if len(shape) == 3 else st[1], st[-2])
+
+
+def _dense(x, shape, like, name, dtype=None):
+    """The pointer of a contiguous tensor, or None."""
+    if x is None:
+        return None
+    if tuple(x.shape) != tuple(shape) or x.dtype != (dtype or like.dtype) or not x.is_contiguous() or \
+            not x.is_cuda or x.get_device() != like.get_device():
+        _bad(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype or like.dtype} on q's device")
+    return x.data_ptr()
+
+
+def _rope_call(q, k, pos, rope, q_weight, k_weight):
+    """Sizes, position pointer and weights that both directions check alike; q and k raw rows."""
+    if q.dim() not in (3, 4) or k.dim() != q.dim():
+        _bad("q and k must be [B, T, heads, D], for a step [B, heads, D]")
+    if q.shape[-1] != rope.D:
+        _bad(f"the rope is for {rope.D} channels, q has {q.shape[-1]}")
+    step = q.dim() == 3
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    T, Hkv = 1 if step else q.shape[1], k.shape[-2]
+    if Hkv == 0 or Hq % Hkv:
+        _bad("Hq must be a multiple of Hkv")
+    axes, tokens = rope.desc.n_axes, (B,) if step else (B, T)
+    if tuple(pos.shape) != (axes,) + tokens and (axes > 1 or tuple(pos.shape) != tokens):
+        _bad(f"pos must be [{axes}, {', '.join(map(str, tokens))}], got {list(pos.shape)}")
+    pp = _dense(pos, pos.shape, q, "pos", torch.int32)
+    f32 = [w.dtype == torch.float32 for w in (q_weight, k_weight) if w is not None]
+    if any(f32) and not all(f32):
+        raise TypeError("q_weight and k_weight must share one dtype")
+    wdt = torch.float32 if any(f32) else q.dtype
+    return step, B, T, Hq, Hkv, D, pp, _dense(q_weight, (D,), q, "q_weight", wdt), \
+        _dense(k_weight, (D,), q, "k_weight", wdt), 1 if any(f32) else 0
+
+
+def qk_norm_rope(q, k, v, pos, rope, q_weight=None, k_weight=None, eps=1e-6, out=None, stream=None):
+    """From a projection to attention: q [B, T, Hq, D], k, v [B, T, Hkv, D] (views of one projection, any strides;
+    for a step [B, heads, D]; v may be None) to (q, k, v) [B, heads, T, D] ([B, heads, D]), q and k RMS-normed per
+    head (q_weight, k_weight [D]; None: no norm) and turned by pos (int32 [B, T], with several axes [axes, B, T];
+    for a step without T)."""
+    dt = _dt(q)
+    step, B, T, Hq, Hkv, D, pp, qw, kw, f32 = _rope_call(q, k, pos, rope, q_weight, k_weight)
+    rows = (B,) if step else (B, T)
+    qp, qs = _heads(q, rows + (Hq, D), q, "q")
+    kp, ks = _heads(k, rows + (Hkv, D), q, "k")
+    vp, vs = _heads(v, rows + (Hkv, D), q, "v") if v is not None else (None, (0, 0, 0))
+    raw = _call_stream(q.get_device(), stream)
+    shapes = [(B, h, D) if step else (B, h, T, D) for h in (Hq, Hkv)]
+    if out is None:
+        qo, ko = _new(shapes[0], q, q.dtype, stream), _new(shapes[1], q, q.dtype, stream)
+        vo = _new(shapes[1], q, q.dtype, stream) if v is not None else None
+    else:
+        qo, ko, vo = out
+        if (vo is None) != (v is None):
+            _bad("out must have a v where there is one")
+    _check(lib().qk_norm_rope(rope._ref, dt, B, T, Hq, Hkv, D, qp, kp, vp, (ctypes.c_int64 * 9)(*qs, *ks, *vs), pp, qw,
+                              kw, f32, float(eps), _dense(qo, shapes[0], q, "out[0]"), _dense(ko, shapes[1], q, "out[1]"),
+                              _dense(vo, shapes[1], q, "out[2]"), raw))
+    if stream is not None:
+        _used8(stream, q, k, v, pos, q_weight, k_weight, qo, ko, vo)
+    return qo, ko, vo
+
+
+def qk_norm_rope_bwd(dq, dk, dv, q, k, pos, rope, q_weight=None, k_weight=None, eps=1e-6, out=None, ws=None,
+                     stream=None):
+    """The gradient of qk_norm_rope: dq, dk, dv are those of its outputs (dv may be None), the others its arguments.
+    Returns (gq, gk, gv, gq_weight, gk_weight), the first three [B, T, heads, D] as views of one [B, T, Hq + 2 Hkv, D]
+    (or as given in out[:3], any strides), the last two float32 [D] (None without that norm).  ws: a uint8 workspace
+    of qk_norm_rope_bwd_ws_bytes(q) + 256 bytes to share between calls that never overlap on the GPU."""
+    dt = _dt(q)
+    step, B, T, Hq, Hkv, D, pp, qw, kw, f32 = _rope_call(q, k, pos, rope, q_weight, k_weight)
+    rows, like = (B,) if step else (B, T), q
+    qp, qs = _heads(q, rows + (Hq, D), q, "q")
+    kp, ks = _heads(k, rows + (Hkv, D), q, "k")
+    raw = _call_stream(q.get_device(), stream)
+    shapes = [(B, h, D) if step else (B, h, T, D) for h in (Hq, Hkv)]
+    grads = [_dense(x, s, q, n) for x, s, n in ((dq, shapes[0], "dq"), (dk, shapes[1], "dk"), (dv, shapes[1], "dv"))]
+    if grads[0] is None or grads[1] is None:
+        _bad("dq and dk are needed")
+    if out is None:
+        both = _new(rows + (Hq + (2 if dv is not None else 1) * Hkv, D), q, q.dtype, stream)
+        gq, gk = both[..., :Hq, :], both[..., Hq:Hq + Hkv, :]
+        gv = both[..., Hq + Hkv:, :] if dv is not None else None
+        gqw, gkw = (None if w is None else _new((D,), q, torch.float32, stream) for w in (q_weight, k_weight))
+    else:
+        gq, gk, gv, gqw, gkw = out
+        if any((a is None) != (b is None) for a, b in ((gv, dv), (gqw, q_weight), (gkw, k_weight))):
+            _bad("out must have a gradient for each of dv, q_weight and k_weight that is there, and for no other")
+    gqp, gqs = _heads(gq, rows + (Hq, D), q, "out[0]")
+    gkp, gks = _heads(gk, rows + (Hkv, D), q, "out[1]")
+    gvp, gvs = _heads(gv, rows + (Hkv, D), q, "out[2]") if gv is not None else (None, (0, 0, 0))
+    wsp, ws_bytes, ws = _workspace(lib().qk_norm_rope_bwd_workspace_bytes(B, T, D, 1 if qw or kw else 0), like, ws, stream)
+    i9 = ctypes.c_int64 * 9
+    _check(lib().qk_norm_rope_bwd(rope._ref, dt, B, T, Hq, Hkv, D, *grads, qp, kp, i9(*qs, *ks, 0, 0, 0), pp, qw, kw, f32,
+                                  float(eps), gqp, gkp, gvp, i9(*gqs, *gks, *gvs),
+                                  _dense(gqw, (D,), q, "out[3]", torch.float32),
+                                  _dense(gkw, (D,), q, "out[4]", torch.float32), wsp, ws_bytes, raw))
+    if stream is not None:
+        _used8(stream, dq, dk, dv, q, k, pos, q_weight, k_weight, gq, gk, gv, gqw, gkw, ws)
+    return gq, gk, gv, gqw, gkw
+
+
+def qk_norm_rope_bwd_ws_bytes(q):
+    """Workspace of qk_norm_rope_bwd with norms for raw queries q."""
+    return lib().qk_norm_rope_bwd_workspace_bytes(q.shape[0], 1 if q.dim() == 3 else q.shape[1], q.shape[-1], 1)
+
+
+def _workspace(need, like, ws, stream):
+    """Pointer (256-byte aligned), bytes and tensor of a workspace: `ws` if given, else a new one."""
+    if need == ctypes.c_size_t(-1).value:
+        raise KvqError(KVQ_EINVAL, lib().kvq_last_error().decode())
+    if need == 0:
+        return None, 0, ws
+    if ws is None:
+        ws = _new((need + 256,), like, torch.uint8, stream)
+    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or not ws.is_cuda or ws.get_device() != like.get_device():
+        _bad("ws must be a contiguous uint8 CUDA tensor on q's device")
+    shift = -ws.data_ptr() % 256
+    return ws.data_ptr() + shift, max(ws.numel() - shift, 0), ws

@@ -516,6 +516,60 @@ size_t block8_select_workspace_bytes(const kvq_block8* c, int n_q);
 kvq_status block8_evict(kvq_block8* c, const int32_t* keep, int n_first, int n_last, int32_t* n_evicted,
                         void* stream);
 
+/* Rotation of queries and keys by position.  The first `rot` channels of a
+ * head form rot/2 pairs: pair i is the channels (i, i + rot/2), or (2i, 2i+1)
+ * with interleaved != 0.  Pair i turns by pos * f_i radians, where pos is the
+ * token's position on axis[i] (text: one axis; images and clips: rows,
+ * columns, time) and f_i is given as a fraction of a turn,
+ *   turn[i] = RN(2^64 f_i / (2 pi)) mod 2^64,
+ * so that the angle modulo a turn is exact for every int32 position.  The
+ * struct is read during the call only. */
+#define KVQ_ROPE_MAX_AXES 4
+typedef struct {
+    int32_t rot;            /* rotated channels: a multiple of 16 in [0, D] */
+    int32_t interleaved;    /* 0 or 1 */
+    int32_t n_axes;         /* 1 .. KVQ_ROPE_MAX_AXES */
+    uint8_t axis[64];       /* < n_axes */
+    uint64_t turn[64];
+} kvq_rope;
+
+/* qk_norm_rope -- from a layer's projection to attention and the caches:
+ * RMS norm of each head's query and key, rotation, change of layout.
+ *   q [B, T, Hq, D], k, v [B, T, Hkv, D] (device; v may be NULL) f16 or bf16,
+ *   D 64 or 128, Hq % Hkv == 0.  strides (host, NULL: contiguous): {b, t,
+ *   head} of q, of k, of v in elements, each >= 0 and a multiple of 8; D
+ *   contiguous, bases 16-byte aligned.
+ *   pos (device) [n_axes, B, T] int32, any value.
+ *   q_weight, k_weight (device, each may be NULL: that norm is left out) [D]
+ *   of the activations' type, or float32 (weight_f32 != 0), 16-byte aligned:
+ *     y = x * rsqrt(mean(x^2) + eps) * weight, eps >= 0.
+ *   q_out [B, Hq, T, D], k_out, v_out [B, Hkv, T, D] (device) contiguous, not
+ *   overlapping the inputs: what prefill_attn_scores takes, with T = 1 what
+ *   block8_append, block8_attn and decode_attn_qkv take.
+ * float32 arithmetic, one rounding. */
+kvq_status qk_norm_rope(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D,
+                        const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* pos,
+                        const void* q_weight, const void* k_weight, int weight_f32, float eps,
+                        void* q_out, void* k_out, void* v_out, void* stream);
+
+/* qk_norm_rope_bwd -- the gradient of qk_norm_rope.
+ *   dq, dk, dv (device) [B, heads, T, D] contiguous: gradients of q_out, k_out,
+ *   v_out (dv may be NULL).  q, k, strides: the raw rows of the forward call
+ *   (strides of q and of k; not read where the norm is left out, and then q or
+ *   k may be NULL).
+ *   gq, gk, gv (device) [B, T, heads, D]: gradients of q, k, v; g_strides as
+ *   strides above (of gq, gk, gv), the rows must not overlap.
+ *   gq_weight, gk_weight (device) [D] float32: written where that norm is there.
+ *   ws (device) of qk_norm_rope_bwd_workspace_bytes(), 256-byte aligned
+ *   (0 without norms).  Sums run in a fixed order: a call repeats itself bit
+ *   for bit. */
+kvq_status qk_norm_rope_bwd(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D,
+                            const void* dq, const void* dk, const void* dv, const void* q, const void* k,
+                            const int64_t* strides, const int32_t* pos, const void* q_weight, const void* k_weight,
+                            int weight_f32, float eps, void* gq, void* gk, void* gv, const int64_t* g_strides,
+                            float* gq_weight, float* gk_weight, void* ws, size_t ws_bytes, void* stream);
+size_t qk_norm_rope_bwd_workspace_bytes(int B, int T, int D, int norm);
+
 /* Bytes each device array of a cache with these sizes needs; out[i] in the
  * order of the kvq_cache fields (see kvq_cache_layout in the Python
  * binding).  Returns the total, 0 on invalid sizes. */
