@@ -12,6 +12,7 @@
 
 extern "C" cudaError_t kvq_internal_status_quant(cudaStream_t, uint32_t*);
 extern "C" cudaError_t kvq_internal_status_prefill(cudaStream_t, uint32_t*);
+extern "C" cudaError_t kvq_internal_status_prefill_bwd(cudaStream_t, uint32_t*);
 extern "C" cudaError_t kvq_internal_status_select(cudaStream_t, uint32_t*);
 extern "C" cudaError_t kvq_internal_status_decode(cudaStream_t, uint32_t*);
 extern "C" cudaError_t kvq_internal_status_policy(cudaStream_t, uint32_t*);
@@ -509,6 +510,43 @@ kvq_status block8_evict(kvq_block8* c, const int32_t* keep, int n_first, int n_l
                        "block8_evict launch");
 }
 
+// ---------------------------------------------------------------- gradient of prefill attention
+
+static kvq_status check_prefill_bwd(int B, int Hq, int Hkv, int T, const char* who) {
+    KVQ_REQUIRE(B > 0 && Hq > 0 && Hkv > 0 && T > 0, KVQ_EINVAL, "%s: sizes must be positive", who);
+    KVQ_REQUIRE(Hq % Hkv == 0, KVQ_EINVAL, "%s: Hq %% Hkv != 0", who);
+    // the row statistics' grid has a head per row, the others a CTA per head and tile
+    KVQ_REQUIRE((long long)B * Hq <= 65535 && T <= (1 << 24) && (long long)B * Hq * ((T + 127) / 128) <= (1LL << 30),
+                KVQ_EUNSUPPORTED, "%s: too large", who);
+    return KVQ_OK;
+}
+
+size_t prefill_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int T) {
+    if (check_prefill_bwd(B, Hq, Hkv, T, "prefill_attn_bwd_workspace_bytes") != KVQ_OK) return (size_t)-1;
+    return kvq::prefill_bwd_bytes(B, Hq, Hkv, T);
+}
+
+kvq_status prefill_attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* go, kvq_dtype dt,
+                            int B, int Hq, int Hkv, int T, int D, float sm_scale, int causal, const float* lse,
+                            const float* glse, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream) {
+    const char* who = "prefill_attn_bwd";
+    KVQ_REQUIRE(q && k && v && o && go && lse && dq && dk && dv, KVQ_EINVAL, "%s: null pointer", who);
+    KVQ_REQUIRE(dt == KVQ_F16 || dt == KVQ_BF16, KVQ_EINVAL, "%s: dtype must be f16 or bf16", who);
+    kvq_status st = check_prefill_bwd(B, Hq, Hkv, T, who);
+    if (st != KVQ_OK) return st;
+    KVQ_REQUIRE(D == 64 || D == 128, KVQ_EUNSUPPORTED, "%s: head dim %d unsupported (64 or 128)", who, D);
+    KVQ_REQUIRE(causal == 1, KVQ_EUNSUPPORTED, "%s: only causal attention", who);
+    KVQ_REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && aligned(o, 16) && aligned(go, 16) &&
+                    aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16) && aligned(lse, 4) && aligned(glse, 4),
+                KVQ_EINVAL, "%s: q/k/v/o/go/dq/dk/dv must be 16-byte aligned", who);
+    KVQ_REQUIRE(sm_scale > 0.0f && sm_scale < 1e30f, KVQ_EINVAL, "%s: sm_scale must be positive and finite", who);
+    if ((st = check_ws(ws, ws_bytes, kvq::prefill_bwd_bytes(B, Hq, Hkv, T), who)) != KVQ_OK) return st;
+    kvq::PrefillBwdCall c = {};
+    c.dt = dt, c.B = B, c.Hq = Hq, c.Hkv = Hkv, c.T = T, c.D = D, c.q = q, c.k = k, c.v = v, c.o = o, c.go = go;
+    c.lse = lse, c.glse = glse, c.sm_scale = sm_scale, c.dq = dq, c.dk = dk, c.dv = dv, c.ws = ws;
+    return kvq::run_prefill_bwd(c, (cudaStream_t)stream);
+}
+
 // ---------------------------------------------------------------- norm and rotation per head
 
 static kvq_status check_rope(const kvq_rope* r, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D, float eps,
@@ -635,7 +673,7 @@ kvq_status kvq_debug_withhold_copy(int on) {
 kvq_status kvq_device_status(void* stream, uint32_t* out) {
     KVQ_REQUIRE(out, KVQ_EINVAL, "kvq_device_status: null out");
     cudaStream_t s = (cudaStream_t)stream;
-    uint32_t v[7] = {0, 0, 0, 0, 0, 0, 0};
+    uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     cudaError_t e = kvq_internal_status_quant(s, &v[0]);
     if (e == cudaSuccess) e = kvq_internal_status_prefill(s, &v[1]);
     if (e == cudaSuccess) e = kvq_internal_status_select(s, &v[2]);
@@ -643,8 +681,9 @@ kvq_status kvq_device_status(void* stream, uint32_t* out) {
     if (e == cudaSuccess) e = kvq_internal_status_policy(s, &v[4]);
     if (e == cudaSuccess) e = kvq_internal_status_block8(s, &v[5]);
     if (e == cudaSuccess) e = kvq_internal_status_block8_attn(s, &v[6]);
+    if (e == cudaSuccess) e = kvq_internal_status_prefill_bwd(s, &v[7]);
     if (e != cudaSuccess) return cuda_status(e, "kvq_device_status");
-    uint32_t all = v[0] | v[1] | v[2] | v[3] | v[4] | v[5] | v[6];
+    uint32_t all = v[0] | v[1] | v[2] | v[3] | v[4] | v[5] | v[6] | v[7];
     *out = (all & 1u) ? (uint32_t)KVQ_ETIMEOUT : ((all & 2u) ? (uint32_t)KVQ_EDEVICE : 0u);
     return KVQ_OK;
 }

@@ -90,4 +90,15 @@ cudaError_t launch_rope(const RopeCall& c, cudaStream_t s);
 cudaError_t launch_rope_bwd(const RopeCall& c, cudaStream_t s);
 int rope_bwd_ctas(int B, int T);
 
+// Gradient of prefill attention (arguments validated by the caller).
+struct PrefillBwdCall {
+    int dt, B, Hq, Hkv, T, D;
+    const void *q, *k, *v, *o, *go;
+    const float *lse, *glse;        // glse NULL: none
+    float sm_scale;
+    void *dq, *dk, *dv, *ws;
+};
+size_t prefill_bwd_bytes(int B, int Hq, int Hkv, int T);
+kvq_status run_prefill_bwd(const PrefillBwdCall& c, cudaStream_t s);
+
 }  // namespace kvq

@@ -24,12 +24,11 @@
 // Every mbarrier wait is bounded (2 s, or at once after another warp gave
 // up); a timed-out CTA drains its copies and MMAs, frees TMEM and records
 // KVQ_ETIMEOUT in the device status word.
-#include <mutex>
-
 #include <algorithm>
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
+#include "prefill_tiles.cuh"
 
 namespace kvq {
 
@@ -37,11 +36,8 @@ KVQ_DEFINE_STATUS(prefill)
 
 namespace {
 
-constexpr int kTile = 128;                 // rows per tile (queries or keys)
-constexpr uint32_t kHalfBytes = 128 * 128;       // one 128-row x 64-column 128B-swizzled half
 constexpr int kBN = 64;                          // keys per K/V tile of pass 1
 constexpr uint32_t kKVHalf = kBN * 128;          // one 64-row x 64-column swizzled half
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
 // pass 2: two warpgroups sum the exponentials (each half of a tile's query columns), then
@@ -78,20 +74,6 @@ enum P1Bar { B_Q = 0, B_KF = 1, B_VF = 3, B_KVE = 5, B_SF = 7, B_SCONS = 8, B_SF
 enum P2Bar { C_KF = 0, C_QF = 1, C_QE = 3, C_SF = 5, C_SFREE = 7, C_DRAIN = 9, C_LSE = 10,
              P2_NBAR = 12 };
 
-template <typename T> struct Pack2;
-template <> struct Pack2<__half> {
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&h);
-    }
-};
-template <> struct Pack2<__nv_bfloat16> {
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<uint32_t*>(&h);
-    }
-};
-
 // Bounded wait whose outcome is the same for every lane of the warp, so that
 // the warp-collective tcgen05.ld/st after it stay convergent.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -101,20 +83,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 __device__ __forceinline__ void give_up(volatile int* abort_flag) {
     *abort_flag = 1;
     atomicOr(&g_status_prefill, kDevTimeout);
-}
-
-// K-major operand (rows x 128 elements as two 128B-swizzled 64-column halves):
-// descriptor of the 16-element K slice kk (0..7).
-__device__ __forceinline__ uint64_t kmajor_desc(uint32_t tile, int kk, uint32_t half = kHalfBytes) {
-    return sdesc_sw128(tile + (uint32_t)(kk >> 2) * half + (uint32_t)(kk & 3) * 32u, 16u,
-                       1024u);
-}
-
-// MN-major operand (128 K-rows of 128 N-elements, two 64-column halves):
-// descriptor of K rows 16*kk .. 16*kk+15.  LBO = stride between the N
-// halves, SBO = stride between groups of 8 K rows.
-__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t tile, int kk, uint32_t half = kHalfBytes) {
-    return sdesc_sw128(tile + (uint32_t)kk * 16u * 128u, half, 1024u);
 }
 
 template <typename T, int AB, int D>
@@ -602,40 +570,6 @@ __global__ void __launch_bounds__(kP2Threads, 2)
 }
 
 // ------------------------------------------------------------------ host
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// [rows = BH][T][D] 16-bit tensor, box 64 x box_rows x 1, 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* ptr, int dt, int BH, int T, int D, int box_rows = kTile) {
-    EncodeTiledFn enc = get_encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)BH};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)T * D * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(m, dt == KVQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     3, const_cast<void*>(ptr), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
 
 template <typename T, int AB, int D>
 kvq_status run_typed(const void* q, const void* k, const void* v, int B, int Hq, int Hkv, int T_len,

@@ -1,0 +1,735 @@
+// prefill_attn_bwd: gradients of q, k and v through prefill_attn_scores' o and lse, the probabilities recomputed.
+//
+//   P_ij = exp(sigma q_i.k_j - lse_i) for j <= i, 0 above;   delta_i = do_i.o_i - dlse_i
+//   dS_ij = P_ij (do_i.v_j - delta_i)
+//   dV_j = sum_i P_ij do_i;   dK_j = sigma sum_i dS_ij q_i;   dQ_i = sigma sum_j dS_ij k_j
+//
+// Two kernels over 128 x 128 tiles, so that every sum stays in one CTA's tensor memory in a fixed order: no atomics, no
+// float32 buffer, and a call repeats itself bit for bit.  The price is that S and dO V^T are computed in both (seven
+// products for the five of the formulas).
+//   dkv: CTA = (KV head, key tile), over the query heads of its group and their query tiles at and below the diagonal,
+//        S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and dK += dS^T Q with P^T and dS^T read from tensor memory, where
+//        they replace S^T and dP^T.  The tensor pipe runs what one thread issues in order, so S^T of the next tile may
+//        be issued right behind the dV product that reads P^T from its place.
+//   dq:  CTA = (query head, query tile), over the key tiles up to the diagonal: S = Q K^T, dP = dO V^T, dQ += dS K.
+// Eight warps do the exponentials and dS (two warpgroups, each half of a tile's columns, a thread per row), one warp
+// issues the copies, one the products, in dkv one brings the rows' lse and delta.
+// A first kernel computes delta and brings lse to base 2.
+//
+// Rounding: P and dS enter their products in the inputs' type.  In bf16 that is 2^-9 of each term, as much as the
+// output's own rounding.  fp16 has the range problem instead: P of long rows and dS of small gradients fall below its
+// normal numbers.  So P is kept times 2^15 (P <= 1) and dS times a power of two c as well, chosen per KV head (dkv) or
+// query head (dq) from the largest |do_i|, |v_j| (2-norms) and |delta_i| so that |do_i.v_j - delta_i| c <= 1; the sums'
+// factors are undone in the epilogue.
+//
+// Every mbarrier wait is bounded; a CTA that gives up drains its copies and products, frees TMEM, stores nothing and
+// records KVQ_ETIMEOUT in the device status word.
+#include <algorithm>
+
+#include "kvq_common.cuh"
+#include "kvq_internal.h"
+#include "prefill_tiles.cuh"
+
+namespace kvq {
+
+KVQ_DEFINE_STATUS(prefill_bwd)
+
+namespace {
+
+constexpr int kSoftWarps = 8;
+constexpr int kDkvThreads = 32 * (kSoftWarps + 3);   // + copies, products, row statistics
+constexpr int kDqThreads = 32 * (kSoftWarps + 2);
+constexpr int kPrepThreads = 256;
+constexpr uint32_t kTmemCols = 512;
+
+// What the first kernel leaves in the workspace (n_t tiles, Tp = 128 n_t rows a head).
+struct BwdWs {
+    float* nlse;        // [B*Hq][Tp] minus lse in base 2, plus the probabilities' shift; -inf behind the last row
+    float* delta;       // [B*Hq][Tp]
+    float* do_max;      // [B*Hq][n_t] largest 2-norm of a row of do        (fp16 only, also the next two)
+    float* dl_max;      // [B*Hq][n_t] largest |delta|
+    float* v_max;       // [B*Hkv][n_t] largest 2-norm of a row of v
+};
+
+struct BwdArgs {
+    BwdWs ws;
+    int B, Hq, Hkv, T_len, n_t;
+    float sm_scale, scale_log2;
+    int group;          // heads (dkv: KV heads) whose tiles are launched side by side
+};
+
+__device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+}
+
+__device__ __forceinline__ void bwd_give_up(volatile int* abort_flag) {
+    *abort_flag = 1;
+    atomicOr(&g_status_prefill_bwd, kDevTimeout);
+}
+
+// Probabilities are kept times 2^kShift.
+template <int AB> struct Shift { static constexpr float value = AB == 0 ? 15.0f : 0.0f; };
+
+// ------------------------------------------------------------------ row statistics
+
+// CTA = (tile of 128 rows, query head); D / 8 lanes of 16 bytes per row.
+template <typename T, int AB, int D>
+__global__ void __launch_bounds__(kPrepThreads)
+    bwd_prep_kernel(const T* __restrict__ o, const T* __restrict__ go, const T* __restrict__ v,
+                    const float* __restrict__ lse, const float* __restrict__ glse, const BwdArgs a) {
+    constexpr int kLanes = D / 8, kRows = kPrepThreads / kLanes;
+    const int tile = blockIdx.x, bh = blockIdx.y;
+    const int b = bh / a.Hq, hq = bh % a.Hq, g = a.Hq / a.Hkv;
+    const int l = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
+    const int64_t Tp = (int64_t)a.n_t * kTile;
+    const bool with_v = AB == 0 && hq % g == 0;
+    const int u = b * a.Hkv + hq / g;
+    float most_do = 0.0f, most_dl = 0.0f, most_v = 0.0f;
+#pragma unroll 4
+    for (int r0 = 0; r0 < kTile; r0 += kRows) {
+        const int i = tile * kTile + r0 + sub;
+        const bool there = i < a.T_len;
+        float dot = 0.0f, sq = 0.0f, vv = 0.0f;
+        if (there) {
+            const int64_t at = ((int64_t)bh * a.T_len + i) * kLanes + l;
+            const uint4 x = reinterpret_cast<const uint4*>(o)[at], y = reinterpret_cast<const uint4*>(go)[at];
+            const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = Elem<T>::to_f(ye[e]);
+                dot = fmaf(Elem<T>::to_f(xe[e]), d, dot);
+                sq = fmaf(d, d, sq);
+            }
+            if (with_v) {
+                const uint4 z = reinterpret_cast<const uint4*>(v)[((int64_t)u * a.T_len + i) * kLanes + l];
+                const T* ze = reinterpret_cast<const T*>(&z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) vv = fmaf(Elem<T>::to_f(ze[e]), Elem<T>::to_f(ze[e]), vv);
+            }
+        }
+#pragma unroll
+        for (int m = kLanes / 2; m > 0; m >>= 1) {
+            dot += __shfl_xor_sync(0xffffffffu, dot, m);
+            if (AB == 0) sq += __shfl_xor_sync(0xffffffffu, sq, m);
+            if (AB == 0) vv += __shfl_xor_sync(0xffffffffu, vv, m);
+        }
+        float nl = -__int_as_float(0x7f800000), dl = 0.0f;
+        if (there) {
+            const int64_t row = (int64_t)bh * a.T_len + i;
+            dl = dot - (glse ? glse[row] : 0.0f);
+            const float x = lse[row];
+            if (!isinf(x)) nl = Shift<AB>::value - x * kLog2e;      // a row that saw nothing has no gradient
+        }
+        if (l == 0) {
+            a.ws.nlse[bh * Tp + i] = nl;
+            a.ws.delta[bh * Tp + i] = dl;
+        }
+        if (AB == 0) {
+            most_do = fmaxf(most_do, sq), most_dl = fmaxf(most_dl, fabsf(dl)), most_v = fmaxf(most_v, vv);
+        }
+    }
+    if (AB == 0) {
+        __shared__ float red[kPrepThreads / 32][3];
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) {
+            most_do = fmaxf(most_do, __shfl_xor_sync(0xffffffffu, most_do, m));
+            most_dl = fmaxf(most_dl, __shfl_xor_sync(0xffffffffu, most_dl, m));
+            most_v = fmaxf(most_v, __shfl_xor_sync(0xffffffffu, most_v, m));
+        }
+        if ((threadIdx.x & 31) == 0) {
+            float* x = red[threadIdx.x >> 5];
+            x[0] = most_do, x[1] = most_dl, x[2] = most_v;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kPrepThreads / 32; ++w) {
+                most_do = fmaxf(most_do, red[w][0]), most_dl = fmaxf(most_dl, red[w][1]), most_v = fmaxf(most_v, red[w][2]);
+            }
+            a.ws.do_max[(int64_t)bh * a.n_t + tile] = sqrtf(most_do);
+            a.ws.dl_max[(int64_t)bh * a.n_t + tile] = most_dl;
+            if (with_v) a.ws.v_max[(int64_t)u * a.n_t + tile] = sqrtf(most_v);
+        }
+    }
+}
+
+// The power of two c with |do_i.v_j - delta_i| c <= 1 over query heads [h0, h0 + nh) of unit u (fp16; else 1).  Called
+// by the whole CTA; `red` has 3 floats a warp; a __syncthreads() lies between the two halves.
+template <int AB> __device__ __forceinline__ void largest(const BwdArgs& a, int h0, int nh, int u, float* red) {
+    if (AB != 0) return;
+    float x = 0.0f, d = 0.0f, v = 0.0f;
+    for (int i = threadIdx.x; i < nh * a.n_t; i += blockDim.x) {
+        x = fmaxf(x, a.ws.do_max[(int64_t)h0 * a.n_t + i]);
+        d = fmaxf(d, a.ws.dl_max[(int64_t)h0 * a.n_t + i]);
+    }
+    for (int i = threadIdx.x; i < a.n_t; i += blockDim.x) v = fmaxf(v, a.ws.v_max[(int64_t)u * a.n_t + i]);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+        d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, m));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
+    }
+    if ((threadIdx.x & 31) == 0) {
+        float* r = red + 3 * (threadIdx.x >> 5);
+        r[0] = x, r[1] = d, r[2] = v;
+    }
+}
+template <int AB> __device__ __forceinline__ float scale_of(const float* red) {
+    if (AB != 0) return 1.0f;
+    float x = 0.0f, d = 0.0f, v = 0.0f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w)
+        x = fmaxf(x, red[3 * w]), d = fmaxf(d, red[3 * w + 1]), v = fmaxf(v, red[3 * w + 2]);
+    const float most = fmaf(x, v, d);
+    if (!(most > 0.0f)) return 1.0f;
+    const int e = most < 1e30f ? min(max(ilogbf(most) + 1, -60), 60) : 60;
+    return __int_as_float((127 - e) << 23);
+}
+
+// blockIdx.x -> (tile rank, head): heads in groups, all tiles of a group before the next group, the longest tiles of
+// every head first.  A group's streamed operands stay in L2 while its CTAs run.
+__device__ __forceinline__ void place(const BwdArgs& a, int heads, int& rank, int& head) {
+    const int per = a.group * a.n_t, g = (int)(blockIdx.x / per), in = (int)(blockIdx.x % per);
+    const int size = min(a.group, heads - g * a.group);
+    rank = in / size;
+    head = g * a.group + in % size;
+}
+
+// Shared memory of both kernels: K, V (dkv) or Q, dO (dq) once, three and two stages of the streamed operands.
+template <int D> struct BwdLayout {
+    static constexpr uint32_t kTileBytes = kTile * D * 2;
+    static constexpr uint32_t A0 = 0, A1 = kTileBytes;
+    static constexpr uint32_t S0 = 2 * kTileBytes;              // 3 stages: Q (dkv), K (dq)
+    static constexpr uint32_t S1 = S0 + 3 * kTileBytes;         // 2 stages: dO (dkv), V (dq)
+    static constexpr uint32_t STAT = S1 + 2 * kTileBytes;       // dkv: 2 stages of 128 (nlse) and 128 (delta) floats
+    static constexpr uint32_t RED = STAT + 2048;
+    static constexpr uint32_t BAR = RED + 12 * 12 + 48;
+    // no alignment slack at D = 128: the kernels require (and check) a 1024-aligned base
+    static constexpr uint32_t BYTES = BAR + 256;
+};
+static_assert(BwdLayout<128>::BYTES <= 232448, "shared memory");
+
+// 32 columns of a thread's row: exponentials, packed pairs.
+template <typename T> __device__ __forceinline__ void store_pairs(uint32_t taddr, const float* x) {
+    float w[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) w[c] = __uint_as_float(Pack2<T>::pack(x[2 * c], x[2 * c + 1]));
+    tmem_st32(taddr, w);
+}
+
+// One thread's row of D float32 TMEM columns, times f, to `out` in T.
+template <typename T, int D> __device__ __forceinline__ void store_row(uint32_t taddr, float f, bool there, T* out) {
+#pragma unroll
+    for (int c4 = 0; c4 < D / 32; ++c4) {
+        float x[32];
+        tmem_ld32(taddr + (uint32_t)c4 * 32u, x);
+        tmem_wait_ld();
+        if (there) {
+#pragma unroll
+            for (int c8 = 0; c8 < 4; ++c8) {
+                uint4 w;
+                w.x = Pack2<T>::pack(x[c8 * 8 + 0] * f, x[c8 * 8 + 1] * f);
+                w.y = Pack2<T>::pack(x[c8 * 8 + 2] * f, x[c8 * 8 + 3] * f);
+                w.z = Pack2<T>::pack(x[c8 * 8 + 4] * f, x[c8 * 8 + 5] * f);
+                w.w = Pack2<T>::pack(x[c8 * 8 + 6] * f, x[c8 * 8 + 7] * f);
+                *reinterpret_cast<uint4*>(out + c4 * 32 + c8 * 8) = w;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ dK and dV
+
+enum DkvBar { V_KV = 0, V_QF = 1, V_QE = 4, V_GF = 7, V_GE = 9, V_TF = 11, V_TE = 13, V_SF = 15, V_PR = 16, V_DF = 17,
+              V_DR = 18, V_END = 19, DKV_NBAR = 20 };
+
+template <typename T, int AB, int D>
+__global__ void __launch_bounds__(kDkvThreads, 1)
+    bwd_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg, T* __restrict__ dk,
+                   T* __restrict__ dv, const BwdArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    if (base & 1023u) {                                 // layout assumption broken: do nothing
+        if (threadIdx.x == 0) atomicOr(&g_status_prefill_bwd, kDevCheck);
+        return;
+    }
+    using Lay = BwdLayout<D>;
+    constexpr uint32_t kTileBytes = Lay::kTileBytes;
+    constexpr int kHalves = D / 64;
+    const uint32_t sK = base + Lay::A0, sV = base + Lay::A1, sQ = base + Lay::S0, sG = base + Lay::S1;
+    auto BAR = [&](int i) -> uint32_t { return base + Lay::BAR + 8u * (uint32_t)i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::BAR + 8 * DKV_NBAR);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR + 8 * DKV_NBAR + 4);
+    float* red = reinterpret_cast<float*>(smem + Lay::RED);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int kt, u;
+    place(a, a.B * a.Hkv, kt, u);
+    const int g = a.Hq / a.Hkv, h0 = u * g;             // head u * g + h of all B * Hq is the unit's h-th
+    const int m = a.n_t - kt, n = g * m;                // query tiles of a head; of all heads
+
+    if (threadIdx.x == 0) {
+        mbar_init(BAR(V_KV), 1);
+        for (int s = 0; s < 3; ++s) mbar_init(BAR(V_QF + s), 1), mbar_init(BAR(V_QE + s), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(BAR(V_GF + s), 1), mbar_init(BAR(V_GE + s), 1);
+            mbar_init(BAR(V_TF + s), 1), mbar_init(BAR(V_TE + s), kSoftWarps);
+        }
+        mbar_init(BAR(V_SF), 1), mbar_init(BAR(V_PR), kSoftWarps);
+        mbar_init(BAR(V_DF), 1), mbar_init(BAR(V_DR), kSoftWarps);
+        mbar_init(BAR(V_END), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kSoftWarps + 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    largest<AB>(a, h0, g, u, red);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
+    const float c = scale_of<AB>(red);
+
+    if (warp == kSoftWarps) {
+        if (lane == 0) {
+            prefetch_tmap(&tq), prefetch_tmap(&tk), prefetch_tmap(&tv), prefetch_tmap(&tg);
+            mbar_expect_tx(BAR(V_KV), 2 * kTileBytes);
+            for (int hf = 0; hf < kHalves; ++hf) {
+                tma_load_3d(sK + hf * kHalfBytes, &tk, 64 * hf, kt * kTile, u, BAR(V_KV));
+                tma_load_3d(sV + hf * kHalfBytes, &tv, 64 * hf, kt * kTile, u, BAR(V_KV));
+            }
+            int it = 0, lastq[3] = {-1, -1, -1}, lastg[2] = {-1, -1};
+            for (; it < n; ++it) {
+                const int bh = h0 + it / m, row = (kt + it % m) * kTile, s3 = it % 3, s2 = it & 1;
+                if (it >= 3 && !mbar_wait(BAR(V_QE + s3), (it / 3 - 1) & 1, abort_flag)) break;
+                mbar_expect_tx(BAR(V_QF + s3), kTileBytes);
+                for (int hf = 0; hf < kHalves; ++hf)
+                    tma_load_3d(sQ + s3 * kTileBytes + hf * kHalfBytes, &tq, 64 * hf, row, bh, BAR(V_QF + s3));
+                lastq[s3] = it / 3;
+                if (it >= 2 && !mbar_wait(BAR(V_GE + s2), (it / 2 - 1) & 1, abort_flag)) break;
+                mbar_expect_tx(BAR(V_GF + s2), kTileBytes);
+                for (int hf = 0; hf < kHalves; ++hf)
+                    tma_load_3d(sG + s2 * kTileBytes + hf * kHalfBytes, &tg, 64 * hf, row, bh, BAR(V_GF + s2));
+                lastg[s2] = it / 2;
+            }
+            if (it < n) bwd_give_up(abort_flag);
+            // every issued copy has landed before the CTA may exit
+            mbar_wait(BAR(V_KV), 0, nullptr);
+            for (int s = 0; s < 3; ++s)
+                if (lastq[s] >= 0) mbar_wait(BAR(V_QF + s), lastq[s] & 1, nullptr);
+            for (int s = 0; s < 2; ++s)
+                if (lastg[s] >= 0) mbar_wait(BAR(V_GF + s), lastg[s] & 1, nullptr);
+        }
+    } else if (warp == kSoftWarps + 1) {
+        if (lane == 0) {
+            const uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
+            auto scores = [&](int it) -> bool {         // S^T = K Q^T
+                if (!mbar_wait(BAR(V_QF + it % 3), (it / 3) & 1, abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t t = sQ + (uint32_t)(it % 3) * kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) tc_mma_f16(tS, kmajor_desc(sK, kk), kmajor_desc(t, kk), idS, kk > 0);
+                tc_commit(BAR(V_SF));
+                return true;
+            };
+            auto grads = [&](int it) -> bool {          // dP^T = V dO^T
+                if (!mbar_wait(BAR(V_GF + (it & 1)), (it / 2) & 1, abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t t = sG + (uint32_t)(it & 1) * kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) tc_mma_f16(tP, kmajor_desc(sV, kk), kmajor_desc(t, kk), idS, kk > 0);
+                tc_commit(BAR(V_DF));
+                return true;
+            };
+            bool ok = mbar_wait(BAR(V_KV), 0, abort_flag) && scores(0) && grads(0);
+            for (int it = 0; ok && it < n; ++it) {
+                // P^T and dS^T: queries 0-63 in the first 32 columns of their place, 64-127 from column 64 on
+                if (!(ok = mbar_wait(BAR(V_PR), it & 1, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t tg_ = sG + (uint32_t)(it & 1) * kTileBytes, tq_ = sQ + (uint32_t)(it % 3) * kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc_mma_f16_ta(tDV, tS + (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u, mnmajor_desc(tg_, kk), idD,
+                                  it > 0 || kk > 0);
+                tc_commit(BAR(V_GE + (it & 1)));
+                if (it + 1 < n && !(ok = scores(it + 1))) break;
+                if (!(ok = mbar_wait(BAR(V_DR), it & 1, abort_flag))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc_mma_f16_ta(tDK, tP + (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u, mnmajor_desc(tq_, kk), idD,
+                                  it > 0 || kk > 0);
+                tc_commit(BAR(V_QE + it % 3));
+                if (it + 1 < n && !(ok = grads(it + 1))) break;
+            }
+            if (!ok) bwd_give_up(abort_flag);
+            // all products complete before the sums are read and TMEM is released
+            tc_commit(BAR(V_END));
+            mbar_wait(BAR(V_END), 0, nullptr);
+        }
+    } else if (warp == kSoftWarps + 2) {
+        // the query rows' statistics, delta times c
+        bool ok = true;
+        for (int it = 0; it < n; ++it) {
+            const int s = it & 1;
+            const int64_t row = (int64_t)(h0 + it / m) * a.n_t * kTile + (kt + it % m) * kTile + 4 * lane;
+            const float4 x = *reinterpret_cast<const float4*>(a.ws.nlse + row);
+            float4 y = *reinterpret_cast<const float4*>(a.ws.delta + row);
+            y.x *= -c, y.y *= -c, y.z *= -c, y.w *= -c;
+            if (it >= 2 && !(ok = bwd_wait(BAR(V_TE + s), (it / 2 - 1) & 1, abort_flag))) break;
+            float4* to = reinterpret_cast<float4*>(smem + Lay::STAT + s * 1024);
+            to[lane] = x;
+            to[32 + lane] = y;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(V_TF + s));
+        }
+        if (!ok) bwd_give_up(abort_flag);
+    } else {
+        // thread r of either warpgroup owns key r (TMEM lane r) and queries 64 wg .. 64 wg + 63 of each tile
+        const int wg = warp >> 2, r = threadIdx.x & 127, j = kt * kTile + r;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t mine = lanes + 64u * (uint32_t)wg;
+        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
+        bool ok = true;
+        for (int it = 0; it < n; ++it) {
+            const int s = it & 1;
+            const bool diag = it % m == 0;
+            if (!bwd_wait(BAR(V_TF + s), (it / 2) & 1, abort_flag)) { ok = false; break; }
+            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * 1024 + 256 * wg);
+            const ulonglong2* nd = nl + 32;
+            if (!bwd_wait(BAR(V_SF), it & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            float p[64];
+            tmem_ld32(tS + mine, p);
+            tmem_ld32(tS + mine + 32u, p + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q4 = 0; q4 < 16; ++q4) {
+                const ulonglong2 x = nl[q4];
+                float e0, e1, e2, e3;
+                f2_unpack(f2_fma(f2_pack(p[4 * q4], p[4 * q4 + 1]), sc2, x.x), e0, e1);
+                f2_unpack(f2_fma(f2_pack(p[4 * q4 + 2], p[4 * q4 + 3]), sc2, x.y), e2, e3);
+                p[4 * q4] = ex2_approx(e0), p[4 * q4 + 1] = ex2_approx(e1);
+                p[4 * q4 + 2] = ex2_approx(e2), p[4 * q4 + 3] = ex2_approx(e3);
+            }
+            if (diag) {
+#pragma unroll
+                for (int q = 0; q < 64; ++q) p[q] = 64 * wg + q >= r ? p[q] : 0.0f;
+            }
+            store_pairs<T>(tS + mine, p);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(V_PR));
+            if (!bwd_wait(BAR(V_DF), it & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            float d[64];
+            tmem_ld32(tP + mine, d);
+            tmem_ld32(tP + mine + 32u, d + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q4 = 0; q4 < 16; ++q4) {
+                const ulonglong2 x = nd[q4];
+                float e0, e1, e2, e3;
+                f2_unpack(f2_fma(f2_pack(d[4 * q4], d[4 * q4 + 1]), c2, x.x), e0, e1);
+                f2_unpack(f2_fma(f2_pack(d[4 * q4 + 2], d[4 * q4 + 3]), c2, x.y), e2, e3);
+                d[4 * q4] = p[4 * q4] * e0, d[4 * q4 + 1] = p[4 * q4 + 1] * e1;
+                d[4 * q4 + 2] = p[4 * q4 + 2] * e2, d[4 * q4 + 3] = p[4 * q4 + 3] * e3;
+            }
+            if (diag) {
+#pragma unroll
+                for (int q = 0; q < 64; ++q) d[q] = 64 * wg + q >= r ? d[q] : 0.0f;
+            }
+            store_pairs<T>(tP + mine, d);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(BAR(V_DR));
+                mbar_arrive(BAR(V_TE + s));
+            }
+        }
+        if (!ok) bwd_give_up(abort_flag);
+        ok = bwd_wait(BAR(V_END), 0, nullptr) && ok && !*abort_flag;
+        tc_fence_after();
+        // warpgroup 0 stores dV, warpgroup 1 dK
+        const int64_t row = (int64_t)u * a.T_len + (j < a.T_len ? j : 0);
+        const float unshift = AB == 0 ? 0x1p-15f : 1.0f;
+        if (wg == 0) store_row<T, D>(tDV + lanes, unshift, ok && j < a.T_len, dv + row * D);
+        else store_row<T, D>(tDK + lanes, a.sm_scale * unshift / c, ok && j < a.T_len, dk + row * D);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftWarps + 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ dQ
+
+enum DqBar { W_QG = 0, W_KF = 1, W_KE = 4, W_VF = 7, W_VE = 9, W_SF = 11, W_SC = 12, W_DF = 13, W_DC = 14, W_DR = 15,
+             W_DE = 17, W_END = 19, DQ_NBAR = 20 };
+
+template <typename T, int AB, int D>
+__global__ void __launch_bounds__(kDqThreads, 1)
+    bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg, T* __restrict__ dq,
+                  const BwdArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    if (base & 1023u) {                                 // layout assumption broken: do nothing
+        if (threadIdx.x == 0) atomicOr(&g_status_prefill_bwd, kDevCheck);
+        return;
+    }
+    using Lay = BwdLayout<D>;
+    constexpr uint32_t kTileBytes = Lay::kTileBytes;
+    constexpr int kHalves = D / 64;
+    const uint32_t sQ = base + Lay::A0, sG = base + Lay::A1, sK = base + Lay::S0, sV = base + Lay::S1;
+    auto BAR = [&](int i) -> uint32_t { return base + Lay::BAR + 8u * (uint32_t)i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::BAR + 8 * DQ_NBAR);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR + 8 * DQ_NBAR + 4);
+    float* red = reinterpret_cast<float*>(smem + Lay::RED);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int rank, bh;
+    place(a, a.B * a.Hq, rank, bh);
+    const int qt = a.n_t - 1 - rank, n = qt + 1;
+    const int u = bh / a.Hq * a.Hkv + bh % a.Hq / (a.Hq / a.Hkv);
+
+    if (threadIdx.x == 0) {
+        mbar_init(BAR(W_QG), 1);
+        for (int s = 0; s < 3; ++s) mbar_init(BAR(W_KF + s), 1), mbar_init(BAR(W_KE + s), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(BAR(W_VF + s), 1), mbar_init(BAR(W_VE + s), 1);
+            mbar_init(BAR(W_DR + s), kSoftWarps), mbar_init(BAR(W_DE + s), 1);
+        }
+        mbar_init(BAR(W_SF), 1), mbar_init(BAR(W_SC), kSoftWarps);
+        mbar_init(BAR(W_DF), 1), mbar_init(BAR(W_DC), kSoftWarps);
+        mbar_init(BAR(W_END), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kSoftWarps + 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    largest<AB>(a, bh, 1, u, red);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // S, dP, two buffers of dS (64 columns each), dQ
+    const uint32_t tS = tmem, tP = tmem + 128, tDS = tmem + 256, tDQ = tmem + 384;
+    const float c = scale_of<AB>(red);
+
+    if (warp == kSoftWarps) {
+        if (lane == 0) {
+            prefetch_tmap(&tq), prefetch_tmap(&tk), prefetch_tmap(&tv), prefetch_tmap(&tg);
+            mbar_expect_tx(BAR(W_QG), 2 * kTileBytes);
+            for (int hf = 0; hf < kHalves; ++hf) {
+                tma_load_3d(sQ + hf * kHalfBytes, &tq, 64 * hf, qt * kTile, bh, BAR(W_QG));
+                tma_load_3d(sG + hf * kHalfBytes, &tg, 64 * hf, qt * kTile, bh, BAR(W_QG));
+            }
+            int it = 0, lastk[3] = {-1, -1, -1}, lastv[2] = {-1, -1};
+            for (; it < n; ++it) {
+                const int s3 = it % 3, s2 = it & 1;
+                if (it >= 3 && !mbar_wait(BAR(W_KE + s3), (it / 3 - 1) & 1, abort_flag)) break;
+                mbar_expect_tx(BAR(W_KF + s3), kTileBytes);
+                for (int hf = 0; hf < kHalves; ++hf)
+                    tma_load_3d(sK + s3 * kTileBytes + hf * kHalfBytes, &tk, 64 * hf, it * kTile, u, BAR(W_KF + s3));
+                lastk[s3] = it / 3;
+                if (it >= 2 && !mbar_wait(BAR(W_VE + s2), (it / 2 - 1) & 1, abort_flag)) break;
+                mbar_expect_tx(BAR(W_VF + s2), kTileBytes);
+                for (int hf = 0; hf < kHalves; ++hf)
+                    tma_load_3d(sV + s2 * kTileBytes + hf * kHalfBytes, &tv, 64 * hf, it * kTile, u, BAR(W_VF + s2));
+                lastv[s2] = it / 2;
+            }
+            if (it < n) bwd_give_up(abort_flag);
+            mbar_wait(BAR(W_QG), 0, nullptr);
+            for (int s = 0; s < 3; ++s)
+                if (lastk[s] >= 0) mbar_wait(BAR(W_KF + s), lastk[s] & 1, nullptr);
+            for (int s = 0; s < 2; ++s)
+                if (lastv[s] >= 0) mbar_wait(BAR(W_VF + s), lastv[s] & 1, nullptr);
+        }
+    } else if (warp == kSoftWarps + 1) {
+        if (lane == 0) {
+            const uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
+            auto scores = [&](int it) -> bool {         // S = Q K^T
+                if (!mbar_wait(BAR(W_KF + it % 3), (it / 3) & 1, abort_flag)) return false;
+                if (it > 0 && !mbar_wait(BAR(W_SC), (it - 1) & 1, abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t t = sK + (uint32_t)(it % 3) * kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) tc_mma_f16(tS, kmajor_desc(sQ, kk), kmajor_desc(t, kk), idS, kk > 0);
+                tc_commit(BAR(W_SF));
+                return true;
+            };
+            auto grads = [&](int it) -> bool {          // dP = dO V^T
+                if (!mbar_wait(BAR(W_VF + (it & 1)), (it / 2) & 1, abort_flag)) return false;
+                if (it > 0 && !mbar_wait(BAR(W_DC), (it - 1) & 1, abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t t = sV + (uint32_t)(it & 1) * kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) tc_mma_f16(tP, kmajor_desc(sG, kk), kmajor_desc(t, kk), idS, kk > 0);
+                tc_commit(BAR(W_DF));
+                tc_commit(BAR(W_VE + (it & 1)));
+                return true;
+            };
+            bool ok = mbar_wait(BAR(W_QG), 0, abort_flag) && scores(0) && grads(0);
+            for (int it = 0; ok && it < n; ++it) {
+                if (it + 1 < n && !(ok = scores(it + 1) && grads(it + 1))) break;
+                const int s = it & 1;
+                if (!(ok = mbar_wait(BAR(W_DR + s), (it / 2) & 1, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t t = sK + (uint32_t)(it % 3) * kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    tc_mma_f16_ta(tDQ, tDS + 64u * (uint32_t)s + (uint32_t)kk * 8u, mnmajor_desc(t, kk), idD,
+                                  it > 0 || kk > 0);
+                tc_commit(BAR(W_KE + it % 3));
+                tc_commit(BAR(W_DE + s));
+            }
+            if (!ok) bwd_give_up(abort_flag);
+            tc_commit(BAR(W_END));
+            mbar_wait(BAR(W_END), 0, nullptr);
+        }
+    } else {
+        // thread r of either warpgroup owns query r and keys 64 wg .. 64 wg + 63 of each tile
+        const int wg = warp >> 2, r = threadIdx.x & 127, i = qt * kTile + r;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t mine = lanes + 64u * (uint32_t)wg;
+        const int64_t stat = (int64_t)bh * a.n_t * kTile + i;
+        const float nl = a.ws.nlse[stat], nd = -c * a.ws.delta[stat];
+        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
+        const unsigned long long nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+        bool ok = true;
+        for (int it = 0; it < n; ++it) {
+            const int s = it & 1;
+            const bool diag = it == qt;
+            if (!bwd_wait(BAR(W_SF), it & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            float p[64];
+            tmem_ld32(tS + mine, p);
+            tmem_ld32(tS + mine + 32u, p + 32);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(W_SC));
+#pragma unroll
+            for (int q = 0; q < 64; q += 2) {
+                float e0, e1;
+                f2_unpack(f2_fma(f2_pack(p[q], p[q + 1]), sc2, nl2), e0, e1);
+                p[q] = ex2_approx(e0), p[q + 1] = ex2_approx(e1);
+            }
+            if (!bwd_wait(BAR(W_DF), it & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            float d[64];
+            tmem_ld32(tP + mine, d);
+            tmem_ld32(tP + mine + 32u, d + 32);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(W_DC));
+#pragma unroll
+            for (int q = 0; q < 64; q += 2) {
+                float e0, e1;
+                f2_unpack(f2_fma(f2_pack(d[q], d[q + 1]), c2, nd2), e0, e1);
+                d[q] = p[q] * e0, d[q + 1] = p[q + 1] * e1;
+            }
+            if (diag) {
+#pragma unroll
+                for (int q = 0; q < 64; ++q) d[q] = 64 * wg + q <= r ? d[q] : 0.0f;
+            }
+            if (it >= 2 && !bwd_wait(BAR(W_DE + s), (it / 2 - 1) & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            store_pairs<T>(tDS + lanes + 64u * (uint32_t)s + 32u * (uint32_t)wg, d);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(W_DR + s));
+        }
+        if (!ok) bwd_give_up(abort_flag);
+        ok = bwd_wait(BAR(W_END), 0, nullptr) && ok && !*abort_flag;
+        tc_fence_after();
+        // each warpgroup stores half of the columns
+        const int64_t row = (int64_t)bh * a.T_len + (i < a.T_len ? i : 0);
+        const float f = a.sm_scale * (AB == 0 ? 0x1p-15f : 1.0f) / c;
+        if (D == 128) store_row<T, 64>(tDQ + mine, f, ok && i < a.T_len, dq + row * D + 64 * wg);
+        else store_row<T, 32>(tDQ + lanes + 32u * (uint32_t)wg, f, ok && i < a.T_len, dq + row * D + 32 * wg);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftWarps + 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ host
+
+size_t ws_layout(int B, int Hq, int Hkv, int T, char* base, BwdWs* w) {
+    const size_t n_t = (size_t)(T + kTile - 1) / kTile, rows = (size_t)B * Hq * n_t * kTile, tiles = (size_t)B * Hq * n_t;
+    size_t at = 0;
+    auto take = [&](size_t floats) {
+        float* p = reinterpret_cast<float*>(base + at);
+        at += (floats * sizeof(float) + 255) / 256 * 256;
+        return p;
+    };
+    BwdWs x;
+    x.nlse = take(rows), x.delta = take(rows), x.do_max = take(tiles), x.dl_max = take(tiles);
+    x.v_max = take((size_t)B * Hkv * n_t);
+    if (w) *w = x;
+    return at;
+}
+
+// Heads launched side by side: as many as keep `bytes` a head within about a third of L2.
+int head_group(int heads, long long bytes) {
+    return (int)std::max<long long>(1, std::min<long long>(heads, (40ll << 20) / std::max<long long>(bytes, 1)));
+}
+
+template <typename T, int AB, int D>
+kvq_status run_typed(const PrefillBwdCall& c, cudaStream_t s) {
+    using Lay = BwdLayout<D>;
+    CUtensorMap mq, mk, mv, mg;
+    const int dt = AB == 0 ? KVQ_F16 : KVQ_BF16;
+    if (!make_map(&mq, c.q, dt, c.B * c.Hq, c.T, D) || !make_map(&mk, c.k, dt, c.B * c.Hkv, c.T, D) ||
+        !make_map(&mv, c.v, dt, c.B * c.Hkv, c.T, D) || !make_map(&mg, c.go, dt, c.B * c.Hq, c.T, D)) {
+        set_error("prefill_attn_bwd: tensor map encoding failed");
+        return KVQ_ECUDA;
+    }
+    cudaError_t e = cudaFuncSetAttribute(bwd_dkv_kernel<T, AB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Lay::BYTES);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(bwd_dq_kernel<T, AB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::BYTES);
+    if (e == cudaSuccess) {
+        BwdArgs a;
+        ws_layout(c.B, c.Hq, c.Hkv, c.T, (char*)c.ws, &a.ws);
+        a.B = c.B, a.Hq = c.Hq, a.Hkv = c.Hkv, a.T_len = c.T, a.n_t = (c.T + kTile - 1) / kTile;
+        a.sm_scale = c.sm_scale, a.scale_log2 = c.sm_scale * kLog2e;
+        a.group = 1;
+        const int g = c.Hq / c.Hkv;
+        bwd_prep_kernel<T, AB, D><<<dim3(a.n_t, c.B * c.Hq), kPrepThreads, 0, s>>>(
+            (const T*)c.o, (const T*)c.go, (const T*)c.v, c.lse, c.glse, a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) {
+            a.group = head_group(c.B * c.Hkv, (long long)c.T * D * 4 * g);
+            bwd_dkv_kernel<T, AB, D><<<a.n_t * c.B * c.Hkv, kDkvThreads, Lay::BYTES, s>>>(mq, mk, mv, mg, (T*)c.dk,
+                                                                                          (T*)c.dv, a);
+            e = cudaGetLastError();
+        }
+        if (e == cudaSuccess) {
+            a.group = head_group(c.B * c.Hq, (long long)c.T * D * 4 / g);
+            bwd_dq_kernel<T, AB, D><<<a.n_t * c.B * c.Hq, kDqThreads, Lay::BYTES, s>>>(mq, mk, mv, mg, (T*)c.dq, a);
+            e = cudaGetLastError();
+        }
+    }
+    if (e != cudaSuccess) {
+        set_error("prefill_attn_bwd launch: %s", cudaGetErrorString(e));
+        return KVQ_ECUDA;
+    }
+    return KVQ_OK;
+}
+
+}  // namespace
+
+size_t prefill_bwd_bytes(int B, int Hq, int Hkv, int T) { return ws_layout(B, Hq, Hkv, T, nullptr, nullptr); }
+
+kvq_status run_prefill_bwd(const PrefillBwdCall& c, cudaStream_t s) {
+    if (c.dt == KVQ_F16) return c.D == 64 ? run_typed<__half, 0, 64>(c, s) : run_typed<__half, 0, 128>(c, s);
+    return c.D == 64 ? run_typed<__nv_bfloat16, 1, 64>(c, s) : run_typed<__nv_bfloat16, 1, 128>(c, s);
+}
+
+}  // namespace kvq

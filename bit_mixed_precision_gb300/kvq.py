@@ -29,6 +29,7 @@ EXPORTS = ["kv_quant_pack", "prefill_attn_scores", "prefill_window_scores", "kvq
            "kvq_pages_init", "kvq_pages_release",
            "block8_reset", "block8_append", "block8_attn", "block8_attn_workspace_bytes", "block8_select",
            "block8_select_workspace_bytes", "block8_evict",
+           "prefill_attn_bwd", "prefill_attn_bwd_workspace_bytes",
            "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
            "kvq_decode_workspace_bytes", "kvq_decode_launches", "kvq_tier_bytes",
            "kvq_last_error", "kvq_device_status", "kvq_debug_withhold_copy", "kvq_version"]
@@ -130,6 +131,10 @@ def lib():
         L.block8_select_workspace_bytes.argtypes = [cache8, i32]
         L.block8_select_workspace_bytes.restype = sz
         L.block8_evict.argtypes = [cache8, vp, i32, i32, vp, vp]
+        L.prefill_attn_bwd.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, vp, vp, vp, vp, vp,
+                                       sz, vp]
+        L.prefill_attn_bwd_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.prefill_attn_bwd_workspace_bytes.restype = sz
         rope = ctypes.POINTER(KvqRope)
         L.qk_norm_rope.argtypes = [rope, i32, i32, i32, i32, i32, i32, vp, vp, vp, strides, vp, vp, vp, i32, f32, vp, vp,
                                    vp, vp]
@@ -145,7 +150,7 @@ def lib():
         for name in ["kv_quant_pack", "prefill_attn_scores", "prefill_window_scores", "kvq_score_reduce", "select_tokens",
                      "minikv_prefill_build", "requant_demote", "kvq_pages_init", "kvq_pages_release", "decode_attn_qkv", "kvq_device_status", "kvq_debug_withhold_copy",
                      "block8_reset", "block8_append", "block8_attn", "block8_select", "block8_evict",
-                     "qk_norm_rope", "qk_norm_rope_bwd"]:
+                     "prefill_attn_bwd", "qk_norm_rope", "qk_norm_rope_bwd"]:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -1038,3 +1043,37 @@ def _workspace(need, like, ws, stream):
         _bad("ws must be a contiguous uint8 CUDA tensor on q's device")
     shift = -ws.data_ptr() % 256
     return ws.data_ptr() + shift, max(ws.numel() - shift, 0), ws
+
+
+# ----------------------------------------------------------- gradient of prefill attention
+
+def prefill_attn_bwd(do, q, k, v, o, lse, sm_scale=None, dlse=None, out=None, ws=None, stream=None):
+    """Gradients (dq, dk, dv) of q [B, Hq, T, D], k, v [B, Hkv, T, D] through prefill_attn_scores' o and lse: do is the
+    gradient of o, dlse (float32 [B, Hq, T], may be None) that of lse.  All contiguous.  ws: a uint8 workspace of
+    prefill_attn_bwd_ws_bytes(q, k) + 256 bytes to share between calls that never overlap on the GPU."""
+    dt = _dt(q)
+    _check_qk(q, k, v)
+    B, Hq, T, D = q.shape
+    Hkv = k.shape[1]
+    args = [_dense(x, s, q, n, d) for x, s, n, d in (
+        (q, q.shape, "q", None), (k, k.shape, "k", None), (v, k.shape, "v", None), (o, q.shape, "o", None),
+        (do, q.shape, "do", None), (lse, q.shape[:3], "lse", torch.float32), (dlse, q.shape[:3], "dlse", torch.float32))]
+    if None in args[:6]:
+        _bad("do, q, k, v, o and lse are needed")
+    raw = _call_stream(q.get_device(), stream)
+    dq, dk, dv = [_new(x.shape, q, q.dtype, stream) for x in (q, k, k)] if out is None else out
+    outs = [_dense(x, s, q, f"out[{i}]") for i, (x, s) in enumerate(((dq, q.shape), (dk, k.shape), (dv, k.shape)))]
+    wsp, ws_bytes, ws = _workspace(lib().prefill_attn_bwd_workspace_bytes(B, Hq, Hkv, T), q, ws, stream)
+    _check(lib().prefill_attn_bwd(*args[:5], dt, B, Hq, Hkv, T, D, D ** -0.5 if sm_scale is None else float(sm_scale), 1,
+                                  args[5], args[6], *outs, wsp, ws_bytes, raw))
+    if stream is not None:
+        _used8(stream, do, q, k, v, o, lse, dlse, dq, dk, dv, ws)
+    return dq, dk, dv
+
+
+def prefill_attn_bwd_ws_bytes(q, k):
+    """Workspace of prefill_attn_bwd for q [B, Hq, T, D] and k [B, Hkv, T, D]."""
+    need = lib().prefill_attn_bwd_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2])
+    if need == ctypes.c_size_t(-1).value:
+        raise KvqError(KVQ_EINVAL, lib().kvq_last_error().decode())
+    return need

@@ -203,6 +203,27 @@ kvq_status prefill_attn_scores(const void* q, const void* k, const void* v, kvq_
                                void* o, float* lse, float* colscore,
                                void* ws, size_t ws_bytes, void* stream);
 
+/* prefill_attn_bwd -- gradients of q, k and v through prefill_attn_scores' o
+ * and lse (not through its column scores):
+ *   P_ij = exp(sm_scale q_i.k_j - lse_i), j <= i;  delta_i = go_i.o_i - glse_i;
+ *   dS_ij = P_ij (go_i.v_j - delta_i);
+ *   dq_i = sm_scale sum_j dS_ij k_j;  dk_j = sm_scale sum_i dS_ij q_i;
+ *   dv_j = sum_i P_ij go_i, dk and dv summed over the query heads of a group.
+ *   q, k, v, o, lse: the forward call's arguments and results, all finite (the
+ *   tile products also multiply the zeros above the diagonal).  go (device)
+ *   [B, Hq, T, D]: gradient of o; glse (device, nullable) [B, Hq, T]: of lse.
+ *   dq (device) [B, Hq, T, D]; dk, dv (device) [B, Hkv, T, D], no overlap with
+ *   the inputs.  q, k, v, o, go, dq, dk, dv 16-byte aligned.  A row with
+ *   lse = -inf (one that saw nothing) has no gradient.
+ *   ws (device) of prefill_attn_bwd_workspace_bytes(), 256-byte aligned.
+ * Sums are float32; P and dS enter their products in the activations' type.
+ * A call repeats itself bit for bit. */
+kvq_status prefill_attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* go,
+                            kvq_dtype dt, int B, int Hq, int Hkv, int T, int D, float sm_scale, int causal,
+                            const float* lse, const float* glse, void* dq, void* dk, void* dv, void* ws,
+                            size_t ws_bytes, void* stream);
+size_t prefill_attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int T);
+
 /* prefill_window_scores -- column scores over an observation window of the
  * last queries, SnapKV-style ([MiniKV-J]: SnapKV is a LongBench baseline and
  * the SnapKV + KIVI combination the failure that drops 35 to 32 points; the

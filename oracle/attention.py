@@ -152,3 +152,27 @@ def decode_head(q, keys, values, sm_scale):
     l = e.sum()
     p = e / l
     return p @ _f64(values), float(m + np.log(l)), p
+
+
+def prefill_backward(q, k, v, o, do, lse, sm_scale, dlse=None):
+    """Gradients of one KV head's group through causal attention, float64: q, o, do [g, T, D], k, v [T, D], lse (and dlse)
+    [g, T] as the forward pass gave them.  Returns dq [g, T, D], dk, dv [T, D] and, for error bounds, the terms they
+    are sums of: lists over the group of (P, do v^T, delta, dS) matrices.
+
+    With z_ij = sigma q_i.k_j and P = exp(z - lse) below and on the diagonal: dv = P^T do; the softmax's Jacobian gives
+    dz = P (do v^T - delta) with delta_i = do_i.o_i, less dlse_i because d lse_i / d z_ij = P_ij."""
+    q, k, v, o, do, lse = (_f64(x) for x in (q, k, v, o, do, lse))
+    dq, dk, dv, terms = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v), []
+    keep = np.tril(np.ones((k.shape[0], k.shape[0]), dtype=bool))
+    for h in range(q.shape[0]):
+        z = q[h] @ k.T * F64(sm_scale)
+        row = np.where(np.isinf(lse[h]), np.inf, lse[h])[:, None]
+        P = np.where(keep, np.exp(np.where(keep, z, 0.0) - row), 0.0)
+        dP = do[h] @ v.T
+        delta = (do[h] * o[h]).sum(-1, keepdims=True) - (0.0 if dlse is None else _f64(dlse[h])[:, None])
+        dS = P * (dP - delta)
+        dv += P.T @ do[h]
+        dk += dS.T @ q[h] * F64(sm_scale)
+        dq[h] = dS @ k * F64(sm_scale)
+        terms.append((P, dP, delta, dS))
+    return dq, dk, dv, terms
