@@ -12,8 +12,8 @@
 //        they replace S^T and dP^T.  The tensor pipe runs what one thread issues in order, so S^T of the next tile may
 //        be issued right behind the dV product that reads P^T from its place.
 //   dq:  CTA = (query head, query tile), over the key tiles up to the diagonal: S = Q K^T, dP = dO V^T, dQ += dS K.
-// Eight warps do the exponentials and dS (two warpgroups, each half of a tile's columns, a thread per row), one warp
-// issues the copies, one the products, in dkv one brings the rows' lse and delta.
+// Sixteen warps do the exponentials and dS (four warpgroups, each a quarter of a tile's columns, a thread per row), one
+// warp issues the copies, one the products, in dkv one brings the rows' lse and delta.
 // A first kernel computes delta and brings lse to base 2.
 //
 // Rounding: P and dS enter their products in the inputs' type.  In bf16 that is 2^-9 of each term, as much as the
@@ -36,7 +36,7 @@ KVQ_DEFINE_STATUS(prefill_bwd)
 
 namespace {
 
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 16;                        // four warpgroups, each a quarter of a tile's columns
 constexpr int kDkvThreads = 32 * (kSoftWarps + 3);   // + copies, products, row statistics
 constexpr int kDqThreads = 32 * (kSoftWarps + 2);
 constexpr int kPrepThreads = 256;
@@ -201,18 +201,39 @@ template <int D> struct BwdLayout {
     static constexpr uint32_t S1 = S0 + 3 * kTileBytes;         // 2 stages: dO (dkv), V (dq)
     static constexpr uint32_t STAT = S1 + 2 * kTileBytes;       // dkv: 2 stages of 128 (nlse) and 128 (delta) floats
     static constexpr uint32_t RED = STAT + 2048;
-    static constexpr uint32_t BAR = RED + 12 * 12 + 48;
+    static constexpr uint32_t BAR = RED + 256;                  // 3 floats a warp
     // no alignment slack at D = 128: the kernels require (and check) a 1024-aligned base
     static constexpr uint32_t BYTES = BAR + 256;
 };
 static_assert(BwdLayout<128>::BYTES <= 232448, "shared memory");
 
-// 32 columns of a thread's row: exponentials, packed pairs.
-template <typename T> __device__ __forceinline__ void store_pairs(uint32_t taddr, const float* x) {
-    float w[32];
+// C = A B^T of two K-major tiles of 128 rows (one thread).
+template <int D> __device__ __forceinline__ void products_k(uint32_t c, uint32_t ta, uint32_t tb, uint32_t idesc) {
+    const uint64_t da = kmajor_desc(ta, 0), db = kmajor_desc(tb, 0);
 #pragma unroll
-    for (int c = 0; c < 32; ++c) w[c] = __uint_as_float(Pack2<T>::pack(x[2 * c], x[2 * c + 1]));
-    tmem_st32(taddr, w);
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = ((uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32u) >> 4;
+        tc_mma_f16(c, da + off, db + off, idesc, kk > 0);
+    }
+}
+
+// C (+)= A B, A [128, 128] packed pairs in tensor memory (every 32 values in 16 columns, STEP columns apart), B a tile of
+// 128 rows (one thread).
+template <int STEP>
+__device__ __forceinline__ void products_mn(uint32_t c, uint32_t ta, uint32_t tb, uint32_t idesc, bool accumulate) {
+    const uint64_t db = mnmajor_desc(tb, 0);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        tc_mma_f16_ta(c, ta + (uint32_t)(kk >> 1) * STEP + (uint32_t)(kk & 1) * 8u, db + (uint64_t)(kk * 16 * 128 >> 4), idesc,
+                      accumulate || kk > 0);
+}
+
+// 32 values of a thread's row as 16 columns of packed pairs.
+template <typename T> __device__ __forceinline__ void store_pairs(uint32_t taddr, const float* x) {
+    uint32_t w[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) w[c] = Pack2<T>::pack(x[2 * c], x[2 * c + 1]);
+    tmem_st16(taddr, w);
 }
 
 // One thread's row of D float32 TMEM columns, times f, to `out` in T.
@@ -261,7 +282,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR + 8 * DKV_NBAR + 4);
     float* red = reinterpret_cast<float*>(smem + Lay::RED);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     int kt, u;
     place(a, a.B * a.Hkv, kt, u);
     const int g = a.Hq / a.Hkv, h0 = u * g;             // head u * g + h of all B * Hq is the unit's h-th
@@ -285,7 +306,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
     const float c = scale_of<AB>(red);
 
@@ -320,52 +341,52 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                 if (lastg[s] >= 0) mbar_wait(BAR(V_GF + s), lastg[s] & 1, nullptr);
         }
     } else if (warp == kSoftWarps + 1) {
-        if (lane == 0) {
-            const uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
-            auto scores = [&](int it) -> bool {         // S^T = K Q^T
-                if (!mbar_wait(BAR(V_QF + it % 3), (it / 3) & 1, abort_flag)) return false;
-                tc_fence_after();
-                const uint32_t t = sQ + (uint32_t)(it % 3) * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) tc_mma_f16(tS, kmajor_desc(sK, kk), kmajor_desc(t, kk), idS, kk > 0);
+        constexpr uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
+        auto scores = [&](int it) -> bool {             // S^T = K Q^T
+            if (!bwd_wait(BAR(V_QF + it % 3), (it / 3) & 1, abort_flag)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                products_k<D>(tS, sK, sQ + (uint32_t)(it % 3) * kTileBytes, idS);
                 tc_commit(BAR(V_SF));
-                return true;
-            };
-            auto grads = [&](int it) -> bool {          // dP^T = V dO^T
-                if (!mbar_wait(BAR(V_GF + (it & 1)), (it / 2) & 1, abort_flag)) return false;
-                tc_fence_after();
-                const uint32_t t = sG + (uint32_t)(it & 1) * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) tc_mma_f16(tP, kmajor_desc(sV, kk), kmajor_desc(t, kk), idS, kk > 0);
-                tc_commit(BAR(V_DF));
-                return true;
-            };
-            bool ok = mbar_wait(BAR(V_KV), 0, abort_flag) && scores(0) && grads(0);
-            for (int it = 0; ok && it < n; ++it) {
-                // P^T and dS^T: queries 0-63 in the first 32 columns of their place, 64-127 from column 64 on
-                if (!(ok = mbar_wait(BAR(V_PR), it & 1, abort_flag))) break;
-                tc_fence_after();
-                const uint32_t tg_ = sG + (uint32_t)(it & 1) * kTileBytes, tq_ = sQ + (uint32_t)(it % 3) * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_f16_ta(tDV, tS + (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u, mnmajor_desc(tg_, kk), idD,
-                                  it > 0 || kk > 0);
-                tc_commit(BAR(V_GE + (it & 1)));
-                if (it + 1 < n && !(ok = scores(it + 1))) break;
-                if (!(ok = mbar_wait(BAR(V_DR), it & 1, abort_flag))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_f16_ta(tDK, tP + (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u, mnmajor_desc(tq_, kk), idD,
-                                  it > 0 || kk > 0);
-                tc_commit(BAR(V_QE + it % 3));
-                if (it + 1 < n && !(ok = grads(it + 1))) break;
             }
-            if (!ok) bwd_give_up(abort_flag);
-            // all products complete before the sums are read and TMEM is released
-            tc_commit(BAR(V_END));
-            mbar_wait(BAR(V_END), 0, nullptr);
+            __syncwarp();
+            return true;
+        };
+        auto grads = [&](int it) -> bool {              // dP^T = V dO^T
+            if (!bwd_wait(BAR(V_GF + (it & 1)), (it / 2) & 1, abort_flag)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                products_k<D>(tP, sV, sG + (uint32_t)(it & 1) * kTileBytes, idS);
+                tc_commit(BAR(V_DF));
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = bwd_wait(BAR(V_KV), 0, abort_flag) && scores(0) && grads(0);
+        for (int it = 0; ok && it < n; ++it) {
+            // P^T and dS^T: every 32 queries in the first 16 of the 32 columns that their scores had
+            if (!(ok = bwd_wait(BAR(V_PR), it & 1, abort_flag))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                products_mn<32>(tDV, tS, sG + (uint32_t)(it & 1) * kTileBytes, idD, it > 0);
+                tc_commit(BAR(V_GE + (it & 1)));
+            }
+            __syncwarp();
+            if (it + 1 < n && !(ok = scores(it + 1))) break;
+            if (!(ok = bwd_wait(BAR(V_DR), it & 1, abort_flag))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                products_mn<32>(tDK, tP, sQ + (uint32_t)(it % 3) * kTileBytes, idD, it > 0);
+                tc_commit(BAR(V_QE + it % 3));
+            }
+            __syncwarp();
+            if (it + 1 < n && !(ok = grads(it + 1))) break;
         }
+        if (!ok) bwd_give_up(abort_flag);
+        // all products complete before the sums are read and TMEM is released
+        if (elect_one()) tc_commit(BAR(V_END));
+        __syncwarp();
+        bwd_wait(BAR(V_END), 0, nullptr);
     } else if (warp == kSoftWarps + 2) {
         // the query rows' statistics, delta times c
         bool ok = true;
@@ -384,26 +405,25 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         }
         if (!ok) bwd_give_up(abort_flag);
     } else {
-        // thread r of either warpgroup owns key r (TMEM lane r) and queries 64 wg .. 64 wg + 63 of each tile
+        // thread r of warpgroup wg owns key r (TMEM lane r) and queries 32 wg .. 32 wg + 31 of each tile
         const int wg = warp >> 2, r = threadIdx.x & 127, j = kt * kTile + r;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t mine = lanes + 64u * (uint32_t)wg;
+        const uint32_t mine = lanes + 32u * (uint32_t)wg;
         const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
             const bool diag = it % m == 0;
             if (!bwd_wait(BAR(V_TF + s), (it / 2) & 1, abort_flag)) { ok = false; break; }
-            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * 1024 + 256 * wg);
+            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * 1024 + 128 * wg);
             const ulonglong2* nd = nl + 32;
             if (!bwd_wait(BAR(V_SF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            float p[64];
+            float p[32];
             tmem_ld32(tS + mine, p);
-            tmem_ld32(tS + mine + 32u, p + 32);
             tmem_wait_ld();
 #pragma unroll
-            for (int q4 = 0; q4 < 16; ++q4) {
+            for (int q4 = 0; q4 < 8; ++q4) {
                 const ulonglong2 x = nl[q4];
                 float e0, e1, e2, e3;
                 f2_unpack(f2_fma(f2_pack(p[4 * q4], p[4 * q4 + 1]), sc2, x.x), e0, e1);
@@ -413,7 +433,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             }
             if (diag) {
 #pragma unroll
-                for (int q = 0; q < 64; ++q) p[q] = 64 * wg + q >= r ? p[q] : 0.0f;
+                for (int q = 0; q < 32; ++q) p[q] = 32 * wg + q >= r ? p[q] : 0.0f;
             }
             store_pairs<T>(tS + mine, p);
             tmem_wait_st();
@@ -422,12 +442,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             if (lane == 0) mbar_arrive(BAR(V_PR));
             if (!bwd_wait(BAR(V_DF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            float d[64];
+            float d[32];
             tmem_ld32(tP + mine, d);
-            tmem_ld32(tP + mine + 32u, d + 32);
             tmem_wait_ld();
 #pragma unroll
-            for (int q4 = 0; q4 < 16; ++q4) {
+            for (int q4 = 0; q4 < 8; ++q4) {
                 const ulonglong2 x = nd[q4];
                 float e0, e1, e2, e3;
                 f2_unpack(f2_fma(f2_pack(d[4 * q4], d[4 * q4 + 1]), c2, x.x), e0, e1);
@@ -437,7 +456,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             }
             if (diag) {
 #pragma unroll
-                for (int q = 0; q < 64; ++q) d[q] = 64 * wg + q >= r ? d[q] : 0.0f;
+                for (int q = 0; q < 32; ++q) d[q] = 32 * wg + q >= r ? d[q] : 0.0f;
             }
             store_pairs<T>(tP + mine, d);
             tmem_wait_st();
@@ -451,11 +470,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         if (!ok) bwd_give_up(abort_flag);
         ok = bwd_wait(BAR(V_END), 0, nullptr) && ok && !*abort_flag;
         tc_fence_after();
-        // warpgroup 0 stores dV, warpgroup 1 dK
+        // warpgroups 0 and 1 store the halves of dV, 2 and 3 those of dK
         const int64_t row = (int64_t)u * a.T_len + (j < a.T_len ? j : 0);
         const float unshift = AB == 0 ? 0x1p-15f : 1.0f;
-        if (wg == 0) store_row<T, D>(tDV + lanes, unshift, ok && j < a.T_len, dv + row * D);
-        else store_row<T, D>(tDK + lanes, a.sm_scale * unshift / c, ok && j < a.T_len, dk + row * D);
+        const uint32_t half = lanes + (uint32_t)((wg & 1) * (D / 2));
+        if (wg < 2) store_row<T, D / 2>(tDV + half, unshift, ok && j < a.T_len, dv + row * D + (wg & 1) * (D / 2));
+        else store_row<T, D / 2>(tDK + half, a.sm_scale * unshift / c, ok && j < a.T_len, dk + row * D + (wg & 1) * (D / 2));
     }
     tc_fence_before();
     __syncthreads();
@@ -488,7 +508,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR + 8 * DQ_NBAR + 4);
     float* red = reinterpret_cast<float*>(smem + Lay::RED);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     int rank, bh;
     place(a, a.B * a.Hq, rank, bh);
     const int qt = a.n_t - 1 - rank, n = qt + 1;
@@ -512,7 +532,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     // S, dP, two buffers of dS (64 columns each), dQ
     const uint32_t tS = tmem, tP = tmem + 128, tDS = tmem + 256, tDQ = tmem + 384;
     const float c = scale_of<AB>(red);
@@ -547,52 +567,52 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 if (lastv[s] >= 0) mbar_wait(BAR(W_VF + s), lastv[s] & 1, nullptr);
         }
     } else if (warp == kSoftWarps + 1) {
-        if (lane == 0) {
-            const uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
-            auto scores = [&](int it) -> bool {         // S = Q K^T
-                if (!mbar_wait(BAR(W_KF + it % 3), (it / 3) & 1, abort_flag)) return false;
-                if (it > 0 && !mbar_wait(BAR(W_SC), (it - 1) & 1, abort_flag)) return false;
-                tc_fence_after();
-                const uint32_t t = sK + (uint32_t)(it % 3) * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) tc_mma_f16(tS, kmajor_desc(sQ, kk), kmajor_desc(t, kk), idS, kk > 0);
+        constexpr uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
+        auto scores = [&](int it) -> bool {             // S = Q K^T
+            if (!bwd_wait(BAR(W_KF + it % 3), (it / 3) & 1, abort_flag)) return false;
+            if (it > 0 && !bwd_wait(BAR(W_SC), (it - 1) & 1, abort_flag)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                products_k<D>(tS, sQ, sK + (uint32_t)(it % 3) * kTileBytes, idS);
                 tc_commit(BAR(W_SF));
-                return true;
-            };
-            auto grads = [&](int it) -> bool {          // dP = dO V^T
-                if (!mbar_wait(BAR(W_VF + (it & 1)), (it / 2) & 1, abort_flag)) return false;
-                if (it > 0 && !mbar_wait(BAR(W_DC), (it - 1) & 1, abort_flag)) return false;
-                tc_fence_after();
-                const uint32_t t = sV + (uint32_t)(it & 1) * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) tc_mma_f16(tP, kmajor_desc(sG, kk), kmajor_desc(t, kk), idS, kk > 0);
+            }
+            __syncwarp();
+            return true;
+        };
+        auto grads = [&](int it) -> bool {              // dP = dO V^T
+            if (!bwd_wait(BAR(W_VF + (it & 1)), (it / 2) & 1, abort_flag)) return false;
+            if (it > 0 && !bwd_wait(BAR(W_DC), (it - 1) & 1, abort_flag)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                products_k<D>(tP, sG, sV + (uint32_t)(it & 1) * kTileBytes, idS);
                 tc_commit(BAR(W_DF));
                 tc_commit(BAR(W_VE + (it & 1)));
-                return true;
-            };
-            bool ok = mbar_wait(BAR(W_QG), 0, abort_flag) && scores(0) && grads(0);
-            for (int it = 0; ok && it < n; ++it) {
-                if (it + 1 < n && !(ok = scores(it + 1) && grads(it + 1))) break;
-                const int s = it & 1;
-                if (!(ok = mbar_wait(BAR(W_DR + s), (it / 2) & 1, abort_flag))) break;
-                tc_fence_after();
-                const uint32_t t = sK + (uint32_t)(it % 3) * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_f16_ta(tDQ, tDS + 64u * (uint32_t)s + (uint32_t)kk * 8u, mnmajor_desc(t, kk), idD,
-                                  it > 0 || kk > 0);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = bwd_wait(BAR(W_QG), 0, abort_flag) && scores(0) && grads(0);
+        for (int it = 0; ok && it < n; ++it) {
+            if (it + 1 < n && !(ok = scores(it + 1) && grads(it + 1))) break;
+            const int s = it & 1;
+            if (!(ok = bwd_wait(BAR(W_DR + s), (it / 2) & 1, abort_flag))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                products_mn<16>(tDQ, tDS + 64u * (uint32_t)s, sK + (uint32_t)(it % 3) * kTileBytes, idD, it > 0);
                 tc_commit(BAR(W_KE + it % 3));
                 tc_commit(BAR(W_DE + s));
             }
-            if (!ok) bwd_give_up(abort_flag);
-            tc_commit(BAR(W_END));
-            mbar_wait(BAR(W_END), 0, nullptr);
+            __syncwarp();
         }
+        if (!ok) bwd_give_up(abort_flag);
+        if (elect_one()) tc_commit(BAR(W_END));
+        __syncwarp();
+        bwd_wait(BAR(W_END), 0, nullptr);
     } else {
-        // thread r of either warpgroup owns query r and keys 64 wg .. 64 wg + 63 of each tile
+        // thread r of warpgroup wg owns query r and keys 32 wg .. 32 wg + 31 of each tile
         const int wg = warp >> 2, r = threadIdx.x & 127, i = qt * kTile + r;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t mine = lanes + 64u * (uint32_t)wg;
+        const uint32_t mine = lanes + 32u * (uint32_t)wg;
         const int64_t stat = (int64_t)bh * a.n_t * kTile + i;
         const float nl = a.ws.nlse[stat], nd = -c * a.ws.delta[stat];
         const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
@@ -603,41 +623,39 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             const bool diag = it == qt;
             if (!bwd_wait(BAR(W_SF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            float p[64];
+            float p[32];
             tmem_ld32(tS + mine, p);
-            tmem_ld32(tS + mine + 32u, p + 32);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(W_SC));
 #pragma unroll
-            for (int q = 0; q < 64; q += 2) {
+            for (int q = 0; q < 32; q += 2) {
                 float e0, e1;
                 f2_unpack(f2_fma(f2_pack(p[q], p[q + 1]), sc2, nl2), e0, e1);
                 p[q] = ex2_approx(e0), p[q + 1] = ex2_approx(e1);
             }
             if (!bwd_wait(BAR(W_DF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            float d[64];
+            float d[32];
             tmem_ld32(tP + mine, d);
-            tmem_ld32(tP + mine + 32u, d + 32);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(W_DC));
 #pragma unroll
-            for (int q = 0; q < 64; q += 2) {
+            for (int q = 0; q < 32; q += 2) {
                 float e0, e1;
                 f2_unpack(f2_fma(f2_pack(d[q], d[q + 1]), c2, nd2), e0, e1);
                 d[q] = p[q] * e0, d[q + 1] = p[q + 1] * e1;
             }
             if (diag) {
 #pragma unroll
-                for (int q = 0; q < 64; ++q) d[q] = 64 * wg + q <= r ? d[q] : 0.0f;
+                for (int q = 0; q < 32; ++q) d[q] = 32 * wg + q <= r ? d[q] : 0.0f;
             }
             if (it >= 2 && !bwd_wait(BAR(W_DE + s), (it / 2 - 1) & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            store_pairs<T>(tDS + lanes + 64u * (uint32_t)s + 32u * (uint32_t)wg, d);
+            store_pairs<T>(tDS + lanes + 64u * (uint32_t)s + 16u * (uint32_t)wg, d);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -646,11 +664,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         if (!ok) bwd_give_up(abort_flag);
         ok = bwd_wait(BAR(W_END), 0, nullptr) && ok && !*abort_flag;
         tc_fence_after();
-        // each warpgroup stores half of the columns
+        // 32 columns a warpgroup
         const int64_t row = (int64_t)bh * a.T_len + (i < a.T_len ? i : 0);
         const float f = a.sm_scale * (AB == 0 ? 0x1p-15f : 1.0f) / c;
-        if (D == 128) store_row<T, 64>(tDQ + mine, f, ok && i < a.T_len, dq + row * D + 64 * wg);
-        else store_row<T, 32>(tDQ + lanes + 32u * (uint32_t)wg, f, ok && i < a.T_len, dq + row * D + 32 * wg);
+        if (32 * wg < D) store_row<T, 32>(tDQ + mine, f, ok && i < a.T_len, dq + row * D + 32 * wg);
     }
     tc_fence_before();
     __syncthreads();
