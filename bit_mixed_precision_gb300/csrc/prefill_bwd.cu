@@ -12,8 +12,8 @@
 //        they replace S^T and dP^T.  The tensor pipe runs what one thread issues in order, so S^T of the next tile may
 //        be issued right behind the dV product that reads P^T from its place.
 //   dq:  CTA = (query head, query tile), over the key tiles up to the diagonal: S = Q K^T, dP = dO V^T, dQ += dS K.
-// Sixteen warps do the exponentials and dS (four warpgroups, each a quarter of a tile's columns, a thread per row), one
-// warp issues the copies, one the products, in dkv one brings the rows' lse and delta.
+// Sixteen warps do the exponentials and dS (four warpgroups, each a quarter of a tile's columns), one warp issues the
+// copies, one the products, in dkv one brings the rows' lse and delta.
 // A first kernel computes delta and brings lse to base 2.
 //
 // Rounding: P and dS enter their products in the inputs' type.  In bf16 that is 2^-9 of each term, as much as the
@@ -25,6 +25,7 @@
 // Every mbarrier wait is bounded; a CTA that gives up drains its copies and products, frees TMEM, stores nothing and
 // records KVQ_ETIMEOUT in the device status word.
 #include <algorithm>
+#include <type_traits>
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
@@ -66,6 +67,8 @@ __device__ __forceinline__ void bwd_give_up(volatile int* abort_flag) {
     *abort_flag = 1;
     atomicOr(&g_status_prefill_bwd, kDevTimeout);
 }
+
+template <int N> using Int = std::integral_constant<int, N>;
 
 // Probabilities are kept times 2^kShift.
 template <int AB> struct Shift { static constexpr float value = AB == 0 ? 15.0f : 0.0f; };
@@ -193,12 +196,13 @@ __device__ __forceinline__ void place(const BwdArgs& a, int heads, int& rank, in
     head = g * a.group + in % size;
 }
 
-// Shared memory of both kernels: K, V (dkv) or Q, dO (dq) once, three and two stages of the streamed operands.
+// Shared memory of both kernels: dkv has K, V, three stages of Q and two of dO; dq has dO, four stages of K (from A1 on)
+// and two of V.
 template <int D> struct BwdLayout {
     static constexpr uint32_t kTileBytes = kTile * D * 2;
     static constexpr uint32_t A0 = 0, A1 = kTileBytes;
-    static constexpr uint32_t S0 = 2 * kTileBytes;              // 3 stages: Q (dkv), K (dq)
-    static constexpr uint32_t S1 = S0 + 3 * kTileBytes;         // 2 stages: dO (dkv), V (dq)
+    static constexpr uint32_t S0 = 2 * kTileBytes;
+    static constexpr uint32_t S1 = S0 + 3 * kTileBytes;
     static constexpr uint32_t STAT = S1 + 2 * kTileBytes;       // dkv: 2 stages of 128 (nlse) and 128 (delta) floats
     static constexpr uint32_t RED = STAT + 2048;
     static constexpr uint32_t BAR = RED + 256;                  // 3 floats a warp
@@ -214,6 +218,16 @@ template <int D> __device__ __forceinline__ void products_k(uint32_t c, uint32_t
     for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = ((uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32u) >> 4;
         tc_mma_f16(c, da + off, db + off, idesc, kk > 0);
+    }
+}
+
+// The same with A packed in tensor memory.
+template <int D> __device__ __forceinline__ void products_k_ta(uint32_t c, uint32_t ta, uint32_t tb, uint32_t idesc) {
+    const uint64_t db = kmajor_desc(tb, 0);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = ((uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32u) >> 4;
+        tc_mma_f16_ta(c, ta + (uint32_t)kk * 8u, db + off, idesc, kk > 0);
     }
 }
 
@@ -260,7 +274,7 @@ template <typename T, int D> __device__ __forceinline__ void store_row(uint32_t 
 // ------------------------------------------------------------------ dK and dV
 
 enum DkvBar { V_KV = 0, V_QF = 1, V_QE = 4, V_GF = 7, V_GE = 9, V_TF = 11, V_TE = 13, V_SF = 15, V_PR = 16, V_DF = 17,
-              V_DR = 18, V_END = 19, DKV_NBAR = 20 };
+              V_DR = 18, V_END = 19, V_SC = 20, V_DC = 21, DKV_NBAR = 22 };
 
 template <typename T, int AB, int D>
 __global__ void __launch_bounds__(kDkvThreads, 1)
@@ -298,6 +312,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         mbar_init(BAR(V_SF), 1), mbar_init(BAR(V_PR), kSoftWarps);
         mbar_init(BAR(V_DF), 1), mbar_init(BAR(V_DR), kSoftWarps);
         mbar_init(BAR(V_END), 1);
+        mbar_init(BAR(V_SC), kSoftWarps), mbar_init(BAR(V_DC), kSoftWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -307,7 +322,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    // S^T, dP^T, dV, dK; packed P^T and dS^T have places of their own at D = 64, at D = 128 they replace S^T and dP^T
+    constexpr bool kApart = D == 64;
+    constexpr uint32_t kStep = kApart ? 16 : 32;        // columns between the packed 32 queries of two warpgroups
     const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
+    const uint32_t tPq = kApart ? tmem + 384 : tS, tDS = kApart ? tmem + 448 : tP;
     const float c = scale_of<AB>(red);
 
     if (warp == kSoftWarps) {
@@ -342,45 +361,73 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         }
     } else if (warp == kSoftWarps + 1) {
         constexpr uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
-        auto scores = [&](int it) -> bool {             // S^T = K Q^T
-            if (!bwd_wait(BAR(V_QF + it % 3), (it / 3) & 1, abort_flag)) return false;
+        // (one lane) S^T = K Q^T, dP^T = V dO^T with the streamed tile in stage s
+        auto scores = [&](int s) {
+            products_k<D>(tS, sK, sQ + (uint32_t)s * kTileBytes, idS);
+            tc_commit(BAR(V_SF));
+        };
+        auto grads = [&](int s) {
+            products_k<D>(tP, sV, sG + (uint32_t)s * kTileBytes, idS);
+            tc_commit(BAR(V_DF));
+        };
+        auto q_there = [&](int it, int s) { return bwd_wait(BAR(V_QF + s), (it / 3) & 1, abort_flag); };
+        auto g_there = [&](int it, int s) { return bwd_wait(BAR(V_GF + s), (it / 2) & 1, abort_flag); };
+        bool ok = bwd_wait(BAR(V_KV), 0, abort_flag) && q_there(0, 0) && g_there(0, 0) && (n == 1 || q_there(1, 1));
+        if (ok) {
+            if (elect_one()) scores(0), grads(0);
+            __syncwarp();
+        }
+        // One tile, PH = it mod 6: the stages are constants, so that descriptors stay in uniform registers (computed from
+        // the tile's number they made a product's issue three times as long).
+        // The next S^T and dP^T are issued as soon as theirs has been read (kApart), or behind the product that reads what
+        // replaced it.  A wait costs one to three products' time even where there is nothing to wait for, and the tensor
+        // pipe has about four products ahead of it: no two waits follow one another without products between.
+        auto step = [&](auto phase, int it) -> bool {
+            constexpr int PH = decltype(phase)::value, q0 = PH % 3, q1 = (PH + 1) % 3, q2 = (PH + 2) % 3, g0 = PH & 1, g1 = g0 ^ 1;
+            const bool more = it + 1 < n;
+            if (kApart && more) {
+                if (!bwd_wait(BAR(V_SC), PH & 1, abort_flag)) return false;
+                tc_fence_after();
+                if (elect_one()) scores(q1);
+                __syncwarp();
+            }
+            if (!bwd_wait(BAR(V_PR), PH & 1, abort_flag)) return false;
             tc_fence_after();
-            if (elect_one()) {
-                products_k<D>(tS, sK, sQ + (uint32_t)(it % 3) * kTileBytes, idS);
-                tc_commit(BAR(V_SF));
+            if (elect_one()) {                          // dV += P^T dO
+                products_mn<kStep>(tDV, tPq, sG + (uint32_t)g0 * kTileBytes, idD, it > 0);
+                tc_commit(BAR(V_GE + g0));
             }
             __syncwarp();
+            if (more) {
+                if (!g_there(it + 1, g1)) return false;
+                if (kApart) {
+                    if (!bwd_wait(BAR(V_DC), PH & 1, abort_flag)) return false;
+                    tc_fence_after();
+                }
+                if (elect_one()) {
+                    if (kApart) grads(g1);
+                    else scores(q1);
+                }
+                __syncwarp();
+            }
+            if (!bwd_wait(BAR(V_DR), PH & 1, abort_flag)) return false;
+            tc_fence_after();
+            if (elect_one()) {                          // dK += dS^T Q
+                products_mn<kStep>(tDK, tDS, sQ + (uint32_t)q0 * kTileBytes, idD, it > 0);
+                tc_commit(BAR(V_QE + q0));
+            }
+            __syncwarp();
+            if (it + 2 < n && !q_there(it + 2, q2)) return false;
+            if (!kApart && more) {
+                if (elect_one()) grads(g1);
+                __syncwarp();
+            }
             return true;
         };
-        auto grads = [&](int it) -> bool {              // dP^T = V dO^T
-            if (!bwd_wait(BAR(V_GF + (it & 1)), (it / 2) & 1, abort_flag)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-                products_k<D>(tP, sV, sG + (uint32_t)(it & 1) * kTileBytes, idS);
-                tc_commit(BAR(V_DF));
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = bwd_wait(BAR(V_KV), 0, abort_flag) && scores(0) && grads(0);
-        for (int it = 0; ok && it < n; ++it) {
-            // P^T and dS^T: every 32 queries in the first 16 of the 32 columns that their scores had
-            if (!(ok = bwd_wait(BAR(V_PR), it & 1, abort_flag))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                products_mn<32>(tDV, tS, sG + (uint32_t)(it & 1) * kTileBytes, idD, it > 0);
-                tc_commit(BAR(V_GE + (it & 1)));
-            }
-            __syncwarp();
-            if (it + 1 < n && !(ok = scores(it + 1))) break;
-            if (!(ok = bwd_wait(BAR(V_DR), it & 1, abort_flag))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                products_mn<32>(tDK, tP, sQ + (uint32_t)(it % 3) * kTileBytes, idD, it > 0);
-                tc_commit(BAR(V_QE + it % 3));
-            }
-            __syncwarp();
-            if (it + 1 < n && !(ok = grads(it + 1))) break;
+        for (int it = 0; ok && it < n; it += 6) {
+            ok = step(Int<0>{}, it) && (it + 1 >= n || step(Int<1>{}, it + 1)) && (it + 2 >= n || step(Int<2>{}, it + 2)) &&
+                 (it + 3 >= n || step(Int<3>{}, it + 3)) && (it + 4 >= n || step(Int<4>{}, it + 4)) &&
+                 (it + 5 >= n || step(Int<5>{}, it + 5));
         }
         if (!ok) bwd_give_up(abort_flag);
         // all products complete before the sums are read and TMEM is released
@@ -405,37 +452,55 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         }
         if (!ok) bwd_give_up(abort_flag);
     } else {
-        // thread r of warpgroup wg owns key r (TMEM lane r) and queries 32 wg .. 32 wg + 31 of each tile
+        // Warpgroup wg has queries 32 wg .. 32 wg + 31 of each tile, warp w of it keys 32 w .. 32 w + 31, in fragments: a
+        // thread has 4 keys and 8 queries, so that it needs the statistics of 8 queries only (with a thread per key the
+        // broadcasts of 32 took as many cycles of shared memory as the tensor pipe's operands left).
         const int wg = warp >> 2, r = threadIdx.x & 127, j = kt * kTile + r;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t mine = lanes + 32u * (uint32_t)wg;
+        const uint32_t mine = lanes + 32u * (uint32_t)wg, packed = lanes + kStep * (uint32_t)wg;
+        const int first = 32 * wg + 2 * (lane & 3) - (32 * (warp & 3) + (lane >> 2));    // query - key of element 0
         const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
             const bool diag = it % m == 0;
             if (!bwd_wait(BAR(V_TF + s), (it / 2) & 1, abort_flag)) { ok = false; break; }
-            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(smem + Lay::STAT + s * 1024 + 128 * wg);
-            const ulonglong2* nd = nl + 32;
+            const unsigned long long* stat =
+                reinterpret_cast<const unsigned long long*>(smem + Lay::STAT + s * 1024 + 128 * wg) + (lane & 3);
+            unsigned long long nl[4], nd[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) nl[t] = stat[4 * t], nd[t] = stat[64 + 4 * t];
             if (!bwd_wait(BAR(V_SF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            float p[32];
-            tmem_ld32(tS + mine, p);
+            float p[32];                                // [16 keys][tile of 8 queries][8 keys][2 queries]
+            tmem_ld_frag32(tS + mine, p);
+            tmem_ld_frag32(tS + mine + (16u << 16), p + 16);
             tmem_wait_ld();
+            if (kApart) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(V_SC));
+            }
+            uint32_t w[16];
 #pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4) {
-                const ulonglong2 x = nl[q4];
-                float e0, e1, e2, e3;
-                f2_unpack(f2_fma(f2_pack(p[4 * q4], p[4 * q4 + 1]), sc2, x.x), e0, e1);
-                f2_unpack(f2_fma(f2_pack(p[4 * q4 + 2], p[4 * q4 + 3]), sc2, x.y), e2, e3);
-                p[4 * q4] = ex2_approx(e0), p[4 * q4 + 1] = ex2_approx(e1);
-                p[4 * q4 + 2] = ex2_approx(e2), p[4 * q4 + 3] = ex2_approx(e3);
+            for (int i = 0; i < 32; i += 2) {
+                float e0, e1;
+                f2_unpack(f2_fma(f2_pack(p[i], p[i + 1]), sc2, nl[(i >> 2) & 3]), e0, e1);
+                p[i] = ex2_approx(e0), p[i + 1] = ex2_approx(e1);
             }
             if (diag) {
 #pragma unroll
-                for (int q = 0; q < 32; ++q) p[q] = 32 * wg + q >= r ? p[q] : 0.0f;
+                for (int i = 0; i < 32; ++i)
+                    p[i] = first + 8 * ((i >> 2) & 3) + (i & 1) - 16 * (i >> 4) - 8 * ((i >> 1) & 1) >= 0 ? p[i] : 0.0f;
             }
-            store_pairs<T>(tS + mine, p);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = Pack2<T>::pack(p[2 * i], p[2 * i + 1]);
+            if (kApart) {                               // the last tile's P^T has been read
+                if (it > 0 && !bwd_wait(BAR(V_GE + (s ^ 1)), ((it - 1) / 2) & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+            }
+            tmem_st_frag16(tPq + packed, w);
+            tmem_st_frag16(tPq + packed + (16u << 16), w + 8);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -443,22 +508,33 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             if (!bwd_wait(BAR(V_DF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             float d[32];
-            tmem_ld32(tP + mine, d);
+            tmem_ld_frag32(tP + mine, d);
+            tmem_ld_frag32(tP + mine + (16u << 16), d + 16);
             tmem_wait_ld();
+            if (kApart) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR(V_DC));
+            }
 #pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4) {
-                const ulonglong2 x = nd[q4];
-                float e0, e1, e2, e3;
-                f2_unpack(f2_fma(f2_pack(d[4 * q4], d[4 * q4 + 1]), c2, x.x), e0, e1);
-                f2_unpack(f2_fma(f2_pack(d[4 * q4 + 2], d[4 * q4 + 3]), c2, x.y), e2, e3);
-                d[4 * q4] = p[4 * q4] * e0, d[4 * q4 + 1] = p[4 * q4 + 1] * e1;
-                d[4 * q4 + 2] = p[4 * q4 + 2] * e2, d[4 * q4 + 3] = p[4 * q4 + 3] * e3;
+            for (int i = 0; i < 32; i += 2) {
+                float e0, e1;
+                f2_unpack(f2_fma(f2_pack(d[i], d[i + 1]), c2, nd[(i >> 2) & 3]), e0, e1);
+                d[i] = p[i] * e0, d[i + 1] = p[i + 1] * e1;
             }
             if (diag) {
 #pragma unroll
-                for (int q = 0; q < 32; ++q) d[q] = 32 * wg + q >= r ? d[q] : 0.0f;
+                for (int i = 0; i < 32; ++i)
+                    d[i] = first + 8 * ((i >> 2) & 3) + (i & 1) - 16 * (i >> 4) - 8 * ((i >> 1) & 1) >= 0 ? d[i] : 0.0f;
             }
-            store_pairs<T>(tP + mine, d);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = Pack2<T>::pack(d[2 * i], d[2 * i + 1]);
+            if (kApart) {
+                if (it > 0 && !bwd_wait(BAR(V_QE + (it - 1) % 3), ((it - 1) / 3) & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+            }
+            tmem_st_frag16(tDS + packed, w);
+            tmem_st_frag16(tDS + packed + (16u << 16), w + 8);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -485,14 +561,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 
 // ------------------------------------------------------------------ dQ
 
-enum DqBar { W_QG = 0, W_KF = 1, W_KE = 4, W_VF = 7, W_VE = 9, W_SF = 11, W_SC = 12, W_DF = 13, W_DC = 14, W_DR = 15,
-             W_DE = 17, W_END = 19, DQ_NBAR = 20 };
+enum DqBar { W_QG = 0, W_KF = 1, W_KE = 5, W_VF = 9, W_VE = 11, W_SF = 13, W_SC = 14, W_DF = 15, W_DC = 16, W_DR = 17,
+             W_DE = 18, W_END = 19, W_AT = 20, DQ_NBAR = 21 };
 
 template <typename T, int AB, int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
-    bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg, T* __restrict__ dq,
-                  const BwdArgs a) {
+    bwd_dq_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                  const __grid_constant__ CUtensorMap tg,
+                  const T* __restrict__ q, const T* __restrict__ go, T* __restrict__ dq, const BwdArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     if (base & 1023u) {                                 // layout assumption broken: do nothing
@@ -502,7 +578,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     using Lay = BwdLayout<D>;
     constexpr uint32_t kTileBytes = Lay::kTileBytes;
     constexpr int kHalves = D / 64;
-    const uint32_t sQ = base + Lay::A0, sG = base + Lay::A1, sK = base + Lay::S0, sV = base + Lay::S1;
+    const uint32_t sG = base + Lay::A0, sK = base + Lay::A1, sV = base + Lay::S1;   // four stages of K, two of V
     auto BAR = [&](int i) -> uint32_t { return base + Lay::BAR + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::BAR + 8 * DQ_NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR + 8 * DQ_NBAR + 4);
@@ -516,11 +592,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(BAR(W_QG), 1);
-        for (int s = 0; s < 3; ++s) mbar_init(BAR(W_KF + s), 1), mbar_init(BAR(W_KE + s), 1);
+        for (int s = 0; s < 4; ++s) mbar_init(BAR(W_KF + s), 1), mbar_init(BAR(W_KE + s), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(BAR(W_VF + s), 1), mbar_init(BAR(W_VE + s), 1);
-            mbar_init(BAR(W_DR + s), kSoftWarps), mbar_init(BAR(W_DE + s), 1);
         }
+        mbar_init(BAR(W_DR), kSoftWarps), mbar_init(BAR(W_DE), 1), mbar_init(BAR(W_AT), kSoftWarps);
         mbar_init(BAR(W_SF), 1), mbar_init(BAR(W_SC), kSoftWarps);
         mbar_init(BAR(W_DF), 1), mbar_init(BAR(W_DC), kSoftWarps);
         mbar_init(BAR(W_END), 1);
@@ -533,26 +609,28 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    // S, dP, two buffers of dS (64 columns each), dQ
-    const uint32_t tS = tmem, tP = tmem + 128, tDS = tmem + 256, tDQ = tmem + 384;
+    // S, dP, packed dS, packed Q (at D = 64 and packed dO), dQ
+    constexpr bool kBoth = D == 64;
+    const uint32_t tS = tmem, tP = tmem + 128, tDS = tmem + 256, tQ = tmem + 320, tG = tmem + 352, tDQ = tmem + 384;
     const float c = scale_of<AB>(red);
 
     if (warp == kSoftWarps) {
         if (lane == 0) {
-            prefetch_tmap(&tq), prefetch_tmap(&tk), prefetch_tmap(&tv), prefetch_tmap(&tg);
-            mbar_expect_tx(BAR(W_QG), 2 * kTileBytes);
-            for (int hf = 0; hf < kHalves; ++hf) {
-                tma_load_3d(sQ + hf * kHalfBytes, &tq, 64 * hf, qt * kTile, bh, BAR(W_QG));
-                tma_load_3d(sG + hf * kHalfBytes, &tg, 64 * hf, qt * kTile, bh, BAR(W_QG));
-            }
-            int it = 0, lastk[3] = {-1, -1, -1}, lastv[2] = {-1, -1};
-            for (; it < n; ++it) {
-                const int s3 = it % 3, s2 = it & 1;
-                if (it >= 3 && !mbar_wait(BAR(W_KE + s3), (it / 3 - 1) & 1, abort_flag)) break;
-                mbar_expect_tx(BAR(W_KF + s3), kTileBytes);
+            prefetch_tmap(&tk), prefetch_tmap(&tv);
+            if (!kBoth) {
+                prefetch_tmap(&tg);
+                mbar_expect_tx(BAR(W_QG), kTileBytes);
                 for (int hf = 0; hf < kHalves; ++hf)
-                    tma_load_3d(sK + s3 * kTileBytes + hf * kHalfBytes, &tk, 64 * hf, it * kTile, u, BAR(W_KF + s3));
-                lastk[s3] = it / 3;
+                    tma_load_3d(sG + hf * kHalfBytes, &tg, 64 * hf, qt * kTile, bh, BAR(W_QG));
+            }
+            int it = 0, lastk[4] = {-1, -1, -1, -1}, lastv[2] = {-1, -1};
+            for (; it < n; ++it) {
+                const int s4 = it & 3, s2 = it & 1;
+                if (it >= 4 && !mbar_wait(BAR(W_KE + s4), (it / 4 - 1) & 1, abort_flag)) break;
+                mbar_expect_tx(BAR(W_KF + s4), kTileBytes);
+                for (int hf = 0; hf < kHalves; ++hf)
+                    tma_load_3d(sK + s4 * kTileBytes + hf * kHalfBytes, &tk, 64 * hf, it * kTile, u, BAR(W_KF + s4));
+                lastk[s4] = it / 4;
                 if (it >= 2 && !mbar_wait(BAR(W_VE + s2), (it / 2 - 1) & 1, abort_flag)) break;
                 mbar_expect_tx(BAR(W_VF + s2), kTileBytes);
                 for (int hf = 0; hf < kHalves; ++hf)
@@ -560,49 +638,60 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                 lastv[s2] = it / 2;
             }
             if (it < n) bwd_give_up(abort_flag);
-            mbar_wait(BAR(W_QG), 0, nullptr);
-            for (int s = 0; s < 3; ++s)
+            if (!kBoth) mbar_wait(BAR(W_QG), 0, nullptr);
+            for (int s = 0; s < 4; ++s)
                 if (lastk[s] >= 0) mbar_wait(BAR(W_KF + s), lastk[s] & 1, nullptr);
             for (int s = 0; s < 2; ++s)
                 if (lastv[s] >= 0) mbar_wait(BAR(W_VF + s), lastv[s] & 1, nullptr);
         }
     } else if (warp == kSoftWarps + 1) {
         constexpr uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
-        auto scores = [&](int it) -> bool {             // S = Q K^T
-            if (!bwd_wait(BAR(W_KF + it % 3), (it / 3) & 1, abort_flag)) return false;
-            if (it > 0 && !bwd_wait(BAR(W_SC), (it - 1) & 1, abort_flag)) return false;
+        // (one lane) S = Q K^T, dP = dO V^T with the streamed tile in stage s
+        auto scores = [&](int s) {
+            products_k_ta<D>(tS, tQ, sK + (uint32_t)s * kTileBytes, idS);
+            tc_commit(BAR(W_SF));
+        };
+        auto grads = [&](int s) {
+            if (kBoth) products_k_ta<D>(tP, tG, sV + (uint32_t)s * kTileBytes, idS);
+            else products_k<D>(tP, sG, sV + (uint32_t)s * kTileBytes, idS);
+            tc_commit(BAR(W_DF));
+            tc_commit(BAR(W_VE + s));
+        };
+        auto k_there = [&](int it, int s) { return bwd_wait(BAR(W_KF + s), (it / 4) & 1, abort_flag); };
+        auto v_there = [&](int it, int s) { return bwd_wait(BAR(W_VF + s), (it / 2) & 1, abort_flag); };
+        bool ok = bwd_wait(BAR(W_AT), 0, abort_flag) && (kBoth || bwd_wait(BAR(W_QG), 0, abort_flag)) && k_there(0, 0) &&
+                  v_there(0, 0) && (n == 1 || k_there(1, 1));
+        if (ok) {
             tc_fence_after();
-            if (elect_one()) {
-                products_k<D>(tS, sQ, sK + (uint32_t)(it % 3) * kTileBytes, idS);
-                tc_commit(BAR(W_SF));
+            if (elect_one()) scores(0), grads(0);
+            __syncwarp();
+        }
+        auto step = [&](auto phase, int it) -> bool {   // PH = it mod 4, see dkv
+            constexpr int PH = decltype(phase)::value, k0 = PH, k1 = (PH + 1) % 4, k2 = (PH + 2) % 4, v1 = (PH & 1) ^ 1;
+            if (it + 1 < n) {
+                if (!bwd_wait(BAR(W_SC), PH & 1, abort_flag)) return false;
+                tc_fence_after();
+                if (elect_one()) scores(k1);
+                __syncwarp();
+                if (!v_there(it + 1, v1) || !bwd_wait(BAR(W_DC), PH & 1, abort_flag)) return false;
+                tc_fence_after();
+                if (elect_one()) grads(v1);
+                __syncwarp();
+                if (it + 2 < n && !k_there(it + 2, k2)) return false;
+            }
+            if (!bwd_wait(BAR(W_DR), PH & 1, abort_flag)) return false;
+            tc_fence_after();
+            if (elect_one()) {                          // dQ += dS K
+                products_mn<16>(tDQ, tDS, sK + (uint32_t)k0 * kTileBytes, idD, it > 0);
+                tc_commit(BAR(W_KE + k0));
+                tc_commit(BAR(W_DE));
             }
             __syncwarp();
             return true;
         };
-        auto grads = [&](int it) -> bool {              // dP = dO V^T
-            if (!bwd_wait(BAR(W_VF + (it & 1)), (it / 2) & 1, abort_flag)) return false;
-            if (it > 0 && !bwd_wait(BAR(W_DC), (it - 1) & 1, abort_flag)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-                products_k<D>(tP, sG, sV + (uint32_t)(it & 1) * kTileBytes, idS);
-                tc_commit(BAR(W_DF));
-                tc_commit(BAR(W_VE + (it & 1)));
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = bwd_wait(BAR(W_QG), 0, abort_flag) && scores(0) && grads(0);
-        for (int it = 0; ok && it < n; ++it) {
-            if (it + 1 < n && !(ok = scores(it + 1) && grads(it + 1))) break;
-            const int s = it & 1;
-            if (!(ok = bwd_wait(BAR(W_DR + s), (it / 2) & 1, abort_flag))) break;
-            tc_fence_after();
-            if (elect_one()) {
-                products_mn<16>(tDQ, tDS + 64u * (uint32_t)s, sK + (uint32_t)(it % 3) * kTileBytes, idD, it > 0);
-                tc_commit(BAR(W_KE + it % 3));
-                tc_commit(BAR(W_DE + s));
-            }
-            __syncwarp();
+        for (int it = 0; ok && it < n; it += 4) {
+            ok = step(Int<0>{}, it) && (it + 1 >= n || step(Int<1>{}, it + 1)) && (it + 2 >= n || step(Int<2>{}, it + 2)) &&
+                 (it + 3 >= n || step(Int<3>{}, it + 3));
         }
         if (!ok) bwd_give_up(abort_flag);
         if (elect_one()) tc_commit(BAR(W_END));
@@ -617,9 +706,31 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         const float nl = a.ws.nlse[stat], nd = -c * a.ws.delta[stat];
         const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
         const unsigned long long nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+        // The thread's share of Q (and dO) to tensor memory: as the products' first operands they would take as much of
+        // shared memory's bandwidth as the second ones.
         bool ok = true;
+        {
+            constexpr int kWords = D / 8;               // 32-bit columns of a warpgroup
+            const int64_t row = ((int64_t)bh * a.T_len + (i < a.T_len ? i : 0)) * D + 2 * kWords * wg;
+            uint32_t w[kWords];
+#pragma unroll
+            for (int x = 0; x < (kBoth ? 2 : 1); ++x) {
+                const uint4* from = reinterpret_cast<const uint4*>((x ? go : q) + row);
+#pragma unroll
+                for (int e = 0; e < kWords / 4; ++e) {
+                    const uint4 y = i < a.T_len ? from[e] : make_uint4(0, 0, 0, 0);
+                    w[4 * e] = y.x, w[4 * e + 1] = y.y, w[4 * e + 2] = y.z, w[4 * e + 3] = y.w;
+                }
+                const uint32_t to = (x ? tG : tQ) + lanes + (uint32_t)(kWords * wg);
+                if (D == 128) tmem_st16(to, w);
+                else tmem_st8(to, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(W_AT));
+        }
         for (int it = 0; it < n; ++it) {
-            const int s = it & 1;
             const bool diag = it == qt;
             if (!bwd_wait(BAR(W_SF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
@@ -653,13 +764,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 32; ++q) d[q] = 32 * wg + q <= r ? d[q] : 0.0f;
             }
-            if (it >= 2 && !bwd_wait(BAR(W_DE + s), (it / 2 - 1) & 1, abort_flag)) { ok = false; break; }
+            if (it >= 1 && !bwd_wait(BAR(W_DE), (it - 1) & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            store_pairs<T>(tDS + lanes + 64u * (uint32_t)s + 16u * (uint32_t)wg, d);
+            store_pairs<T>(tDS + lanes + 16u * (uint32_t)wg, d);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(W_DR + s));
+            if (lane == 0) mbar_arrive(BAR(W_DR));
         }
         if (!ok) bwd_give_up(abort_flag);
         ok = bwd_wait(BAR(W_END), 0, nullptr) && ok && !*abort_flag;
@@ -729,7 +840,8 @@ kvq_status run_typed(const PrefillBwdCall& c, cudaStream_t s) {
         }
         if (e == cudaSuccess) {
             a.group = head_group(c.B * c.Hq, (long long)c.T * D * 4 / g);
-            bwd_dq_kernel<T, AB, D><<<a.n_t * c.B * c.Hq, kDqThreads, Lay::BYTES, s>>>(mq, mk, mv, mg, (T*)c.dq, a);
+            bwd_dq_kernel<T, AB, D><<<a.n_t * c.B * c.Hq, kDqThreads, Lay::BYTES, s>>>(mk, mv, mg, (const T*)c.q, (const T*)c.go,
+                                                                                       (T*)c.dq, a);
             e = cudaGetLastError();
         }
     }
