@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     bwd_prep_kernel(const T* __restrict__ o, const T* __restrict__ go, const T* __restrict__ v,
                     const float* __restrict__ lse, const float* __restrict__ glse, const BwdArgs a) {
     constexpr int kLanes = D / 8, kRows = kPrepThreads / kLanes;
+    grid_launch_dependents();
     const int tile = blockIdx.x, bh = blockIdx.y;
     const int b = bh / a.Hq, hq = bh % a.Hq, g = a.Hq / a.Hkv;
     const int l = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
@@ -161,10 +162,10 @@ template <int AB> __device__ __forceinline__ void largest(const BwdArgs& a, int 
     if (AB != 0) return;
     float x = 0.0f, d = 0.0f, v = 0.0f;
     for (int i = threadIdx.x; i < nh * a.n_t; i += blockDim.x) {
-        x = fmaxf(x, a.ws.do_max[(int64_t)h0 * a.n_t + i]);
-        d = fmaxf(d, a.ws.dl_max[(int64_t)h0 * a.n_t + i]);
+        x = fmaxf(x, __ldcg(a.ws.do_max + (int64_t)h0 * a.n_t + i));
+        d = fmaxf(d, __ldcg(a.ws.dl_max + (int64_t)h0 * a.n_t + i));
     }
-    for (int i = threadIdx.x; i < a.n_t; i += blockDim.x) v = fmaxf(v, a.ws.v_max[(int64_t)u * a.n_t + i]);
+    for (int i = threadIdx.x; i < a.n_t; i += blockDim.x) v = fmaxf(v, __ldcg(a.ws.v_max + (int64_t)u * a.n_t + i));
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
@@ -232,14 +233,14 @@ template <int D> __device__ __forceinline__ void products_k_ta(uint32_t c, uint3
 }
 
 // C (+)= A B, A [128, 128] packed pairs in tensor memory (every 32 values in 16 columns, STEP columns apart), B a tile of
-// 128 rows (one thread).
-template <int STEP>
+// 128 rows (one thread).  HALF 0 and 1: the first and the second 16 of every 32 terms; 2: all.
+template <int STEP, int HALF = 2>
 __device__ __forceinline__ void products_mn(uint32_t c, uint32_t ta, uint32_t tb, uint32_t idesc, bool accumulate) {
     const uint64_t db = mnmajor_desc(tb, 0);
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
+    for (int kk = HALF == 1; kk < 8; kk += HALF == 2 ? 1 : 2)
         tc_mma_f16_ta(c, ta + (uint32_t)(kk >> 1) * STEP + (uint32_t)(kk & 1) * 8u, db + (uint64_t)(kk * 16 * 128 >> 4), idesc,
-                      accumulate || kk > 0);
+                      kk > 0 || accumulate);
 }
 
 // 32 values of a thread's row as 16 columns of packed pairs.
@@ -250,23 +251,30 @@ template <typename T> __device__ __forceinline__ void store_pairs(uint32_t taddr
     tmem_st16(taddr, w);
 }
 
-// One thread's row of D float32 TMEM columns, times f, to `out` in T.
-template <typename T, int D> __device__ __forceinline__ void store_row(uint32_t taddr, float f, bool there, T* out) {
+// Zeros where the query comes before the key, in a thread's 16 keys by 16 queries; d: query - key of element 0.
+__device__ __forceinline__ void mask16(float* x, int d) {
 #pragma unroll
-    for (int c4 = 0; c4 < D / 32; ++c4) {
+    for (int i = 0; i < 16; ++i) x[i] = d + 8 * ((i >> 2) & 1) + (i & 1) - 16 * (i >> 3) - 8 * ((i >> 1) & 1) >= 0 ? x[i] : 0.0f;
+}
+
+// N float32 TMEM columns of a thread's row (lane r), times f, in T to a 64-column half of a swizzled tile in shared memory,
+// from its column c0 on.
+template <typename T, int N>
+__device__ __forceinline__ void stage_row(uint32_t taddr, float f, uint8_t* half, int r, int c0) {
+    uint8_t* row = half + r * 128;
+#pragma unroll
+    for (int c4 = 0; c4 < N / 32; ++c4) {
         float x[32];
         tmem_ld32(taddr + (uint32_t)c4 * 32u, x);
         tmem_wait_ld();
-        if (there) {
 #pragma unroll
-            for (int c8 = 0; c8 < 4; ++c8) {
-                uint4 w;
-                w.x = Pack2<T>::pack(x[c8 * 8 + 0] * f, x[c8 * 8 + 1] * f);
-                w.y = Pack2<T>::pack(x[c8 * 8 + 2] * f, x[c8 * 8 + 3] * f);
-                w.z = Pack2<T>::pack(x[c8 * 8 + 4] * f, x[c8 * 8 + 5] * f);
-                w.w = Pack2<T>::pack(x[c8 * 8 + 6] * f, x[c8 * 8 + 7] * f);
-                *reinterpret_cast<uint4*>(out + c4 * 32 + c8 * 8) = w;
-            }
+        for (int c8 = 0; c8 < 4; ++c8) {
+            uint4 w;
+            w.x = Pack2<T>::pack(x[c8 * 8 + 0] * f, x[c8 * 8 + 1] * f);
+            w.y = Pack2<T>::pack(x[c8 * 8 + 2] * f, x[c8 * 8 + 3] * f);
+            w.z = Pack2<T>::pack(x[c8 * 8 + 4] * f, x[c8 * 8 + 5] * f);
+            w.w = Pack2<T>::pack(x[c8 * 8 + 6] * f, x[c8 * 8 + 7] * f);
+            *reinterpret_cast<uint4*>(row + ((c0 / 8 + c4 * 4 + c8) ^ (r & 7)) * 16) = w;
         }
     }
 }
@@ -274,13 +282,13 @@ template <typename T, int D> __device__ __forceinline__ void store_row(uint32_t 
 // ------------------------------------------------------------------ dK and dV
 
 enum DkvBar { V_KV = 0, V_QF = 1, V_QE = 4, V_GF = 7, V_GE = 9, V_TF = 11, V_TE = 13, V_SF = 15, V_PR = 16, V_DF = 17,
-              V_DR = 18, V_END = 19, V_SC = 20, V_DC = 21, DKV_NBAR = 22 };
+              V_DR = 18, V_END = 19, V_SC = 20, V_DC = 21, V_PH = 22, DKV_NBAR = 23 };
 
 template <typename T, int AB, int D>
 __global__ void __launch_bounds__(kDkvThreads, 1)
     bwd_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg, T* __restrict__ dk,
-                   T* __restrict__ dv, const BwdArgs a) {
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg,
+                   const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, const BwdArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     if (base & 1023u) {                                 // layout assumption broken: do nothing
@@ -302,7 +310,20 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const int g = a.Hq / a.Hkv, h0 = u * g;             // head u * g + h of all B * Hq is the unit's h-th
     const int m = a.n_t - kt, n = g * m;                // query tiles of a head; of all heads
 
-    if (threadIdx.x == 0) {
+    // (one lane) tile it of Q or dO into its stage
+    auto load_q = [&](int it) {
+        const int s = it % 3;
+        mbar_expect_tx(BAR(V_QF + s), kTileBytes);
+        for (int hf = 0; hf < kHalves; ++hf)
+            tma_load_3d(sQ + s * kTileBytes + hf * kHalfBytes, &tq, 64 * hf, (kt + it % m) * kTile, h0 + it / m, BAR(V_QF + s));
+    };
+    auto load_g = [&](int it) {
+        const int s = it & 1;
+        mbar_expect_tx(BAR(V_GF + s), kTileBytes);
+        for (int hf = 0; hf < kHalves; ++hf)
+            tma_load_3d(sG + s * kTileBytes + hf * kHalfBytes, &tg, 64 * hf, (kt + it % m) * kTile, h0 + it / m, BAR(V_GF + s));
+    };
+    if (warp == kSoftWarps && lane == 0) {
         mbar_init(BAR(V_KV), 1);
         for (int s = 0; s < 3; ++s) mbar_init(BAR(V_QF + s), 1), mbar_init(BAR(V_QE + s), 1);
         for (int s = 0; s < 2; ++s) {
@@ -312,11 +333,19 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         mbar_init(BAR(V_SF), 1), mbar_init(BAR(V_PR), kSoftWarps);
         mbar_init(BAR(V_DF), 1), mbar_init(BAR(V_DR), kSoftWarps);
         mbar_init(BAR(V_END), 1);
-        mbar_init(BAR(V_SC), kSoftWarps), mbar_init(BAR(V_DC), kSoftWarps);
+        mbar_init(BAR(V_SC), kSoftWarps), mbar_init(BAR(V_DC), kSoftWarps), mbar_init(BAR(V_PH), kSoftWarps);
         *abort_flag = 0;
         fence_mbar_init();
+        // the first copies do not wait for the rest of the CTA, nor for the grid before this one
+        mbar_expect_tx(BAR(V_KV), 2 * kTileBytes);
+        for (int hf = 0; hf < kHalves; ++hf) tma_load_3d(sK + hf * kHalfBytes, &tk, 64 * hf, kt * kTile, u, BAR(V_KV));
+        load_q(0);
+        for (int hf = 0; hf < kHalves; ++hf) tma_load_3d(sV + hf * kHalfBytes, &tv, 64 * hf, kt * kTile, u, BAR(V_KV));
+        load_g(0);
     }
     if (warp == kSoftWarps + 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    grid_dependency_wait();                             // the rows' statistics
+    grid_launch_dependents();                           // dQ's CTAs take the SMs that this grid leaves free
     largest<AB>(a, h0, g, u, red);
     tc_fence_before();
     __syncthreads();
@@ -331,25 +360,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 
     if (warp == kSoftWarps) {
         if (lane == 0) {
-            prefetch_tmap(&tq), prefetch_tmap(&tk), prefetch_tmap(&tv), prefetch_tmap(&tg);
-            mbar_expect_tx(BAR(V_KV), 2 * kTileBytes);
-            for (int hf = 0; hf < kHalves; ++hf) {
-                tma_load_3d(sK + hf * kHalfBytes, &tk, 64 * hf, kt * kTile, u, BAR(V_KV));
-                tma_load_3d(sV + hf * kHalfBytes, &tv, 64 * hf, kt * kTile, u, BAR(V_KV));
-            }
-            int it = 0, lastq[3] = {-1, -1, -1}, lastg[2] = {-1, -1};
+            int it = 1, lastq[3] = {0, -1, -1}, lastg[2] = {0, -1};
             for (; it < n; ++it) {
-                const int bh = h0 + it / m, row = (kt + it % m) * kTile, s3 = it % 3, s2 = it & 1;
-                if (it >= 3 && !mbar_wait(BAR(V_QE + s3), (it / 3 - 1) & 1, abort_flag)) break;
-                mbar_expect_tx(BAR(V_QF + s3), kTileBytes);
-                for (int hf = 0; hf < kHalves; ++hf)
-                    tma_load_3d(sQ + s3 * kTileBytes + hf * kHalfBytes, &tq, 64 * hf, row, bh, BAR(V_QF + s3));
-                lastq[s3] = it / 3;
-                if (it >= 2 && !mbar_wait(BAR(V_GE + s2), (it / 2 - 1) & 1, abort_flag)) break;
-                mbar_expect_tx(BAR(V_GF + s2), kTileBytes);
-                for (int hf = 0; hf < kHalves; ++hf)
-                    tma_load_3d(sG + s2 * kTileBytes + hf * kHalfBytes, &tg, 64 * hf, row, bh, BAR(V_GF + s2));
-                lastg[s2] = it / 2;
+                if (it >= 3 && !mbar_wait(BAR(V_QE + it % 3), (it / 3 - 1) & 1, abort_flag)) break;
+                load_q(it);
+                lastq[it % 3] = it / 3;
+                if (it >= 2 && !mbar_wait(BAR(V_GE + (it & 1)), (it / 2 - 1) & 1, abort_flag)) break;
+                load_g(it);
+                lastg[it & 1] = it / 2;
             }
             if (it < n) bwd_give_up(abort_flag);
             // every issued copy has landed before the CTA may exit
@@ -370,13 +388,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             products_k<D>(tP, sV, sG + (uint32_t)s * kTileBytes, idS);
             tc_commit(BAR(V_DF));
         };
-        auto q_there = [&](int it, int s) { return bwd_wait(BAR(V_QF + s), (it / 3) & 1, abort_flag); };
-        auto g_there = [&](int it, int s) { return bwd_wait(BAR(V_GF + s), (it / 2) & 1, abort_flag); };
-        bool ok = bwd_wait(BAR(V_KV), 0, abort_flag) && q_there(0, 0) && g_there(0, 0) && (n == 1 || q_there(1, 1));
-        if (ok) {
-            if (elect_one()) scores(0), grads(0);
-            __syncwarp();
-        }
+        auto wait = [&](int bar, int parity) { return mbar_wait(BAR(bar), (uint32_t)(parity & 1), abort_flag); };
+        auto q_there = [&](int it, int s) { return wait(V_QF + s, it / 3); };
+        auto g_there = [&](int it, int s) { return wait(V_GF + s, it / 2); };
         // One tile, PH = it mod 6: the stages are constants, so that descriptors stay in uniform registers (computed from
         // the tile's number they made a product's issue three times as long).
         // The next S^T and dP^T are issued as soon as theirs has been read (kApart), or behind the product that reads what
@@ -386,54 +400,49 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             constexpr int PH = decltype(phase)::value, q0 = PH % 3, q1 = (PH + 1) % 3, q2 = (PH + 2) % 3, g0 = PH & 1, g1 = g0 ^ 1;
             const bool more = it + 1 < n;
             if (kApart && more) {
-                if (!bwd_wait(BAR(V_SC), PH & 1, abort_flag)) return false;
+                if (!wait(V_SC, PH)) return false;
                 tc_fence_after();
-                if (elect_one()) scores(q1);
-                __syncwarp();
+                scores(q1);
             }
-            if (!bwd_wait(BAR(V_PR), PH & 1, abort_flag)) return false;
+            if (!wait(V_PH, PH)) return false;          // dV += P^T dO, half of P^T at a time
             tc_fence_after();
-            if (elect_one()) {                          // dV += P^T dO
-                products_mn<kStep>(tDV, tPq, sG + (uint32_t)g0 * kTileBytes, idD, it > 0);
-                tc_commit(BAR(V_GE + g0));
-            }
-            __syncwarp();
+            products_mn<kStep, 0>(tDV, tPq, sG + (uint32_t)g0 * kTileBytes, idD, it > 0);
+            if (!wait(V_PR, PH)) return false;
+            tc_fence_after();
+            products_mn<kStep, 1>(tDV, tPq, sG + (uint32_t)g0 * kTileBytes, idD, true);
+            tc_commit(BAR(V_GE + g0));
             if (more) {
                 if (!g_there(it + 1, g1)) return false;
                 if (kApart) {
-                    if (!bwd_wait(BAR(V_DC), PH & 1, abort_flag)) return false;
+                    if (!wait(V_DC, PH)) return false;
                     tc_fence_after();
+                    grads(g1);
+                } else {
+                    scores(q1);
                 }
-                if (elect_one()) {
-                    if (kApart) grads(g1);
-                    else scores(q1);
-                }
-                __syncwarp();
             }
-            if (!bwd_wait(BAR(V_DR), PH & 1, abort_flag)) return false;
+            if (!wait(V_DR, PH)) return false;
             tc_fence_after();
-            if (elect_one()) {                          // dK += dS^T Q
-                products_mn<kStep>(tDK, tDS, sQ + (uint32_t)q0 * kTileBytes, idD, it > 0);
-                tc_commit(BAR(V_QE + q0));
-            }
-            __syncwarp();
+            products_mn<kStep>(tDK, tDS, sQ + (uint32_t)q0 * kTileBytes, idD, it > 0);      // dK += dS^T Q
+            tc_commit(BAR(V_QE + q0));
             if (it + 2 < n && !q_there(it + 2, q2)) return false;
-            if (!kApart && more) {
-                if (elect_one()) grads(g1);
-                __syncwarp();
-            }
+            if (!kApart && more) grads(g1);
             return true;
         };
-        for (int it = 0; ok && it < n; it += 6) {
-            ok = step(Int<0>{}, it) && (it + 1 >= n || step(Int<1>{}, it + 1)) && (it + 2 >= n || step(Int<2>{}, it + 2)) &&
-                 (it + 3 >= n || step(Int<3>{}, it + 3)) && (it + 4 >= n || step(Int<4>{}, it + 4)) &&
-                 (it + 5 >= n || step(Int<5>{}, it + 5));
+        if (elect_one()) {
+            bool ok = wait(V_KV, 0) && q_there(0, 0) && g_there(0, 0) && (n == 1 || q_there(1, 1));
+            if (ok) scores(0), grads(0);
+            for (int it = 0; ok && it < n; it += 6) {
+                ok = step(Int<0>{}, it) && (it + 1 >= n || step(Int<1>{}, it + 1)) && (it + 2 >= n || step(Int<2>{}, it + 2)) &&
+                     (it + 3 >= n || step(Int<3>{}, it + 3)) && (it + 4 >= n || step(Int<4>{}, it + 4)) &&
+                     (it + 5 >= n || step(Int<5>{}, it + 5));
+            }
+            if (!ok) bwd_give_up(abort_flag);
+            // all products complete before the sums are read and TMEM is released
+            tc_commit(BAR(V_END));
+            mbar_wait(BAR(V_END), 0, nullptr);
         }
-        if (!ok) bwd_give_up(abort_flag);
-        // all products complete before the sums are read and TMEM is released
-        if (elect_one()) tc_commit(BAR(V_END));
         __syncwarp();
-        bwd_wait(BAR(V_END), 0, nullptr);
     } else if (warp == kSoftWarps + 2) {
         // the query rows' statistics, delta times c
         bool ok = true;
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         // Warpgroup wg has queries 32 wg .. 32 wg + 31 of each tile, warp w of it keys 32 w .. 32 w + 31, in fragments: a
         // thread has 4 keys and 8 queries, so that it needs the statistics of 8 queries only (with a thread per key the
         // broadcasts of 32 took as many cycles of shared memory as the tensor pipe's operands left).
-        const int wg = warp >> 2, r = threadIdx.x & 127, j = kt * kTile + r;
+        const int wg = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t mine = lanes + 32u * (uint32_t)wg, packed = lanes + kStep * (uint32_t)wg;
         const int first = 32 * wg + 2 * (lane & 3) - (32 * (warp & 3) + (lane >> 2));    // query - key of element 0
@@ -472,44 +481,52 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             for (int t = 0; t < 4; ++t) nl[t] = stat[4 * t], nd[t] = stat[64 + 4 * t];
             if (!bwd_wait(BAR(V_SF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            float p[32];                                // [16 keys][tile of 8 queries][8 keys][2 queries]
-            tmem_ld_frag32(tS + mine, p);
-            tmem_ld_frag32(tS + mine + (16u << 16), p + 16);
+            // P^T in two halves of 16 queries, so that dV's products start on the first: [half][16 keys][tile of 8 queries]
+            // [8 keys][2 queries]
+            float p[32];
+            uint32_t w[8];
+            tmem_ld_frag16(tS + mine, p);
+            tmem_ld_frag16(tS + mine + (16u << 16), p + 8);
             tmem_wait_ld();
-            if (kApart) {
+            tmem_ld_frag16(tS + mine + 16u, p + 16);
+            tmem_ld_frag16(tS + mine + 16u + (16u << 16), p + 24);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                float* x = p + 16 * hf;
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    float e0, e1;
+                    f2_unpack(f2_fma(f2_pack(x[i], x[i + 1]), sc2, nl[2 * hf + ((i >> 2) & 1)]), e0, e1);
+                    x[i] = ex2_approx(e0), x[i + 1] = ex2_approx(e1);
+                }
+                if (diag) mask16(x, first + 16 * hf);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = Pack2<T>::pack(x[2 * i], x[2 * i + 1]);
+                if (kApart && hf == 0) {                // the last tile's P^T has been read
+                    if (it > 0 && !bwd_wait(BAR(V_GE + (s ^ 1)), ((it - 1) / 2) & 1, abort_flag)) { ok = false; break; }
+                    tc_fence_after();
+                }
+                if (hf == 0) tmem_wait_ld();            // the second half of S^T, before its place is written to
+                if (kApart && hf == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(BAR(V_SC));
+                }
+                tmem_st_frag8(tPq + packed + 8u * (uint32_t)hf, w);
+                tmem_st_frag8(tPq + packed + 8u * (uint32_t)hf + (16u << 16), w + 4);
+                tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(V_SC));
+                if (lane == 0) mbar_arrive(BAR(hf == 0 ? V_PH : V_PR));
             }
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                float e0, e1;
-                f2_unpack(f2_fma(f2_pack(p[i], p[i + 1]), sc2, nl[(i >> 2) & 3]), e0, e1);
-                p[i] = ex2_approx(e0), p[i + 1] = ex2_approx(e1);
-            }
-            if (diag) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    p[i] = first + 8 * ((i >> 2) & 3) + (i & 1) - 16 * (i >> 4) - 8 * ((i >> 1) & 1) >= 0 ? p[i] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = Pack2<T>::pack(p[2 * i], p[2 * i + 1]);
-            if (kApart) {                               // the last tile's P^T has been read
-                if (it > 0 && !bwd_wait(BAR(V_GE + (s ^ 1)), ((it - 1) / 2) & 1, abort_flag)) { ok = false; break; }
-                tc_fence_after();
-            }
-            tmem_st_frag16(tPq + packed, w);
-            tmem_st_frag16(tPq + packed + (16u << 16), w + 8);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(V_PR));
+            if (!ok) break;
             if (!bwd_wait(BAR(V_DF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             float d[32];
-            tmem_ld_frag32(tP + mine, d);
-            tmem_ld_frag32(tP + mine + (16u << 16), d + 16);
+            tmem_ld_frag16(tP + mine, d);
+            tmem_ld_frag16(tP + mine + (16u << 16), d + 8);
+            tmem_ld_frag16(tP + mine + 16u, d + 16);
+            tmem_ld_frag16(tP + mine + 16u + (16u << 16), d + 24);
             tmem_wait_ld();
             if (kApart) {
                 tc_fence_before();
@@ -519,22 +536,21 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
                 float e0, e1;
-                f2_unpack(f2_fma(f2_pack(d[i], d[i + 1]), c2, nd[(i >> 2) & 3]), e0, e1);
+                f2_unpack(f2_fma(f2_pack(d[i], d[i + 1]), c2, nd[2 * (i >> 4) + ((i >> 2) & 1)]), e0, e1);
                 d[i] = p[i] * e0, d[i + 1] = p[i + 1] * e1;
             }
-            if (diag) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    d[i] = first + 8 * ((i >> 2) & 3) + (i & 1) - 16 * (i >> 4) - 8 * ((i >> 1) & 1) >= 0 ? d[i] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = Pack2<T>::pack(d[2 * i], d[2 * i + 1]);
-            if (kApart) {
+            if (diag) mask16(d, first), mask16(d + 16, first + 16);
+            if (kApart) {                               // the last tile's dS^T has been read
                 if (it > 0 && !bwd_wait(BAR(V_QE + (it - 1) % 3), ((it - 1) / 3) & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
             }
-            tmem_st_frag16(tDS + packed, w);
-            tmem_st_frag16(tDS + packed + (16u << 16), w + 8);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = Pack2<T>::pack(d[16 * hf + 2 * i], d[16 * hf + 2 * i + 1]);
+                tmem_st_frag8(tDS + packed + 8u * (uint32_t)hf, w);
+                tmem_st_frag8(tDS + packed + 8u * (uint32_t)hf + (16u << 16), w + 4);
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -544,14 +560,23 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             }
         }
         if (!ok) bwd_give_up(abort_flag);
-        ok = bwd_wait(BAR(V_END), 0, nullptr) && ok && !*abort_flag;
+        if (!bwd_wait(BAR(V_END), 0, nullptr)) bwd_give_up(abort_flag);
         tc_fence_after();
-        // warpgroups 0 and 1 store the halves of dV, 2 and 3 those of dK
-        const int64_t row = (int64_t)u * a.T_len + (j < a.T_len ? j : 0);
+        // dV (warpgroups 0 and 1, half of the columns each) and dK (2 and 3) through the stages that held Q
         const float unshift = AB == 0 ? 0x1p-15f : 1.0f;
-        const uint32_t half = lanes + (uint32_t)((wg & 1) * (D / 2));
-        if (wg < 2) store_row<T, D / 2>(tDV + half, unshift, ok && j < a.T_len, dv + row * D + (wg & 1) * (D / 2));
-        else store_row<T, D / 2>(tDK + half, a.sm_scale * unshift / c, ok && j < a.T_len, dk + row * D + (wg & 1) * (D / 2));
+        const int part = wg & 1, to_dk = wg >> 1;
+        uint8_t* half = smem + Lay::S0 + (uint32_t)(to_dk * kHalves + (D == 128 ? part : 0)) * kHalfBytes;
+        stage_row<T, D / 2>((to_dk ? tDK : tDV) + lanes + (uint32_t)(part * (D / 2)),
+                            to_dk ? a.sm_scale * unshift / c : unshift, half, r, D == 128 ? 0 : 32 * part);
+        fence_proxy_async_smem();
+        named_barrier_sync(1, 32 * kSoftWarps);
+        if (threadIdx.x == 0 && !*abort_flag) {
+            for (int hf = 0; hf < kHalves; ++hf) {
+                tma_store_3d(&tdv, sQ + (uint32_t)hf * kHalfBytes, 64 * hf, kt * kTile, u);
+                tma_store_3d(&tdk, sQ + (uint32_t)(kHalves + hf) * kHalfBytes, 64 * hf, kt * kTile, u);
+            }
+            bulk_store_done();
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -568,7 +593,8 @@ template <typename T, int AB, int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __grid_constant__ CUtensorMap tg,
-                  const T* __restrict__ q, const T* __restrict__ go, T* __restrict__ dq, const BwdArgs a) {
+                  const __grid_constant__ CUtensorMap tdq, const T* __restrict__ q, const T* __restrict__ go,
+                  const BwdArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     if (base & 1023u) {                                 // layout assumption broken: do nothing
@@ -589,8 +615,36 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     place(a, a.B * a.Hq, rank, bh);
     const int qt = a.n_t - 1 - rank, n = qt + 1;
     const int u = bh / a.Hq * a.Hkv + bh % a.Hq / (a.Hq / a.Hkv);
+    const int wg = warp >> 2, r = threadIdx.x & 127, i = qt * kTile + r;
 
-    if (threadIdx.x == 0) {
+    // (one lane) tile it of K or V into its stage
+    auto load_k = [&](int it) {
+        const int s = it & 3;
+        mbar_expect_tx(BAR(W_KF + s), kTileBytes);
+        for (int hf = 0; hf < kHalves; ++hf)
+            tma_load_3d(sK + s * kTileBytes + hf * kHalfBytes, &tk, 64 * hf, it * kTile, u, BAR(W_KF + s));
+    };
+    auto load_v = [&](int it) {
+        const int s = it & 1;
+        mbar_expect_tx(BAR(W_VF + s), kTileBytes);
+        for (int hf = 0; hf < kHalves; ++hf)
+            tma_load_3d(sV + s * kTileBytes + hf * kHalfBytes, &tv, 64 * hf, it * kTile, u, BAR(W_VF + s));
+    };
+    // The thread's share of Q (at D = 64 and dO), for tensor memory: as the products' first operands they would take as
+    // much of shared memory's bandwidth as the second ones.
+    constexpr bool kBoth = D == 64;
+    uint32_t mine_q[16];
+    if (warp < kSoftWarps) {
+        constexpr int kChunks = D / 32;                 // 16-byte pieces of a warpgroup's columns
+        const int64_t row = ((int64_t)bh * a.T_len + (i < a.T_len ? i : 0)) * D + 8 * kChunks * wg;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const T* from = (kBoth && e >= 2 ? go : q) + row;
+            const uint4 y = i < a.T_len ? reinterpret_cast<const uint4*>(from)[e % kChunks] : make_uint4(0, 0, 0, 0);
+            mine_q[4 * e] = y.x, mine_q[4 * e + 1] = y.y, mine_q[4 * e + 2] = y.z, mine_q[4 * e + 3] = y.w;
+        }
+    }
+    if (warp == kSoftWarps && lane == 0) {
         mbar_init(BAR(W_QG), 1);
         for (int s = 0; s < 4; ++s) mbar_init(BAR(W_KF + s), 1), mbar_init(BAR(W_KE + s), 1);
         for (int s = 0; s < 2; ++s) {
@@ -602,40 +656,35 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         mbar_init(BAR(W_END), 1);
         *abort_flag = 0;
         fence_mbar_init();
+        load_k(0);                                      // the first copies, see dkv
+        if (!kBoth) {
+            mbar_expect_tx(BAR(W_QG), kTileBytes);
+            for (int hf = 0; hf < kHalves; ++hf) tma_load_3d(sG + hf * kHalfBytes, &tg, 64 * hf, qt * kTile, bh, BAR(W_QG));
+        }
+        load_v(0);
     }
     if (warp == kSoftWarps + 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    // No wait for the grid before this one: it waited for the statistics' grid before it let this one start (the
+    // statistics are read from L2).
     largest<AB>(a, bh, 1, u, red);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     // S, dP, packed dS, packed Q (at D = 64 and packed dO), dQ
-    constexpr bool kBoth = D == 64;
     const uint32_t tS = tmem, tP = tmem + 128, tDS = tmem + 256, tQ = tmem + 320, tG = tmem + 352, tDQ = tmem + 384;
     const float c = scale_of<AB>(red);
 
     if (warp == kSoftWarps) {
         if (lane == 0) {
-            prefetch_tmap(&tk), prefetch_tmap(&tv);
-            if (!kBoth) {
-                prefetch_tmap(&tg);
-                mbar_expect_tx(BAR(W_QG), kTileBytes);
-                for (int hf = 0; hf < kHalves; ++hf)
-                    tma_load_3d(sG + hf * kHalfBytes, &tg, 64 * hf, qt * kTile, bh, BAR(W_QG));
-            }
-            int it = 0, lastk[4] = {-1, -1, -1, -1}, lastv[2] = {-1, -1};
+            int it = 1, lastk[4] = {0, -1, -1, -1}, lastv[2] = {0, -1};
             for (; it < n; ++it) {
-                const int s4 = it & 3, s2 = it & 1;
-                if (it >= 4 && !mbar_wait(BAR(W_KE + s4), (it / 4 - 1) & 1, abort_flag)) break;
-                mbar_expect_tx(BAR(W_KF + s4), kTileBytes);
-                for (int hf = 0; hf < kHalves; ++hf)
-                    tma_load_3d(sK + s4 * kTileBytes + hf * kHalfBytes, &tk, 64 * hf, it * kTile, u, BAR(W_KF + s4));
-                lastk[s4] = it / 4;
-                if (it >= 2 && !mbar_wait(BAR(W_VE + s2), (it / 2 - 1) & 1, abort_flag)) break;
-                mbar_expect_tx(BAR(W_VF + s2), kTileBytes);
-                for (int hf = 0; hf < kHalves; ++hf)
-                    tma_load_3d(sV + s2 * kTileBytes + hf * kHalfBytes, &tv, 64 * hf, it * kTile, u, BAR(W_VF + s2));
-                lastv[s2] = it / 2;
+                if (it >= 4 && !mbar_wait(BAR(W_KE + (it & 3)), (it / 4 - 1) & 1, abort_flag)) break;
+                load_k(it);
+                lastk[it & 3] = it / 4;
+                if (it >= 2 && !mbar_wait(BAR(W_VE + (it & 1)), (it / 2 - 1) & 1, abort_flag)) break;
+                load_v(it);
+                lastv[it & 1] = it / 2;
             }
             if (it < n) bwd_give_up(abort_flag);
             if (!kBoth) mbar_wait(BAR(W_QG), 0, nullptr);
@@ -657,79 +706,60 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             tc_commit(BAR(W_DF));
             tc_commit(BAR(W_VE + s));
         };
-        auto k_there = [&](int it, int s) { return bwd_wait(BAR(W_KF + s), (it / 4) & 1, abort_flag); };
-        auto v_there = [&](int it, int s) { return bwd_wait(BAR(W_VF + s), (it / 2) & 1, abort_flag); };
-        bool ok = bwd_wait(BAR(W_AT), 0, abort_flag) && (kBoth || bwd_wait(BAR(W_QG), 0, abort_flag)) && k_there(0, 0) &&
-                  v_there(0, 0) && (n == 1 || k_there(1, 1));
-        if (ok) {
-            tc_fence_after();
-            if (elect_one()) scores(0), grads(0);
-            __syncwarp();
-        }
+        auto wait = [&](int bar, int parity) { return mbar_wait(BAR(bar), (uint32_t)(parity & 1), abort_flag); };
+        auto k_there = [&](int it, int s) { return wait(W_KF + s, it / 4); };
+        auto v_there = [&](int it, int s) { return wait(W_VF + s, it / 2); };
         auto step = [&](auto phase, int it) -> bool {   // PH = it mod 4, see dkv
             constexpr int PH = decltype(phase)::value, k0 = PH, k1 = (PH + 1) % 4, k2 = (PH + 2) % 4, v1 = (PH & 1) ^ 1;
             if (it + 1 < n) {
-                if (!bwd_wait(BAR(W_SC), PH & 1, abort_flag)) return false;
+                if (!wait(W_SC, PH)) return false;
                 tc_fence_after();
-                if (elect_one()) scores(k1);
-                __syncwarp();
-                if (!v_there(it + 1, v1) || !bwd_wait(BAR(W_DC), PH & 1, abort_flag)) return false;
+                scores(k1);
+                if (!v_there(it + 1, v1) || (it + 2 < n && !k_there(it + 2, k2)) || !wait(W_DC, PH)) return false;
                 tc_fence_after();
-                if (elect_one()) grads(v1);
-                __syncwarp();
-                if (it + 2 < n && !k_there(it + 2, k2)) return false;
+                grads(v1);
             }
-            if (!bwd_wait(BAR(W_DR), PH & 1, abort_flag)) return false;
+            if (!wait(W_DR, PH)) return false;
             tc_fence_after();
-            if (elect_one()) {                          // dQ += dS K
-                products_mn<16>(tDQ, tDS, sK + (uint32_t)k0 * kTileBytes, idD, it > 0);
-                tc_commit(BAR(W_KE + k0));
-                tc_commit(BAR(W_DE));
-            }
-            __syncwarp();
+            products_mn<16>(tDQ, tDS, sK + (uint32_t)k0 * kTileBytes, idD, it > 0);         // dQ += dS K
+            tc_commit(BAR(W_KE + k0));
+            tc_commit(BAR(W_DE));
             return true;
         };
-        for (int it = 0; ok && it < n; it += 4) {
-            ok = step(Int<0>{}, it) && (it + 1 >= n || step(Int<1>{}, it + 1)) && (it + 2 >= n || step(Int<2>{}, it + 2)) &&
-                 (it + 3 >= n || step(Int<3>{}, it + 3));
+        if (elect_one()) {
+            bool ok = wait(W_AT, 0) && (kBoth || wait(W_QG, 0)) && k_there(0, 0) && v_there(0, 0) && (n == 1 || k_there(1, 1));
+            if (ok) {
+                tc_fence_after();
+                scores(0), grads(0);
+            }
+            for (int it = 0; ok && it < n; it += 4) {
+                ok = step(Int<0>{}, it) && (it + 1 >= n || step(Int<1>{}, it + 1)) && (it + 2 >= n || step(Int<2>{}, it + 2)) &&
+                     (it + 3 >= n || step(Int<3>{}, it + 3));
+            }
+            if (!ok) bwd_give_up(abort_flag);
+            tc_commit(BAR(W_END));
+            mbar_wait(BAR(W_END), 0, nullptr);
         }
-        if (!ok) bwd_give_up(abort_flag);
-        if (elect_one()) tc_commit(BAR(W_END));
         __syncwarp();
-        bwd_wait(BAR(W_END), 0, nullptr);
     } else {
         // thread r of warpgroup wg owns query r and keys 32 wg .. 32 wg + 31 of each tile
-        const int wg = warp >> 2, r = threadIdx.x & 127, i = qt * kTile + r;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t mine = lanes + 32u * (uint32_t)wg;
         const int64_t stat = (int64_t)bh * a.n_t * kTile + i;
-        const float nl = a.ws.nlse[stat], nd = -c * a.ws.delta[stat];
+        const float nl = __ldcg(a.ws.nlse + stat), nd = -c * __ldcg(a.ws.delta + stat);
         const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
         const unsigned long long nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
-        // The thread's share of Q (and dO) to tensor memory: as the products' first operands they would take as much of
-        // shared memory's bandwidth as the second ones.
         bool ok = true;
-        {
-            constexpr int kWords = D / 8;               // 32-bit columns of a warpgroup
-            const int64_t row = ((int64_t)bh * a.T_len + (i < a.T_len ? i : 0)) * D + 2 * kWords * wg;
-            uint32_t w[kWords];
-#pragma unroll
-            for (int x = 0; x < (kBoth ? 2 : 1); ++x) {
-                const uint4* from = reinterpret_cast<const uint4*>((x ? go : q) + row);
-#pragma unroll
-                for (int e = 0; e < kWords / 4; ++e) {
-                    const uint4 y = i < a.T_len ? from[e] : make_uint4(0, 0, 0, 0);
-                    w[4 * e] = y.x, w[4 * e + 1] = y.y, w[4 * e + 2] = y.z, w[4 * e + 3] = y.w;
-                }
-                const uint32_t to = (x ? tG : tQ) + lanes + (uint32_t)(kWords * wg);
-                if (D == 128) tmem_st16(to, w);
-                else tmem_st8(to, w);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(BAR(W_AT));
+        if (kBoth) {
+            tmem_st8(tQ + lanes + 8u * (uint32_t)wg, mine_q);
+            tmem_st8(tG + lanes + 8u * (uint32_t)wg, mine_q + 8);
+        } else {
+            tmem_st16(tQ + lanes + 16u * (uint32_t)wg, mine_q);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(W_AT));
         for (int it = 0; it < n; ++it) {
             const bool diag = it == qt;
             if (!bwd_wait(BAR(W_SF), it & 1, abort_flag)) { ok = false; break; }
@@ -773,13 +803,20 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             if (lane == 0) mbar_arrive(BAR(W_DR));
         }
         if (!ok) bwd_give_up(abort_flag);
-        ok = bwd_wait(BAR(W_END), 0, nullptr) && ok && !*abort_flag;
+        if (!bwd_wait(BAR(W_END), 0, nullptr)) bwd_give_up(abort_flag);
         tc_fence_after();
-        // 32 columns a warpgroup
-        const int64_t row = (int64_t)bh * a.T_len + (i < a.T_len ? i : 0);
+        // 32 columns a warpgroup, through the stages that held K
         const float f = a.sm_scale * (AB == 0 ? 0x1p-15f : 1.0f) / c;
-        if (32 * wg < D) store_row<T, 32>(tDQ + mine, f, ok && i < a.T_len, dq + row * D + 32 * wg);
+        if (32 * wg < D) stage_row<T, 32>(tDQ + mine, f, smem + Lay::A1 + (uint32_t)(wg >> 1) * kHalfBytes, r, 32 * (wg & 1));
+        fence_proxy_async_smem();
+        named_barrier_sync(1, 32 * kSoftWarps);
+        if (threadIdx.x == 0 && !*abort_flag) {
+            for (int hf = 0; hf < kHalves; ++hf) tma_store_3d(&tdq, sK + (uint32_t)hf * kHalfBytes, 64 * hf, qt * kTile, bh);
+            bulk_store_done();
+        }
     }
+    // What follows this grid on the stream may start when it is done: the last CTA stays until the grid before it is too.
+    if (blockIdx.x == gridDim.x - 1) grid_dependency_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -803,18 +840,38 @@ size_t ws_layout(int B, int Hq, int Hkv, int T, char* base, BwdWs* w) {
     return at;
 }
 
-// Heads launched side by side: as many as keep `bytes` a head within about a third of L2.
+// Heads launched side by side: groups of one size, the largest that keeps `bytes` a head within a third of L2.
 int head_group(int heads, long long bytes) {
-    return (int)std::max<long long>(1, std::min<long long>(heads, (40ll << 20) / std::max<long long>(bytes, 1)));
+    const long long most = std::max<long long>(1, (40ll << 20) / std::max<long long>(bytes, 1));
+    const int groups = (int)((heads + most - 1) / most);
+    return (heads + groups - 1) / groups;
+}
+
+// A launch whose CTAs may start while the grid before it still runs (they wait for it where they need it).
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), int ctas, int threads, size_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename T, int AB, int D>
 kvq_status run_typed(const PrefillBwdCall& c, cudaStream_t s) {
     using Lay = BwdLayout<D>;
-    CUtensorMap mq, mk, mv, mg;
+    CUtensorMap mq, mk, mv, mg, mdq, mdk, mdv;
     const int dt = AB == 0 ? KVQ_F16 : KVQ_BF16;
     if (!make_map(&mq, c.q, dt, c.B * c.Hq, c.T, D) || !make_map(&mk, c.k, dt, c.B * c.Hkv, c.T, D) ||
-        !make_map(&mv, c.v, dt, c.B * c.Hkv, c.T, D) || !make_map(&mg, c.go, dt, c.B * c.Hq, c.T, D)) {
+        !make_map(&mv, c.v, dt, c.B * c.Hkv, c.T, D) || !make_map(&mg, c.go, dt, c.B * c.Hq, c.T, D) ||
+        !make_map(&mdq, c.dq, dt, c.B * c.Hq, c.T, D) || !make_map(&mdk, c.dk, dt, c.B * c.Hkv, c.T, D) ||
+        !make_map(&mdv, c.dv, dt, c.B * c.Hkv, c.T, D)) {
         set_error("prefill_attn_bwd: tensor map encoding failed");
         return KVQ_ECUDA;
     }
@@ -834,15 +891,13 @@ kvq_status run_typed(const PrefillBwdCall& c, cudaStream_t s) {
         e = cudaGetLastError();
         if (e == cudaSuccess) {
             a.group = head_group(c.B * c.Hkv, (long long)c.T * D * 4 * g);
-            bwd_dkv_kernel<T, AB, D><<<a.n_t * c.B * c.Hkv, kDkvThreads, Lay::BYTES, s>>>(mq, mk, mv, mg, (T*)c.dk,
-                                                                                          (T*)c.dv, a);
-            e = cudaGetLastError();
+            e = launch_early(bwd_dkv_kernel<T, AB, D>, a.n_t * c.B * c.Hkv, kDkvThreads, Lay::BYTES, s, mq, mk, mv, mg, mdk,
+                             mdv, a);
         }
         if (e == cudaSuccess) {
             a.group = head_group(c.B * c.Hq, (long long)c.T * D * 4 / g);
-            bwd_dq_kernel<T, AB, D><<<a.n_t * c.B * c.Hq, kDqThreads, Lay::BYTES, s>>>(mk, mv, mg, (const T*)c.q, (const T*)c.go,
-                                                                                       (T*)c.dq, a);
-            e = cudaGetLastError();
+            e = launch_early(bwd_dq_kernel<T, AB, D>, a.n_t * c.B * c.Hq, kDqThreads, Lay::BYTES, s, mk, mv, mg, mdq,
+                             (const T*)c.q, (const T*)c.go, a);
         }
     }
     if (e != cudaSuccess) {
