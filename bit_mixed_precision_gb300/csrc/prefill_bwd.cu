@@ -57,6 +57,7 @@ struct BwdArgs {
     int B, Hq, Hkv, T_len, n_t;
     float sm_scale, scale_log2;
     int group;          // heads (dkv: KV heads) whose tiles are launched side by side
+    int split;          // dkv: CTAs of a cluster that share a tile's query tiles
 };
 
 __device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -188,10 +189,10 @@ template <int AB> __device__ __forceinline__ float scale_of(const float* red) {
     return __int_as_float((127 - e) << 23);
 }
 
-// blockIdx.x -> (tile rank, head): heads in groups, all tiles of a group before the next group, the longest tiles of
+// block -> (tile rank, head): heads in groups, all tiles of a group before the next group, the longest tiles of
 // every head first.  A group's streamed operands stay in L2 while its CTAs run.
-__device__ __forceinline__ void place(const BwdArgs& a, int heads, int& rank, int& head) {
-    const int per = a.group * a.n_t, g = (int)(blockIdx.x / per), in = (int)(blockIdx.x % per);
+__device__ __forceinline__ void place(const BwdArgs& a, int block, int heads, int& rank, int& head) {
+    const int per = a.group * a.n_t, g = block / per, in = block % per;
     const int size = min(a.group, heads - g * a.group);
     rank = in / size;
     head = g * a.group + in % size;
@@ -288,7 +289,8 @@ template <typename T, int AB, int D>
 __global__ void __launch_bounds__(kDkvThreads, 1)
     bwd_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tg,
-                   const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, const BwdArgs a) {
+                   const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv, T* __restrict__ dk,
+                   T* __restrict__ dv, const BwdArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     if (base & 1023u) {                                 // layout assumption broken: do nothing
@@ -306,22 +308,26 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     int kt, u;
-    place(a, a.B * a.Hkv, kt, u);
+    place(a, (int)blockIdx.x / a.split, a.B * a.Hkv, kt, u);
     const int g = a.Hq / a.Hkv, h0 = u * g;             // head u * g + h of all B * Hq is the unit's h-th
-    const int m = a.n_t - kt, n = g * m;                // query tiles of a head; of all heads
+    // query tiles of a head; tiles of all heads, of which this CTA of the cluster has n from `from` on
+    const int m = a.n_t - kt, mine_of = (int)blockIdx.x % a.split, from = g * m * mine_of / a.split;
+    const int n = g * m * (mine_of + 1) / a.split - from;
 
     // (one lane) tile it of Q or dO into its stage
     auto load_q = [&](int it) {
         const int s = it % 3;
         mbar_expect_tx(BAR(V_QF + s), kTileBytes);
         for (int hf = 0; hf < kHalves; ++hf)
-            tma_load_3d(sQ + s * kTileBytes + hf * kHalfBytes, &tq, 64 * hf, (kt + it % m) * kTile, h0 + it / m, BAR(V_QF + s));
+            tma_load_3d(sQ + s * kTileBytes + hf * kHalfBytes, &tq, 64 * hf, (kt + (from + it) % m) * kTile, h0 + (from + it) / m,
+                        BAR(V_QF + s));
     };
     auto load_g = [&](int it) {
         const int s = it & 1;
         mbar_expect_tx(BAR(V_GF + s), kTileBytes);
         for (int hf = 0; hf < kHalves; ++hf)
-            tma_load_3d(sG + s * kTileBytes + hf * kHalfBytes, &tg, 64 * hf, (kt + it % m) * kTile, h0 + it / m, BAR(V_GF + s));
+            tma_load_3d(sG + s * kTileBytes + hf * kHalfBytes, &tg, 64 * hf, (kt + (from + it) % m) * kTile, h0 + (from + it) / m,
+                        BAR(V_GF + s));
     };
     if (warp == kSoftWarps && lane == 0) {
         mbar_init(BAR(V_KV), 1);
@@ -337,11 +343,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
         // the first copies do not wait for the rest of the CTA, nor for the grid before this one
-        mbar_expect_tx(BAR(V_KV), 2 * kTileBytes);
-        for (int hf = 0; hf < kHalves; ++hf) tma_load_3d(sK + hf * kHalfBytes, &tk, 64 * hf, kt * kTile, u, BAR(V_KV));
-        load_q(0);
-        for (int hf = 0; hf < kHalves; ++hf) tma_load_3d(sV + hf * kHalfBytes, &tv, 64 * hf, kt * kTile, u, BAR(V_KV));
-        load_g(0);
+        if (n > 0) {
+            mbar_expect_tx(BAR(V_KV), 2 * kTileBytes);
+            for (int hf = 0; hf < kHalves; ++hf) tma_load_3d(sK + hf * kHalfBytes, &tk, 64 * hf, kt * kTile, u, BAR(V_KV));
+            load_q(0);
+            for (int hf = 0; hf < kHalves; ++hf) tma_load_3d(sV + hf * kHalfBytes, &tv, 64 * hf, kt * kTile, u, BAR(V_KV));
+            load_g(0);
+        }
     }
     if (warp == kSoftWarps + 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     grid_dependency_wait();                             // the rows' statistics
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const float c = scale_of<AB>(red);
 
     if (warp == kSoftWarps) {
-        if (lane == 0) {
+        if (lane == 0 && n > 0) {
             int it = 1, lastq[3] = {0, -1, -1}, lastg[2] = {0, -1};
             for (; it < n; ++it) {
                 if (it >= 3 && !mbar_wait(BAR(V_QE + it % 3), (it / 3 - 1) & 1, abort_flag)) break;
@@ -430,8 +438,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             return true;
         };
         if (elect_one()) {
-            bool ok = wait(V_KV, 0) && q_there(0, 0) && g_there(0, 0) && (n == 1 || q_there(1, 1));
-            if (ok) scores(0), grads(0);
+            bool ok = n == 0 || (wait(V_KV, 0) && q_there(0, 0) && g_there(0, 0) && (n == 1 || q_there(1, 1)));
+            if (ok && n > 0) scores(0), grads(0);
             for (int it = 0; ok && it < n; it += 6) {
                 ok = step(Int<0>{}, it) && (it + 1 >= n || step(Int<1>{}, it + 1)) && (it + 2 >= n || step(Int<2>{}, it + 2)) &&
                      (it + 3 >= n || step(Int<3>{}, it + 3)) && (it + 4 >= n || step(Int<4>{}, it + 4)) &&
@@ -448,7 +456,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
-            const int64_t row = (int64_t)(h0 + it / m) * a.n_t * kTile + (kt + it % m) * kTile + 4 * lane;
+            const int64_t row = (int64_t)(h0 + (from + it) / m) * a.n_t * kTile + (kt + (from + it) % m) * kTile + 4 * lane;
             const float4 x = *reinterpret_cast<const float4*>(a.ws.nlse + row);
             float4 y = *reinterpret_cast<const float4*>(a.ws.delta + row);
             y.x *= -c, y.y *= -c, y.z *= -c, y.w *= -c;
@@ -472,7 +480,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
-            const bool diag = it % m == 0;
+            const bool diag = (from + it) % m == 0;
             if (!bwd_wait(BAR(V_TF + s), (it / 2) & 1, abort_flag)) { ok = false; break; }
             const unsigned long long* stat =
                 reinterpret_cast<const unsigned long long*>(smem + Lay::STAT + s * 1024 + 128 * wg) + (lane & 3);
@@ -565,18 +573,72 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         // dV (warpgroups 0 and 1, half of the columns each) and dK (2 and 3) through the stages that held Q
         const float unshift = AB == 0 ? 0x1p-15f : 1.0f;
         const int part = wg & 1, to_dk = wg >> 1;
-        uint8_t* half = smem + Lay::S0 + (uint32_t)(to_dk * kHalves + (D == 128 ? part : 0)) * kHalfBytes;
-        stage_row<T, D / 2>((to_dk ? tDK : tDV) + lanes + (uint32_t)(part * (D / 2)),
-                            to_dk ? a.sm_scale * unshift / c : unshift, half, r, D == 128 ? 0 : 32 * part);
-        fence_proxy_async_smem();
-        named_barrier_sync(1, 32 * kSoftWarps);
-        if (threadIdx.x == 0 && !*abort_flag) {
-            for (int hf = 0; hf < kHalves; ++hf) {
-                tma_store_3d(&tdv, sQ + (uint32_t)hf * kHalfBytes, 64 * hf, kt * kTile, u);
-                tma_store_3d(&tdk, sQ + (uint32_t)(kHalves + hf) * kHalfBytes, 64 * hf, kt * kTile, u);
+        const uint32_t sums = (to_dk ? tDK : tDV) + lanes + (uint32_t)(part * (D / 2));
+        if (a.split == 1) {
+            uint8_t* half = smem + Lay::S0 + (uint32_t)(to_dk * kHalves + (D == 128 ? part : 0)) * kHalfBytes;
+            stage_row<T, D / 2>(sums, to_dk ? a.sm_scale * unshift / c : unshift, half, r, D == 128 ? 0 : 32 * part);
+            fence_proxy_async_smem();
+            named_barrier_sync(1, 32 * kSoftWarps);
+            if (threadIdx.x == 0 && !*abort_flag) {
+                for (int hf = 0; hf < kHalves; ++hf) {
+                    tma_store_3d(&tdv, sQ + (uint32_t)hf * kHalfBytes, 64 * hf, kt * kTile, u);
+                    tma_store_3d(&tdk, sQ + (uint32_t)(kHalves + hf) * kHalfBytes, 64 * hf, kt * kTile, u);
+                }
+                bulk_store_done();
             }
-            bulk_store_done();
+        } else {
+            // the cluster's sums meet in shared memory: row r has 2 D floats, dV then dK, 16-byte pieces swizzled
+            float4* row = reinterpret_cast<float4*>(smem + Lay::S0) + r * (D / 2);
+#pragma unroll
+            for (int c4 = 0; c4 < D / 64; ++c4) {
+                float x[32];
+                if (n > 0) {
+                    tmem_ld32(sums + (uint32_t)c4 * 32u, x);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    row[((to_dk * D + part * (D / 2)) / 4 + c4 * 8 + e) ^ (r & 7)] =
+                        make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
         }
+    }
+    if (a.split > 1) {
+        __syncwarp();
+        cluster_arrive_release();
+        cluster_wait_acquire();
+        if (warp < kSoftWarps) {
+            // every CTA adds up its share of the rows, always in the order of the CTAs
+            bool fine = true;
+            const uint32_t flag = smem_u32(const_cast<int*>(abort_flag)), at = base + Lay::S0;
+            for (int p = 0; p < a.split; ++p) fine = fine && cluster_ld_u32(cluster_map(flag, (uint32_t)p)) == 0;
+            const float unshift = AB == 0 ? 0x1p-15f : 1.0f, fk = a.sm_scale * unshift / c;
+            const int rows = kTile / a.split;
+            for (int e = threadIdx.x; e < rows * (D / 2); e += 32 * kSoftWarps) {
+                const int r = mine_of * rows + e / (D / 2), piece = e % (D / 2);
+                const uint32_t off = at + (uint32_t)(r * (D / 2) + (piece ^ (r & 7))) * 16u;
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int p = 0; p < a.split; ++p) {
+                    const float4 y = cluster_ld_f4(cluster_map(off, (uint32_t)p));
+                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
+                const bool to_dk = piece >= D / 4;
+                const float f = to_dk ? fk : unshift;
+                const int j = kt * kTile + r;
+                if (fine && j < a.T_len) {
+                    uint2 w;
+                    w.x = Pack2<T>::pack(x.x * f, x.y * f);
+                    w.y = Pack2<T>::pack(x.z * f, x.w * f);
+                    *reinterpret_cast<uint2*>((to_dk ? dk : dv) + ((int64_t)u * a.T_len + j) * D + 4 * (piece % (D / 4))) = w;
+                }
+            }
+        }
+        __syncwarp();
+        cluster_arrive_release();                       // nobody reads this CTA's memory any more
+        cluster_wait_acquire();
     }
     tc_fence_before();
     __syncthreads();
@@ -612,7 +674,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     int rank, bh;
-    place(a, a.B * a.Hq, rank, bh);
+    place(a, (int)blockIdx.x, a.B * a.Hq, rank, bh);
     const int qt = a.n_t - 1 - rank, n = qt + 1;
     const int u = bh / a.Hq * a.Hkv + bh % a.Hq / (a.Hq / a.Hkv);
     const int wg = warp >> 2, r = threadIdx.x & 127, i = qt * kTile + r;
@@ -847,19 +909,45 @@ int head_group(int heads, long long bytes) {
     return (heads + groups - 1) / groups;
 }
 
+// CTAs that share a key tile in dkv (a cluster that adds up its sums through shared memory).  In thousands of clocks, a
+// tile takes about 2.3 in dkv and 1.9 in dq, a CTA's start and end 6 and with a cluster's sum 9; the call takes at least
+// its longest CTA and, as dq fills the SMs that dkv leaves, all work over the SMs.  The size with the least such bound.
+int cluster_size(int units, int g, int n_t) {
+    int sms = 0, dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        sms = 152;
+    }
+    const double tiles = 0.5 * units * g * n_t * (n_t + 1.0), ctas = (double)units * n_t;
+    int best = 1;
+    double least = 0.0;
+    for (int c = 1; c <= 8; c *= 2) {
+        const double longest = 2.3 * g * n_t / c + (c > 1 ? 9.0 : 6.0);
+        const double all = (4.2 * tiles + ctas * (c * (c > 1 ? 9.0 : 6.0) + 6.0 * g)) / sms;
+        const double bound = std::max(longest, all);
+        if (c == 1 || bound < 0.95 * least) best = c, least = bound;
+    }
+    return best;
+}
+
 // A launch whose CTAs may start while the grid before it still runs (they wait for it where they need it).
 template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), int ctas, int threads, size_t smem, cudaStream_t s, Args... args) {
+cudaError_t launch_early(void (*kernel)(Params...), int ctas, int cluster, int threads, size_t smem, cudaStream_t s,
+                         Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -884,19 +972,20 @@ kvq_status run_typed(const PrefillBwdCall& c, cudaStream_t s) {
         ws_layout(c.B, c.Hq, c.Hkv, c.T, (char*)c.ws, &a.ws);
         a.B = c.B, a.Hq = c.Hq, a.Hkv = c.Hkv, a.T_len = c.T, a.n_t = (c.T + kTile - 1) / kTile;
         a.sm_scale = c.sm_scale, a.scale_log2 = c.sm_scale * kLog2e;
-        a.group = 1;
+        a.group = a.split = 1;
         const int g = c.Hq / c.Hkv;
         bwd_prep_kernel<T, AB, D><<<dim3(a.n_t, c.B * c.Hq), kPrepThreads, 0, s>>>(
             (const T*)c.o, (const T*)c.go, (const T*)c.v, c.lse, c.glse, a);
         e = cudaGetLastError();
         if (e == cudaSuccess) {
             a.group = head_group(c.B * c.Hkv, (long long)c.T * D * 4 * g);
-            e = launch_early(bwd_dkv_kernel<T, AB, D>, a.n_t * c.B * c.Hkv, kDkvThreads, Lay::BYTES, s, mq, mk, mv, mg, mdk,
-                             mdv, a);
+            a.split = cluster_size(c.B * c.Hkv, g, a.n_t);
+            e = launch_early(bwd_dkv_kernel<T, AB, D>, a.n_t * c.B * c.Hkv * a.split, a.split, kDkvThreads, Lay::BYTES, s, mq,
+                             mk, mv, mg, mdk, mdv, (T*)c.dk, (T*)c.dv, a);
         }
         if (e == cudaSuccess) {
             a.group = head_group(c.B * c.Hq, (long long)c.T * D * 4 / g);
-            e = launch_early(bwd_dq_kernel<T, AB, D>, a.n_t * c.B * c.Hq, kDqThreads, Lay::BYTES, s, mk, mv, mg, mdq,
+            e = launch_early(bwd_dq_kernel<T, AB, D>, a.n_t * c.B * c.Hq, 1, kDqThreads, Lay::BYTES, s, mk, mv, mg, mdq,
                              (const T*)c.q, (const T*)c.go, a);
         }
     }
