@@ -4,6 +4,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <atomic>
 #include <string>
 
 #include <algorithm>
@@ -30,6 +31,24 @@ void set_error(const char* fmt, ...) {
     vsnprintf(buf, sizeof(buf), fmt, ap);
     va_end(ap);
     g_last_error = buf;
+}
+
+int device_sms(int* device) {
+    static std::atomic<int> known[64];
+    int dev = -1, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        dev = -1;
+    }
+    if (device) *device = dev;
+    if (dev < 0) return 152;
+    if (dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 152;
+    }
+    if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    return sms;
 }
 
 }  // namespace kvq
@@ -567,13 +586,15 @@ static kvq_status check_rope(const kvq_rope* r, kvq_dtype dt, int B, int T, int 
     return KVQ_OK;
 }
 
-// Strides {b, t, head} of rows [B, T, H, D].
-static kvq_status head_strides(const void* x, const int64_t* given, int T, int H, int D, const char* who, int64_t* out) {
+// Strides {b, t, head} of rows [B, T, H, D]; that of an axis of one entry counts for nothing.
+static kvq_status head_strides(const void* x, const int64_t* given, int B, int T, int H, int D, const char* who,
+                               int64_t* out) {
     KVQ_REQUIRE(x, KVQ_EINVAL, "%s: null pointer", who);
     KVQ_REQUIRE(aligned(x, 16), KVQ_EINVAL, "%s: activations must be 16-byte aligned", who);
     const int64_t dense[3] = {(int64_t)T * H * D, (int64_t)H * D, D};
+    const int size[3] = {B, T, H};
     for (int i = 0; i < 3; ++i) {
-        out[i] = given ? given[i] : dense[i];
+        out[i] = size[i] == 1 ? 0 : given ? given[i] : dense[i];
         KVQ_REQUIRE(out[i] >= 0 && out[i] % 8 == 0, KVQ_EINVAL, "%s: strides must be >= 0 and multiples of 8 elements",
                     who);
     }
@@ -591,9 +612,9 @@ kvq_status qk_norm_rope(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq
     c.rope = rope, c.dt = dt, c.B = B, c.T = T, c.Hq = Hq, c.Hkv = Hkv, c.D = D, c.q = q, c.k = k, c.v = v;
     c.pos = pos, c.qw = q_weight, c.kw = k_weight, c.w_f32 = weight_f32 != 0, c.eps = eps;
     c.qo = q_out, c.ko = k_out, c.vo = v_out;
-    if ((st = head_strides(q, strides, T, Hq, D, who, c.strides[0])) != KVQ_OK) return st;
-    if ((st = head_strides(k, strides ? strides + 3 : nullptr, T, Hkv, D, who, c.strides[1])) != KVQ_OK) return st;
-    if (v && (st = head_strides(v, strides ? strides + 6 : nullptr, T, Hkv, D, who, c.strides[2])) != KVQ_OK) return st;
+    if ((st = head_strides(q, strides, B, T, Hq, D, who, c.strides[0])) != KVQ_OK) return st;
+    if ((st = head_strides(k, strides ? strides + 3 : nullptr, B, T, Hkv, D, who, c.strides[1])) != KVQ_OK) return st;
+    if (v && (st = head_strides(v, strides ? strides + 6 : nullptr, B, T, Hkv, D, who, c.strides[2])) != KVQ_OK) return st;
     KVQ_REQUIRE(q_out && k_out && (v_out || !v) && (pos || rope->rot == 0), KVQ_EINVAL, "%s: null pointer", who);
     KVQ_REQUIRE(aligned(q_out, 16) && aligned(k_out, 16) && aligned(v_out, 16) && aligned(q_weight, 16) &&
                     aligned(k_weight, 16) && aligned(pos, 4),
@@ -630,12 +651,12 @@ kvq_status qk_norm_rope_bwd(const kvq_rope* rope, kvq_dtype dt, int B, int T, in
     c.pos = pos, c.qw = q_weight, c.kw = k_weight, c.w_f32 = weight_f32 != 0, c.eps = eps;
     c.qo = const_cast<void*>(dq), c.ko = const_cast<void*>(dk), c.vo = const_cast<void*>(dv);
     c.gq = gq, c.gk = gk, c.gv = gv, c.gqw = gq_weight, c.gkw = gk_weight, c.ws = ws;
-    if (q_weight && (st = head_strides(q, strides, T, Hq, D, who, c.strides[0])) != KVQ_OK) return st;
-    if (k_weight && (st = head_strides(k, strides ? strides + 3 : nullptr, T, Hkv, D, who, c.strides[1])) != KVQ_OK)
+    if (q_weight && (st = head_strides(q, strides, B, T, Hq, D, who, c.strides[0])) != KVQ_OK) return st;
+    if (k_weight && (st = head_strides(k, strides ? strides + 3 : nullptr, B, T, Hkv, D, who, c.strides[1])) != KVQ_OK)
         return st;
-    if ((st = head_strides(gq, g_strides, T, Hq, D, who, c.gstrides[0])) != KVQ_OK) return st;
-    if ((st = head_strides(gk, g_strides ? g_strides + 3 : nullptr, T, Hkv, D, who, c.gstrides[1])) != KVQ_OK) return st;
-    if (dv && (st = head_strides(gv, g_strides ? g_strides + 6 : nullptr, T, Hkv, D, who, c.gstrides[2])) != KVQ_OK)
+    if ((st = head_strides(gq, g_strides, B, T, Hq, D, who, c.gstrides[0])) != KVQ_OK) return st;
+    if ((st = head_strides(gk, g_strides ? g_strides + 3 : nullptr, B, T, Hkv, D, who, c.gstrides[1])) != KVQ_OK) return st;
+    if (dv && (st = head_strides(gv, g_strides ? g_strides + 6 : nullptr, B, T, Hkv, D, who, c.gstrides[2])) != KVQ_OK)
         return st;
     KVQ_REQUIRE(dq && dk && (pos || rope->rot == 0), KVQ_EINVAL, "%s: null pointer", who);
     KVQ_REQUIRE(aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16) && aligned(q_weight, 16) && aligned(k_weight, 16) &&

@@ -12,6 +12,9 @@ namespace kvq {
 // Records the thread-local message returned by kvq_last_error().
 void set_error(const char* fmt, ...);
 
+// The current device and its multiprocessors (asked for once per device; 152 where the query fails).
+int device_sms(int* device);
+
 cudaError_t launch_quant_pack(const void* x, int dt, int units, int T, int D,
                               const int32_t* gather, int n, int bits, int G, int axis,
                               uint32_t* codes, uint16_t* scale, uint16_t* zero, cudaStream_t s);

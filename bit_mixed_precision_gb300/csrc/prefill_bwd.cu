@@ -25,6 +25,7 @@
 // Every mbarrier wait is bounded; a CTA that gives up drains its copies and products, frees TMEM, stores nothing and
 // records KVQ_ETIMEOUT in the device status word.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kvq_common.cuh"
@@ -913,12 +914,7 @@ int head_group(int heads, long long bytes) {
 // tile takes about 2.3 in dkv and 1.9 in dq, a CTA's start and end 6 and with a cluster's sum 9; the call takes at least
 // its longest CTA and, as dq fills the SMs that dkv leaves, all work over the SMs.  The size with the least such bound.
 int cluster_size(int units, int g, int n_t) {
-    int sms = 0, dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        sms = 152;
-    }
+    const int sms = device_sms(nullptr);
     const double tiles = 0.5 * units * g * n_t * (n_t + 1.0), ctas = (double)units * n_t;
     int best = 1;
     double least = 0.0;
@@ -963,10 +959,16 @@ kvq_status run_typed(const PrefillBwdCall& c, cudaStream_t s) {
         set_error("prefill_attn_bwd: tensor map encoding failed");
         return KVQ_ECUDA;
     }
-    cudaError_t e = cudaFuncSetAttribute(bwd_dkv_kernel<T, AB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Lay::BYTES);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(bwd_dq_kernel<T, AB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::BYTES);
+    static std::atomic<uint64_t> ready{0};              // devices whose attributes are set
+    int dev = -1;
+    device_sms(&dev);
+    cudaError_t e = cudaSuccess;
+    if (dev < 0 || dev > 63 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(bwd_dkv_kernel<T, AB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::BYTES);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(bwd_dq_kernel<T, AB, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::BYTES);
+        if (e == cudaSuccess && dev >= 0 && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
     if (e == cudaSuccess) {
         BwdArgs a;
         ws_layout(c.B, c.Hq, c.Hkv, c.T, (char*)c.ws, &a.ws);

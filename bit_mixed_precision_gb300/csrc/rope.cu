@@ -337,16 +337,6 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-int sm_count() {
-    int sms = 0, dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        sms = 152;
-    }
-    return sms;
-}
-
 template <typename T> RopeArgs<T> make_args(const RopeCall& c) {
     RopeArgs<T> a;
     a.q = (const T*)c.q, a.k = (const T*)c.k, a.v = (const T*)c.v;
@@ -368,7 +358,7 @@ template <typename T, int D> cudaError_t forward(const RopeCall& c, cudaStream_t
     const RopeArgs<T> a = make_args<T>(c);
     constexpr int rows = Place<D>::kRows;
     const int groups = (c.Hq + rows - 1) / rows + (c.v ? 2 : 1) * ((c.Hkv + rows - 1) / rows);
-    const int64_t tokens = (int64_t)c.B * c.T, want = (int64_t)sm_count() * 16;
+    const int64_t tokens = (int64_t)c.B * c.T, want = (int64_t)device_sms(nullptr) * 16;
     const int split = (int)std::min<int64_t>(groups, (want + tokens - 1) / tokens);
     const int per_part = (groups + split - 1) / split, parts = (groups + per_part - 1) / per_part;
     const int64_t ctas = (tokens * parts + kWarps - 1) / kWarps;
@@ -398,7 +388,7 @@ template <typename T, int D> cudaError_t backward(const RopeCall& c, cudaStream_
 
 int rope_bwd_ctas(int B, int T) {
     const int64_t tokens = (int64_t)B * T;
-    return (int)std::min<int64_t>((tokens + kWarps - 1) / kWarps, (int64_t)sm_count() * 2);
+    return (int)std::min<int64_t>((tokens + kWarps - 1) / kWarps, (int64_t)device_sms(nullptr) * 2);
 }
 
 cudaError_t launch_rope(const RopeCall& c, cudaStream_t s) {

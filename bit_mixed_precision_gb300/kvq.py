@@ -870,7 +870,7 @@ class Rope:
     desc: KvqRope = field(repr=False)
 
     def __post_init__(self):
-        self._ref = ctypes.byref(self.desc)
+        self._ref, self.axes = ctypes.byref(self.desc), self.desc.n_axes
 
 
 def make_rope(D, rot=None, base=10000.0, inv_freq=None, axis=None, interleaved=False):
@@ -915,48 +915,61 @@ def _new(shape, like, dtype, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _heads(x, shape, like, name):
-    """Rows of x, [B, T, H, D] or for a step [B, H, D], D contiguous: pointer and strides {b, t, head}."""
-    if tuple(x.shape) != shape or x.dtype != like.dtype or x.get_device() != like.get_device() or not x.is_cuda:
-        _bad(f"{name} must be a CUDA tensor {list(shape)} of {like.dtype} on q's device, got {list(x.shape)} of {x.dtype}")
+_I9 = ctypes.c_int64 * 9
+
+
+def _heads(x, shape, dtype, index, name):
+    """Rows [B, T, H, D] or for a step [B, H, D], D contiguous: pointer and strides {b, t, head}."""
     st = x.stride()
+    if x.shape != shape or x.dtype != dtype or x.get_device() != index:
+        _bad(f"{name} must be a CUDA tensor {list(shape)} of {dtype} on q's device, got {list(x.shape)} of {x.dtype}")
     if st[-1] != 1:
         _bad(f"{name}: the last axis must be contiguous")
-    st = [s if n > 1 else 0 for n, s in zip(shape, st)]
-    return x.data_ptr(), (st[0], 0 if len(shape) == 3 else st[1], st[-2])
+    return x.data_ptr(), (st[:3] if len(st) == 4 else (st[0], 0, st[1]))
 
 
-def _dense(x, shape, like, name, dtype=None):
-    """The pointer of a contiguous tensor, or None."""
-    if x is None:
-        return None
-    if tuple(x.shape) != tuple(shape) or x.dtype != (dtype or like.dtype) or not x.is_contiguous() or \
-            not x.is_cuda or x.get_device() != like.get_device():
-        _bad(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype or like.dtype} on q's device")
+def _dense(x, shape, dtype, index, name):
+    """The pointer of a contiguous tensor."""
+    if x.shape != shape or x.dtype != dtype or x.get_device() != index or not x.is_contiguous():
+        _bad(f"{name} must be a contiguous CUDA tensor {list(shape)} of {dtype} on q's device")
     return x.data_ptr()
 
 
 def _rope_call(q, k, pos, rope, q_weight, k_weight):
-    """Sizes, position pointer and weights that both directions check alike; q and k raw rows."""
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
+    """What both directions check alike, q and k raw rows: device, [B] or [B, T], sizes, position pointer, weight pointers
+    and whether the weights are float32."""
+    index, shape = q.get_device(), q.shape
+    if len(shape) not in (3, 4) or k.dim() != len(shape):
         _bad("q and k must be [B, T, heads, D], for a step [B, heads, D]")
-    if q.shape[-1] != rope.D:
-        _bad(f"the rope is for {rope.D} channels, q has {q.shape[-1]}")
-    step = q.dim() == 3
-    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
-    T, Hkv = 1 if step else q.shape[1], k.shape[-2]
+    Hq, D = shape[-2:]
+    Hkv = k.shape[-2]
+    if D != rope.D:
+        _bad(f"the rope is for {rope.D} channels, q has {D}")
     if Hkv == 0 or Hq % Hkv:
         _bad("Hq must be a multiple of Hkv")
-    axes, tokens = rope.desc.n_axes, (B,) if step else (B, T)
-    if tuple(pos.shape) != (axes,) + tokens and (axes > 1 or tuple(pos.shape) != tokens):
-        _bad(f"pos must be [{axes}, {', '.join(map(str, tokens))}], got {list(pos.shape)}")
-    pp = _dense(pos, pos.shape, q, "pos", torch.int32)
-    f32 = [w.dtype == torch.float32 for w in (q_weight, k_weight) if w is not None]
-    if any(f32) and not all(f32):
-        raise TypeError("q_weight and k_weight must share one dtype")
-    wdt = torch.float32 if any(f32) else q.dtype
-    return step, B, T, Hq, Hkv, D, pp, _dense(q_weight, (D,), q, "q_weight", wdt), \
-        _dense(k_weight, (D,), q, "k_weight", wdt), 1 if any(f32) else 0
+    rows, axes = shape[:-2], rope.axes
+    if pos.shape != (axes,) + rows and (axes > 1 or pos.shape != rows):
+        _bad(f"pos must be [{axes}, {', '.join(map(str, rows))}], got {list(pos.shape)}")
+    if pos.dtype != torch.int32 or pos.get_device() != index or not pos.is_contiguous():
+        _bad("pos must be a contiguous tensor of torch.int32 on q's device")
+    if index < 0:
+        _bad("q must be a CUDA tensor")
+    qw = kw = None
+    f32 = 0
+    w = q_weight if q_weight is not None else k_weight
+    if w is not None:
+        wdt = w.dtype
+        if k_weight is not None and k_weight.dtype != wdt:
+            raise TypeError("q_weight and k_weight must share one dtype")
+        if wdt == torch.float32:
+            f32 = 1
+        else:
+            wdt = q.dtype
+        if q_weight is not None:
+            qw = _dense(q_weight, (D,), wdt, index, "q_weight")
+        if k_weight is not None:
+            kw = _dense(k_weight, (D,), wdt, index, "k_weight")
+    return index, rows, Hq, Hkv, D, pos.data_ptr(), qw, kw, f32
 
 
 def qk_norm_rope(q, k, v, pos, rope, q_weight=None, k_weight=None, eps=1e-6, out=None, stream=None):
@@ -964,24 +977,27 @@ def qk_norm_rope(q, k, v, pos, rope, q_weight=None, k_weight=None, eps=1e-6, out
     for a step [B, heads, D]; v may be None) to (q, k, v) [B, heads, T, D] ([B, heads, D]), q and k RMS-normed per
     head (q_weight, k_weight [D]; None: no norm) and turned by pos (int32 [B, T], with several axes [axes, B, T];
     for a step without T)."""
-    dt = _dt(q)
-    step, B, T, Hq, Hkv, D, pp, qw, kw, f32 = _rope_call(q, k, pos, rope, q_weight, k_weight)
-    rows = (B,) if step else (B, T)
-    qp, qs = _heads(q, rows + (Hq, D), q, "q")
-    kp, ks = _heads(k, rows + (Hkv, D), q, "k")
-    vp, vs = _heads(v, rows + (Hkv, D), q, "v") if v is not None else (None, (0, 0, 0))
-    raw = _call_stream(q.get_device(), stream)
-    shapes = [(B, h, D) if step else (B, h, T, D) for h in (Hq, Hkv)]
+    dt, dtype = _dt(q), q.dtype
+    index, rows, Hq, Hkv, D, pp, qw, kw, f32 = _rope_call(q, k, pos, rope, q_weight, k_weight)
+    qp, qs = _heads(q, rows + (Hq, D), dtype, index, "q")
+    kv_in = rows + (Hkv, D)
+    kp, ks = _heads(k, kv_in, dtype, index, "k")
+    vp, vs = (None, (0, 0, 0)) if v is None else _heads(v, kv_in, dtype, index, "v")
+    raw = _call_stream(index, stream)
+    B = rows[0]
+    T, q_shape, kv_shape = (1, q.shape, kv_in) if len(rows) == 1 else (rows[1], (B, Hq, rows[1], D), (B, Hkv, rows[1], D))
     if out is None:
-        qo, ko = _new(shapes[0], q, q.dtype, stream), _new(shapes[1], q, q.dtype, stream)
-        vo = _new(shapes[1], q, q.dtype, stream) if v is not None else None
+        qo, ko = _new(q_shape, q, dtype, stream), _new(kv_shape, q, dtype, stream)
+        vo = None if v is None else _new(kv_shape, q, dtype, stream)
+        qop, kop, vop = qo.data_ptr(), ko.data_ptr(), None if v is None else vo.data_ptr()
     else:
         qo, ko, vo = out
         if (vo is None) != (v is None):
             _bad("out must have a v where there is one")
-    _check(lib().qk_norm_rope(rope._ref, dt, B, T, Hq, Hkv, D, qp, kp, vp, (ctypes.c_int64 * 9)(*qs, *ks, *vs), pp, qw,
-                              kw, f32, float(eps), _dense(qo, shapes[0], q, "out[0]"), _dense(ko, shapes[1], q, "out[1]"),
-                              _dense(vo, shapes[1], q, "out[2]"), raw))
+        qop, kop = _dense(qo, q_shape, dtype, index, "out[0]"), _dense(ko, kv_shape, dtype, index, "out[1]")
+        vop = None if vo is None else _dense(vo, kv_shape, dtype, index, "out[2]")
+    _check((_lib or lib()).qk_norm_rope(rope._ref, dt, B, T, Hq, Hkv, D, qp, kp, vp, _I9(*qs, *ks, *vs), pp, qw, kw, f32,
+                                        eps, qop, kop, vop, raw))
     if stream is not None:
         _used8(stream, q, k, v, pos, q_weight, k_weight, qo, ko, vo)
     return qo, ko, vo
@@ -993,34 +1009,40 @@ def qk_norm_rope_bwd(dq, dk, dv, q, k, pos, rope, q_weight=None, k_weight=None, 
     Returns (gq, gk, gv, gq_weight, gk_weight), the first three [B, T, heads, D] as views of one [B, T, Hq + 2 Hkv, D]
     (or as given in out[:3], any strides), the last two float32 [D] (None without that norm).  ws: a uint8 workspace
     of qk_norm_rope_bwd_ws_bytes(q) + 256 bytes to share between calls that never overlap on the GPU."""
-    dt = _dt(q)
-    step, B, T, Hq, Hkv, D, pp, qw, kw, f32 = _rope_call(q, k, pos, rope, q_weight, k_weight)
-    rows, like = (B,) if step else (B, T), q
-    qp, qs = _heads(q, rows + (Hq, D), q, "q")
-    kp, ks = _heads(k, rows + (Hkv, D), q, "k")
-    raw = _call_stream(q.get_device(), stream)
-    shapes = [(B, h, D) if step else (B, h, T, D) for h in (Hq, Hkv)]
-    grads = [_dense(x, s, q, n) for x, s, n in ((dq, shapes[0], "dq"), (dk, shapes[1], "dk"), (dv, shapes[1], "dv"))]
-    if grads[0] is None or grads[1] is None:
+    dt, dtype = _dt(q), q.dtype
+    index, rows, Hq, Hkv, D, pp, qw, kw, f32 = _rope_call(q, k, pos, rope, q_weight, k_weight)
+    q_in, kv_in = rows + (Hq, D), rows + (Hkv, D)
+    qp, qs = _heads(q, q_in, dtype, index, "q")
+    kp, ks = _heads(k, kv_in, dtype, index, "k")
+    raw = _call_stream(index, stream)
+    B = rows[0]
+    T, q_shape, kv_shape = (1, q_in, kv_in) if len(rows) == 1 else (rows[1], (B, Hq, rows[1], D), (B, Hkv, rows[1], D))
+    if dq is None or dk is None:
         _bad("dq and dk are needed")
+    dqp, dkp = _dense(dq, q_shape, dtype, index, "dq"), _dense(dk, kv_shape, dtype, index, "dk")
+    dvp = None if dv is None else _dense(dv, kv_shape, dtype, index, "dv")
+    f = torch.float32
     if out is None:
-        both = _new(rows + (Hq + (2 if dv is not None else 1) * Hkv, D), q, q.dtype, stream)
-        gq, gk = both[..., :Hq, :], both[..., Hq:Hq + Hkv, :]
-        gv = both[..., Hq + Hkv:, :] if dv is not None else None
-        gqw, gkw = (None if w is None else _new((D,), q, torch.float32, stream) for w in (q_weight, k_weight))
+        both = _new(rows + (Hq + (1 if dv is None else 2) * Hkv, D), q, dtype, stream)
+        gq, gk, *gv = both.split_with_sizes([Hq, Hkv] if dv is None else [Hq, Hkv, Hkv], -2)
+        gv = gv[0] if gv else None
+        gqw = None if qw is None else _new((D,), q, f, stream)
+        gkw = None if kw is None else _new((D,), q, f, stream)
     else:
         gq, gk, gv, gqw, gkw = out
         if any((a is None) != (b is None) for a, b in ((gv, dv), (gqw, q_weight), (gkw, k_weight))):
             _bad("out must have a gradient for each of dv, q_weight and k_weight that is there, and for no other")
-    gqp, gqs = _heads(gq, rows + (Hq, D), q, "out[0]")
-    gkp, gks = _heads(gk, rows + (Hkv, D), q, "out[1]")
-    gvp, gvs = _heads(gv, rows + (Hkv, D), q, "out[2]") if gv is not None else (None, (0, 0, 0))
-    wsp, ws_bytes, ws = _workspace(lib().qk_norm_rope_bwd_workspace_bytes(B, T, D, 1 if qw or kw else 0), like, ws, stream)
-    i9 = ctypes.c_int64 * 9
-    _check(lib().qk_norm_rope_bwd(rope._ref, dt, B, T, Hq, Hkv, D, *grads, qp, kp, i9(*qs, *ks, 0, 0, 0), pp, qw, kw, f32,
-                                  float(eps), gqp, gkp, gvp, i9(*gqs, *gks, *gvs),
-                                  _dense(gqw, (D,), q, "out[3]", torch.float32),
-                                  _dense(gkw, (D,), q, "out[4]", torch.float32), wsp, ws_bytes, raw))
+    gqp, gqs = _heads(gq, q_in, dtype, index, "out[0]")
+    gkp, gks = _heads(gk, kv_in, dtype, index, "out[1]")
+    gvp, gvs = (None, (0, 0, 0)) if gv is None else _heads(gv, kv_in, dtype, index, "out[2]")
+    gqwp = None if gqw is None else _dense(gqw, (D,), f, index, "out[3]")
+    gkwp = None if gkw is None else _dense(gkw, (D,), f, index, "out[4]")
+    L = _lib or lib()
+    wsp = ws_bytes = 0
+    if qw or kw:
+        wsp, ws_bytes, ws = _workspace(L.qk_norm_rope_bwd_workspace_bytes(B, T, D, 1), q, ws, stream)
+    _check(L.qk_norm_rope_bwd(rope._ref, dt, B, T, Hq, Hkv, D, dqp, dkp, dvp, qp, kp, _I9(*qs, *ks, 0, 0, 0), pp, qw, kw,
+                              f32, eps, gqp, gkp, gvp, _I9(*gqs, *gks, *gvs), gqwp, gkwp, wsp, ws_bytes, raw))
     if stream is not None:
         _used8(stream, dq, dk, dv, q, k, pos, q_weight, k_weight, gq, gk, gv, gqw, gkw, ws)
     return gq, gk, gv, gqw, gkw
@@ -1031,9 +1053,12 @@ def qk_norm_rope_bwd_ws_bytes(q):
     return lib().qk_norm_rope_bwd_workspace_bytes(q.shape[0], 1 if q.dim() == 3 else q.shape[1], q.shape[-1], 1)
 
 
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
 def _workspace(need, like, ws, stream):
     """Pointer (256-byte aligned), bytes and tensor of a workspace: `ws` if given, else a new one."""
-    if need == ctypes.c_size_t(-1).value:
+    if need == _NO_SIZE:
         raise KvqError(KVQ_EINVAL, lib().kvq_last_error().decode())
     if need == 0:
         return None, 0, ws
@@ -1051,21 +1076,29 @@ def prefill_attn_bwd(do, q, k, v, o, lse, sm_scale=None, dlse=None, out=None, ws
     """Gradients (dq, dk, dv) of q [B, Hq, T, D], k, v [B, Hkv, T, D] through prefill_attn_scores' o and lse: do is the
     gradient of o, dlse (float32 [B, Hq, T], may be None) that of lse.  All contiguous.  ws: a uint8 workspace of
     prefill_attn_bwd_ws_bytes(q, k) + 256 bytes to share between calls that never overlap on the GPU."""
-    dt = _dt(q)
+    dt, dtype = _dt(q), q.dtype
     _check_qk(q, k, v)
-    B, Hq, T, D = q.shape
-    Hkv = k.shape[1]
-    args = [_dense(x, s, q, n, d) for x, s, n, d in (
-        (q, q.shape, "q", None), (k, k.shape, "k", None), (v, k.shape, "v", None), (o, q.shape, "o", None),
-        (do, q.shape, "do", None), (lse, q.shape[:3], "lse", torch.float32), (dlse, q.shape[:3], "dlse", torch.float32))]
-    if None in args[:6]:
-        _bad("do, q, k, v, o and lse are needed")
-    raw = _call_stream(q.get_device(), stream)
-    dq, dk, dv = [_new(x.shape, q, q.dtype, stream) for x in (q, k, k)] if out is None else out
-    outs = [_dense(x, s, q, f"out[{i}]") for i, (x, s) in enumerate(((dq, q.shape), (dk, k.shape), (dv, k.shape)))]
-    wsp, ws_bytes, ws = _workspace(lib().prefill_attn_bwd_workspace_bytes(B, Hq, Hkv, T), q, ws, stream)
-    _check(lib().prefill_attn_bwd(*args[:5], dt, B, Hq, Hkv, T, D, D ** -0.5 if sm_scale is None else float(sm_scale), 1,
-                                  args[5], args[6], *outs, wsp, ws_bytes, raw))
+    q_shape, kv_shape, index = q.shape, k.shape, q.get_device()
+    B, Hq, T, D = q_shape
+    Hkv, rows = kv_shape[1], q_shape[:3]
+    if index < 0:
+        _bad("q must be a CUDA tensor")
+    qp, op, gp = (_dense(x, q_shape, dtype, index, n) for x, n in ((q, "q"), (o, "o"), (do, "do")))
+    kp, vp = _dense(k, kv_shape, dtype, index, "k"), _dense(v, kv_shape, dtype, index, "v")
+    lp = _dense(lse, rows, torch.float32, index, "lse")
+    glp = None if dlse is None else _dense(dlse, rows, torch.float32, index, "dlse")
+    raw = _call_stream(index, stream)
+    if out is None:
+        dq, dk, dv = _new(q_shape, q, dtype, stream), _new(kv_shape, q, dtype, stream), _new(kv_shape, q, dtype, stream)
+        dqp, dkp, dvp = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
+    else:
+        dq, dk, dv = out
+        dqp, dkp = _dense(dq, q_shape, dtype, index, "out[0]"), _dense(dk, kv_shape, dtype, index, "out[1]")
+        dvp = _dense(dv, kv_shape, dtype, index, "out[2]")
+    L = _lib or lib()
+    wsp, ws_bytes, ws = _workspace(L.prefill_attn_bwd_workspace_bytes(B, Hq, Hkv, T), q, ws, stream)
+    _check(L.prefill_attn_bwd(qp, kp, vp, op, gp, dt, B, Hq, Hkv, T, D, D ** -0.5 if sm_scale is None else sm_scale, 1, lp,
+                              glp, dqp, dkp, dvp, wsp, ws_bytes, raw))
     if stream is not None:
         _used8(stream, do, q, k, v, o, lse, dlse, dq, dk, dv, ws)
     return dq, dk, dv

@@ -558,8 +558,8 @@ typedef struct {
  * RMS norm of each head's query and key, rotation, change of layout.
  *   q [B, T, Hq, D], k, v [B, T, Hkv, D] (device; v may be NULL) f16 or bf16,
  *   D 64 or 128, Hq % Hkv == 0.  strides (host, NULL: contiguous): {b, t,
- *   head} of q, of k, of v in elements, each >= 0 and a multiple of 8; D
- *   contiguous, bases 16-byte aligned.
+ *   head} of q, of k, of v in elements, each >= 0 and a multiple of 8 (that of
+ *   an axis of one entry is not looked at); D contiguous, bases 16-byte aligned.
  *   pos (device) [n_axes, B, T] int32, any value.
  *   q_weight, k_weight (device, each may be NULL: that norm is left out) [D]
  *   of the activations' type, or float32 (weight_f32 != 0), 16-byte aligned:

@@ -125,16 +125,16 @@ def test_bad_arguments_are_refused(L):
         assert call(q=None) == E and call(k=None) == E and call(q=odd) == E and call(k=odd) == E and call(pos=None) == E
         assert call(qw=odd) == E and call(kw=odd) == E
         for i in range(6):
-            assert call(st=st9(i, 4)) == E and call(st=st9(i, -8)) == E
+            assert call(B=2, st=st9(i, 4)) == E and call(B=2, st=st9(i, -8)) == E
     assert fwd(B=0, q=None) == OK and fwd(T=0) == OK
     assert fwd(v=odd) == E and fwd(qo=None) == E and fwd(ko=None) == E and fwd(vo=None) == E
-    assert fwd(qo=odd) == E and fwd(ko=odd) == E and fwd(vo=odd) == E and fwd(st=st9(7, 4)) == E
+    assert fwd(qo=odd) == E and fwd(ko=odd) == E and fwd(vo=odd) == E and fwd(B=2, st=st9(7, 4)) == E
     for name in ("dq", "dk", "gq", "gk", "gv", "gqw", "gkw"):
         assert bwd(**{name: None}) == E, name
     for name in ("dq", "dk", "dv", "gq", "gk", "gv"):
         assert bwd(**{name: odd}) == E, name
     for i in range(9):
-        assert bwd(gst=st9(i, 4)) == E
+        assert bwd(B=2, gst=st9(i, 4)) == E
     need = L.qk_norm_rope_bwd_workspace_bytes(1, 2, 128, 1)
     assert need > 0 and bwd(ws=None) == W and bwd(wsb=need - 1) == W and bwd(ws=odd) == E
     assert L.qk_norm_rope_bwd_workspace_bytes(1, 2, 128, 0) == 0
