@@ -627,7 +627,7 @@ size_t qk_norm_rope_bwd_workspace_bytes(int B, int T, int D, int norm) {
         set_error("qk_norm_rope_bwd_workspace_bytes: bad sizes");
         return (size_t)-1;
     }
-    return norm ? (size_t)kvq::rope_bwd_ctas(B, T) * 2 * D * sizeof(float) : 0;
+    return norm ? (size_t)kvq::rope_bwd_ctas(B, T) * D * sizeof(float) : 0;
 }
 
 kvq_status qk_norm_rope_bwd(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D, const void* dq,

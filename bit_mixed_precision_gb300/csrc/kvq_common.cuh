@@ -416,6 +416,12 @@ __device__ __forceinline__ unsigned long long f2_add(unsigned long long a, unsig
     return d;
 }
 
+__device__ __forceinline__ unsigned long long f2_mul(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // max(a, b, c) in one instruction (three-input form, sm_100 and later).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;
