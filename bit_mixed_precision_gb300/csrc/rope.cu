@@ -328,8 +328,15 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
     const uint32_t step = (is_q ? q_ctas : gridDim.x - q_ctas) * kWarps;
     const uint32_t start = (is_q ? blockIdx.x : blockIdx.x - q_ctas) * kWarps + warp;
     const Angles<D> angle(a, lane, n_tokens);
-    Sides wt, dw = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    if (norm) wt = load_weight<T, IL>(w, a.w_f32, at.c0, at.c1);
+    // the weights of a lane's 16 channels, in shared memory to leave registers to the rest
+    __shared__ __align__(16) F2 weight[4][D / 16][2];
+    if (norm && warp == 0 && sub == 0) {
+        const Sides x = load_weight<T, IL>(w, a.w_f32, at.c0, at.c1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) weight[i][lane][0] = x.a[i], weight[i][lane][1] = x.b[i];
+    }
+    if (NORM) __syncthreads();
+    Sides dw = {{0, 0, 0, 0}, {0, 0, 0, 0}};
     // the next group to ask for: its number, its token, the lane's row in it (of d, of x)
     uint32_t ask = start;
     int ask_g = 0;
@@ -403,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
                     for (int i = 0; i < 4; ++i) {
                         x.a[i] = f2_mul(x.a[i], r2), x.b[i] = f2_mul(x.b[i], r2);
                         dw.a[i] = f2_fma(d.a[i], x.a[i], dw.a[i]), dw.b[i] = f2_fma(d.b[i], x.b[i], dw.b[i]);
-                        d.a[i] = f2_mul(d.a[i], wt.a[i]), d.b[i] = f2_mul(d.b[i], wt.b[i]);
+                        const ulonglong2 wt = *reinterpret_cast<const ulonglong2*>(weight[i][lane % P::kLanes]);
+                        d.a[i] = f2_mul(d.a[i], wt.x), d.b[i] = f2_mul(d.b[i], wt.y);
                     }
                     const float m = row_sum<D / 16>(dot(d, x)) * (-1.0f / D);
                     const F2 m2 = f2_pack(m, m);
