@@ -61,8 +61,13 @@ struct BwdArgs {
     int split;          // dkv: CTAs of a cluster that share a tile's query tiles
 };
 
-__device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+// Bounded wait of a whole warp, the same outcome in every lane; the loop is kept out of the callers' code.
+__device__ __noinline__ bool bwd_wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+}
+__device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return bwd_wait_on(bar, parity, abort_flag);
 }
 
 __device__ __forceinline__ void bwd_give_up(volatile int* abort_flag) {
@@ -544,9 +549,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-                float e0, e1;
-                f2_unpack(f2_fma(f2_pack(d[i], d[i + 1]), c2, nd[2 * (i >> 4) + ((i >> 2) & 1)]), e0, e1);
-                d[i] = p[i] * e0, d[i + 1] = p[i + 1] * e1;
+                f2_unpack(f2_mul(f2_pack(p[i], p[i + 1]),
+                                 f2_fma(f2_pack(d[i], d[i + 1]), c2, nd[2 * (i >> 4) + ((i >> 2) & 1)])),
+                          d[i], d[i + 1]);
             }
             if (diag) mask16(d, first), mask16(d + 16, first + 16);
             if (kApart) {                               // the last tile's dS^T has been read
@@ -849,9 +854,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             if (lane == 0) mbar_arrive(BAR(W_DC));
 #pragma unroll
             for (int q = 0; q < 32; q += 2) {
-                float e0, e1;
-                f2_unpack(f2_fma(f2_pack(d[q], d[q + 1]), c2, nd2), e0, e1);
-                d[q] = p[q] * e0, d[q + 1] = p[q + 1] * e1;
+                f2_unpack(f2_mul(f2_pack(p[q], p[q + 1]), f2_fma(f2_pack(d[q], d[q + 1]), c2, nd2)), d[q], d[q + 1]);
             }
             if (diag) {
 #pragma unroll

@@ -15,6 +15,7 @@
 // in flight (backward 8) without registers to hold it.
 // All arithmetic is float32; an output is rounded once.
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
@@ -517,8 +518,16 @@ template <typename T, int D> cudaError_t backward(const RopeCall& c, cudaStream_
     constexpr size_t smem = kWarps * (kBwdStages * 128 * sizeof(uint4) + 128 * sizeof(float));
     auto kernel = p.f.interleaved ? (norm ? rope_bwd_kernel<T, D, true, true> : rope_bwd_kernel<T, D, false, true>)
                                   : (norm ? rope_bwd_kernel<T, D, true, false> : rope_bwd_kernel<T, D, false, false>);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> ready[4];              // devices whose attribute is set, by kernel
+    std::atomic<uint64_t>& done = ready[2 * p.f.interleaved + norm];
+    int dev = -1;
+    device_sms(&dev);
+    cudaError_t e = cudaSuccess;
+    if (dev < 0 || dev > 63 || !(done.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    }
     kernel<<<ctas, kThreads, smem, s>>>(p, q_ctas);
     e = cudaGetLastError();
     if (e != cudaSuccess || !norm) return e;
