@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     int kt, u;
     place(a, (int)blockIdx.x / a.split, a.B * a.Hkv, kt, u);
     const int g = a.Hq / a.Hkv, h0 = u * g;             // head u * g + h of all B * Hq is the unit's h-th
+    if (threadIdx.x == 0) prefetch_tmap(&tk), prefetch_tmap(&tq), prefetch_tmap(&tv), prefetch_tmap(&tg);
     // query tiles of a head; tiles of all heads, of which this CTA of the cluster has n from `from` on
     const int m = a.n_t - kt, mine_of = (int)blockIdx.x % a.split, from = g * m * mine_of / a.split;
     const int n = g * m * (mine_of + 1) / a.split - from;
@@ -335,19 +336,15 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             tma_load_3d(sG + s * kTileBytes + hf * kHalfBytes, &tg, 64 * hf, (kt + (from + it) % m) * kTile, h0 + (from + it) / m,
                         BAR(V_GF + s));
     };
-    if (warp == kSoftWarps && lane == 0) {
-        mbar_init(BAR(V_KV), 1);
-        for (int s = 0; s < 3; ++s) mbar_init(BAR(V_QF + s), 1), mbar_init(BAR(V_QE + s), 1);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(BAR(V_GF + s), 1), mbar_init(BAR(V_GE + s), 1);
-            mbar_init(BAR(V_TF + s), 1), mbar_init(BAR(V_TE + s), kSoftWarps);
-        }
-        mbar_init(BAR(V_SF), 1), mbar_init(BAR(V_PR), kSoftWarps);
-        mbar_init(BAR(V_DF), 1), mbar_init(BAR(V_DR), kSoftWarps);
-        mbar_init(BAR(V_END), 1);
-        mbar_init(BAR(V_SC), kSoftWarps), mbar_init(BAR(V_DC), kSoftWarps), mbar_init(BAR(V_PH), kSoftWarps);
-        *abort_flag = 0;
+    if (warp == kSoftWarps) {
+        // a lane per barrier; the softmax warps all arrive at some
+        constexpr uint32_t kMany = 1u << V_TE | 1u << (V_TE + 1) | 1u << V_PR | 1u << V_DR | 1u << V_SC | 1u << V_DC | 1u << V_PH;
+        if (lane < DKV_NBAR) mbar_init(BAR(lane), kMany >> lane & 1 ? kSoftWarps : 1);
+        if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
+    }
+    __syncwarp();
+    if (warp == kSoftWarps && lane == 0) {
         // the first copies do not wait for the rest of the CTA, nor for the grid before this one
         if (n > 0) {
             mbar_expect_tx(BAR(V_KV), 2 * kTileBytes);
@@ -360,6 +357,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (warp == kSoftWarps + 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     grid_dependency_wait();                             // the rows' statistics
     grid_launch_dependents();                           // dQ's CTAs take the SMs that this grid leaves free
+    float4 stat_l = make_float4(0.0f, 0.0f, 0.0f, 0.0f), stat_d = stat_l;   // of the lane's four rows, a tile ahead
+    auto load_stat = [&](int it) {
+        const int64_t row = (int64_t)(h0 + (from + it) / m) * a.n_t * kTile + (kt + (from + it) % m) * kTile + 4 * lane;
+        stat_l = *reinterpret_cast<const float4*>(a.ws.nlse + row);
+        stat_d = *reinterpret_cast<const float4*>(a.ws.delta + row);
+    };
+    if (warp == kSoftWarps + 2 && n > 0) load_stat(0);
     largest<AB>(a, h0, g, u, red);
     tc_fence_before();
     __syncthreads();
@@ -462,10 +466,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
-            const int64_t row = (int64_t)(h0 + (from + it) / m) * a.n_t * kTile + (kt + (from + it) % m) * kTile + 4 * lane;
-            const float4 x = *reinterpret_cast<const float4*>(a.ws.nlse + row);
-            float4 y = *reinterpret_cast<const float4*>(a.ws.delta + row);
-            y.x *= -c, y.y *= -c, y.z *= -c, y.w *= -c;
+            const float4 x = stat_l;
+            const float4 y = make_float4(-c * stat_d.x, -c * stat_d.y, -c * stat_d.z, -c * stat_d.w);
+            if (it + 1 < n) load_stat(it + 1);
             if (it >= 2 && !(ok = bwd_wait(BAR(V_TE + s), (it / 2 - 1) & 1, abort_flag))) break;
             float4* to = reinterpret_cast<float4*>(smem + Lay::STAT + s * 1024);
             to[lane] = x;
@@ -684,6 +687,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const int qt = a.n_t - 1 - rank, n = qt + 1;
     const int u = bh / a.Hq * a.Hkv + bh % a.Hq / (a.Hq / a.Hkv);
     const int wg = warp >> 2, r = threadIdx.x & 127, i = qt * kTile + r;
+    if (threadIdx.x == 0) prefetch_tmap(&tk), prefetch_tmap(&tg), prefetch_tmap(&tv);
 
     // (one lane) tile it of K or V into its stage
     auto load_k = [&](int it) {
@@ -712,18 +716,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             mine_q[4 * e] = y.x, mine_q[4 * e + 1] = y.y, mine_q[4 * e + 2] = y.z, mine_q[4 * e + 3] = y.w;
         }
     }
-    if (warp == kSoftWarps && lane == 0) {
-        mbar_init(BAR(W_QG), 1);
-        for (int s = 0; s < 4; ++s) mbar_init(BAR(W_KF + s), 1), mbar_init(BAR(W_KE + s), 1);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(BAR(W_VF + s), 1), mbar_init(BAR(W_VE + s), 1);
-        }
-        mbar_init(BAR(W_DR), kSoftWarps), mbar_init(BAR(W_DE), 1), mbar_init(BAR(W_AT), kSoftWarps);
-        mbar_init(BAR(W_SF), 1), mbar_init(BAR(W_SC), kSoftWarps);
-        mbar_init(BAR(W_DF), 1), mbar_init(BAR(W_DC), kSoftWarps);
-        mbar_init(BAR(W_END), 1);
-        *abort_flag = 0;
+    if (warp == kSoftWarps) {
+        constexpr uint32_t kMany = 1u << W_SC | 1u << W_DC | 1u << W_DR | 1u << W_AT;
+        if (lane < DQ_NBAR) mbar_init(BAR(lane), kMany >> lane & 1 ? kSoftWarps : 1);
+        if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
+    }
+    __syncwarp();
+    if (warp == kSoftWarps && lane == 0) {
         load_k(0);                                      // the first copies, see dkv
         if (!kBoth) {
             mbar_expect_tx(BAR(W_QG), kTileBytes);
@@ -914,16 +914,17 @@ int head_group(int heads, long long bytes) {
 }
 
 // CTAs that share a key tile in dkv (a cluster that adds up its sums through shared memory).  In thousands of clocks, a
-// tile takes about 2.3 in dkv and 1.9 in dq, a CTA's start and end 6 and with a cluster's sum 9; the call takes at least
+// tile takes about 2.3 in dkv and 1.9 in dq, a CTA's start and end 6 and with a cluster's sum 16; the call takes at least
 // its longest CTA and, as dq fills the SMs that dkv leaves, all work over the SMs.  The size with the least such bound.
+// (32/4 heads x 1024 tokens: 4 CTAs 45 us, one 92; 2 heads x 256: dkv alone 10 us with one, 14 with 8.)
 int cluster_size(int units, int g, int n_t) {
     const int sms = device_sms(nullptr);
     const double tiles = 0.5 * units * g * n_t * (n_t + 1.0), ctas = (double)units * n_t;
     int best = 1;
     double least = 0.0;
     for (int c = 1; c <= 8; c *= 2) {
-        const double longest = 2.3 * g * n_t / c + (c > 1 ? 9.0 : 6.0);
-        const double all = (4.2 * tiles + ctas * (c * (c > 1 ? 9.0 : 6.0) + 6.0 * g)) / sms;
+        const double longest = 2.3 * g * n_t / c + (c > 1 ? 16.0 : 6.0);
+        const double all = (4.2 * tiles + ctas * (c * (c > 1 ? 16.0 : 6.0) + 6.0 * g)) / sms;
         const double bound = std::max(longest, all);
         if (c == 1 || bound < 0.95 * least) best = c, least = bound;
     }

@@ -988,7 +988,7 @@ def qk_norm_rope(q, k, v, pos, rope, q_weight=None, k_weight=None, eps=1e-6, out
     T, q_shape, kv_shape = (1, q.shape, kv_in) if len(rows) == 1 else (rows[1], (B, Hq, rows[1], D), (B, Hkv, rows[1], D))
     if out is None:
         qo, ko = _new(q_shape, q, dtype, stream), _new(kv_shape, q, dtype, stream)
-        vo = None if v is None else _new(kv_shape, q, dtype, stream)
+        vo = None if v is None else torch.empty_like(ko) if stream is None else _new(kv_shape, q, dtype, stream)
         qop, kop, vop = qo.data_ptr(), ko.data_ptr(), None if v is None else vo.data_ptr()
     else:
         qo, ko, vo = out
@@ -1083,13 +1083,17 @@ def prefill_attn_bwd(do, q, k, v, o, lse, sm_scale=None, dlse=None, out=None, ws
     Hkv, rows = kv_shape[1], q_shape[:3]
     if index < 0:
         _bad("q must be a CUDA tensor")
-    qp, op, gp = (_dense(x, q_shape, dtype, index, n) for x, n in ((q, "q"), (o, "o"), (do, "do")))
+    qp, op, gp = _dense(q, q_shape, dtype, index, "q"), _dense(o, q_shape, dtype, index, "o"), \
+        _dense(do, q_shape, dtype, index, "do")
     kp, vp = _dense(k, kv_shape, dtype, index, "k"), _dense(v, kv_shape, dtype, index, "v")
     lp = _dense(lse, rows, torch.float32, index, "lse")
     glp = None if dlse is None else _dense(dlse, rows, torch.float32, index, "dlse")
     raw = _call_stream(index, stream)
     if out is None:
-        dq, dk, dv = _new(q_shape, q, dtype, stream), _new(kv_shape, q, dtype, stream), _new(kv_shape, q, dtype, stream)
+        if stream is None:
+            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+        else:
+            dq, dk, dv = _new(q_shape, q, dtype, stream), _new(kv_shape, q, dtype, stream), _new(kv_shape, q, dtype, stream)
         dqp, dkp, dvp = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
     else:
         dq, dk, dv = out
