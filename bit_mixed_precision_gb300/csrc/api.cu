@@ -658,6 +658,11 @@ kvq_status qk_norm_rope_bwd(const kvq_rope* rope, kvq_dtype dt, int B, int T, in
     if ((st = head_strides(gk, g_strides ? g_strides + 3 : nullptr, B, T, Hkv, D, who, c.gstrides[1])) != KVQ_OK) return st;
     if (dv && (st = head_strides(gv, g_strides ? g_strides + 6 : nullptr, B, T, Hkv, D, who, c.gstrides[2])) != KVQ_OK)
         return st;
+    for (int i = 0; i < 9; ++i) {
+        const int size = i % 3 == 0 ? B : i % 3 == 1 ? T : i == 2 ? Hq : Hkv;
+        KVQ_REQUIRE(size == 1 || c.gstrides[i / 3][i % 3] > 0 || (i >= 6 && !dv), KVQ_EINVAL,
+                    "%s: rows of a gradient must not overlap", who);
+    }
     KVQ_REQUIRE(dq && dk && (pos || rope->rot == 0), KVQ_EINVAL, "%s: null pointer", who);
     KVQ_REQUIRE(aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16) && aligned(q_weight, 16) && aligned(k_weight, 16) &&
                     aligned(pos, 4),

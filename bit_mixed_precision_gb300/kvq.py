@@ -997,7 +997,7 @@ def qk_norm_rope(q, k, v, pos, rope, q_weight=None, k_weight=None, eps=1e-6, out
         qop, kop = _dense(qo, q_shape, dtype, index, "out[0]"), _dense(ko, kv_shape, dtype, index, "out[1]")
         vop = None if vo is None else _dense(vo, kv_shape, dtype, index, "out[2]")
     _check((_lib or lib()).qk_norm_rope(rope._ref, dt, B, T, Hq, Hkv, D, qp, kp, vp, _I9(*qs, *ks, *vs), pp, qw, kw, f32,
-                                        eps, qop, kop, vop, raw))
+                                        float(eps), qop, kop, vop, raw))
     if stream is not None:
         _used8(stream, q, k, v, pos, q_weight, k_weight, qo, ko, vo)
     return qo, ko, vo
@@ -1042,7 +1042,7 @@ def qk_norm_rope_bwd(dq, dk, dv, q, k, pos, rope, q_weight=None, k_weight=None, 
     if qw or kw:
         wsp, ws_bytes, ws = _workspace(L.qk_norm_rope_bwd_workspace_bytes(B, T, D, 1), q, ws, stream)
     _check(L.qk_norm_rope_bwd(rope._ref, dt, B, T, Hq, Hkv, D, dqp, dkp, dvp, qp, kp, _I9(*qs, *ks, 0, 0, 0), pp, qw, kw,
-                              f32, eps, gqp, gkp, gvp, _I9(*gqs, *gks, *gvs), gqwp, gkwp, wsp, ws_bytes, raw))
+                              f32, float(eps), gqp, gkp, gvp, _I9(*gqs, *gks, *gvs), gqwp, gkwp, wsp, ws_bytes, raw))
     if stream is not None:
         _used8(stream, dq, dk, dv, q, k, pos, q_weight, k_weight, gq, gk, gv, gqw, gkw, ws)
     return gq, gk, gv, gqw, gkw
@@ -1101,7 +1101,8 @@ def prefill_attn_bwd(do, q, k, v, o, lse, sm_scale=None, dlse=None, out=None, ws
         dvp = _dense(dv, kv_shape, dtype, index, "out[2]")
     L = _lib or lib()
     wsp, ws_bytes, ws = _workspace(L.prefill_attn_bwd_workspace_bytes(B, Hq, Hkv, T), q, ws, stream)
-    _check(L.prefill_attn_bwd(qp, kp, vp, op, gp, dt, B, Hq, Hkv, T, D, D ** -0.5 if sm_scale is None else sm_scale, 1, lp,
+    _check(L.prefill_attn_bwd(qp, kp, vp, op, gp, dt, B, Hq, Hkv, T, D, D ** -0.5 if sm_scale is None else float(sm_scale), 1,
+                              lp,
                               glp, dqp, dkp, dvp, wsp, ws_bytes, raw))
     if stream is not None:
         _used8(stream, do, q, k, v, o, lse, dlse, dq, dk, dv, ws)

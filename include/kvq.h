@@ -209,8 +209,9 @@ kvq_status prefill_attn_scores(const void* q, const void* k, const void* v, kvq_
  *   dS_ij = P_ij (go_i.v_j - delta_i);
  *   dq_i = sm_scale sum_j dS_ij k_j;  dk_j = sm_scale sum_i dS_ij q_i;
  *   dv_j = sum_i P_ij go_i, dk and dv summed over the query heads of a group.
- *   q, k, v, o, lse: the forward call's arguments and results, all finite (the
- *   tile products also multiply the zeros above the diagonal).  go (device)
+ *   q, k, v, sm_scale, o, lse: the forward call's arguments and results, all
+ *   finite (the tile products also multiply the zeros above the diagonal; in
+ *   f16 a P of 2 and more, which no row's own lse gives, overflows).  go (device)
  *   [B, Hq, T, D]: gradient of o; glse (device, nullable) [B, Hq, T]: of lse.
  *   dq (device) [B, Hq, T, D]; dk, dv (device) [B, Hkv, T, D], no overlap with
  *   the inputs.  q, k, v, o, go, dq, dk, dv 16-byte aligned.  A row with

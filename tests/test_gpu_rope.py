@@ -361,3 +361,44 @@ def test_prompt_and_steps_through_the_block_cache(kvq):
             p = np.exp(s - s.max())
             logit = 2.0 ** -10.9 * size(rq[b, h]) * size(dk) / math.sqrt(D)
             assert np.abs(np_(o1[b, h]) - p / p.sum() @ dv).max() <= (np.expm1(2 * logit) + 2.0 ** -10) * np.abs(dv).max()
+
+
+@pytest.mark.parametrize("dtype,D,rot", [(F16, 64, 32), (BF16, 128, 128)])
+def test_training_step(kvq, dtype, D, rot):
+    """Forward and backward pass of a layer between its projection and its output: every call on what the calls before it
+    gave, each within its own bounds, and the gradient of the projection's output against float64 autograd."""
+    from tests.test_gpu_prefill_bwd import check
+    B, T, Hq, Hkv = 2, 200, 4, 2
+    c = Case(kvq, B=B, T=T, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, rot=rot, seed=5)
+    got = c.forward()
+    c.check_forward(got)
+    q, k, v = got
+    o, lse, _ = kvq.prefill_attn_scores(q, k, v)
+    do = torch.randn(o.shape, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    d = kvq.prefill_attn_bwd(do, q, k, v, o, lse)
+    check(d, do, q, k, v, o, lse)
+    c.d = list(d)
+    grads = c.backward()
+    c.check_backward(grads)
+    # the whole in float64
+    x = c.x.double().cpu().requires_grad_()
+    w = [y.double().cpu().requires_grad_() for y in (c.qw, c.kw)]
+    phi, n = torch.from_numpy(c.angle)[:, :, None], rot // 2
+    def normed(y, w):
+        y = y / torch.sqrt(y.square().mean(-1, keepdim=True) + c.eps) * w
+        a, b = y[..., :n], y[..., n:rot]
+        return torch.cat([a * phi.cos() - b * phi.sin(), b * phi.cos() + a * phi.sin(), y[..., rot:]], -1).transpose(1, 2)
+    rq, rk = normed(x[:, :, :Hq], w[0]), normed(x[:, :, Hq:Hq + Hkv], w[1])
+    rk, rv = (y.repeat_interleave(Hq // Hkv, 1) for y in (rk, x[:, :, Hq + Hkv:].transpose(1, 2)))
+    s = (rq @ rk.transpose(-1, -2) * D ** -0.5).masked_fill(torch.ones(T, T, dtype=torch.bool).triu(1), -math.inf)
+    ((s.softmax(-1) @ rv) * do.double().cpu()).sum().backward()
+    # q, k rounded: a logit is off by at most `logit`, weights by expm1(2 logit) relatively; v, o, do, P, dS, dq, dk and dv
+    # are off by half a step h each, relatively to terms that add up to sums sqrt(T) times smaller at worst (random signs):
+    # in the 2-norm (8 h + expm1(2 logit)) times that, taken for the largest row norms
+    h = torch.finfo(dtype).eps / 2
+    logit = 2 * h * float(rq.norm(dim=-1).max() * rk.norm(dim=-1).max()) * D ** -0.5
+    bound = (8 * h + math.expm1(2 * logit)) * math.sqrt(T)
+    for a, ref in ((grads[0], x.grad[:, :, :Hq]), (grads[1], x.grad[:, :, Hq:Hq + Hkv]), (grads[2], x.grad[:, :, Hq + Hkv:]),
+                   (grads[3], w[0].grad), (grads[4], w[1].grad)):
+        off = float((a.double().cpu() - ref).norm() / ref.norm())
+        assert off <= min(bound, 0.1), (off, bound)

@@ -134,7 +134,7 @@ def test_bad_arguments_are_refused(L):
     for name in ("dq", "dk", "dv", "gq", "gk", "gv"):
         assert bwd(**{name: odd}) == E, name
     for i in range(9):
-        assert bwd(B=2, gst=st9(i, 4)) == E
+        assert bwd(B=2, gst=st9(i, 4)) == E and bwd(B=2, gst=st9(i, 0)) == E
     need = L.qk_norm_rope_bwd_workspace_bytes(1, 2, 128, 1)
     assert need > 0 and bwd(ws=None) == W and bwd(wsb=need - 1) == W and bwd(ws=odd) == E
     assert L.qk_norm_rope_bwd_workspace_bytes(1, 2, 128, 0) == 0
