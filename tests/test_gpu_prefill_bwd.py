@@ -126,6 +126,16 @@ def test_many_heads():
     check(kvq.prefill_attn_bwd(*x), *x, heads=[0, 63, 127])
     x = make(2, 40, 8, 1537, 128, F16)
     check(kvq.prefill_attn_bwd(*x), *x, heads=[0, 15])
+    # many sequences of one and of several tiles; a sequence's dQ is the same in a call of its own, whose launch order differs
+    for B, Hq, Hkv, T, D, dtype in ((37, 64, 64, 100, 128, BF16), (31, 64, 16, 130, 64, F16), (9, 32, 8, 1290, 64, BF16),
+                                    (7, 40, 40, 1290, 128, F16)):
+        x = make(B, Hq, Hkv, T, D, dtype, seed=T)
+        got = kvq.prefill_attn_bwd(*x)
+        check(got, *x, heads=[0, B * Hkv - 1])
+        assert all(torch.equal(a, b) for a, b in zip(got, kvq.prefill_attn_bwd(*x)))
+        for b in (0, B // 2, B - 1):
+            alone = kvq.prefill_attn_bwd(*[y[b:b + 1].contiguous() for y in x])
+            assert torch.equal(alone[0][0], got[0][b])
 
 
 @pytest.mark.parametrize("dtype,size", [(F16, 2.0 ** -14), (F16, 3000.0), (BF16, 2.0 ** -60), (BF16, 2.0 ** 40)])
