@@ -240,12 +240,12 @@ template <int D> __device__ __forceinline__ void products_k_ta(uint32_t c, uint3
 }
 
 // C (+)= A B, A [128, 128] packed pairs in tensor memory (every 32 values in 16 columns, STEP columns apart), B a tile of
-// 128 rows (one thread).  HALF 0 and 1: the first and the second 16 of every 32 terms; 2: all.
-template <int STEP, int HALF = 2>
+// 128 rows (one thread).
+template <int STEP>
 __device__ __forceinline__ void products_mn(uint32_t c, uint32_t ta, uint32_t tb, uint32_t idesc, bool accumulate) {
     const uint64_t db = mnmajor_desc(tb, 0);
 #pragma unroll
-    for (int kk = HALF == 1; kk < 8; kk += HALF == 2 ? 1 : 2)
+    for (int kk = 0; kk < 8; ++kk)
         tc_mma_f16_ta(c, ta + (uint32_t)(kk >> 1) * STEP + (uint32_t)(kk & 1) * 8u, db + (uint64_t)(kk * 16 * 128 >> 4), idesc,
                       kk > 0 || accumulate);
 }
@@ -256,6 +256,23 @@ template <typename T> __device__ __forceinline__ void store_pairs(uint32_t taddr
 #pragma unroll
     for (int c = 0; c < 16; ++c) w[c] = Pack2<T>::pack(x[2 * c], x[2 * c + 1]);
     tmem_st16(taddr, w);
+}
+
+// A warp's 32 keys by 32 queries, as [16 queries][16 keys][tile of 8 queries][8 keys][2 queries] a thread, and their pairs
+// in the first 16 of the 32 columns.
+__device__ __forceinline__ void load_frags(uint32_t taddr, float* x) {
+    tmem_ld_frag16(taddr, x);
+    tmem_ld_frag16(taddr + (16u << 16), x + 8);
+    tmem_ld_frag16(taddr + 16u, x + 16);
+    tmem_ld_frag16(taddr + 16u + (16u << 16), x + 24);
+    tmem_wait_ld();
+}
+__device__ __forceinline__ void store_frags(uint32_t taddr, const uint32_t* w) {
+    tmem_st_frag8(taddr, w);
+    tmem_st_frag8(taddr + (16u << 16), w + 4);
+    tmem_st_frag8(taddr + 8u, w + 8);
+    tmem_st_frag8(taddr + 8u + (16u << 16), w + 12);
+    tmem_wait_st();
 }
 
 // Zeros where the query comes before the key, in a thread's 16 keys by 16 queries; d: query - key of element 0.
@@ -289,7 +306,7 @@ __device__ __forceinline__ void stage_row(uint32_t taddr, float f, uint8_t* half
 // ------------------------------------------------------------------ dK and dV
 
 enum DkvBar { V_KV = 0, V_QF = 1, V_QE = 4, V_GF = 7, V_GE = 9, V_TF = 11, V_TE = 13, V_SF = 15, V_PR = 16, V_DF = 17,
-              V_DR = 18, V_END = 19, V_SC = 20, V_DC = 21, V_PH = 22, DKV_NBAR = 23 };
+              V_DR = 18, V_END = 19, DKV_NBAR = 20 };
 
 template <typename T, int AB, int D>
 __global__ void __launch_bounds__(kDkvThreads, 1)
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     };
     if (warp == kSoftWarps) {
         // a lane per barrier; the softmax warps all arrive at some
-        constexpr uint32_t kMany = 1u << V_TE | 1u << (V_TE + 1) | 1u << V_PR | 1u << V_DR | 1u << V_SC | 1u << V_DC | 1u << V_PH;
+        constexpr uint32_t kMany = 1u << V_TE | 1u << (V_TE + 1) | 1u << V_PR | 1u << V_DR;
         if (lane < DKV_NBAR) mbar_init(BAR(lane), kMany >> lane & 1 ? kSoftWarps : 1);
         if (lane == 0) *abort_flag = 0;
         fence_mbar_init();
@@ -369,11 +386,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    // S^T, dP^T, dV, dK; packed P^T and dS^T have places of their own at D = 64, at D = 128 they replace S^T and dP^T
-    constexpr bool kApart = D == 64;
-    constexpr uint32_t kStep = kApart ? 16 : 32;        // columns between the packed 32 queries of two warpgroups
+    // S^T, dP^T, dV, dK; packed P^T and dS^T replace S^T and dP^T, every 32 queries in the first 16 of their columns
     const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
-    const uint32_t tPq = kApart ? tmem + 384 : tS, tDS = kApart ? tmem + 448 : tP;
     const float c = scale_of<AB>(red);
 
     if (warp == kSoftWarps) {
@@ -411,40 +425,26 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         auto g_there = [&](int it, int s) { return wait(V_GF + s, it / 2); };
         // One tile, PH = it mod 6: the stages are constants, so that descriptors stay in uniform registers (computed from
         // the tile's number they made a product's issue three times as long).
-        // The next S^T and dP^T are issued as soon as theirs has been read (kApart), or behind the product that reads what
-        // replaced it.  A wait costs one to three products' time even where there is nothing to wait for, and the tensor
-        // pipe has about four products ahead of it: no two waits follow one another without products between.
+        // The next S^T and dP^T are issued behind the product that reads what replaced them.  A wait costs one to three
+        // products' time even where there is nothing to wait for, and the tensor pipe has about four products ahead of it:
+        // no two waits follow one another without products between.
         auto step = [&](auto phase, int it) -> bool {
             constexpr int PH = decltype(phase)::value, q0 = PH % 3, q1 = (PH + 1) % 3, q2 = (PH + 2) % 3, g0 = PH & 1, g1 = g0 ^ 1;
             const bool more = it + 1 < n;
-            if (kApart && more) {
-                if (!wait(V_SC, PH)) return false;
-                tc_fence_after();
-                scores(q1);
-            }
-            if (!wait(V_PH, PH)) return false;          // dV += P^T dO, half of P^T at a time
-            tc_fence_after();
-            products_mn<kStep, 0>(tDV, tPq, sG + (uint32_t)g0 * kTileBytes, idD, it > 0);
             if (!wait(V_PR, PH)) return false;
             tc_fence_after();
-            products_mn<kStep, 1>(tDV, tPq, sG + (uint32_t)g0 * kTileBytes, idD, true);
+            products_mn<32>(tDV, tS, sG + (uint32_t)g0 * kTileBytes, idD, it > 0);          // dV += P^T dO
             tc_commit(BAR(V_GE + g0));
             if (more) {
                 if (!g_there(it + 1, g1)) return false;
-                if (kApart) {
-                    if (!wait(V_DC, PH)) return false;
-                    tc_fence_after();
-                    grads(g1);
-                } else {
-                    scores(q1);
-                }
+                scores(q1);
             }
             if (!wait(V_DR, PH)) return false;
             tc_fence_after();
-            products_mn<kStep>(tDK, tDS, sQ + (uint32_t)q0 * kTileBytes, idD, it > 0);      // dK += dS^T Q
+            products_mn<32>(tDK, tP, sQ + (uint32_t)q0 * kTileBytes, idD, it > 0);          // dK += dS^T Q
             tc_commit(BAR(V_QE + q0));
             if (it + 2 < n && !q_there(it + 2, q2)) return false;
-            if (!kApart && more) grads(g1);
+            if (more) grads(g1);
             return true;
         };
         if (elect_one()) {
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         // broadcasts of 32 took as many cycles of shared memory as the tensor pipe's operands left).
         const int wg = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t mine = lanes + 32u * (uint32_t)wg, packed = lanes + kStep * (uint32_t)wg;
+        const uint32_t mine = lanes + 32u * (uint32_t)wg;
         const int first = 32 * wg + 2 * (lane & 3) - (32 * (warp & 3) + (lane >> 2));    // query - key of element 0
         const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
         bool ok = true;
@@ -498,58 +498,26 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             for (int t = 0; t < 4; ++t) nl[t] = stat[4 * t], nd[t] = stat[64 + 4 * t];
             if (!bwd_wait(BAR(V_SF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            // P^T in two halves of 16 queries, so that dV's products start on the first: [half][16 keys][tile of 8 queries]
-            // [8 keys][2 queries]
-            float p[32];
-            uint32_t w[8];
-            tmem_ld_frag16(tS + mine, p);
-            tmem_ld_frag16(tS + mine + (16u << 16), p + 8);
-            tmem_wait_ld();
-            tmem_ld_frag16(tS + mine + 16u, p + 16);
-            tmem_ld_frag16(tS + mine + 16u + (16u << 16), p + 24);
+            float p[32];                                // [16 queries][16 keys][tile of 8 queries][8 keys][2 queries]
+            uint32_t w[16];
+            load_frags(tS + mine, p);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float* x = p + 16 * hf;
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    float e0, e1;
-                    f2_unpack(f2_fma(f2_pack(x[i], x[i + 1]), sc2, nl[2 * hf + ((i >> 2) & 1)]), e0, e1);
-                    x[i] = ex2_approx(e0), x[i + 1] = ex2_approx(e1);
-                }
-                if (diag) mask16(x, first + 16 * hf);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = Pack2<T>::pack(x[2 * i], x[2 * i + 1]);
-                if (kApart && hf == 0) {                // the last tile's P^T has been read
-                    if (it > 0 && !bwd_wait(BAR(V_GE + (s ^ 1)), ((it - 1) / 2) & 1, abort_flag)) { ok = false; break; }
-                    tc_fence_after();
-                }
-                if (hf == 0) tmem_wait_ld();            // the second half of S^T, before its place is written to
-                if (kApart && hf == 0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(BAR(V_SC));
-                }
-                tmem_st_frag8(tPq + packed + 8u * (uint32_t)hf, w);
-                tmem_st_frag8(tPq + packed + 8u * (uint32_t)hf + (16u << 16), w + 4);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(hf == 0 ? V_PH : V_PR));
+            for (int i = 0; i < 32; i += 2) {
+                float e0, e1;
+                f2_unpack(f2_fma(f2_pack(p[i], p[i + 1]), sc2, nl[2 * (i >> 4) + ((i >> 2) & 1)]), e0, e1);
+                p[i] = ex2_approx(e0), p[i + 1] = ex2_approx(e1);
             }
-            if (!ok) break;
+            if (diag) mask16(p, first), mask16(p + 16, first + 16);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = Pack2<T>::pack(p[2 * i], p[2 * i + 1]);
+            store_frags(tS + mine, w);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(V_PR));
             if (!bwd_wait(BAR(V_DF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             float d[32];
-            tmem_ld_frag16(tP + mine, d);
-            tmem_ld_frag16(tP + mine + (16u << 16), d + 8);
-            tmem_ld_frag16(tP + mine + 16u, d + 16);
-            tmem_ld_frag16(tP + mine + 16u + (16u << 16), d + 24);
-            tmem_wait_ld();
-            if (kApart) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(V_DC));
-            }
+            load_frags(tP + mine, d);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
                 f2_unpack(f2_mul(f2_pack(p[i], p[i + 1]),
@@ -557,18 +525,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                           d[i], d[i + 1]);
             }
             if (diag) mask16(d, first), mask16(d + 16, first + 16);
-            if (kApart) {                               // the last tile's dS^T has been read
-                if (it > 0 && !bwd_wait(BAR(V_QE + (it - 1) % 3), ((it - 1) / 3) & 1, abort_flag)) { ok = false; break; }
-                tc_fence_after();
-            }
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = Pack2<T>::pack(d[16 * hf + 2 * i], d[16 * hf + 2 * i + 1]);
-                tmem_st_frag8(tDS + packed + 8u * (uint32_t)hf, w);
-                tmem_st_frag8(tDS + packed + 8u * (uint32_t)hf + (16u << 16), w + 4);
-            }
-            tmem_wait_st();
+            for (int i = 0; i < 16; ++i) w[i] = Pack2<T>::pack(d[2 * i], d[2 * i + 1]);
+            store_frags(tP + mine, w);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
