@@ -163,32 +163,23 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
 }
 
-// The power of two c with |do_i.v_j - delta_i| c <= 1 over query heads [h0, h0 + nh) of unit u (fp16; else 1).  Called
-// by the whole CTA; `red` has 3 floats a warp; a __syncthreads() lies between the two halves.
-template <int AB> __device__ __forceinline__ void largest(const BwdArgs& a, int h0, int nh, int u, float* red) {
-    if (AB != 0) return;
+// The power of two c with |do_i.v_j - delta_i| c <= 1 over query heads [h0, h0 + nh) of unit u (fp16; else 1), by a warp.
+template <int AB> __device__ __forceinline__ float unit_scale(const BwdArgs& a, int h0, int nh, int u, int lane) {
+    if (AB != 0) return 1.0f;
     float x = 0.0f, d = 0.0f, v = 0.0f;
-    for (int i = threadIdx.x; i < nh * a.n_t; i += blockDim.x) {
+#pragma unroll 4
+    for (int i = lane; i < nh * a.n_t; i += 32) {
         x = fmaxf(x, __ldcg(a.ws.do_max + (int64_t)h0 * a.n_t + i));
         d = fmaxf(d, __ldcg(a.ws.dl_max + (int64_t)h0 * a.n_t + i));
     }
-    for (int i = threadIdx.x; i < a.n_t; i += blockDim.x) v = fmaxf(v, __ldcg(a.ws.v_max + (int64_t)u * a.n_t + i));
+#pragma unroll 4
+    for (int i = lane; i < a.n_t; i += 32) v = fmaxf(v, __ldcg(a.ws.v_max + (int64_t)u * a.n_t + i));
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
         d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, m));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
     }
-    if ((threadIdx.x & 31) == 0) {
-        float* r = red + 3 * (threadIdx.x >> 5);
-        r[0] = x, r[1] = d, r[2] = v;
-    }
-}
-template <int AB> __device__ __forceinline__ float scale_of(const float* red) {
-    if (AB != 0) return 1.0f;
-    float x = 0.0f, d = 0.0f, v = 0.0f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w)
-        x = fmaxf(x, red[3 * w]), d = fmaxf(d, red[3 * w + 1]), v = fmaxf(v, red[3 * w + 2]);
     const float most = fmaf(x, v, d);
     if (!(most > 0.0f)) return 1.0f;
     const int e = most < 1e30f ? min(max(ilogbf(most) + 1, -60), 60) : 60;
@@ -212,8 +203,8 @@ template <int D> struct BwdLayout {
     static constexpr uint32_t S0 = 2 * kTileBytes;
     static constexpr uint32_t S1 = S0 + 3 * kTileBytes;
     static constexpr uint32_t STAT = S1 + 2 * kTileBytes;       // dkv: 2 stages of 128 (nlse) and 128 (delta) floats
-    static constexpr uint32_t RED = STAT + 2048;
-    static constexpr uint32_t BAR = RED + 256;                  // 3 floats a warp
+    static constexpr uint32_t SCALE = STAT + 2048;              // unit_scale()
+    static constexpr uint32_t BAR = SCALE + 16;
     // no alignment slack at D = 128: the kernels require (and check) a 1024-aligned base
     static constexpr uint32_t BYTES = BAR + 256;
 };
@@ -327,7 +318,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     auto BAR = [&](int i) -> uint32_t { return base + Lay::BAR + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::BAR + 8 * DKV_NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR + 8 * DKV_NBAR + 4);
-    float* red = reinterpret_cast<float*>(smem + Lay::RED);
+    float* scale = reinterpret_cast<float*>(smem + Lay::SCALE);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     int kt, u;
@@ -381,14 +372,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         stat_d = *reinterpret_cast<const float4*>(a.ws.delta + row);
     };
     if (warp == kSoftWarps + 2 && n > 0) load_stat(0);
-    largest<AB>(a, h0, g, u, red);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     // S^T, dP^T, dV, dK; packed P^T and dS^T replace S^T and dP^T, every 32 queries in the first 16 of their columns
     const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
-    const float c = scale_of<AB>(red);
 
     if (warp == kSoftWarps) {
         if (lane == 0 && n > 0) {
@@ -462,7 +451,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         }
         __syncwarp();
     } else if (warp == kSoftWarps + 2) {
-        // the query rows' statistics, delta times c
+        // the scale, and the query rows' statistics, delta times it
+        const float c = unit_scale<AB>(a, h0, g, u, lane);
+        if (lane == 0) *scale = c;
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
@@ -485,12 +476,15 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t mine = lanes + 32u * (uint32_t)wg;
         const int first = 32 * wg + 2 * (lane & 3) - (32 * (warp & 3) + (lane >> 2));    // query - key of element 0
-        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
+        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2);
+        float c = 1.0f;
         bool ok = true;
         for (int it = 0; it < n; ++it) {
             const int s = it & 1;
             const bool diag = (from + it) % m == 0;
             if (!bwd_wait(BAR(V_TF + s), (it / 2) & 1, abort_flag)) { ok = false; break; }
+            if (AB == 0 && it == 0) c = *scale;         // written before the first statistics
+            const unsigned long long c2 = f2_pack(c, c);
             const unsigned long long* stat =
                 reinterpret_cast<const unsigned long long*>(smem + Lay::STAT + s * 1024 + 128 * wg) + (lane & 3);
             unsigned long long nl[4], nd[4];
@@ -583,7 +577,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             bool fine = true;
             const uint32_t flag = smem_u32(const_cast<int*>(abort_flag)), at = base + Lay::S0;
             for (int p = 0; p < a.split; ++p) fine = fine && cluster_ld_u32(cluster_map(flag, (uint32_t)p)) == 0;
-            const float unshift = AB == 0 ? 0x1p-15f : 1.0f, fk = a.sm_scale * unshift / c;
+            const float unshift = AB == 0 ? 0x1p-15f : 1.0f, fk = a.sm_scale * unshift / *scale;
             const int rows = kTile / a.split;
             for (int e = threadIdx.x; e < rows * (D / 2); e += 32 * kSoftWarps) {
                 const int r = mine_of * rows + e / (D / 2), piece = e % (D / 2);
@@ -617,7 +611,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 // ------------------------------------------------------------------ dQ
 
 enum DqBar { W_QG = 0, W_KF = 1, W_KE = 5, W_VF = 9, W_VE = 11, W_SF = 13, W_SC = 14, W_DF = 15, W_DC = 16, W_DR = 17,
-             W_DE = 18, W_END = 19, W_AT = 20, DQ_NBAR = 21 };
+             W_DE = 18, W_END = 19, W_AT = 20, W_CS = 21, DQ_NBAR = 22 };
 
 template <typename T, int AB, int D>
 __global__ void __launch_bounds__(kDqThreads, 1)
@@ -638,7 +632,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     auto BAR = [&](int i) -> uint32_t { return base + Lay::BAR + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::BAR + 8 * DQ_NBAR);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::BAR + 8 * DQ_NBAR + 4);
-    float* red = reinterpret_cast<float*>(smem + Lay::RED);
+    float* scale = reinterpret_cast<float*>(smem + Lay::SCALE);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     int rank, bh;
@@ -693,14 +687,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     if (warp == kSoftWarps + 1) tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     // No wait for the grid before this one: it waited for the statistics' grid before it let this one start (the
     // statistics are read from L2).
-    largest<AB>(a, bh, 1, u, red);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     // S, dP, packed dS, packed Q (at D = 64 and packed dO), dQ
     const uint32_t tS = tmem, tP = tmem + 128, tDS = tmem + 256, tQ = tmem + 320, tG = tmem + 352, tDQ = tmem + 384;
-    const float c = scale_of<AB>(red);
 
     if (warp == kSoftWarps) {
         if (lane == 0) {
@@ -722,6 +714,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         }
     } else if (warp == kSoftWarps + 1) {
         constexpr uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
+        if (AB == 0) {                                  // the scale, while the first tiles are on their way
+            const float c = unit_scale<AB>(a, bh, 1, u, lane);
+            if (lane == 0) {
+                *scale = c;
+                mbar_arrive(BAR(W_CS));
+            }
+            __syncwarp();
+        }
         // (one lane) S = Q K^T, dP = dO V^T with the streamed tile in stage s
         auto scores = [&](int s) {
             products_k_ta<D>(tS, tQ, sK + (uint32_t)s * kTileBytes, idS);
@@ -773,9 +773,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t mine = lanes + 32u * (uint32_t)wg;
         const int64_t stat = (int64_t)bh * a.n_t * kTile + i;
-        const float nl = __ldcg(a.ws.nlse + stat), nd = -c * __ldcg(a.ws.delta + stat);
-        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), c2 = f2_pack(c, c);
-        const unsigned long long nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+        const float nl = __ldcg(a.ws.nlse + stat), delta = __ldcg(a.ws.delta + stat);
+        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), nl2 = f2_pack(nl, nl);
         bool ok = true;
         if (kBoth) {
             tmem_st8(tQ + lanes + 8u * (uint32_t)wg, mine_q);
@@ -787,7 +786,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(W_AT));
-        for (int it = 0; it < n; ++it) {
+        if (AB == 0 && !bwd_wait(BAR(W_CS), 0, abort_flag)) ok = false;
+        const float c = AB == 0 && ok ? *scale : 1.0f, nd = -c * delta;
+        const unsigned long long c2 = f2_pack(c, c), nd2 = f2_pack(nd, nd);
+        for (int it = 0; ok && it < n; ++it) {
             const bool diag = it == qt;
             if (!bwd_wait(BAR(W_SF), it & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();

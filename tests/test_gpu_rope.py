@@ -396,7 +396,7 @@ def test_training_step(kvq, dtype, D, rot):
     # are off by half a step h each, relatively to terms that add up to sums sqrt(T) times smaller at worst (random signs):
     # in the 2-norm (8 h + expm1(2 logit)) times that, taken for the largest row norms
     h = torch.finfo(dtype).eps / 2
-    logit = 2 * h * float(rq.norm(dim=-1).max() * rk.norm(dim=-1).max()) * D ** -0.5
+    logit = 2 * h * float((rq.norm(dim=-1).max() * rk.norm(dim=-1).max()).detach()) * D ** -0.5
     bound = (8 * h + math.expm1(2 * logit)) * math.sqrt(T)
     for a, ref in ((grads[0], x.grad[:, :, :Hq]), (grads[1], x.grad[:, :, Hq:Hq + Hkv]), (grads[2], x.grad[:, :, Hq + Hkv:]),
                    (grads[3], w[0].grad), (grads[4], w[1].grad)):
