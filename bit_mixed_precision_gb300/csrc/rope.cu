@@ -10,10 +10,13 @@
 // [-1/2, 1/2) turns, becomes float32 and cosine and sine.
 // Bound: HBM, each row is read and written once.  D / 16 lanes share a row, each with the two 16-byte pieces that hold
 // the two sides of its eight pairs, so that the rotation needs no exchange and the norm's sum two or three shuffles; a
-// warp holds 64 / (D / 8) rows of one token at a time and computes the token's eight angles a lane once for all heads.
-// The rows come through a ring in shared memory that every lane fills for itself with asynchronous copies: 5 KB a warp
-// in flight (backward 8) without registers to hold it.
-// All arithmetic is float32; an output is rounded once.
+// warp holds 64 / (D / 8) rows of one token at a time, and the token's angles are computed once for all heads, a share
+// by each lane.  The rows come through a ring in shared memory that every lane fills for itself with asynchronous
+// copies: 5 KB a warp in flight (backward 8) without registers to hold it.
+// All arithmetic is float32, two numbers to an instruction; an output is rounded once.
+// Measured: 4 x 16384 tokens of 32/8 heads of 128 in bf16 236 us, 6.8 TB/s (loads to registers two groups ahead: 318);
+// their gradient, 16 x 4096 tokens, 384 us, 5.9 TB/s (eight sines a lane and weights in registers: 523).  One token
+// 2.8 us.
 #include <algorithm>
 #include <atomic>
 
