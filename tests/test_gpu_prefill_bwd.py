@@ -225,7 +225,7 @@ def test_repeats_itself_on_any_workspace():
 
 
 def test_graph_replay_and_streams():
-    """First calls inside a capture; two graphs on one workspace; calls on a given stream with temporaries dropped."""
+    """Two graphs on one workspace and one with its own; calls on a given stream with temporaries dropped."""
     x = make(1, 4, 2, 333, 128, BF16)
     want = kvq.prefill_attn_bwd(*x)
     double = kvq.prefill_attn_bwd(x[0] * 2, *x[1:])
@@ -249,6 +249,36 @@ def test_graph_replay_and_streams():
     s.synchronize()
     assert all(torch.equal(a, b) for out in outs for a, b in zip(out, want))
     del junk
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls of all three operators are captured, with a second capture on another stream's graph."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from bit_mixed_precision_gb300 import kvq
+g = torch.Generator().manual_seed(0)
+x = torch.randn((2, 70, 8, 64), generator=g).half().cuda()
+w, pos, rope = torch.ones(64).half().cuda(), torch.arange(70).int().repeat(2, 1).cuda(), kvq.make_rope(64, interleaved=True)
+def step():
+    q, k, v = kvq.qk_norm_rope(x[:, :, :4], x[:, :, 4:6], x[:, :, 6:], pos, rope, w, w)
+    o, lse, _ = kvq.prefill_attn_scores(q, k, v, colscore=False)
+    d = kvq.prefill_attn_bwd(o, q, k, v, o, lse)
+    return kvq.qk_norm_rope_bwd(*d, x[:, :, :4], x[:, :, 4:6], pos, rope, w, w)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step())) and kvq.device_status() == 0
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_calls_at_once():

@@ -263,8 +263,8 @@ def test_no_tokens(kvq):
 
 
 def test_graph_replay_and_streams(kvq):
-    """First calls inside a capture; two graphs that share a workspace, replayed with new inputs in place; a call on a
-    stream given, whose temporaries go back to the allocator at once."""
+    """Two graphs that share a workspace, replayed with new inputs in place; a call on a stream given, whose temporaries go
+    back to the allocator at once."""
     c = Case(kvq, B=2, T=200, Hq=8, Hkv=2, D=128, dtype=BF16)
     want, grads = c.forward(), c.backward()
     c.x.mul_(2.0)
