@@ -534,9 +534,9 @@ kvq_status block8_evict(kvq_block8* c, const int32_t* keep, int n_first, int n_l
 static kvq_status check_prefill_bwd(int B, int Hq, int Hkv, int T, const char* who) {
     KVQ_REQUIRE(B > 0 && Hq > 0 && Hkv > 0 && T > 0, KVQ_EINVAL, "%s: sizes must be positive", who);
     KVQ_REQUIRE(Hq % Hkv == 0, KVQ_EINVAL, "%s: Hq %% Hkv != 0", who);
-    // the row statistics' grid has a head per row, the others a CTA per head and tile
-    KVQ_REQUIRE((long long)B * Hq <= 65535 && T <= (1 << 24) && (long long)B * Hq * ((T + 127) / 128) <= (1LL << 30),
-                KVQ_EUNSUPPORTED, "%s: too large", who);
+    // a CTA per head and tile of 128 tokens
+    KVQ_REQUIRE(T <= (1 << 24) && (long long)B * Hq <= (1LL << 30) / ((T + 127) / 128), KVQ_EUNSUPPORTED, "%s: too large",
+                who);
     return KVQ_OK;
 }
 

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kPrepThreads)
                     const float* __restrict__ lse, const float* __restrict__ glse, const BwdArgs a) {
     constexpr int kLanes = D / 8, kRows = kPrepThreads / kLanes;
     grid_launch_dependents();
-    const int tile = blockIdx.x, bh = blockIdx.y;
+    const int tile = (int)blockIdx.x % a.n_t, bh = (int)blockIdx.x / a.n_t;
     const int b = bh / a.Hq, hq = bh % a.Hq, g = a.Hq / a.Hkv;
     const int l = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
     const int64_t Tp = (int64_t)a.n_t * kTile;
@@ -946,7 +946,7 @@ kvq_status run_typed(const PrefillBwdCall& c, cudaStream_t s) {
         a.sm_scale = c.sm_scale, a.scale_log2 = c.sm_scale * kLog2e;
         a.group = a.split = 1;
         const int g = c.Hq / c.Hkv;
-        bwd_prep_kernel<T, AB, D><<<dim3(a.n_t, c.B * c.Hq), kPrepThreads, 0, s>>>(
+        bwd_prep_kernel<T, AB, D><<<a.n_t * c.B * c.Hq, kPrepThreads, 0, s>>>(
             (const T*)c.o, (const T*)c.go, (const T*)c.v, c.lse, c.glse, a);
         e = cudaGetLastError();
         if (e == cudaSuccess) {

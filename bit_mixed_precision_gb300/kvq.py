@@ -1022,21 +1022,35 @@ def qk_norm_rope_bwd(dq, dk, dv, q, k, pos, rope, q_weight=None, k_weight=None, 
     dqp, dkp = _dense(dq, q_shape, dtype, index, "dq"), _dense(dk, kv_shape, dtype, index, "dk")
     dvp = None if dv is None else _dense(dv, kv_shape, dtype, index, "dv")
     f = torch.float32
+    gvp, gvs, gqwp, gkwp = None, (0, 0, 0), None, None
     if out is None:
-        both = _new(rows + (Hq + (1 if dv is None else 2) * Hkv, D), q, dtype, stream)
+        n = Hq + (1 if dv is None else 2) * Hkv
+        both = _new(rows + (n, D), q, dtype, stream)
         gq, gk, *gv = both.split_with_sizes([Hq, Hkv] if dv is None else [Hq, Hkv, Hkv], -2)
         gv = gv[0] if gv else None
-        gqw = None if qw is None else _new((D,), q, f, stream)
-        gkw = None if kw is None else _new((D,), q, f, stream)
+        gqs = gks = gvs = (T * n * D, n * D, D)
+        gqp = both.data_ptr()
+        gkp = gqp + 2 * D * Hq
+        gvp = None if dv is None else gkp + 2 * D * Hkv
+        gqw = gkw = None
+        if qw:
+            gqw = _new((D,), q, f, stream)
+            gqwp = gqw.data_ptr()
+        if kw:
+            gkw = _new((D,), q, f, stream)
+            gkwp = gkw.data_ptr()
     else:
         gq, gk, gv, gqw, gkw = out
         if any((a is None) != (b is None) for a, b in ((gv, dv), (gqw, q_weight), (gkw, k_weight))):
             _bad("out must have a gradient for each of dv, q_weight and k_weight that is there, and for no other")
-    gqp, gqs = _heads(gq, q_in, dtype, index, "out[0]")
-    gkp, gks = _heads(gk, kv_in, dtype, index, "out[1]")
-    gvp, gvs = (None, (0, 0, 0)) if gv is None else _heads(gv, kv_in, dtype, index, "out[2]")
-    gqwp = None if gqw is None else _dense(gqw, (D,), f, index, "out[3]")
-    gkwp = None if gkw is None else _dense(gkw, (D,), f, index, "out[4]")
+        gqp, gqs = _heads(gq, q_in, dtype, index, "out[0]")
+        gkp, gks = _heads(gk, kv_in, dtype, index, "out[1]")
+        if gv is not None:
+            gvp, gvs = _heads(gv, kv_in, dtype, index, "out[2]")
+        if gqw is not None:
+            gqwp = _dense(gqw, (D,), f, index, "out[3]")
+        if gkw is not None:
+            gkwp = _dense(gkw, (D,), f, index, "out[4]")
     L = _lib or lib()
     wsp = ws_bytes = 0
     if qw or kw:

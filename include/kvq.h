@@ -214,8 +214,9 @@ kvq_status prefill_attn_scores(const void* q, const void* k, const void* v, kvq_
  *   f16 a P of 2 and more, which no row's own lse gives, overflows).  go (device)
  *   [B, Hq, T, D]: gradient of o; glse (device, nullable) [B, Hq, T]: of lse.
  *   dq (device) [B, Hq, T, D]; dk, dv (device) [B, Hkv, T, D], no overlap with
- *   the inputs.  q, k, v, o, go, dq, dk, dv 16-byte aligned.  A row with
- *   lse = -inf (one that saw nothing) has no gradient.
+ *   the inputs.  q, k, v, o, go, dq, dk, dv 16-byte aligned.  T <= 2^24, and
+ *   B * Hq heads have at most 2^30 tiles of 128 tokens.  A row with lse = -inf
+ *   (one that saw nothing) has no gradient.
  *   ws (device) of prefill_attn_bwd_workspace_bytes(), 256-byte aligned.
  * Sums are float32; P and dS enter their products in the activations' type.
  * A call repeats itself bit for bit. */
@@ -567,7 +568,7 @@ typedef struct {
  *     y = x * rsqrt(mean(x^2) + eps) * weight, eps >= 0.
  *   q_out [B, Hq, T, D], k_out, v_out [B, Hkv, T, D] (device) contiguous, not
  *   overlapping the inputs: what prefill_attn_scores takes, with T = 1 what
- *   block8_append, block8_attn and decode_attn_qkv take.
+ *   block8_append, block8_attn and decode_attn_qkv take.  B * T <= 2^30.
  * float32 arithmetic, one rounding. */
 kvq_status qk_norm_rope(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D,
                         const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* pos,

@@ -138,6 +138,12 @@ def test_many_heads():
             assert torch.equal(alone[0][0], got[0][b])
 
 
+def test_many_short_sequences():
+    """More heads than a grid's second axis could count."""
+    x = make(2200, 32, 8, 20, 64, BF16)
+    check(kvq.prefill_attn_bwd(*x), *x, heads=[0, 9999, 2200 * 8 - 1])
+
+
 @pytest.mark.parametrize("dtype,size", [(F16, 2.0 ** -14), (F16, 3000.0), (BF16, 2.0 ** -60), (BF16, 2.0 ** 40)])
 def test_gradients_of_any_size(dtype, size):
     """fp16: dS below its normal range, or do.v beyond its largest number; results that overflow the type are avoided by

@@ -87,7 +87,7 @@ def test_bad_arguments_are_refused(L):
         assert call(**{n: odd}) == E, n
     assert call(glse=ctypes.c_void_p(2)) == E and call(lse=ctypes.c_void_p(2)) == E
     assert call(dt=2) == E and call(Hq=3) == E and call(T=0) == E and call(B=0) == E and call(B=-1) == E
-    assert call(D=96) == X and call(causal=0) == X and call(B=65535, Hq=2) == X and call(T=(1 << 24) + 1) == X
+    assert call(D=96) == X and call(causal=0) == X and call(B=1 << 20, Hq=2048) == X and call(T=(1 << 24) + 1) == X
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert call(scale=s) == E
     need = L.prefill_attn_bwd_workspace_bytes(1, 4, 2, 100)
