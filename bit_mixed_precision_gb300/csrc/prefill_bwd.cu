@@ -33,6 +33,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "grad_device.cuh"
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
 #include "prefill_tiles.cuh"

@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "grad_device.cuh"
 #include "kvq_common.cuh"
 #include "kvq_internal.h"
 
