@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
             if (!v) {
                 turn_pairs<true>(d, cs, sn);
                 if (norm) {
-                    const float r = row_scale<D>(x, a.eps);
+                    // lanes without a head hold zeros, whose 1 / sqrt(0 + eps) may be infinite: 0 for them
+                    const float s = row_scale<D>(x, a.eps), r = h < H ? s : 0.0f;
                     const F2 r2 = f2_pack(r, r);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

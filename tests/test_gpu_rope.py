@@ -402,3 +402,19 @@ def test_training_step(kvq, dtype, D, rot):
                    (grads[3], w[0].grad), (grads[4], w[1].grad)):
         off = float((a.double().cpu() - ref).norm() / ref.norm())
         assert off <= min(bound, 0.1), (off, bound)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,interleaved,norm", [
+    (64, 4, 4, False, (1, 1)),
+    (64, 9, 3, True, (1, 1)),
+    (128, 6, 2, False, (1, 1)),
+    (128, 5, 1, True, (1, 0)),
+    (64, 20, 4, False, (0, 1)),
+    (128, 8, 4, False, (1, 1)),
+])
+def test_backward_without_eps(kvq, D, Hq, Hkv, interleaved, norm):
+    """eps = 0 on rows that are not zero, also where the heads do not fill a warp's rows: 1 / sqrt(0) of a row that is not
+    there must not reach the weights' gradients."""
+    c = Case(kvq, B=2, T=9, Hq=Hq, Hkv=Hkv, D=D, interleaved=interleaved, norm=norm, eps=0.0, seed=7)
+    c.check_forward(c.forward())
+    c.check_backward(c.backward())
