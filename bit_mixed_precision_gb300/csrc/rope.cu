@@ -185,8 +185,10 @@ template <int D> struct Angles {
 
 __device__ __forceinline__ F2 f2_neg(F2 x) { return x ^ 0x8000000080000000ull; }
 
-// The pairs turned by phi, or with BACK by -phi.
-template <bool BACK> __device__ __forceinline__ void turn_pairs(Sides& x, const F2* cs, const F2* sn) {
+// The pairs turned by phi, or with BACK by -phi.  A lane whose channels do not turn (all of its eight pairs or none do)
+// leaves them alone: with cosine 1 and sine 0 an infinity would make its neighbour NaN.
+template <bool BACK> __device__ __forceinline__ void turn_pairs(Sides& x, bool turns, const F2* cs, const F2* sn) {
+    if (!turns) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const F2 a = x.a[i], b = x.b[i], s = BACK ? sn[i] : f2_neg(sn[i]), t = BACK ? f2_neg(sn[i]) : sn[i];
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 3)
                     x.b[i] = f2_mul(f2_mul(x.b[i], r2), wt.b[i]);
                 }
             }
-            turn_pairs<false>(x, cs, sn);
+            turn_pairs<false>(x, at.pair < a.rot / 2, cs, sn);
             pieces<T, IL>(x, u0, u1);
         }
         if (h < H) {
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
             request(stage);
             stage = stage + 1 == kBwdStages ? 0 : stage + 1;
             if (!v) {
-                turn_pairs<true>(d, cs, sn);
+                turn_pairs<true>(d, at.pair < a.rot / 2, cs, sn);
                 if (norm) {
                     // lanes without a head hold zeros, whose 1 / sqrt(0 + eps) may be infinite: 0 for them
                     const float s = row_scale<D>(x, a.eps), r = h < H ? s : 0.0f;

@@ -418,3 +418,38 @@ def test_backward_without_eps(kvq, D, Hq, Hkv, interleaved, norm):
     c = Case(kvq, B=2, T=9, Hq=Hq, Hkv=Hkv, D=D, interleaved=interleaved, norm=norm, eps=0.0, seed=7)
     c.check_forward(c.forward())
     c.check_backward(c.backward())
+
+
+BEHIND = [(64, 16, False), (64, 32, True), (128, 48, False), (128, 112, True), (64, 0, False), (128, 0, True)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D,rot,interleaved", BEHIND)
+def test_infinities_behind_the_rotated_channels(kvq, D, rot, interleaved, dtype):
+    """Channels that do not turn leave without a norm as they came, and touch no other channel, both ways."""
+    c = Case(kvq, B=1, T=6, Hq=6, Hkv=3, D=D, rot=rot, interleaved=interleaved, dtype=dtype, norm=(0, 0))
+    base, grads = c.forward(), c.backward()
+    put = [(rot, math.inf), (rot + 3, -math.inf), (D - 1, math.nan), ((rot + D) // 2, math.inf), (rot + 1, -0.0)]
+    for i, (ch, x) in enumerate(put):
+        c.q[0, i, i, ch] = c.k[0, i, i % 3, ch] = x
+        c.d[0][0, i, i, ch] = c.d[1][0, i % 3, i, ch] = x
+    got, back = c.forward(), c.backward()
+    for raw, want, o in ((c.q, base[0], got[0]), (c.k, base[1], got[1])):
+        want = want.clone()
+        want[..., rot:] = raw.transpose(1, 2)[..., rot:]
+        torch.testing.assert_close(o, want, rtol=0, atol=0, equal_nan=True)
+        assert torch.equal(o.signbit()[..., rot:] | o[..., rot:].isnan(), want.signbit()[..., rot:] | want[..., rot:].isnan())
+    for d, want, o in ((c.d[0], grads[0], back[0]), (c.d[1], grads[1], back[1])):
+        want = want.clone()
+        want[..., rot:] = d.transpose(1, 2)[..., rot:]
+        torch.testing.assert_close(o, want, rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("D,rot,interleaved", BEHIND)
+def test_infinities_behind_the_rotated_channels_of_a_normed_row(kvq, D, rot, interleaved):
+    """An infinite sum of squares leaves x * 0: zeros, and NaN in the infinite channel alone."""
+    c = Case(kvq, B=1, T=2, Hq=3, Hkv=1, D=D, rot=rot, interleaved=interleaved)
+    c.q[0, 1, 2, rot + 2], c.k[0, 0, 0, D - 2] = math.inf, -math.inf
+    q, k, _ = c.forward()
+    for row, ch in ((q[0, 2, 1], rot + 2), (k[0, 0, 0], D - 2)):
+        assert row[ch].isnan() and (torch.cat([row[:ch], row[ch + 1:]]) == 0).all()
