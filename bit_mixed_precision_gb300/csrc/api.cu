@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "kvq_internal.h"
+#include "rows.h"
 
 extern "C" cudaError_t kvq_internal_status_quant(cudaStream_t, uint32_t*);
 extern "C" cudaError_t kvq_internal_status_prefill(cudaStream_t, uint32_t*);
@@ -450,6 +451,19 @@ static kvq_status check_ws(const void* ws, size_t given, size_t need, const char
     return KVQ_OK;
 }
 
+// What a call writes shares no memory with what it reads nor with what else it writes (row 0: not there).
+static kvq_status check_apart(const kvq::Rows* out, int n_out, const kvq::Rows* in, int n_in, const char* who) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; out[i].row && j < n_in; ++j)
+            KVQ_REQUIRE(in[j].row == 0 || !kvq::rows_meet(out[i], in[j]), KVQ_EINVAL,
+                        "%s: an output or the workspace overlaps an input", who);
+        for (int j = 0; out[i].row && j < i; ++j)
+            KVQ_REQUIRE(out[j].row == 0 || !kvq::rows_meet(out[i], out[j]), KVQ_EINVAL,
+                        "%s: outputs or the workspace overlap one another", who);
+    }
+    return KVQ_OK;
+}
+
 // Rows of n_sel list entries (0: no lists).  What one call works through, 16 tokens for up to 32 rows
 // at a time (at least 8), is counted in 32 bits.
 static kvq_status check_list(const kvq_block8* c, int n_q, int n_sel, const char* who) {
@@ -559,7 +573,14 @@ kvq_status prefill_attn_bwd(const void* q, const void* k, const void* v, const v
                     aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16) && aligned(lse, 4) && aligned(glse, 4),
                 KVQ_EINVAL, "%s: q/k/v/o/go/dq/dk/dv must be 16-byte aligned", who);
     KVQ_REQUIRE(sm_scale > 0.0f && sm_scale < 1e30f, KVQ_EINVAL, "%s: sm_scale must be positive and finite", who);
-    if ((st = check_ws(ws, ws_bytes, kvq::prefill_bwd_bytes(B, Hq, Hkv, T), who)) != KVQ_OK) return st;
+    const size_t need = kvq::prefill_bwd_bytes(B, Hq, Hkv, T);
+    if ((st = check_ws(ws, ws_bytes, need, who)) != KVQ_OK) return st;
+    // the two kernels of the call run side by side: neither may write what the other still reads
+    const int64_t lse_bytes = (int64_t)B * Hq * T * 4, q_bytes = lse_bytes / 2 * D, kv_bytes = (int64_t)B * Hkv * T * D * 2;
+    const kvq::Rows in[] = {{q, q_bytes}, {k, kv_bytes}, {v, kv_bytes}, {o, q_bytes}, {go, q_bytes}, {lse, lse_bytes},
+                            {glse, glse ? lse_bytes : 0}};
+    const kvq::Rows out[] = {{dq, q_bytes}, {dk, kv_bytes}, {dv, kv_bytes}, {ws, (int64_t)need}};
+    if ((st = check_apart(out, 4, in, 7, who)) != KVQ_OK) return st;
     kvq::PrefillBwdCall c = {};
     c.dt = dt, c.B = B, c.Hq = Hq, c.Hkv = Hkv, c.T = T, c.D = D, c.q = q, c.k = k, c.v = v, c.o = o, c.go = go;
     c.lse = lse, c.glse = glse, c.sm_scale = sm_scale, c.dq = dq, c.dk = dk, c.dv = dv, c.ws = ws;

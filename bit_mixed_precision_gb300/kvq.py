@@ -1088,8 +1088,9 @@ def _workspace(need, like, ws, stream):
 
 def prefill_attn_bwd(do, q, k, v, o, lse, sm_scale=None, dlse=None, out=None, ws=None, stream=None):
     """Gradients (dq, dk, dv) of q [B, Hq, T, D], k, v [B, Hkv, T, D] through prefill_attn_scores' o and lse: do is the
-    gradient of o, dlse (float32 [B, Hq, T], may be None) that of lse.  All contiguous.  ws: a uint8 workspace of
-    prefill_attn_bwd_ws_bytes(q, k) + 256 bytes to share between calls that never overlap on the GPU."""
+    gradient of o, dlse (float32 [B, Hq, T], may be None) that of lse.  All contiguous.  out: (dq, dk, dv) to write, which
+    share no memory with the inputs or one another.  ws: a uint8 workspace of prefill_attn_bwd_ws_bytes(q, k) + 256 bytes
+    to share between calls that never overlap on the GPU."""
     dt, dtype = _dt(q), q.dtype
     _check_qk(q, k, v)
     q_shape, kv_shape, index = q.shape, k.shape, q.get_device()

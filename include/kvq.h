@@ -213,8 +213,9 @@ kvq_status prefill_attn_scores(const void* q, const void* k, const void* v, kvq_
  *   finite (the tile products also multiply the zeros above the diagonal; in
  *   f16 a P of 2 and more, which no row's own lse gives, overflows).  go (device)
  *   [B, Hq, T, D]: gradient of o; glse (device, nullable) [B, Hq, T]: of lse.
- *   dq (device) [B, Hq, T, D]; dk, dv (device) [B, Hkv, T, D], no overlap with
- *   the inputs.  q, k, v, o, go, dq, dk, dv 16-byte aligned.  T <= 2^24, and
+ *   dq (device) [B, Hq, T, D]; dk, dv (device) [B, Hkv, T, D]: no overlap with
+ *   the inputs, one another or ws (refused: KVQ_EINVAL).
+ *   q, k, v, o, go, dq, dk, dv 16-byte aligned.  T <= 2^24, and
  *   B * Hq heads have at most 2^30 tiles of 128 tokens.  A row with lse = -inf
  *   (one that saw nothing) has no gradient.
  *   ws (device) of prefill_attn_bwd_workspace_bytes(), 256-byte aligned.
