@@ -451,11 +451,13 @@ static kvq_status check_ws(const void* ws, size_t given, size_t need, const char
     return KVQ_OK;
 }
 
-// What a call writes shares no memory with what it reads nor with what else it writes (row 0: not there).
-static kvq_status check_apart(const kvq::Rows* out, int n_out, const kvq::Rows* in, int n_in, const char* who) {
+// What a call writes shares no memory with what it reads nor with what else it writes (row 0: not there).  Bit 10 i + j of
+// `same`: output i may be input j, which it replaces row for row.
+static kvq_status check_apart(const kvq::Rows* out, int n_out, const kvq::Rows* in, int n_in, uint64_t same,
+                              const char* who) {
     for (int i = 0; i < n_out; ++i) {
         for (int j = 0; out[i].row && j < n_in; ++j)
-            KVQ_REQUIRE(in[j].row == 0 || !kvq::rows_meet(out[i], in[j]), KVQ_EINVAL,
+            KVQ_REQUIRE(in[j].row == 0 || (same >> (10 * i + j) & 1) || !kvq::rows_meet(out[i], in[j]), KVQ_EINVAL,
                         "%s: an output or the workspace overlaps an input", who);
         for (int j = 0; out[i].row && j < i; ++j)
             KVQ_REQUIRE(out[j].row == 0 || !kvq::rows_meet(out[i], out[j]), KVQ_EINVAL,
@@ -580,7 +582,7 @@ kvq_status prefill_attn_bwd(const void* q, const void* k, const void* v, const v
     const kvq::Rows in[] = {{q, q_bytes}, {k, kv_bytes}, {v, kv_bytes}, {o, q_bytes}, {go, q_bytes}, {lse, lse_bytes},
                             {glse, glse ? lse_bytes : 0}};
     const kvq::Rows out[] = {{dq, q_bytes}, {dk, kv_bytes}, {dv, kv_bytes}, {ws, (int64_t)need}};
-    if ((st = check_apart(out, 4, in, 7, who)) != KVQ_OK) return st;
+    if ((st = check_apart(out, 4, in, 7, 0, who)) != KVQ_OK) return st;
     kvq::PrefillBwdCall c = {};
     c.dt = dt, c.B = B, c.Hq = Hq, c.Hkv = Hkv, c.T = T, c.D = D, c.q = q, c.k = k, c.v = v, c.o = o, c.go = go;
     c.lse = lse, c.glse = glse, c.sm_scale = sm_scale, c.dq = dq, c.dk = dk, c.dv = dv, c.ws = ws;
@@ -622,6 +624,23 @@ static kvq_status head_strides(const void* x, const int64_t* given, int B, int T
     return KVQ_OK;
 }
 
+// Rows [B, T, H, D] of 16-bit elements (strides of head_strides()); x NULL: none.
+static kvq::Rows head_rows(const void* x, int B, int T, int H, int D, const int64_t* st) {
+    if (!x) return {};
+    return kvq::Rows(x, 2 * D, {B, T, H}, {2 * st[0], 2 * st[1], 2 * st[2]});
+}
+
+// Bit `bit` where rows [B, T, H, D] at x with strides st are those at y with strides sy (NULL: contiguous [B, H, T, D]).
+// A row's lanes read it before they write it and no others do, so such an output may replace its input.
+static uint64_t same_rows(int bit, const void* x, const int64_t* st, const void* y, const int64_t* sy, int B, int T, int H,
+                          int D) {
+    const int64_t dense[3] = {(int64_t)H * T * D, D, (int64_t)T * D};
+    const int size[3] = {B, T, H};
+    for (int i = 0; i < 3; ++i)
+        if (x != y || (size[i] != 1 && st[i] != (sy ? sy : dense)[i])) return 0;
+    return 1ull << bit;
+}
+
 kvq_status qk_norm_rope(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D, const void* q,
                         const void* k, const void* v, const int64_t* strides, const int32_t* pos, const void* q_weight,
                         const void* k_weight, int weight_f32, float eps, void* q_out, void* k_out, void* v_out,
@@ -640,6 +659,16 @@ kvq_status qk_norm_rope(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq
     KVQ_REQUIRE(aligned(q_out, 16) && aligned(k_out, 16) && aligned(v_out, 16) && aligned(q_weight, 16) &&
                     aligned(k_weight, 16) && aligned(pos, 4),
                 KVQ_EINVAL, "%s: misaligned pointer", who);
+    const int64_t tokens = (int64_t)B * T, pos_bytes = rope->rot ? 4 * tokens * rope->n_axes : 0;
+    const int64_t q_bytes = 2 * tokens * Hq * D, kv_bytes = 2 * tokens * Hkv * D, w_bytes = (weight_f32 ? 4 : 2) * D;
+    const kvq::Rows in[] = {head_rows(q, B, T, Hq, D, c.strides[0]), head_rows(k, B, T, Hkv, D, c.strides[1]),
+                            head_rows(v, B, T, Hkv, D, c.strides[2]), {pos, pos_bytes},
+                            {q_weight, q_weight ? w_bytes : 0}, {k_weight, k_weight ? w_bytes : 0}};
+    const kvq::Rows out[] = {{q_out, q_bytes}, {k_out, kv_bytes}, {v_out, v ? kv_bytes : 0}};
+    const uint64_t same = same_rows(0, q, c.strides[0], q_out, nullptr, B, T, Hq, D) |
+                          same_rows(11, k, c.strides[1], k_out, nullptr, B, T, Hkv, D) |
+                          (v ? same_rows(22, v, c.strides[2], v_out, nullptr, B, T, Hkv, D) : 0);
+    if ((st = check_apart(out, 3, in, 6, same, who)) != KVQ_OK) return st;
     return cuda_status(kvq::launch_rope(c, (cudaStream_t)stream), "qk_norm_rope launch");
 }
 
@@ -688,8 +717,24 @@ kvq_status qk_norm_rope_bwd(const kvq_rope* rope, kvq_dtype dt, int B, int T, in
     KVQ_REQUIRE(aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16) && aligned(q_weight, 16) && aligned(k_weight, 16) &&
                     aligned(pos, 4),
                 KVQ_EINVAL, "%s: misaligned pointer", who);
-    st = check_ws(ws, ws_bytes, qk_norm_rope_bwd_workspace_bytes(B, T, D, q_weight || k_weight), who);
-    if (st != KVQ_OK) return st;
+    const size_t need = qk_norm_rope_bwd_workspace_bytes(B, T, D, q_weight || k_weight);
+    if ((st = check_ws(ws, ws_bytes, need, who)) != KVQ_OK) return st;
+    const int64_t tokens = (int64_t)B * T, pos_bytes = rope->rot ? 4 * tokens * rope->n_axes : 0;
+    const int64_t q_bytes = 2 * tokens * Hq * D, kv_bytes = 2 * tokens * Hkv * D, w_bytes = (weight_f32 ? 4 : 2) * D;
+    const kvq::Rows in[] = {{dq, q_bytes}, {dk, kv_bytes}, {dv, dv ? kv_bytes : 0},
+                            head_rows(c.q, B, T, Hq, D, c.strides[0]), head_rows(c.k, B, T, Hkv, D, c.strides[1]),
+                            {pos, pos_bytes}, {q_weight, q_weight ? w_bytes : 0}, {k_weight, k_weight ? w_bytes : 0}};
+    const kvq::Rows out[] = {head_rows(gq, B, T, Hq, D, c.gstrides[0]), head_rows(gk, B, T, Hkv, D, c.gstrides[1]),
+                             head_rows(dv ? gv : nullptr, B, T, Hkv, D, c.gstrides[2]), {gq_weight, q_weight ? 4 * D : 0},
+                             {gk_weight, k_weight ? 4 * D : 0}, {ws, (int64_t)need}};
+    for (int i = 0; i < 3; ++i)
+        KVQ_REQUIRE(out[i].nested(), KVQ_EINVAL, "%s: rows of a gradient must not overlap", who);
+    const uint64_t same = same_rows(0, gq, c.gstrides[0], dq, nullptr, B, T, Hq, D) |
+                          same_rows(3, gq, c.gstrides[0], c.q, c.strides[0], B, T, Hq, D) |
+                          same_rows(11, gk, c.gstrides[1], dk, nullptr, B, T, Hkv, D) |
+                          same_rows(14, gk, c.gstrides[1], c.k, c.strides[1], B, T, Hkv, D) |
+                          (dv ? same_rows(22, gv, c.gstrides[2], dv, nullptr, B, T, Hkv, D) : 0);
+    if ((st = check_apart(out, 6, in, 8, same, who)) != KVQ_OK) return st;
     return cuda_status(kvq::launch_rope_bwd(c, (cudaStream_t)stream), "qk_norm_rope_bwd launch");
 }
 

@@ -976,7 +976,8 @@ def qk_norm_rope(q, k, v, pos, rope, q_weight=None, k_weight=None, eps=1e-6, out
     """From a projection to attention: q [B, T, Hq, D], k, v [B, T, Hkv, D] (views of one projection, any strides;
     for a step [B, heads, D]; v may be None) to (q, k, v) [B, heads, T, D] ([B, heads, D]), q and k RMS-normed per
     head (q_weight, k_weight [D]; None: no norm) and turned by pos (int32 [B, T], with several axes [axes, B, T];
-    for a step without T)."""
+    for a step without T).  out: (q, k, v) to write, contiguous; none shares memory with an input or another, but each may
+    be its own input where every row keeps its place (a step, or q as a view of [B, Hq, T, D])."""
     dt, dtype = _dt(q), q.dtype
     index, rows, Hq, Hkv, D, pp, qw, kw, f32 = _rope_call(q, k, pos, rope, q_weight, k_weight)
     qp, qs = _heads(q, rows + (Hq, D), dtype, index, "q")
@@ -1007,8 +1008,9 @@ def qk_norm_rope_bwd(dq, dk, dv, q, k, pos, rope, q_weight=None, k_weight=None, 
                      stream=None):
     """The gradient of qk_norm_rope: dq, dk, dv are those of its outputs (dv may be None), the others its arguments.
     Returns (gq, gk, gv, gq_weight, gk_weight), the first three [B, T, heads, D] as views of one [B, T, Hq + 2 Hkv, D]
-    (or as given in out[:3], any strides), the last two float32 [D] (None without that norm).  ws: a uint8 workspace
-    of qk_norm_rope_bwd_ws_bytes(q) + 256 bytes to share between calls that never overlap on the GPU."""
+    (or as given in out[:3], any strides), the last two float32 [D] (None without that norm).  Nothing in out shares
+    memory with an input or another output, but gq may be q (or dq), gk k, row for row.  ws: a uint8 workspace of
+    qk_norm_rope_bwd_ws_bytes(q) + 256 bytes to share between calls that never overlap on the GPU."""
     dt, dtype = _dt(q), q.dtype
     index, rows, Hq, Hkv, D, pp, qw, kw, f32 = _rope_call(q, k, pos, rope, q_weight, k_weight)
     q_in, kv_in = rows + (Hq, D), rows + (Hkv, D)

@@ -567,9 +567,12 @@ typedef struct {
  *   q_weight, k_weight (device, each may be NULL: that norm is left out) [D]
  *   of the activations' type, or float32 (weight_f32 != 0), 16-byte aligned:
  *     y = x * rsqrt(mean(x^2) + eps) * weight, eps >= 0.
- *   q_out [B, Hq, T, D], k_out, v_out [B, Hkv, T, D] (device) contiguous, not
- *   overlapping the inputs: what prefill_attn_scores takes, with T = 1 what
- *   block8_append, block8_attn and decode_attn_qkv take.  B * T <= 2^30.
+ *   q_out [B, Hq, T, D], k_out, v_out [B, Hkv, T, D] (device) contiguous: what
+ *   prefill_attn_scores takes, with T = 1 what block8_append, block8_attn and
+ *   decode_attn_qkv take.  B * T <= 2^30.
+ *   No output overlaps an input or another output (refused: KVQ_EINVAL), but
+ *   each may be its own input (the same address of every row, as T = 1 or q
+ *   as a view of [B, Hq, T, D] allow).
  * float32 arithmetic, one rounding. */
 kvq_status qk_norm_rope(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq, int Hkv, int D,
                         const void* q, const void* k, const void* v, const int64_t* strides, const int32_t* pos,
@@ -582,8 +585,11 @@ kvq_status qk_norm_rope(const kvq_rope* rope, kvq_dtype dt, int B, int T, int Hq
  *   (strides of q and of k; not read where the norm is left out, and then q or
  *   k may be NULL).
  *   gq, gk, gv (device) [B, T, heads, D]: gradients of q, k, v; g_strides as
- *   strides above (of gq, gk, gv), the rows must not overlap.
+ *   strides above (of gq, gk, gv), each large enough to step over all the axes
+ *   of smaller strides together, as in every slice or transpose of an array.
  *   gq_weight, gk_weight (device) [D] float32: written where that norm is there.
+ *   No output overlaps an input, another output or ws (refused: KVQ_EINVAL), but
+ *   gq may be q or dq, gk k or dk, gv dv, at the same address in every row.
  *   ws (device) of qk_norm_rope_bwd_workspace_bytes(), 256-byte aligned
  *   (0 without norms).  Sums run in a fixed order: a call repeats itself bit
  *   for bit. */

@@ -453,3 +453,44 @@ def test_infinities_behind_the_rotated_channels_of_a_normed_row(kvq, D, rot, int
     q, k, _ = c.forward()
     for row, ch in ((q[0, 2, 1], rot + 2), (k[0, 0, 0], D - 2)):
         assert row[ch].isnan() and (torch.cat([row[:ch], row[ch + 1:]]) == 0).all()
+
+
+@pytest.mark.parametrize("kind", [dict(B=3, T=1, Hq=12, Hkv=4, step=True), dict(B=2, T=301, D=64, dtype=BF16),
+                                  dict(B=1, T=40, Hq=5, Hkv=5, rot=32, interleaved=True)], ids=str)
+def test_in_place(kvq, kind):
+    """Outputs in place of their own inputs, and gradients beside one another in one array."""
+    c = Case(kvq, **kind)
+    base, grads = c.forward(), c.backward()
+    at = (lambda x: x[:, 0]) if c.step else (lambda x: x)
+    q, k, v = (x.clone() for x in base)                     # [B, heads, T, D] storage: raw rows as views of it
+    turned = (lambda x: x) if c.step else (lambda x: x.transpose(1, 2))
+    for dst, src in ((q, c.q), (k, c.k), (v, c.v)):
+        turned(dst).copy_(at(src))
+    pos = c.args()[3]
+    got = kvq.qk_norm_rope(turned(q), turned(k), turned(v), pos, c.rope, c.qw, c.kw, c.eps, out=(q, k, v))
+    assert all(a is b and torch.equal(a, w) for a, b, w in zip(got, (q, k, v), base))
+    # the gradient over the projection itself (the values are not read)
+    x = c.x.clone()
+    parts = [at(y) for y in (x[:, :, :c.Hq], x[:, :, c.Hq:c.Hq + c.Hkv], x[:, :, c.Hq + c.Hkv:])]
+    d = [(y[:, :, 0] if c.step else y).contiguous() for y in c.d]
+    weights = [torch.empty(c.D, device="cuda") for _ in range(2)]
+    got = kvq.qk_norm_rope_bwd(*d, parts[0], parts[1], pos, c.rope, c.qw, c.kw, c.eps, out=(*parts, *weights))
+    assert all(torch.equal(a, w) for a, w in zip(got, grads))
+    # over the gradients that come in
+    d = [y.clone() for y in d]
+    got = kvq.qk_norm_rope_bwd(*d, at(c.q), at(c.k), pos, c.rope, c.qw, c.kw, c.eps, out=(*[turned(y) for y in d], *weights))
+    assert all(torch.equal(a, w) for a, w in zip(got, grads))
+
+
+def test_gradients_as_views_of_one_array(kvq):
+    """Layouts whose rows lie between one another but share nothing are taken."""
+    c = Case(kvq, B=2, T=7, Hq=2, Hkv=2, D=64)
+    grads, w = c.backward(), [torch.empty(64, device="cuda") for _ in range(2)]
+    new = lambda *s: torch.full(s, 7.0, dtype=F16, device="cuda")
+    a, b, e = new(2, 7, 2, 3, 64), new(3, 2, 2, 7, 64), new(2, 6, 14, 72)
+    for out in ([a[:, :, :, i] for i in range(3)],                              # a head's query, key and value side by side
+                [b[i].transpose(1, 2) for i in range(3)],                       # heads first
+                [e[:, i::3, ::2, 8:].transpose(1, 2) for i in range(3)],        # every second token, room before each row
+                [e[:, 2 * i:2 * i + 2, i % 2::2, :64].transpose(1, 2) for i in range(3)]):
+        got = c.backward(out=(*out, *w))
+        assert all(torch.equal(x, y) for x, y in zip(got, grads))

@@ -167,3 +167,59 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         kvq.qk_norm_rope(q[:, :, :3], k, None, pos, r)
     with pytest.raises(ValueError, match="for a step"):
         kvq.qk_norm_rope(q, k[0], None, pos, r)
+
+
+def test_overlapping_outputs_are_refused(L):
+    """Rows that share memory: of one gradient, of two, of an output and an input; addresses are made up, nothing is read."""
+    from bit_mixed_precision_gb300 import kvq
+    B, T, Hq, Hkv, D = 2, 5, 4, 2, 64
+    desc, n = ctypes.byref(kvq.make_rope(D).desc), Hq + 2 * Hkv
+    need = L.qk_norm_rope_bwd_workspace_bytes(B, T, D, 1)
+    room = 1 << 16
+    names = ["q", "k", "v", "pos", "qw", "kw", "qo", "ko", "vo", "gq", "gk", "gv", "gqw", "gkw", "ws"]
+    where = {x: (1 << 20) + i * room for i, x in enumerate(names)}
+    dense = lambda h: [T * h * D, h * D, D]
+    wide = [T * n * D, n * D, D]
+
+    def refused(st):
+        return st == kvq.KVQ_EINVAL and b"overlap" in L.kvq_last_error()
+
+    def fwd(strides=None, **kw):
+        p = {x: ctypes.c_void_p(y) for x, y in {**where, **kw}.items()}
+        st = strides or dense(Hq) + dense(Hkv) + dense(Hkv)
+        return refused(L.qk_norm_rope(desc, 0, B, T, Hq, Hkv, D, p["q"], p["k"], p["v"], (ctypes.c_int64 * 9)(*st), p["pos"],
+                                      p["qw"], p["kw"], 0, ctypes.c_float(1e-6), p["qo"], p["ko"], p["vo"], None))
+
+    def bwd(g=None, **kw):
+        p = {x: ctypes.c_void_p(y) for x, y in {**where, **kw}.items()}
+        g = g or dense(Hq) + dense(Hkv) + dense(Hkv)
+        st = dense(Hq) + dense(Hkv) + dense(Hkv)
+        return refused(L.qk_norm_rope_bwd(desc, 0, B, T, Hq, Hkv, D, p["qo"], p["ko"], p["vo"], p["q"], p["k"],
+                                          (ctypes.c_int64 * 9)(*st), p["pos"], p["qw"], p["kw"], 0, ctypes.c_float(1e-6),
+                                          p["gq"], p["gk"], p["gv"], (ctypes.c_int64 * 9)(*g), p["gqw"], p["gkw"], p["ws"],
+                                          need, None))
+
+    size = dict(q=B * T * Hq * D * 2, k=B * T * Hkv * D * 2, v=B * T * Hkv * D * 2, pos=B * T * 4, qw=D * 2, kw=D * 2)
+    size.update(qo=size["q"], ko=size["k"], vo=size["k"], gq=size["q"], gk=size["k"], gv=size["k"], gqw=D * 4, gkw=D * 4, ws=need)
+    for call, outs, ins in ((fwd, ["qo", "ko", "vo"], ["q", "k", "v", "pos", "qw", "kw"]),
+                            (bwd, ["gq", "gk", "gv", "gqw", "gkw", "ws"], ["qo", "ko", "vo", "q", "k", "pos", "qw", "kw"])):
+        for out in outs:
+            for other in ins + outs:
+                if out == other:
+                    continue
+                step = 256 if out == "ws" else 16
+                assert call(**{out: where[other] + (size[other] - 1) // step * step}), (out, other)
+                assert call(**{out: where[other] - (size[out] - 1) // step * step}), (out, other)
+    # rows of one gradient: a head, a token or a sequence that does not step over what lies inside it
+    for i, x in ((2, 8), (2, D - 8), (1, D), (1, Hq * D - 8), (0, Hq * D), (0, T * Hq * D - 8), (5, 8), (8, 8)):
+        g = dense(Hq) + dense(Hkv) + dense(Hkv)
+        g[i] = x
+        assert bwd(g=g), (i, x)
+    # parts of one array that share a head
+    for gk, gv in ((Hq - 1, Hq + Hkv), (Hq, Hq + Hkv - 1), (Hq, Hq), (0, Hq + Hkv)):
+        assert bwd(g=wide * 3, gk=where["gq"] + 2 * D * gk, gv=where["gq"] + 2 * D * gv)
+    # in place only where every row keeps its place
+    assert fwd(qo=where["q"]) and fwd(ko=where["k"]) and fwd(vo=where["v"])
+    assert fwd(strides=[0, Hq * D, D] + dense(Hkv) * 2, qo=where["q"])
+    assert bwd(gq=where["qo"]) and bwd(gk=where["ko"]) and bwd(gv=where["vo"]) and bwd(g=wide * 3, gq=where["q"])
+    assert bwd(gv=where["k"]) and bwd(gk=where["q"])
