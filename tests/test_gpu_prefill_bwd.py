@@ -354,3 +354,37 @@ def test_binding_refusals():
         kvq.prefill_attn_bwd(do, q, k, v, o, lse, out=(q, q, v))
     with pytest.raises(kvq.KvqError, match="sm_scale"):
         kvq.prefill_attn_bwd(do, q, k, v, o, lse, 0.0)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 2, 1), (128, 2, 2)])
+def test_each_gradient_against_differences(D, Hq, Hkv):
+    """The kernels' forward pass, sum of o * do + lse * dlse, along a step s of +-1 in every channel of q, k or v, as
+    8 (f(s / 2) - f(-s / 2)) - (f(s) - f(-s)): what is cubic in the step drops out, 6 s f' is left.  Noise: an output is off
+    by h for its own rounding and h for those of its weights, relatively to the attention over |v| and independently of the
+    others, so f by `noise`; the four evaluations have 8, 8, 1 and 1 of it, together 11.4, taken six times.  The gradient
+    is off by 8 h in the 2-norm (its own rounding, those of o, P and dS, each h / sqrt(3) of terms about as large as their
+    sum).  A check that could miss a factor is none: the bound stays below 5 % of what is compared."""
+    do, q, k, v, o, lse = make(1, Hq, Hkv, 200, D, F16, seed=5)
+    dlse = torch.randn(lse.shape, generator=torch.Generator().manual_seed(6)).cuda()
+    h = 2.0 ** -11
+    size = kvq.prefill_attn_scores(q, k, v.abs(), colscore=False)[0].double()
+    noise = 2 * h * float((size * do.double()).norm())
+
+    def f(x):
+        o, lse, _ = kvq.prefill_attn_scores(*x, colscore=False)
+        return float((o.double() * do.double()).sum() + (lse.double() * dlse.double()).sum())
+
+    for i, g in enumerate(kvq.prefill_attn_bwd(do, q, k, v, o, lse, dlse=dlse)):
+        found = moved = far = 0.0
+        for s, weight in ((2.0 ** -5, 8.0), (2.0 ** -4, -1.0)):
+            step, x = torch.where(g >= 0, s, -s).half(), [q, k, v]
+            ends = []
+            for sign in (1, -1):
+                x[i] = (q, k, v)[i] + sign * step
+                ends.append((f(x), x[i].double()))
+            found += weight * (ends[0][0] - ends[1][0])
+            moved += weight * float((g.double() * (ends[0][1] - ends[1][1])).sum())
+            far += abs(weight) * float((ends[0][1] - ends[1][1]).norm())
+        tol = 6 * 11.4 * noise + 8 * h * float(g.double().norm()) * far
+        assert tol < 0.05 * moved, ("qkv"[i], tol, moved)
+        assert abs(found - moved) <= tol, ("qkv"[i], found, moved, tol)
