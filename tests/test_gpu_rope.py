@@ -494,3 +494,57 @@ def test_gradients_as_views_of_one_array(kvq):
                 [e[:, 2 * i:2 * i + 2, i % 2::2, :64].transpose(1, 2) for i in range(3)]):
         got = c.backward(out=(*out, *w))
         assert all(torch.equal(x, y) for x, y in zip(got, grads))
+
+
+@pytest.mark.parametrize("dtype,D,rot", [(F16, 64, 32), (BF16, 128, 128)])
+def test_training_step_row_by_row(kvq, dtype, D, rot):
+    """The projection's gradient row by row against a float64 chain over the forward pass' stored q, k, v, o and lse.
+    P and dS round to h each, every one by itself: a row of dq is off by h / sqrt(3) S in the 2-norm, S the root of the sum of
+    its squared terms scale dS_ij |k_j| (dk: |q_i|, dv: P_ij |do_i|), and by h of itself for its own rounding.  The norm's
+    gradient passes that on times r |w| at most, a channel of the weights' gradient times |x r|, rows adding up in
+    squares; the result rounds to h (the weights' to float32).  6 times that, and float32's sums: dP and
+    delta add D products each, so that dS is off by D 2^-23 P |do| |v| also where it is 0 (a sequence's first row)."""
+    B, T, Hq, Hkv = 2, 200, 4, 2
+    g = Hq // Hkv
+    c = Case(kvq, B=B, T=T, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, rot=rot, seed=5)
+    q, k, v = c.forward()
+    o, lse, _ = kvq.prefill_attn_scores(q, k, v)
+    do = torch.randn(o.shape, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    d = kvq.prefill_attn_bwd(do, q, k, v, o, lse)
+    got = kvq.qk_norm_rope_bwd(*d, c.q, c.k, c.pos if c.axes > 1 else c.pos[0], c.rope, c.qw, c.kw, c.eps)
+    from oracle import attention as OA
+    f64 = lambda x: np_(x).astype(np.float64)
+    ref = [np.zeros(x.shape) for x in d]
+    S = [np.zeros(x.shape[:3]) for x in d]
+    F = [np.zeros(x.shape[:3]) for x in d]
+    length = lambda x: np.sqrt((x * x).sum(-1))
+    for b in range(B):
+        for u in range(Hkv):
+            at = slice(u * g, (u + 1) * g)
+            Q, K, V, O, DO, L = f64(q[b, at]), f64(k[b, u]), f64(v[b, u]), f64(o[b, at]), f64(do[b, at]), f64(lse[b, at])
+            ref[0][b, at], ref[1][b, u], ref[2][b, u], terms = OA.prefill_backward(Q, K, V, O, DO, L, D ** -0.5)
+            for i, (P, _, _, dS) in enumerate(terms):
+                S[0][b, u * g + i] = np.sqrt((dS * dS) @ (length(K) ** 2)) * D ** -0.5
+                S[1][b, u] += (dS * dS).T @ (length(Q[i]) ** 2) / D
+                S[2][b, u] += (P * P).T @ (length(DO[i]) ** 2)
+                low = D * 2.0 ** -23 * P * length(DO[i])[:, None] * length(V) * D ** -0.5
+                F[0][b, u * g + i] = low @ length(K)
+                F[1][b, u] += low.T @ length(Q[i])
+    S[1], S[2] = np.sqrt(S[1]), np.sqrt(S[2])
+    h = torch.finfo(dtype).eps / 2
+    for i, (raw, w) in enumerate(((c.q, c.qw), (c.k, c.kw))):
+        x, w = f64(raw), f64(w)
+        dx, dw = OR.backward(ref[i], x, w, c.eps, c.angle, False)
+        r = 1 / np.sqrt((x * x).mean(-1) + c.eps)
+        err = (h * (S[i] + length(ref[i])) + F[i]).transpose(0, 2, 1)
+        tol = 6 * (err * r * np.abs(w).max() + h * length(dx))
+        off = length(f64(got[i]) - dx)
+        assert (off <= tol).all(), (off / tol).max()
+        tol = 6 * np.sqrt(((err[..., None] * x * r[..., None]) ** 2).sum((0, 1, 2)))
+        assert (np.abs(f64(got[3 + i]) - dw) <= tol).all()
+        # the bounds are worth something
+        tol = 6 * (err * r * np.abs(w).max() + h * length(dx))
+        assert np.median(tol) / np.median(length(dx)) < (0.02 if dtype == F16 else 0.15)
+    dv = ref[2].transpose(0, 2, 1, 3)
+    off, tol = length(f64(got[2]) - dv), 6 * h * (S[2].transpose(0, 2, 1) + length(dv))
+    assert (off <= tol).all(), (off / tol).max()
