@@ -18,9 +18,12 @@
 //
 // Rounding: P and dS enter their products in the inputs' type.  In bf16 that is 2^-9 of each term, as much as the
 // output's own rounding.  fp16 has the range problem instead: P of long rows and dS of small gradients fall below its
-// normal numbers.  So P is kept times 2^15 (P <= 1) and dS times a power of two c as well, chosen per KV head (dkv) or
-// query head (dq) from the largest |do_i|, |v_j| (2-norms) and |delta_i| so that |do_i.v_j - delta_i| c <= 1; the sums'
-// factors are undone in the epilogue.
+// normal numbers.  So P is kept times 2^15 (P <= 1) and dS times a power of two c as well, so that
+// |do_i.v_j - delta_i| c <= 1 by |do_i|, |v_j| (2-norms) and |delta_i|: for dK, whose sums run over rows, one c for a key
+// tile, from the rows of its query tiles; for dQ one for each row, from |delta_i| and its |do_i|, which the first kernel
+// leaves as four bits below its tile's largest.  The sums' factors are undone in the epilogue.  (With
+// one c for a head, dq of rows whose do is 2^16 below the largest was off by 6e-4 at 4096 tokens and 2e-3 at 16384; 3e-4
+// now, as for all rows.)
 //
 // Bound: the tensor pipe, and for large calls the card's power.  A tile of 128 x 128 pairs at D = 128 takes about 2200
 // clocks in dkv (products 2048) and 1800 in dq (1536).  4 x 32/8 heads x 4096 tokens: 1256 us, 1.09 PFLOP/s of the five
@@ -54,9 +57,10 @@ constexpr uint32_t kTmemCols = 512;
 struct BwdWs {
     float* nlse;        // [B*Hq][Tp] minus lse in base 2, plus the probabilities' shift; -inf behind the last row
     float* delta;       // [B*Hq][Tp]
-    float* do_max;      // [B*Hq][n_t] largest 2-norm of a row of do        (fp16 only, also the next two)
+    float* do_max;      // [B*Hq][n_t] largest 2-norm of a row of do        (fp16 only, also the next three)
     float* dl_max;      // [B*Hq][n_t] largest |delta|
     float* v_max;       // [B*Hkv][n_t] largest 2-norm of a row of v
+    uint32_t* below;    // [B*Hq][n_t][16] four bits a row, row 0 the lowest: its do's 2-norm is at most do_max 2^-bits
 };
 
 struct BwdArgs {
@@ -102,6 +106,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     const bool with_v = AB == 0 && hq % g == 0;
     const int u = b * a.Hkv + hq / g;
     float most_do = 0.0f, most_dl = 0.0f, most_v = 0.0f;
+    __shared__ float row_sq[AB == 0 ? kTile : 1];       // the rows' |do|^2
 #pragma unroll 4
     for (int r0 = 0; r0 < kTile; r0 += kRows) {
         const int i = tile * kTile + r0 + sub;
@@ -135,11 +140,13 @@ __global__ void __launch_bounds__(kPrepThreads)
             const int64_t row = (int64_t)bh * a.T_len + i;
             dl = dot - (glse ? glse[row] : 0.0f);
             const float x = lse[row];
-            if (!isinf(x)) nl = Shift<AB>::value - x * kLog2e;      // a row that saw nothing has no gradient
+            if (!isinf(x)) nl = Shift<AB>::value - x * kLog2e;
+            else dl = sq = 0.0f;                                    // a row that saw nothing has no gradient
         }
         if (l == 0) {
             a.ws.nlse[bh * Tp + i] = nl;
             a.ws.delta[bh * Tp + i] = dl;
+            if (AB == 0) row_sq[r0 + sub] = sq;
         }
         if (AB == 0) {
             most_do = fmaxf(most_do, sq), most_dl = fmaxf(most_dl, fabsf(dl)), most_v = fmaxf(most_v, vv);
@@ -147,6 +154,8 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
     if (AB == 0) {
         __shared__ float red[kPrepThreads / 32][3];
+        __shared__ uint32_t bits[kTile / 8];
+        if (threadIdx.x < kTile / 8) bits[threadIdx.x] = 0;
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) {
             most_do = fmaxf(most_do, __shfl_xor_sync(0xffffffffu, most_do, m));
@@ -158,10 +167,18 @@ __global__ void __launch_bounds__(kPrepThreads)
             x[0] = most_do, x[1] = most_dl, x[2] = most_v;
         }
         __syncthreads();
+        for (int w = 0; w < kPrepThreads / 32; ++w) {
+            most_do = fmaxf(most_do, red[w][0]), most_dl = fmaxf(most_dl, red[w][1]), most_v = fmaxf(most_v, red[w][2]);
+        }
+        if (threadIdx.x < kTile) {
+            const float ratio = most_do / row_sq[threadIdx.x];      // of squares; infinite or NaN for a row of zeros
+            const uint32_t b = ratio < 0x1p30f ? (uint32_t)ilogbf(fmaxf(ratio, 1.0f)) / 2 : 15;
+            atomicOr(&bits[threadIdx.x / 8], b << (4 * (threadIdx.x & 7)));
+        }
+        __syncthreads();
+        if (threadIdx.x < kTile / 8)
+            a.ws.below[((int64_t)bh * a.n_t + tile) * (kTile / 8) + threadIdx.x] = bits[threadIdx.x];
         if (threadIdx.x == 0) {
-            for (int w = 1; w < kPrepThreads / 32; ++w) {
-                most_do = fmaxf(most_do, red[w][0]), most_dl = fmaxf(most_dl, red[w][1]), most_v = fmaxf(most_v, red[w][2]);
-            }
             a.ws.do_max[(int64_t)bh * a.n_t + tile] = sqrtf(most_do);
             a.ws.dl_max[(int64_t)bh * a.n_t + tile] = most_dl;
             if (with_v) a.ws.v_max[(int64_t)u * a.n_t + tile] = sqrtf(most_v);
@@ -169,27 +186,39 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
 }
 
-// The power of two c with |do_i.v_j - delta_i| c <= 1 over query heads [h0, h0 + nh) of unit u (fp16; else 1), by a warp.
-template <int AB> __device__ __forceinline__ float unit_scale(const BwdArgs& a, int h0, int nh, int u, int lane) {
-    if (AB != 0) return 1.0f;
-    float x = 0.0f, d = 0.0f, v = 0.0f;
-#pragma unroll 4
-    for (int i = lane; i < nh * a.n_t; i += 32) {
-        x = fmaxf(x, __ldcg(a.ws.do_max + (int64_t)h0 * a.n_t + i));
-        d = fmaxf(d, __ldcg(a.ws.dl_max + (int64_t)h0 * a.n_t + i));
-    }
-#pragma unroll 4
-    for (int i = lane; i < a.n_t; i += 32) v = fmaxf(v, __ldcg(a.ws.v_max + (int64_t)u * a.n_t + i));
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
-        d = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, m));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
-    }
-    const float most = fmaf(x, v, d);
-    if (!(most > 0.0f)) return 1.0f;
+// The power of two c with `most` c <= 1, most >= |do_i.v_j - delta_i| (fp16; else 1).
+template <int AB> __device__ __forceinline__ float ds_scale(float most) {
+    if (AB != 0 || !(most > 0.0f)) return 1.0f;
     const int e = most < 1e30f ? min(max(ilogbf(most) + 1, -60), 60) : 60;
     return __int_as_float((127 - e) << 23);
+}
+
+__device__ __forceinline__ float warp_most(float x) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+    return x;
+}
+
+// That of key tile kt of unit u and the query tiles at and below it of the nh query heads from h0 on, by a warp.
+template <int AB> __device__ __forceinline__ float key_tile_scale(const BwdArgs& a, int h0, int nh, int u, int kt, int lane) {
+    if (AB != 0) return 1.0f;
+    float x = 0.0f, d = 0.0f;
+    for (int h = 0; h < nh; ++h) {
+#pragma unroll 4
+        for (int i = kt + lane; i < a.n_t; i += 32) {
+            x = fmaxf(x, __ldcg(a.ws.do_max + (int64_t)(h0 + h) * a.n_t + i));
+            d = fmaxf(d, __ldcg(a.ws.dl_max + (int64_t)(h0 + h) * a.n_t + i));
+        }
+    }
+    return ds_scale<AB>(fmaf(warp_most(x), __ldcg(a.ws.v_max + (int64_t)u * a.n_t + kt), warp_most(d)));
+}
+
+// The largest |do_i| |v_j| of query tile qt of head bh with its keys, by a warp.
+__device__ __forceinline__ float query_tile_most(const BwdArgs& a, int bh, int u, int qt, int lane) {
+    float v = 0.0f;
+#pragma unroll 4
+    for (int i = lane; i <= qt; i += 32) v = fmaxf(v, __ldcg(a.ws.v_max + (int64_t)u * a.n_t + i));
+    return __ldcg(a.ws.do_max + (int64_t)bh * a.n_t + qt) * warp_most(v);
 }
 
 // block -> (tile rank, head): heads in groups, all tiles of a group before the next group, the longest tiles of
@@ -209,7 +238,7 @@ template <int D> struct BwdLayout {
     static constexpr uint32_t S0 = 2 * kTileBytes;
     static constexpr uint32_t S1 = S0 + 3 * kTileBytes;
     static constexpr uint32_t STAT = S1 + 2 * kTileBytes;       // dkv: 2 stages of 128 (nlse) and 128 (delta) floats
-    static constexpr uint32_t SCALE = STAT + 2048;              // unit_scale()
+    static constexpr uint32_t SCALE = STAT + 2048;              // dkv: key_tile_scale(); dq: query_tile_most()
     static constexpr uint32_t BAR = SCALE + 16;
     // no alignment slack at D = 128: the kernels require (and check) a 1024-aligned base
     static constexpr uint32_t BYTES = BAR + 256;
@@ -458,7 +487,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         __syncwarp();
     } else if (warp == kSoftWarps + 2) {
         // the scale, and the query rows' statistics, delta times it
-        const float c = unit_scale<AB>(a, h0, g, u, lane);
+        const float c = key_tile_scale<AB>(a, h0, g, u, kt, lane);
         if (lane == 0) *scale = c;
         bool ok = true;
         for (int it = 0; it < n; ++it) {
@@ -720,10 +749,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         }
     } else if (warp == kSoftWarps + 1) {
         constexpr uint32_t idS = idesc_f16(AB, 128, 128, 0), idD = idesc_f16(AB, 128, D, 1);
-        if (AB == 0) {                                  // the scale, while the first tiles are on their way
-            const float c = unit_scale<AB>(a, bh, 1, u, lane);
+        if (AB == 0) {                                  // for the scales, while the first tiles are on their way
+            const float most = query_tile_most(a, bh, u, qt, lane);
             if (lane == 0) {
-                *scale = c;
+                *scale = most;
                 mbar_arrive(BAR(W_CS));
             }
             __syncwarp();
@@ -780,6 +809,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         const uint32_t mine = lanes + 32u * (uint32_t)wg;
         const int64_t stat = (int64_t)bh * a.n_t * kTile + i;
         const float nl = __ldcg(a.ws.nlse + stat), delta = __ldcg(a.ws.delta + stat);
+        const int below = AB == 0 ? __ldcg(a.ws.below + stat / 8) >> (4 * (r & 7)) & 15 : 0;
         const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), nl2 = f2_pack(nl, nl);
         bool ok = true;
         if (kBoth) {
@@ -793,7 +823,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(W_AT));
         if (AB == 0 && !bwd_wait(BAR(W_CS), 0, abort_flag)) ok = false;
-        const float c = AB == 0 && ok ? *scale : 1.0f, nd = -c * delta;
+        const float c = AB == 0 && ok ? ds_scale<AB>(fmaf(*scale, __int_as_float((127 - below) << 23), fabsf(delta))) : 1.0f;
+        const float nd = -c * delta;
         const unsigned long long c2 = f2_pack(c, c), nd2 = f2_pack(nd, nd);
         for (int it = 0; ok && it < n; ++it) {
             const bool diag = it == qt;
@@ -869,6 +900,7 @@ size_t ws_layout(int B, int Hq, int Hkv, int T, char* base, BwdWs* w) {
     BwdWs x;
     x.nlse = take(rows), x.delta = take(rows), x.do_max = take(tiles), x.dl_max = take(tiles);
     x.v_max = take((size_t)B * Hkv * n_t);
+    x.below = reinterpret_cast<uint32_t*>(take(tiles * (kTile / 8)));
     if (w) *w = x;
     return at;
 }

@@ -388,3 +388,52 @@ def test_each_gradient_against_differences(D, Hq, Hkv):
         tol = 6 * 11.4 * noise + 8 * h * float(g.double().norm()) * far
         assert tol < 0.05 * moved, ("qkv"[i], tol, moved)
         assert abs(found - moved) <= tol, ("qkv"[i], found, moved, tol)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("falling", [False, True])
+def test_fp16_rows_of_differing_size(D, falling):
+    """do of one head from 2^7 down to 2^-14, at random from row to row or falling with the position: fp16's scale of dS is
+    a row's own for dQ (up to 2^15 within a tile, |do_i| taken up to 2), and that of the rows from a key's tile on for dK.
+    Bounds as above, 2^-39 M with M_i = 2 max(|do_i|, 2^-15 its tile's largest) max |v| + |delta_i| for dQ, and for dK the
+    largest |do| max |v| + |delta| of the rows from the key's tile on."""
+    T, h = 700, 2.0 ** -11
+    do, q, k, v, _, _ = make(1, 1, 1, T, D, F16, seed=9)
+    e = torch.linspace(7, -14, T) if falling else 7 - 21 * torch.rand(T, generator=torch.Generator().manual_seed(1))
+    do = (do.float() * torch.exp2(e).cuda()[:, None]).half()
+    size = 64.0 if falling else 2.0 ** -6               # dQ goes with k, dK with q: above fp16's subnormal numbers
+    q, k = (q * size).contiguous(), (k / size).contiguous()
+    o, lse, _ = kvq.prefill_attn_scores(q, k, v, colscore=False)
+    dq, dk, dv = kvq.prefill_attn_bwd(do, q, k, v, o, lse)
+    Q, K, V, O, DO, L = (np_(x[0, 0]).astype(np.float64) for x in (q, k, v, o, do, lse))
+    scale = D ** -0.5
+    rq, rk, rv, ((P, dP, delta, dS),) = OA.prefill_backward(Q[None], K, V, O[None], DO[None], L[None], scale)
+    z, n = np.abs(Q @ K.T).max() * scale, 2 * T * U
+    eP = 2 * D * U * scale * (np.abs(Q) @ np.abs(K).T).max() + 4 * U * (z + np.abs(L).max() + 16) + 2.0 ** -22
+    E = P * ((eP + 4 * U) * np.abs(dP - delta) + 2 * D * U * (np.abs(DO) @ np.abs(V).T)
+             + D * U * (np.abs(DO) * np.abs(O)).sum(-1, keepdims=True) + 2 * U * (np.abs(dP) + np.abs(delta)))
+    E += (h + n) * np.abs(dS)
+    length = lambda x: np.sqrt((x * x).sum(-1))
+    tile = np.arange(T) // 128
+    x, most_v, keep = length(DO), length(V).max(), np.tril(np.ones((T, T)))
+    largest = np.array([x[tile == t].max() for t in tile])
+    M = 2 * np.maximum(x, 2.0 ** -15 * largest) * most_v + np.abs(delta[:, 0])
+    tol = scale * (E + 2.0 ** -39 * M[:, None] * keep) @ np.abs(K) + h * np.abs(rq[0]) + 2.0 ** -25
+    off = np.abs(np_(dq[0, 0]) - rq[0])
+    assert (off <= tol).all(), ("dq", (off / tol).max())
+    M = np.array([x[tile >= t].max() * most_v + np.abs(delta[tile >= t]).max() for t in tile])
+    tol = scale * (E + 2.0 ** -39 * M[None] * keep).T @ np.abs(Q) + h * np.abs(rk) + 2.0 ** -25
+    off = np.abs(np_(dk[0, 0]) - rk)
+    assert (off <= tol).all(), ("dk", (off / tol).max())
+    tol = (P * (eP + h + n)).T @ np.abs(DO) + 2.0 ** -40 * np.abs(DO).sum(0) + h * np.abs(rv) + 2.0 ** -25
+    assert (np.abs(np_(dv[0, 0]) - rv) <= tol).all(), "dv"
+
+
+def test_rows_without_gradient_leave_fp16s_scale():
+    """Rows whose lse is -inf count for nothing, whatever their do: the others come out bit for bit as beside zeros."""
+    do, q, k, v, o, lse = make(1, 2, 1, 300, 64, F16, size=2.0 ** -10)
+    lse[0, :, 100:140] = -math.inf
+    do[0, :, 100:140] = 0
+    want = kvq.prefill_attn_bwd(do, q, k, v, o, lse)
+    do[0, :, 100:140] = 3e4
+    assert all(torch.equal(a, b) for a, b in zip(kvq.prefill_attn_bwd(do, q, k, v, o, lse), want))
