@@ -8,9 +8,7 @@
 // float32 buffer, and a call repeats itself bit for bit.  The price is that S and dO V^T are computed in both (seven
 // products for the five of the formulas).
 //   dkv: CTA = (KV head, key tile), over the query heads of its group and their query tiles at and below the diagonal,
-//        S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and dK += dS^T Q with P^T and dS^T read from tensor memory, where
-//        they replace S^T and dP^T.  The tensor pipe runs what one thread issues in order, so S^T of the next tile may
-//        be issued right behind the dV product that reads P^T from its place.
+//        S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and dK += dS^T Q with P^T and dS^T read from tensor memory.
 //   dq:  CTA = (query head, query tile), over the key tiles up to the diagonal: S = Q K^T, dP = dO V^T, dQ += dS K.
 // Sixteen warps do the exponentials and dS (four warpgroups, each a quarter of a tile's columns), one warp issues the
 // copies, one the products, in dkv one brings the rows' lse and delta.
@@ -411,8 +409,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    // S^T, dP^T, dV, dK; packed P^T and dS^T replace S^T and dP^T, every 32 queries in the first 16 of their columns
+    // S^T, dP^T, dV, dK; packed P^T and dS^T beside them at D = 64 (32 queries in 16 columns), at D = 128, where tensor
+    // memory has no more room, in their place (32 queries in the first 16 of their 32 columns)
+    constexpr bool kBeside = D == 64;
+    constexpr uint32_t kStep = kBeside ? 16 : 32;
     const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
+    const uint32_t tPw = kBeside ? tmem + 384 : tS, tDw = kBeside ? tmem + 448 : tP;
 
     if (warp == kSoftWarps) {
         if (lane == 0 && n > 0) {
@@ -449,26 +451,34 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         auto g_there = [&](int it, int s) { return wait(V_GF + s, it / 2); };
         // One tile, PH = it mod 6: the stages are constants, so that descriptors stay in uniform registers (computed from
         // the tile's number they made a product's issue three times as long).
-        // The next S^T and dP^T are issued behind the product that reads what replaced them.  A wait costs one to three
-        // products' time even where there is nothing to wait for, and the tensor pipe has about four products ahead of it:
-        // no two waits follow one another without products between.
+        // The next S^T and dP^T are issued behind dV and dK.  Only products of one sum are sure to run in the order of their
+        // issue, so what replaces an operand in tensor memory waits until the product that reads it is done.  At D = 64 that
+        // costs nothing: P^T and dS^T lie beside S^T and dP^T, and the softmax warps write the next ones after V_SF and V_DF,
+        // whose commits cover the dV and dK before them.  At D = 128 they lie in the place of S^T and dP^T, and the issuing
+        // lane waits (4 x 32/8 x 4096: 5 % of the call; dK before the next S^T, so that the pipe has work during the waits:
+        // 8 %, the softmax warps then have too little time).
+        // A wait costs one to three products' time even where there is nothing to wait for, and the tensor pipe has about
+        // four products ahead of it: else no two waits follow one another without products between.
         auto step = [&](auto phase, int it) -> bool {
             constexpr int PH = decltype(phase)::value, q0 = PH % 3, q1 = (PH + 1) % 3, q2 = (PH + 2) % 3, g0 = PH & 1, g1 = g0 ^ 1;
             const bool more = it + 1 < n;
             if (!wait(V_PR, PH)) return false;
             tc_fence_after();
-            products_mn<32>(tDV, tS, sG + (uint32_t)g0 * kTileBytes, idD, it > 0);          // dV += P^T dO
+            products_mn<kStep>(tDV, tPw, sG + (uint32_t)g0 * kTileBytes, idD, it > 0);      // dV += P^T dO
             tc_commit(BAR(V_GE + g0));
             if (more) {
-                if (!g_there(it + 1, g1)) return false;
+                if (!g_there(it + 1, g1) || (!kBeside && !wait(V_GE + g0, it / 2))) return false;
                 scores(q1);
             }
             if (!wait(V_DR, PH)) return false;
             tc_fence_after();
-            products_mn<32>(tDK, tP, sQ + (uint32_t)q0 * kTileBytes, idD, it > 0);          // dK += dS^T Q
+            products_mn<kStep>(tDK, tDw, sQ + (uint32_t)q0 * kTileBytes, idD, it > 0);      // dK += dS^T Q
             tc_commit(BAR(V_QE + q0));
             if (it + 2 < n && !q_there(it + 2, q2)) return false;
-            if (more) grads(g1);
+            if (more) {
+                if (!kBeside && !wait(V_QE + q0, it / 3)) return false;
+                grads(g1);
+            }
             return true;
         };
         if (elect_one()) {
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         // broadcasts of 32 took as many cycles of shared memory as the tensor pipe's operands left).
         const int wg = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t mine = lanes + 32u * (uint32_t)wg;
+        const uint32_t mine = lanes + 32u * (uint32_t)wg, packed = lanes + kStep * (uint32_t)wg;
         const int first = 32 * wg + 2 * (lane & 3) - (32 * (warp & 3) + (lane >> 2));    // query - key of element 0
         const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2);
         float c = 1.0f;
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             if (diag) mask16(p, first), mask16(p + 16, first + 16);
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = Pack2<T>::pack(p[2 * i], p[2 * i + 1]);
-            store_frags(tS + mine, w);
+            store_frags(tPw + packed, w);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(BAR(V_PR));
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             if (diag) mask16(d, first), mask16(d + 16, first + 16);
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = Pack2<T>::pack(d[2 * i], d[2 * i + 1]);
-            store_frags(tP + mine, w);
+            store_frags(tDw + packed, w);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
