@@ -4,9 +4,9 @@
 //   dS_ij = P_ij (do_i.v_j - delta_i)
 //   dV_j = sum_i P_ij do_i;   dK_j = sigma sum_i dS_ij q_i;   dQ_i = sigma sum_j dS_ij k_j
 //
-// Two kernels over 128 x 128 tiles, so that every sum stays in one CTA's tensor memory in a fixed order: no atomics, no
-// float32 buffer, and a call repeats itself bit for bit.  The price is that S and dO V^T are computed in both (seven
-// products for the five of the formulas).
+// Two kernels over 128 x 128 tiles, so that every sum stays in one CTA's tensor memory (where key tiles are few, a
+// cluster's, added up in the order of its CTAs) in a fixed order: no atomics, no float32 buffer, and a call repeats itself
+// bit for bit.  The price is that S and dO V^T are computed in both (seven products for the five of the formulas).
 //   dkv: CTA = (KV head, key tile), over the query heads of its group and their query tiles at and below the diagonal,
 //        S^T = K Q^T, dP^T = V dO^T, then dV += P^T dO and dK += dS^T Q with P^T and dS^T read from tensor memory.
 //   dq:  CTA = (query head, query tile), over the key tiles up to the diagonal: S = Q K^T, dP = dO V^T, dQ += dS K.
@@ -14,8 +14,9 @@
 // copies, one the products, in dkv one brings the rows' lse and delta.
 // A first kernel computes delta and brings lse to base 2.
 //
-// Rounding: P and dS enter their products in the inputs' type.  In bf16 that is 2^-9 of each term, as much as the
-// output's own rounding.  fp16 has the range problem instead: P of long rows and dS of small gradients fall below its
+// Rounding: P and dS enter their products in the inputs' type, which the products take: up to half a step of each term
+// (2^-8 in bf16), as much as the output's own rounding; against float64 a gradient is off by 2.4e-3 in bf16 and 2.9e-4 in
+// fp16, where one computed in float32 and rounded at the end is off by 1.7e-3 and 2.1e-4.  fp16 has the range problem instead: P of long rows and dS of small gradients fall below its
 // normal numbers.  So P is kept times 2^15 (P <= 1) and dS times a power of two c as well, so that
 // |do_i.v_j - delta_i| c <= 1 by |do_i|, |v_j| (2-norms) and |delta_i|: for dK, whose sums run over rows, one c for a key
 // tile, from the rows of its query tiles; for dQ one for each row, from |delta_i| and its |do_i|, which the first kernel
@@ -23,10 +24,10 @@
 // one c for a head, dq of rows whose do is 2^16 below the largest was off by 6e-4 at 4096 tokens and 2e-3 at 16384; 3e-4
 // now, as for all rows.)
 //
-// Bound: the tensor pipe, and for large calls the card's power.  A tile of 128 x 128 pairs at D = 128 takes about 2200
-// clocks in dkv (products 2048) and 1800 in dq (1536).  4 x 32/8 heads x 4096 tokens: 1256 us, 1.09 PFLOP/s of the five
-// products, 1.53 of the seven; 8/2 x 16384: 1171 us, 1.17 and 1.64.  At D = 64 the softmax warps are the longer side:
-// 8 x 16 heads x 2048 tokens 320 us.
+// Bound: the tensor pipe and in dkv at D = 128 the waits between its products, and for large calls the card's power.  A tile
+// of 128 x 128 pairs at D = 128 takes about 2600 clocks in dkv (products 2048) and 1800 in dq (1536).  4 x 32/8 heads x
+// 4096 tokens: 1320 us, 1.04 PFLOP/s of the five products, 1.46 of the seven; 8/2 x 16384: 1235 us, 1.11 and 1.56.  At
+// D = 64 the softmax warps are the longer side: 8 x 16 heads x 2048 tokens 322 us.
 //
 // Every mbarrier wait is bounded; a CTA that gives up drains its copies and products, frees TMEM, stores nothing and
 // records KVQ_ETIMEOUT in the device status word.
@@ -923,9 +924,9 @@ int head_group(int heads, long long bytes) {
 }
 
 // CTAs that share a key tile in dkv (a cluster that adds up its sums through shared memory).  In thousands of clocks, a
-// tile takes about 2.3 in dkv and 1.9 in dq, a CTA's start and end 6 and with a cluster's sum 16; the call takes at least
+// tile takes about 2.3 (D = 128: 2.6) in dkv and 1.9 in dq, a CTA's start and end 6 and with a cluster's sum 16; the call takes at least
 // its longest CTA and, as dq fills the SMs that dkv leaves, all work over the SMs.  The size with the least such bound.
-// (32/4 heads x 1024 tokens: 4 CTAs 45 us, one 92; 2 heads x 256: dkv alone 10 us with one, 14 with 8.)
+// (32/4 heads x 1024 tokens: 4 CTAs 48 us, one 92; 2 heads x 256: dkv alone 10 us with one, 14 with 8.)
 int cluster_size(int units, int g, int n_t) {
     const int sms = device_sms(nullptr);
     const double tiles = 0.5 * units * g * n_t * (n_t + 1.0), ctas = (double)units * n_t;

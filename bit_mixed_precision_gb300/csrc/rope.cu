@@ -6,8 +6,9 @@
 //   backward: dy = the pairs of d turned by -phi;  dw = sum over rows of dy x r;  g = dy w;
 //             dx = r (g - (x r) mean(g (x r)))
 // Angles: f is kept as a 64-bit fraction of a turn, so pos * f modulo a turn is one wrapping integer product, exact for
-// every int32 position but for the fraction's own 2^-64 (positions of 2^20 lose 2^-44 of a turn); what is left, in
-// [-1/2, 1/2) turns, becomes float32 and cosine and sine.
+// every int32 position but for the fraction's own error times the position (2^-65 of a turn for a fraction rounded once;
+// one formed in float64 has 2^-52 of f / 2 pi, so that f = 1 at position 2^20 loses at most 2^-34 of a turn); what is left,
+// in [-1/2, 1/2) turns, becomes float32 and cosine and sine.
 // Bound: HBM, each row is read and written once.  D / 16 lanes share a row, each with the two 16-byte pieces that hold
 // the two sides of its eight pairs, so that the rotation needs no exchange and the norm's sum two or three shuffles; a
 // warp holds 64 / (D / 8) rows of one token at a time, and the token's angles are computed once for all heads, a share
@@ -15,7 +16,7 @@
 // copies: 5 KB a warp in flight (backward 8) without registers to hold it.
 // All arithmetic is float32, two numbers to an instruction; an output is rounded once.
 // Measured: 4 x 16384 tokens of 32/8 heads of 128 in bf16 236 us, 6.8 TB/s (loads to registers two groups ahead: 318);
-// their gradient, 16 x 4096 tokens, 384 us, 5.9 TB/s (eight sines a lane and weights in registers: 523).  One token
+// their gradient, 16 x 4096 tokens, 375 us, 6.1 TB/s (eight sines a lane and weights in registers: 523).  One token
 // 2.8 us.
 #include <algorithm>
 #include <atomic>

@@ -861,6 +861,8 @@ def block8_evict(cache, keep, n_first=1, n_last=1, n_evicted=None, stream=None):
 
 
 # ----------------------------------------------------------- norm and rotation per head
+# The calls here and prefill_attn_bwd work on plain tensors, like all of this module: autograd records nothing, also where
+# inputs require gradients.  A training step calls the backward operators itself or wraps both in a torch.autograd.Function.
 
 @dataclass
 class Rope:
@@ -876,7 +878,7 @@ class Rope:
 def make_rope(D, rot=None, base=10000.0, inv_freq=None, axis=None, interleaved=False):
     """A Rope of the first ``rot`` channels (all by default; a multiple of 16): pair i of them turns by
     pos * inv_freq[i] radians, inv_freq[i] = base ** (-2 i / rot) by default (floats, or a float64 tensor, which is
-    read on the host).  ``axis``: each pair's position axis (0 to 3; 0 by default).  Pairs are the
+    read on the host; divided by 2 pi in float64, so an angle is off by up to 2^-52 of itself and float32's 2^-24).  ``axis``: each pair's position axis (0 to 3; 0 by default).  Pairs are the
     channels (i, i + rot / 2), or (2 i, 2 i + 1) if ``interleaved``."""
     if rot is None:
         rot = D if inv_freq is None else 2 * len(inv_freq)

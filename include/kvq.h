@@ -545,9 +545,10 @@ kvq_status block8_evict(kvq_block8* c, const int32_t* keep, int n_first, int n_l
  * with interleaved != 0.  Pair i turns by pos * f_i radians, where pos is the
  * token's position on axis[i] (text: one axis; images and clips: rows,
  * columns, time) and f_i is given as a fraction of a turn,
- *   turn[i] = RN(2^64 f_i / (2 pi)) mod 2^64,
- * so that the angle modulo a turn is exact for every int32 position.  The
- * struct is read during the call only. */
+ *   turn[i] = 2^64 f_i / (2 pi) mod 2^64, rounded to a whole number,
+ * so that the angle modulo a turn is off by no more than pos times what turn[i]
+ * is off by, for every int32 position.  (The Python binding forms f_i / (2 pi)
+ * in float64, to 2^-52 of itself.)  The struct is read during the call only. */
 #define KVQ_ROPE_MAX_AXES 4
 typedef struct {
     int32_t rot;            /* rotated channels: a multiple of 16 in [0, D] */
