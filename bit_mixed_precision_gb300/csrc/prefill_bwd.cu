@@ -16,13 +16,13 @@
 //
 // Rounding: P and dS enter their products in the inputs' type, which the products take: up to half a step of each term
 // (2^-8 in bf16), as much as the output's own rounding; against float64 a gradient is off by 2.4e-3 in bf16 and 2.9e-4 in
-// fp16, where one computed in float32 and rounded at the end is off by 1.7e-3 and 2.1e-4.  fp16 has the range problem instead: P of long rows and dS of small gradients fall below its
-// normal numbers.  So P is kept times 2^15 (P <= 1) and dS times a power of two c as well, so that
-// |do_i.v_j - delta_i| c <= 1 by |do_i|, |v_j| (2-norms) and |delta_i|: for dK, whose sums run over rows, one c for a key
-// tile, from the rows of its query tiles; for dQ one for each row, from |delta_i| and its |do_i|, which the first kernel
-// leaves as four bits below its tile's largest.  The sums' factors are undone in the epilogue.  (With
-// one c for a head, dq of rows whose do is 2^16 below the largest was off by 6e-4 at 4096 tokens and 2e-3 at 16384; 3e-4
-// now, as for all rows.)
+// fp16, where one computed in float32 and rounded at the end is off by 1.7e-3 and 2.1e-4.  fp16 has a problem of range
+// besides: P of long rows and dS of small gradients fall below its normal numbers.  So P is kept times 2^15 (P <= 1) and
+// dS times a power of two c as well, so that |do_i.v_j - delta_i| c <= 1 by |do_i|, |v_j| (2-norms) and |delta_i|: for dK,
+// whose sums run over rows, one c for a key tile, from the rows of its query tiles; for dQ one for each row, from
+// |delta_i| and its |do_i|, which the first kernel leaves as four bits below its tile's largest.  The sums' factors are
+// undone in the epilogue.  (With one c for a head, dq of rows whose do is 2^16 below the largest was off by 6e-4 at 4096
+// tokens and 2e-3 at 16384; 3e-4 now, as for all rows.)
 //
 // Bound: the tensor pipe and in dkv at D = 128 the waits between its products, and for large calls the card's power.  A tile
 // of 128 x 128 pairs at D = 128 takes about 2600 clocks in dkv (products 2048) and 1800 in dq (1536).  4 x 32/8 heads x
@@ -924,8 +924,9 @@ int head_group(int heads, long long bytes) {
 }
 
 // CTAs that share a key tile in dkv (a cluster that adds up its sums through shared memory).  In thousands of clocks, a
-// tile takes about 2.3 (D = 128: 2.6) in dkv and 1.9 in dq, a CTA's start and end 6 and with a cluster's sum 16; the call takes at least
-// its longest CTA and, as dq fills the SMs that dkv leaves, all work over the SMs.  The size with the least such bound.
+// tile takes about 2.3 (D = 128: 2.6) in dkv and 1.9 in dq, a CTA's start and end 6 and with a cluster's sum 16; the call
+// takes at least its longest CTA and, as dq fills the SMs that dkv leaves, all work over the SMs.  The size with the least
+// such bound.
 // (32/4 heads x 1024 tokens: 4 CTAs 48 us, one 92; 2 heads x 256: dkv alone 10 us with one, 14 with 8.)
 int cluster_size(int units, int g, int n_t) {
     const int sms = device_sms(nullptr);
